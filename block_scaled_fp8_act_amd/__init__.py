@@ -44,11 +44,24 @@ tensors' dtype:
     rowwise_gemm(x_q, x_scale, w_q, w_scale) -> y bf16 [M,N]
     linear_rowwise(x, w_q, w_scale) -> y bf16 [M,N]
     swiglu_act_quant(gate_up, scale_fmt) -> (x_q uint8 [M,I], x_scale [M, I/128])
+
+Around the expert products and the shared projections (low-level names
+fp8blk_*, same order of arguments as the wrappers' with the outputs last):
+
+    moe_route(logits, k, mask, renormalize, loss_coef) -> Routing(ids, weights, counts, rows, loss, ...)
+    moe_route_backward(logits, routing, d_weights, d_loss) -> d_logits [T,E]
+    group_rows(ids, groups) -> RowGroups(order, positions, offsets)   (offsets feed grouped_block_gemm)
+    moe_combine(y, weights, positions, base) -> out bf16 [T,N]
+    moe_combine_backward(d_out, y, weights, positions, offsets) -> (d_y, d_weights)
+    lora_add(base, x, a, b, ids, scale, groups, out) -> out bf16 [T,N]
+    lora_linear(x, w_q, w_scale, a, b, ids, scale, groups) -> y bf16 [M,N]   (linear, then its adapters)
+    moe_experts(x, routing, gate_up_q, gate_up_s, down_q, down_s, base) -> y bf16 [T,N]
 """
 from __future__ import annotations
 
 import ctypes
 import os
+from typing import NamedTuple
 
 import torch
 
@@ -65,6 +78,11 @@ __all__ = [
     "fp8_swiglu_act_quant_ue8m0", "swiglu_act_quant",
     "weight_block_quant",
     "act_quant_group", "block_gemm", "grouped_block_gemm", "linear", "SCALE_FMTS",
+    "Routing", "RowGroups", "fp8blk_moe_route", "fp8blk_moe_route_backward",
+    "fp8blk_group_rows", "fp8blk_moe_combine", "fp8blk_moe_combine_backward",
+    "fp8blk_lora_add", "moe_route", "moe_route_backward", "group_rows", "moe_combine",
+    "moe_combine_backward", "lora_add", "lora_linear", "moe_experts",
+    "MAX_GROUPS", "MAX_TOPK", "MAX_RANK",
 ]
 
 BLOCK = 128
@@ -74,6 +92,7 @@ _lib = None
 
 OK, ERR_NULL, ERR_SHAPE, ERR_ALIGN, ERR_DEVICE, ERR_LAUNCH, ERR_SCRATCH = range(7)
 SCRATCH_BYTES = 16 * 1024 * 1024 + 64 * 1024     # FP8BLK_SCRATCH_BYTES
+MAX_GROUPS, MAX_TOPK, MAX_RANK = 1024, 32, 256   # FP8BLK_MAX_*
 
 
 class Fp8BlkError(RuntimeError):
@@ -101,6 +120,7 @@ def load_library() -> ctypes.CDLL:
             "`python -m block_scaled_fp8_act_amd.build` (no CPU fallback exists)")
     lib = ctypes.CDLL(_LIB_PATH)
     vp, i64, i32 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32
+    ci, sz = ctypes.c_int, ctypes.c_size_t
     sigs = {
         "fp8_weight_block_quant": [vp, i64, i64, vp, vp, vp],
         "fp8_act_quant_group": [vp, i64, i64, vp, vp, vp],
@@ -121,6 +141,15 @@ def load_library() -> ctypes.CDLL:
         "fp8_block_gemm_ue8m0": [vp, vp, vp, vp, i64, i64, i64, vp, vp],
         "fp8_block_gemm_ue8m0_ws": [vp, vp, vp, vp, i64, i64, i64, vp, vp, ctypes.c_size_t, vp],
         "fp8_grouped_block_gemm_ue8m0": [vp, vp, vp, vp, vp, i32, i64, i64, i64, vp, vp],
+        "fp8blk_moe_route": [vp, ci, vp, i64, i32, i32, ci, ctypes.c_float, vp, vp, vp, vp, vp,
+                             vp, sz, vp],
+        "fp8blk_moe_route_backward": [vp, ci, i64, i32, i32, ci, ctypes.c_float, vp, vp, vp, vp,
+                                      vp, vp, vp, vp],
+        "fp8blk_group_rows": [vp, i64, i32, vp, vp, vp, vp, sz, vp],
+        "fp8blk_moe_combine": [vp, i64, vp, vp, vp, i64, i32, i64, vp, vp],
+        "fp8blk_moe_combine_backward": [vp, vp, i64, vp, vp, vp, i64, i32, i64, vp, vp, vp],
+        "fp8blk_lora_add": [vp, i64, vp, i64, vp, vp, vp, vp, vp, vp, i64, i64, i64, i32, i32,
+                            vp, i64, vp, sz, vp],
     }
     for name, args in sigs.items():
         fn = getattr(lib, name)
@@ -129,6 +158,11 @@ def load_library() -> ctypes.CDLL:
     for name in ("fp8_block_gemm_workspace_bytes", "fp8_block_gemm_ue8m0_workspace_bytes"):
         getattr(lib, name).argtypes = [i64, i64, i64]
         getattr(lib, name).restype = ctypes.c_size_t
+    for name, args in {"fp8blk_moe_route_workspace_bytes": [i64, i32],
+                       "fp8blk_group_rows_workspace_bytes": [i64, i32],
+                       "fp8blk_lora_add_workspace_bytes": [i64, i64, i32, i32, ci]}.items():
+        getattr(lib, name).argtypes = args
+        getattr(lib, name).restype = sz
     lib.fp8blk_status_string.argtypes = [ctypes.c_int]
     lib.fp8blk_status_string.restype = ctypes.c_char_p
     lib.fp8blk_abi_version.argtypes = []
@@ -583,3 +617,291 @@ def linear_rowwise(x, w_q, w_scale):
     row-scaled GEMM."""
     x_q, x_s = rowwise_quant(x)
     return rowwise_gemm(x_q, x_s, w_q, w_scale)
+
+
+# --------------------------------------------------------------------------
+# routing, rows by group, combine, adapters
+
+class Routing(NamedTuple):
+    """What moe_route found, as moe_route_backward and group_rows take it."""
+    ids: torch.Tensor        # [T,k] int32, -1 in unused slots
+    weights: torch.Tensor    # [T,k] fp32
+    counts: torch.Tensor     # [E] int32
+    rows: torch.Tensor       # [1] int32: rows routed
+    loss: torch.Tensor | None   # fp32 scalar
+    loss_coef: float
+    renormalize: bool
+
+
+class RowGroups(NamedTuple):
+    """Rows listed by group: order[offsets[g]:offsets[g+1]] are group g's."""
+    order: torch.Tensor      # [R] int32
+    positions: torch.Tensor  # as the ids' shape, int32, -1 for rows of no group
+    offsets: torch.Tensor    # [G+1] int32
+
+
+_LOGITS = {torch.float32: 0, torch.bfloat16: 1}    # FP8BLK_F32, FP8BLK_BF16
+_I32 = (torch.int32,)
+_BF16 = (torch.bfloat16,)
+
+
+def _rows_2d(t, name):
+    """A bf16 matrix whose rows are contiguous and a fixed stride apart; the stride."""
+    if not isinstance(t, torch.Tensor) or t.dtype != torch.bfloat16:
+        raise TypeError(f"{name} must be a bfloat16 torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a device (cuda/hip) tensor")
+    if t.dim() != 2:
+        raise ValueError(f"{name} must have 2 dimensions, got {t.dim()}")
+    rows, cols = t.shape
+    if rows <= 1 or cols == 0:
+        if cols > 1 and t.stride(1) != 1:
+            raise ValueError(f"{name}'s rows must be contiguous")
+        return cols
+    if (cols > 1 and t.stride(1) != 1) or t.stride(0) < cols:
+        raise ValueError(f"{name}'s rows must be contiguous and not overlap")
+    return t.stride(0)
+
+
+def _same_device(first, *others):
+    """All on the current device, where the kernels are launched."""
+    d = first.get_device()
+    for t in others:
+        if t is not None and t.get_device() != d:
+            raise ValueError("all tensors must be on one device")
+    if d != torch.cuda.current_device():
+        raise ValueError(f"the tensors are on cuda:{d}, which is not the current device")
+
+
+def _work(need, device):
+    return torch.empty(need, dtype=torch.uint8, device=device) if need else None
+
+
+def _bytes(t):
+    return t.numel() * t.element_size() if t is not None else 0
+
+
+def fp8blk_moe_route(logits, mask, renormalize, loss_coef, ids, weights, counts, rows, loss,
+                     workspace=None):
+    """Routing into preallocated outputs; k is ids' width, ``mask`` (uint8 or
+    bool [T]) and ``loss`` (fp32, one value) may be None, ``workspace`` holds
+    fp8blk_moe_route_workspace_bytes(T, E) bytes."""
+    _need(logits, "logits", tuple(_LOGITS), 2)
+    T, E = logits.shape
+    _need(ids, "ids", _I32, 2); _need(weights, "weights", _F32, 2)
+    _need(counts, "counts", _I32, 1); _need(rows, "rows", _I32)
+    k = ids.shape[1]
+    _shape_eq(ids, (T, k), "ids"); _shape_eq(weights, (T, k), "weights")
+    _shape_eq(counts, (E,), "counts")
+    if rows.numel() != 1 or (loss is not None and loss.numel() != 1):
+        raise ValueError("rows and loss hold one value each")
+    if mask is not None:
+        _need(mask, "mask", (torch.bool, torch.uint8), 1)
+        _shape_eq(mask, (T,), "mask")
+    if loss is not None:
+        _need(loss, "loss", _F32)
+    _same_device(logits, mask, ids, weights, counts, rows, loss, workspace)
+    _check(load_library().fp8blk_moe_route(
+        logits.data_ptr(), _LOGITS[logits.dtype], _ptr(mask), T, E, k, int(renormalize), loss_coef,
+        ids.data_ptr(), weights.data_ptr(), counts.data_ptr(), rows.data_ptr(), _ptr(loss),
+        _ptr(workspace), _bytes(workspace), _stream()), "fp8blk_moe_route")
+
+
+def fp8blk_moe_route_backward(logits, routing, d_weights, d_loss, d_logits):
+    """Gradient of the logits into d_logits; d_weights [T,k] or d_loss (one
+    value) may be None."""
+    _need(logits, "logits", tuple(_LOGITS), 2); _need(d_logits, "d_logits", (logits.dtype,), 2)
+    T, E = logits.shape
+    k = routing.ids.shape[1]
+    _shape_eq(routing.ids, (T, k), "routing.ids")
+    _shape_eq(routing.counts, (E,), "routing.counts")
+    _shape_eq(d_logits, (T, E), "d_logits")
+    if d_weights is not None:
+        _need(d_weights, "d_weights", _F32, 2)
+        _shape_eq(d_weights, (T, k), "d_weights")
+    if d_loss is not None:
+        _need(d_loss, "d_loss", _F32)
+        if d_loss.numel() != 1:
+            raise ValueError("d_loss holds one value")
+    _same_device(logits, routing.ids, d_weights, d_loss, d_logits)
+    _check(load_library().fp8blk_moe_route_backward(
+        logits.data_ptr(), _LOGITS[logits.dtype], T, E, k, int(routing.renormalize),
+        routing.loss_coef, routing.ids.data_ptr(), routing.weights.data_ptr(),
+        routing.counts.data_ptr(), routing.rows.data_ptr(), _ptr(d_weights), _ptr(d_loss),
+        d_logits.data_ptr(), _stream()), "fp8blk_moe_route_backward")
+
+
+def fp8blk_group_rows(ids, order, positions, offsets, workspace=None):
+    """Rows by group into preallocated outputs; G is offsets' length less one,
+    ``workspace`` holds fp8blk_group_rows_workspace_bytes(R, G) bytes."""
+    _need(ids, "ids", _I32); _need(order, "order", _I32)
+    _need(positions, "positions", _I32); _need(offsets, "offsets", _I32, 1)
+    R = ids.numel()
+    if order.numel() != R or positions.numel() != R:
+        raise ValueError("order and positions have an entry per row")
+    _same_device(ids, order, positions, offsets, workspace)
+    _check(load_library().fp8blk_group_rows(
+        ids.data_ptr(), R, offsets.numel() - 1, order.data_ptr(), positions.data_ptr(),
+        offsets.data_ptr(), _ptr(workspace), _bytes(workspace), _stream()), "fp8blk_group_rows")
+
+
+def fp8blk_moe_combine(y, weights, positions, base, out):
+    """Weighted sums of y's rows into out; base may be None or out itself."""
+    _need(y, "y", _BF16, 2); _need(weights, "weights", _F32, 2)
+    _need(positions, "positions", _I32, 2); _need(out, "out", _BF16, 2)
+    T, k = weights.shape
+    R, N = y.shape
+    _shape_eq(positions, (T, k), "positions"); _shape_eq(out, (T, N), "out")
+    if base is not None:
+        _need(base, "base", _BF16, 2)
+        _shape_eq(base, (T, N), "base")
+    _same_device(y, weights, positions, base, out)
+    _check(load_library().fp8blk_moe_combine(
+        y.data_ptr(), R, weights.data_ptr(), positions.data_ptr(), _ptr(base), T, k, N,
+        out.data_ptr(), _stream()), "fp8blk_moe_combine")
+
+
+def fp8blk_moe_combine_backward(d_out, y, weights, positions, rows_used, d_y, d_weights):
+    """Gradients into d_y and d_weights; the last entry of ``rows_used`` (an
+    int32 tensor, e.g. RowGroups.offsets) is the number of y's rows in use."""
+    _need(d_out, "d_out", _BF16, 2); _need(y, "y", _BF16, 2)
+    _need(weights, "weights", _F32, 2); _need(positions, "positions", _I32, 2)
+    _need(rows_used, "rows_used", _I32)
+    _need(d_y, "d_y", _BF16, 2); _need(d_weights, "d_weights", _F32, 2)
+    T, k = weights.shape
+    R, N = y.shape
+    _shape_eq(d_out, (T, N), "d_out"); _shape_eq(positions, (T, k), "positions")
+    _shape_eq(d_y, (R, N), "d_y"); _shape_eq(d_weights, (T, k), "d_weights")
+    if rows_used.numel() < 1:
+        raise ValueError("rows_used holds one value at least")
+    _same_device(d_out, y, weights, positions, rows_used, d_y, d_weights)
+    _check(load_library().fp8blk_moe_combine_backward(
+        d_out.data_ptr(), y.data_ptr(), R, weights.data_ptr(), positions.data_ptr(),
+        rows_used.data_ptr() + 4 * (rows_used.numel() - 1), T, k, N, d_y.data_ptr(),
+        d_weights.data_ptr(), _stream()), "fp8blk_moe_combine_backward")
+
+
+def fp8blk_lora_add(base, x, a, b, ids, scale, groups, out, workspace):
+    """Adapters into out; base, scale and groups may be None; base and out, and
+    x, may be column slices of wider matrices.  ``workspace`` holds
+    fp8blk_lora_add_workspace_bytes(T, K, r, L, listed) bytes."""
+    ldx, ldo = _rows_2d(x, "x"), _rows_2d(out, "out")
+    _need(a, "a", _BF16, 3); _need(b, "b", _BF16, 3); _need(ids, "ids", _I32, 1)
+    T, K = x.shape
+    L, r, K2 = a.shape
+    N = out.shape[1]
+    if K2 != K:
+        raise ValueError("x and a disagree on K")
+    _shape_eq(b, (L, N, r), "b"); _shape_eq(ids, (T,), "ids")
+    _shape_eq(out, (T, N), "out")
+    ldb = 0
+    if base is not None:
+        ldb = _rows_2d(base, "base")
+        _shape_eq(base, (T, N), "base")
+    if scale is not None:
+        _need(scale, "scale", _F32, 1)
+        _shape_eq(scale, (L,), "scale")
+    order = offsets = None
+    if groups is not None:
+        order, offsets = groups.order, groups.offsets
+        _need(order, "groups.order", _I32, 1); _need(offsets, "groups.offsets", _I32, 1)
+        _shape_eq(order, (T,), "groups.order"); _shape_eq(offsets, (L + 1,), "groups.offsets")
+    _same_device(x, base, a, b, ids, scale, order, out, workspace)
+    _check(load_library().fp8blk_lora_add(
+        _ptr(base), ldb, x.data_ptr(), ldx, a.data_ptr(), b.data_ptr(), ids.data_ptr(),
+        _ptr(scale), _ptr(order), _ptr(offsets), T, K, N, r, L, out.data_ptr(), ldo,
+        _ptr(workspace), _bytes(workspace), _stream()), "fp8blk_lora_add")
+
+
+def moe_route(logits, k, mask=None, renormalize=True, loss_coef=None):
+    """The k experts of each token with their softmax weights, and how many
+    rows each expert gets; with ``loss_coef`` also the balance loss
+    loss_coef * sum_e (counts_e E / (k n)) * mean_t p_te.  Rows with mask 0,
+    and experts with logit -inf, are left out; unused slots have id -1 and
+    weight 0."""
+    _need(logits, "logits", tuple(_LOGITS), 2)
+    T, E = logits.shape
+    if not 1 <= k <= E:
+        raise ValueError(f"k must be between 1 and the number of experts, got {k}")
+    dev = logits.device
+    ids = torch.empty((T, k), dtype=torch.int32, device=dev)
+    weights = torch.empty((T, k), dtype=torch.float32, device=dev)
+    counts = torch.empty((E,), dtype=torch.int32, device=dev)
+    rows = torch.empty((1,), dtype=torch.int32, device=dev)
+    loss = torch.empty((), dtype=torch.float32, device=dev) if loss_coef is not None else None
+    coef = float(loss_coef or 0.0)
+    fp8blk_moe_route(logits, mask, renormalize, coef, ids, weights, counts, rows, loss,
+                     _work(load_library().fp8blk_moe_route_workspace_bytes(T, E), dev))
+    return Routing(ids, weights, counts, rows, loss, coef, bool(renormalize))
+
+
+def moe_route_backward(logits, routing, d_weights=None, d_loss=None):
+    """Gradient of the logits (in their type) from those of the weights and of
+    the loss; the choice itself has none."""
+    d_logits = torch.empty_like(logits)
+    fp8blk_moe_route_backward(logits, routing, d_weights, d_loss, d_logits)
+    return d_logits
+
+
+def group_rows(ids, groups):
+    """Rows (entries of ids, any shape) listed by group, in their own order
+    within a group; entries outside [0, groups) belong to none and come last."""
+    _need(ids, "ids", _I32)
+    R, dev = ids.numel(), ids.device
+    order = torch.empty((R,), dtype=torch.int32, device=dev)
+    positions = torch.empty_like(ids)
+    offsets = torch.empty((groups + 1,), dtype=torch.int32, device=dev)
+    fp8blk_group_rows(ids, order, positions, offsets,
+                      _work(load_library().fp8blk_group_rows_workspace_bytes(R, groups), dev))
+    return RowGroups(order, positions, offsets)
+
+
+def moe_combine(y, weights, positions, base=None):
+    """out[t] = base[t] + sum_j weights[t,j] * y[positions[t,j]] in bf16;
+    slots with position -1 add nothing."""
+    out = torch.empty((weights.shape[0], y.shape[1]), dtype=torch.bfloat16, device=y.device)
+    fp8blk_moe_combine(y, weights, positions, base, out)
+    return out
+
+
+def moe_combine_backward(d_out, y, weights, positions, offsets):
+    """(d_y, d_weights) of moe_combine; the last entry of offsets is the number
+    of y's rows in use (rows past it get 0)."""
+    d_y, d_weights = torch.empty_like(y), torch.empty_like(weights)
+    fp8blk_moe_combine_backward(d_out, y, weights, positions, offsets, d_y, d_weights)
+    return d_y, d_weights
+
+
+def lora_add(base, x, a, b, ids, scale=None, groups=None, out=None):
+    """out = base + scale[g] * (x a[g]^T) b[g]^T, g = ids[t] the row's adapter
+    (none outside [0, L)); ``out`` may be base (in place).  ``groups`` =
+    group_rows(ids, L) saves listing the rows again in every projection."""
+    T, K = x.shape
+    L, r = a.shape[0], a.shape[1]
+    if out is None:
+        out = torch.empty((T, b.shape[1]), dtype=torch.bfloat16, device=x.device)
+    need = load_library().fp8blk_lora_add_workspace_bytes(T, K, r, L, groups is not None)
+    fp8blk_lora_add(base, x, a, b, ids, scale, groups, out, _work(need, x.device))
+    return out
+
+
+def lora_linear(x, w_q, w_scale, a, b, ids, scale=None, groups=None):
+    """The FP8 linear layer with the adapters of a batch's requests added."""
+    y = linear(x, w_q, w_scale)
+    return lora_add(y, x, a, b, ids, scale, groups, out=y)
+
+
+def moe_experts(x, routing, gate_up_q, gate_up_s, down_q, down_s, base=None):
+    """The routed experts of a mixture-of-experts layer: x's rows listed by
+    expert and quantized, the gate/up product, SwiGLU, the down product, and
+    the weighted sum back to the tokens, on top of ``base`` (the shared
+    expert's output).  Scale formats as the weights'."""
+    k = routing.ids.shape[1]
+    groups = group_rows(routing.ids, gate_up_q.shape[0])
+    fmt = "ue8m0" if _is_e8m0(gate_up_s) else "float"
+    # rows past the last used one belong to no expert; no product reads them
+    x_q, x_s = act_quant_group(x.index_select(0, groups.order // k), fmt)
+    h = grouped_block_gemm(x_q, x_s, gate_up_q, gate_up_s, groups.offsets)
+    h_q, h_s = swiglu_act_quant(h, fmt)
+    y = grouped_block_gemm(h_q, h_s, down_q, down_s, groups.offsets)
+    return moe_combine(y, routing.weights, groups.positions, base)

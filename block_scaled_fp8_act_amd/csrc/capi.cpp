@@ -4,6 +4,7 @@
 
 #include <atomic>
 #include <cstring>
+#include <initializer_list>
 
 #include "../../include/fp8blk.h"
 #include "fp8blk_launch.h"
@@ -381,6 +382,168 @@ fp8blk_status fp8_grouped_block_gemm_ue8m0(const void *x_q, const uint8_t *x_sca
   return launched(fp8blk::launch_grouped_gemm_e8m0(x_q, x_scale, w_q, w_scale, expert_offsets, E,
                                                    total_M, N, K, y_bf16,
                                                    static_cast<hipStream_t>(stream)));
+}
+
+// ---- routing, rows by group, combine, adapters ---------------------------
+
+namespace {
+
+bool bad_groups(int32_t g) { return g < 1 || g > FP8BLK_MAX_GROUPS; }
+// T rows of k slots with int32 slot numbers
+bool bad_slots(int64_t T, int32_t k) {
+  return bad_rows(T) || k < 1 || k > FP8BLK_MAX_TOPK || T > kMaxRows / k;
+}
+bool bad_route(int type, int64_t T, int32_t E, int32_t k) {
+  return (type != FP8BLK_F32 && type != FP8BLK_BF16) || bad_groups(E) || bad_slots(T, k) || k > E;
+}
+bool any_misaligned(std::initializer_list<const void *> ps, uintptr_t align) {
+  for (const void *p : ps)
+    if (misaligned(p, align)) return true;
+  return false;
+}
+
+}  // namespace
+
+size_t fp8blk_moe_route_workspace_bytes(int64_t T, int32_t E) {
+  return bad_rows(T) || bad_groups(E) ? 0 : fp8blk::route_workspace_bytes(T, E);
+}
+
+fp8blk_status fp8blk_moe_route(const void *logits, int logits_type, const uint8_t *mask, int64_t T,
+                               int32_t E, int32_t k, int renormalize, float loss_coef,
+                               int32_t *ids, float *weights, int32_t *counts, int32_t *rows,
+                               float *loss, void *workspace, size_t workspace_bytes,
+                               void *stream) {
+  if (!counts || !rows || (T > 0 && (!logits || !ids || !weights))) return FP8BLK_ERR_NULL;
+  if (bad_route(logits_type, T, E, k)) return FP8BLK_ERR_SHAPE;
+  const size_t need = fp8blk::route_workspace_bytes(T, E);
+  if (need > 0 && workspace == nullptr) return FP8BLK_ERR_NULL;
+  if (workspace_bytes < need) return FP8BLK_ERR_SHAPE;
+  if ((T > 0 && misaligned(logits)) || (need > 0 && misaligned(workspace)) ||
+      any_misaligned({ids, weights, counts, rows, loss}, 4))
+    return FP8BLK_ERR_ALIGN;
+  if (fp8blk_status d = check_device()) return d;
+  return launched(fp8blk::launch_route(logits, logits_type == FP8BLK_BF16, mask, T, E, k,
+                                       renormalize != 0, loss_coef, ids, weights, counts, rows,
+                                       loss, workspace, static_cast<hipStream_t>(stream)));
+}
+
+fp8blk_status fp8blk_moe_route_backward(const void *logits, int logits_type, int64_t T, int32_t E,
+                                        int32_t k, int renormalize, float loss_coef,
+                                        const int32_t *ids, const float *weights,
+                                        const int32_t *counts, const int32_t *rows,
+                                        const float *d_weights, const float *d_loss,
+                                        void *d_logits, void *stream) {
+  if (T > 0 && (!logits || !ids || !weights || !counts || !rows || !d_logits))
+    return FP8BLK_ERR_NULL;
+  if (bad_route(logits_type, T, E, k)) return FP8BLK_ERR_SHAPE;
+  if (T > 0 && (any_misaligned({logits, d_logits}, 16) ||
+                any_misaligned({ids, weights, counts, rows, d_weights, d_loss}, 4)))
+    return FP8BLK_ERR_ALIGN;
+  if (fp8blk_status d = check_device()) return d;
+  if (T == 0) return FP8BLK_OK;
+  return launched(fp8blk::launch_route_backward(logits, logits_type == FP8BLK_BF16, T, E, k,
+                                                renormalize != 0, loss_coef, ids, weights, counts,
+                                                rows, d_weights, d_loss, d_logits,
+                                                static_cast<hipStream_t>(stream)));
+}
+
+size_t fp8blk_group_rows_workspace_bytes(int64_t R, int32_t G) {
+  return bad_rows(R) || bad_groups(G) ? 0 : fp8blk::group_workspace_bytes(R, G);
+}
+
+fp8blk_status fp8blk_group_rows(const int32_t *ids, int64_t R, int32_t G, int32_t *order,
+                                int32_t *positions, int32_t *offsets, void *workspace,
+                                size_t workspace_bytes, void *stream) {
+  if (!offsets || (R > 0 && (!ids || !order || !positions))) return FP8BLK_ERR_NULL;
+  if (bad_rows(R) || bad_groups(G)) return FP8BLK_ERR_SHAPE;
+  const size_t need = fp8blk::group_workspace_bytes(R, G);
+  if (need > 0 && workspace == nullptr) return FP8BLK_ERR_NULL;
+  if (workspace_bytes < need) return FP8BLK_ERR_SHAPE;
+  if ((need > 0 && misaligned(workspace)) || any_misaligned({ids, order, positions, offsets}, 4))
+    return FP8BLK_ERR_ALIGN;
+  if (fp8blk_status d = check_device()) return d;
+  return launched(fp8blk::launch_group_rows(ids, R, G, order, positions, offsets, workspace,
+                                            static_cast<hipStream_t>(stream)));
+}
+
+fp8blk_status fp8blk_moe_combine(const void *y_bf16, int64_t R, const float *weights,
+                                 const int32_t *positions, const void *base_bf16, int64_t T,
+                                 int32_t k, int64_t N, void *out_bf16, void *stream) {
+  const bool work = T > 0 && N > 0;
+  if (work && ((R > 0 && !y_bf16) || !weights || !positions || !out_bf16)) return FP8BLK_ERR_NULL;
+  if (bad_slots(T, k) || bad_rows(R) || bad_rows(N) || too_big(T, N) || too_big(R, N))
+    return FP8BLK_ERR_SHAPE;
+  if (work && (any_misaligned({y_bf16, base_bf16, out_bf16}, 16) ||
+               any_misaligned({weights, positions}, 4)))
+    return FP8BLK_ERR_ALIGN;
+  if (fp8blk_status d = check_device()) return d;
+  if (!work) return FP8BLK_OK;
+  return launched(fp8blk::launch_combine(y_bf16, R, weights, positions, base_bf16, T, k, N,
+                                         out_bf16, static_cast<hipStream_t>(stream)));
+}
+
+fp8blk_status fp8blk_moe_combine_backward(const void *d_out_bf16, const void *y_bf16, int64_t R,
+                                          const float *weights, const int32_t *positions,
+                                          const int32_t *rows_used, int64_t T, int32_t k,
+                                          int64_t N, void *d_y_bf16, float *d_weights,
+                                          void *stream) {
+  const bool work = T > 0 || (R > 0 && N > 0);
+  if (work && (!rows_used || (R > 0 && N > 0 && (!y_bf16 || !d_y_bf16)) ||
+               (T > 0 && (!weights || !positions || !d_weights || (N > 0 && !d_out_bf16)))))
+    return FP8BLK_ERR_NULL;
+  if (bad_slots(T, k) || bad_rows(R) || bad_rows(N) || too_big(T, N) || too_big(R, N))
+    return FP8BLK_ERR_SHAPE;
+  if (work && (any_misaligned({d_out_bf16, y_bf16, d_y_bf16}, 16) ||
+               any_misaligned({weights, positions, rows_used, d_weights}, 4)))
+    return FP8BLK_ERR_ALIGN;
+  if (fp8blk_status d = check_device()) return d;
+  if (!work) return FP8BLK_OK;
+  return launched(fp8blk::launch_combine_backward(d_out_bf16, y_bf16, R, weights, positions,
+                                                  rows_used, T, k, N, d_y_bf16, d_weights,
+                                                  static_cast<hipStream_t>(stream)));
+}
+
+namespace {
+bool bad_lora(int64_t T, int64_t K, int32_t r, int32_t L) {
+  return bad_rows(T) || bad_k(K) || too_big(T, K) || r < 8 || r > FP8BLK_MAX_RANK || r % 8 != 0 ||
+         bad_groups(L);
+}
+}  // namespace
+
+size_t fp8blk_lora_add_workspace_bytes(int64_t T, int64_t K, int32_t r, int32_t L, int listed) {
+  return T == 0 || bad_lora(T, K, r, L) ? 0
+                                        : fp8blk::lora_workspace_bytes(T, K, r, L, listed != 0);
+}
+
+fp8blk_status fp8blk_lora_add(const void *base_bf16, int64_t base_stride, const void *x_bf16,
+                              int64_t x_stride, const void *a_bf16, const void *b_bf16,
+                              const int32_t *ids, const float *scale, const int32_t *order,
+                              const int32_t *offsets, int64_t T, int64_t K, int64_t N, int32_t r,
+                              int32_t L, void *out_bf16, int64_t out_stride, void *workspace,
+                              size_t workspace_bytes, void *stream) {
+  const bool work = T > 0 && N > 0;
+  if (work && (!x_bf16 || !a_bf16 || !b_bf16 || !ids || !out_bf16 ||
+               (order == nullptr) != (offsets == nullptr)))
+    return FP8BLK_ERR_NULL;
+  if (bad_lora(T, K, r, L) || bad_rows(N) || x_stride < K || out_stride < N ||
+      too_big(T, x_stride) || too_big(T, out_stride) || too_big(int64_t(L) * r, K) ||
+      too_big(int64_t(L) * r, N) ||
+      (base_bf16 && (base_stride < N || too_big(T, base_stride))) ||
+      (base_bf16 == out_bf16 && base_stride != out_stride) ||
+      (T / 16 + L + 64) > kMaxRows / ((N + 255) / 256 + 16))
+    return FP8BLK_ERR_SHAPE;
+  if (work && !workspace) return FP8BLK_ERR_NULL;
+  if (work && workspace_bytes < fp8blk::lora_workspace_bytes(T, K, r, L, order != nullptr))
+    return FP8BLK_ERR_SHAPE;
+  if (work && (any_misaligned({base_bf16, x_bf16, a_bf16, b_bf16, out_bf16, workspace}, 16) ||
+               any_misaligned({ids, scale, order, offsets}, 4)))
+    return FP8BLK_ERR_ALIGN;
+  if (fp8blk_status d = check_device()) return d;
+  if (!work) return FP8BLK_OK;
+  return launched(fp8blk::launch_lora_add(base_bf16, base_stride, x_bf16, x_stride, a_bf16, b_bf16,
+                                          ids, scale, order, offsets, T, K, N, r, L, out_bf16,
+                                          out_stride, workspace,
+                                          static_cast<hipStream_t>(stream)));
 }
 
 }  // extern "C"

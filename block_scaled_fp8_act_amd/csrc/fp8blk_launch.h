@@ -67,4 +67,34 @@ hipError_t launch_grouped_gemm_e8m0(const void *xq, const uint8_t *xs, const voi
                                     int64_t total_M, int64_t N, int64_t K, void *y,
                                     hipStream_t stream);
 
+// Routing, rows by group, combine (route_kernels.hip).
+size_t route_workspace_bytes(int64_t T, int32_t E);
+hipError_t launch_route(const void *logits, bool bf16, const uint8_t *mask, int64_t T, int32_t E,
+                        int32_t k, bool renorm, float coef, int32_t *ids, float *weights,
+                        int32_t *counts, int32_t *rows, float *loss, void *work,
+                        hipStream_t stream);
+hipError_t launch_route_backward(const void *logits, bool bf16, int64_t T, int32_t E, int32_t k,
+                                 bool renorm, float coef, const int32_t *ids, const float *weights,
+                                 const int32_t *counts, const int32_t *rows, const float *dw,
+                                 const float *dloss, void *dlogits, hipStream_t stream);
+size_t group_workspace_bytes(int64_t R, int32_t G);
+hipError_t launch_group_rows(const int32_t *ids, int64_t R, int32_t G, int32_t *order,
+                             int32_t *positions, int32_t *offsets, void *work,
+                             hipStream_t stream);
+hipError_t launch_combine(const void *y, int64_t R, const float *weights, const int32_t *positions,
+                          const void *base, int64_t T, int32_t k, int64_t N, void *out,
+                          hipStream_t stream);
+hipError_t launch_combine_backward(const void *d_out, const void *y, int64_t R,
+                                   const float *weights, const int32_t *positions,
+                                   const int32_t *n_used, int64_t T, int32_t k, int64_t N,
+                                   void *dy, float *dw, hipStream_t stream);
+
+// Low-rank adapters (lora_kernels.hip).
+size_t lora_workspace_bytes(int64_t T, int64_t K, int32_t r, int32_t L, bool listed);
+hipError_t launch_lora_add(const void *base, int64_t ldb, const void *x, int64_t ldx,
+                           const void *a, const void *b, const int32_t *ids, const float *scale,
+                           const int32_t *order, const int32_t *offsets, int64_t T, int64_t K,
+                           int64_t N, int32_t r, int32_t L, void *out, int64_t ldo, void *work,
+                           hipStream_t stream);
+
 }  // namespace fp8blk

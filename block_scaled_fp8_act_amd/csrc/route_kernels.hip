@@ -1,0 +1,915 @@
+// Mixture-of-experts routing for gfx950: the top-k experts of each token with
+// their softmax weights, the rows per expert and the balance loss, and the
+// gradient of the logits; rows listed by group (a stable counting sort); and
+// the weighted sum that brings the experts' rows back to their tokens, with
+// its gradient.
+//
+// All of it is memory work with little arithmetic, except the selection of the
+// top k, which is bound by the vector ALU (see route_kernel).
+#include "fp8blk_device.h"
+#include "fp8blk_launch.h"
+
+#include <math.h>
+
+namespace fp8blk {
+
+namespace {
+
+constexpr float kNegInf = -INFINITY;
+
+// Reductions over the LPR lanes that share a row (16: one DPP row; 64: the
+// wave).  Each step adds the mirror lane's value, so every lane of the row
+// holds the same bits afterwards.
+template <int LPR>
+__device__ __forceinline__ float row_sum(float v) {
+  v += dpp_f<0xB1>(v);    // quad_perm [1,0,3,2]
+  v += dpp_f<0x4E>(v);    // quad_perm [2,3,0,1]
+  v += dpp_f<0x141>(v);   // row_half_mirror
+  v += dpp_f<0x140>(v);   // row_mirror
+  if constexpr (LPR == 64) {
+    v += __shfl_xor(v, 16);
+    v += __shfl_xor(v, 32);
+  }
+  return v;
+}
+
+template <int LPR>
+__device__ __forceinline__ float row_max(float v) {
+  v = row16_max(v);
+  if constexpr (LPR == 64) {
+    v = fmaxf(v, __shfl_xor(v, 16));
+    v = fmaxf(v, __shfl_xor(v, 32));
+  }
+  return v;
+}
+
+template <int CTRL>
+__device__ __forceinline__ int dpp_i(int v) {
+  return __builtin_amdgcn_update_dpp(0, v, CTRL, 0xF, 0xF, false);
+}
+
+template <int LPR>
+__device__ __forceinline__ int row_min(int v) {
+  v = min(v, dpp_i<0xB1>(v));
+  v = min(v, dpp_i<0x4E>(v));
+  v = min(v, dpp_i<0x141>(v));
+  v = min(v, dpp_i<0x140>(v));
+  if constexpr (LPR == 64) {
+    v = min(v, __shfl_xor(v, 16));
+    v = min(v, __shfl_xor(v, 32));
+  }
+  return v;
+}
+
+// e^x for x <= 0 (or NaN): 2^(x log2 e) with the product's rounding error
+// added back to first order, so the relative error stays near that of the
+// hardware exponential (1 ulp) down to the underflow, not |x| times it.
+__device__ __forceinline__ float exp_neg(float x) {
+  constexpr float kL = 0x1.715476p+0f, kLlo = 0x1.4ae0bep-26f;   // log2 e = kL + kLlo
+  const float t = x * kL;
+  // (x = -inf: t = -inf and the correction is NaN, so it is not applied)
+  const float r = t > -200.0f ? fmaf(x, kL, -t) + x * kLlo : 0.0f;
+  const float p = __builtin_amdgcn_exp2f(t);
+  return fmaf(p, r * 0x1.62e43p-1f, p);
+}
+
+// Element c of lane `sub` of a row: VEC consecutive experts per load.
+template <int LPR, int VEC>
+__device__ __forceinline__ int expert_of(int c, int sub) {
+  return ((c / VEC) * LPR + sub) * VEC + c % VEC;
+}
+
+template <typename T, int LPR, int V, int VEC>
+__device__ __forceinline__ void load_row(const T *row, int E, int sub, bool live, float *v) {
+#pragma unroll
+  for (int c = 0; c < V; c += VEC) {
+    const int e = expert_of<LPR, VEC>(c, sub);
+    const bool in = live && e < E;
+    if constexpr (sizeof(T) == 4 && VEC == 4) {
+      const uint4 w = in ? *reinterpret_cast<const uint4 *>(row + e) : make_uint4(0, 0, 0, 0);
+      v[c] = in ? __uint_as_float(w.x) : kNegInf;
+      v[c + 1] = in ? __uint_as_float(w.y) : kNegInf;
+      v[c + 2] = in ? __uint_as_float(w.z) : kNegInf;
+      v[c + 3] = in ? __uint_as_float(w.w) : kNegInf;
+    } else if constexpr (sizeof(T) == 2 && VEC == 4) {
+      const uint2 w = in ? *reinterpret_cast<const uint2 *>(row + e) : make_uint2(0, 0);
+      v[c] = in ? bf16_lo(w.x) : kNegInf;
+      v[c + 1] = in ? bf16_hi(w.x) : kNegInf;
+      v[c + 2] = in ? bf16_lo(w.y) : kNegInf;
+      v[c + 3] = in ? bf16_hi(w.y) : kNegInf;
+    } else {
+      static_assert(VEC == 1, "one element or four per load");
+      if constexpr (sizeof(T) == 4) v[c] = in ? __uint_as_float(row[e]) : kNegInf;
+      else v[c] = in ? bf16_lo(row[e]) : kNegInf;
+    }
+  }
+}
+
+// fp32 -> bf16 bits with the hardware's rounding (nearest even, NaN kept).
+__device__ __forceinline__ uint16_t to_bf16(float f) {
+  return __builtin_bit_cast(uint16_t, (__bf16)f);
+}
+__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
+  return (uint32_t)to_bf16(a) | ((uint32_t)to_bf16(b) << 16);
+}
+
+template <typename T, int LPR, int V, int VEC>
+__device__ __forceinline__ void store_row(T *row, int E, int sub, const float *v) {
+#pragma unroll
+  for (int c = 0; c < V; c += VEC) {
+    const int e = expert_of<LPR, VEC>(c, sub);
+    if (e >= E) continue;
+    if constexpr (sizeof(T) == 4 && VEC == 4) {
+      *reinterpret_cast<uint4 *>(row + e) =
+          make_uint4(__float_as_uint(v[c]), __float_as_uint(v[c + 1]), __float_as_uint(v[c + 2]),
+                     __float_as_uint(v[c + 3]));
+    } else if constexpr (sizeof(T) == 2 && VEC == 4) {
+      *reinterpret_cast<uint2 *>(row + e) =
+          make_uint2(pack_bf16(v[c], v[c + 1]), pack_bf16(v[c + 2], v[c + 3]));
+    } else {
+      if constexpr (sizeof(T) == 4) row[e] = __float_as_uint(v[c]);
+      else row[e] = to_bf16(v[c]);
+    }
+  }
+}
+
+}  // namespace
+
+// ---------------------------------------------------------------------------
+// Routing, forward.
+//
+// For a live row (mask set, some logit above -inf): S = its k largest logits,
+// ties to the lowest expert; m their largest; p_e = e^(l_e - m) / sum over all
+// experts; weights = the same over S alone (renormalize) or p on S.  c_e = the
+// number of rows that chose e, n = the number of live rows, and the balance
+// loss = coef * sum_e (c_e E / (k n)) * (sum_t p_te / n).
+//
+// LPR lanes hold a row, V logits each, so a wave holds 64 / LPR rows and the
+// row reductions are DPP steps (16 lanes) with no LDS.  Each of the k rounds
+// takes the row's best of the lanes' bests; the lane that had it drops it and
+// looks for its next.  The probabilities' sums over rows stay in registers
+// (one per logit slot) over all rows of a wave and are added over waves and
+// workgroups in a fixed order, so results do not vary between runs; counts
+// are integer LDS atomics.  The workgroup's sums go to `part` and
+// route_finish_kernel adds them, except when one workgroup does all rows.
+constexpr int kRouteThreads = 512;
+constexpr int kRouteWaves = kRouteThreads / 64;
+constexpr int kRouteMaxBlocks = 512;
+constexpr int kRouteMaxK = 32;
+
+struct RouteArgs {
+  const void *logits;
+  const uint8_t *mask;
+  int64_t T;
+  int E, k, renorm, loss;   // loss: sums of probabilities wanted
+  float coef;
+  int32_t *ids;
+  float *weights;
+  int32_t *counts, *rows;
+  float *loss_out;
+  // per workgroup: E counts, then one for the live rows, then E fp32 sums
+  int32_t *part;
+  int32_t *ticket;
+};
+
+__device__ __forceinline__ size_t part_stride(int E) { return 2 * (size_t)E + 1; }
+
+__device__ __forceinline__ float balance(double sum, float coef, int E, int k, int64_t n) {
+  const double m = n > 0 ? (double)n : 1.0;
+  return (float)((double)coef * E / ((double)k * m * m) * sum);
+}
+
+template <typename T, int LPR, int V, int VEC>
+__global__ __launch_bounds__(kRouteThreads) void route_kernel(RouteArgs a) {
+  extern __shared__ float lds[];          // [E] counts, [waves][E] sums
+  __shared__ int live_rows[kRouteWaves];
+  constexpr int RPW = 64 / LPR;
+  constexpr int SLOTS = (kRouteMaxK + LPR - 1) / LPR;
+  int *hist = reinterpret_cast<int *>(lds);
+  float *sums = lds + a.E;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int sub = lane % LPR;
+  for (int e = tid; e < a.E; e += kRouteThreads) hist[e] = 0;
+  __syncthreads();
+
+  float acc[V];
+#pragma unroll
+  for (int c = 0; c < V; ++c) acc[c] = 0.0f;
+  int live_count = 0;
+  const bool all = a.loss || !a.renorm;   // probabilities over every expert
+  const int64_t step = (int64_t)gridDim.x * kRouteWaves * RPW;
+  const int64_t first = ((int64_t)blockIdx.x * kRouteWaves + wave) * RPW;
+  for (int64_t r0 = first; r0 < a.T; r0 += step) {
+    const int64_t row = r0 + lane / LPR;
+    const bool in = row < a.T && (!a.mask || a.mask[row]);
+    float v[V];
+    load_row<T, LPR, V, VEC>(static_cast<const T *>(a.logits) + (row < a.T ? row : 0) * a.E, a.E,
+                             sub, in, v);
+    float bestv = kNegInf;
+    int bestc = 0;
+#pragma unroll
+    for (int c = 0; c < V; ++c) bestv = fmaxf(bestv, v[c]);
+#pragma unroll
+    for (int c = V - 1; c >= 0; --c) bestc = v[c] == bestv ? c : bestc;
+    const float peak = row_max<LPR>(bestv);
+    const bool live = peak > kNegInf;
+    float inv = 0.0f;
+    if (all) {
+      float ex[V], total = 0.0f;
+#pragma unroll
+      for (int c = 0; c < V; ++c) {
+        ex[c] = live ? exp_neg(v[c] - peak) : 0.0f;
+        total += ex[c];
+      }
+      total = row_sum<LPR>(total);
+      inv = live ? 1.0f / total : 0.0f;
+#pragma unroll
+      for (int c = 0; c < V; ++c) acc[c] += ex[c] * inv;
+    }
+    float sel_v[SLOTS];
+    int sel_e[SLOTS];
+#pragma unroll
+    for (int s = 0; s < SLOTS; ++s) {
+      sel_v[s] = kNegInf;
+      sel_e[s] = -1;
+    }
+    for (int j = 0; j < a.k; ++j) {
+      const float m = j ? row_max<LPR>(bestv) : peak;
+      const int mine = expert_of<LPR, VEC>(bestc, sub);
+      const int e = row_min<LPR>(m > kNegInf && bestv == m ? mine : INT32_MAX);
+#pragma unroll
+      for (int s = 0; s < SLOTS; ++s) {
+        if (j == s * LPR + sub && e != INT32_MAX) {
+          sel_v[s] = m;
+          sel_e[s] = e;
+        }
+      }
+      if (j + 1 == a.k) break;
+      const int drop = mine == e ? bestc : -1;
+      bestv = kNegInf;
+#pragma unroll
+      for (int c = 0; c < V; ++c) {
+        v[c] = c == drop ? kNegInf : v[c];
+        bestv = fmaxf(bestv, v[c]);
+      }
+#pragma unroll
+      for (int c = V - 1; c >= 0; --c) bestc = v[c] == bestv ? c : bestc;
+    }
+    float w[SLOTS], total = 0.0f;
+#pragma unroll
+    for (int s = 0; s < SLOTS; ++s) {
+      w[s] = sel_e[s] >= 0 ? exp_neg(sel_v[s] - peak) : 0.0f;
+      total += w[s];
+    }
+    if (a.renorm) {
+      total = row_sum<LPR>(total);
+      inv = live ? 1.0f / total : 0.0f;
+    }
+#pragma unroll
+    for (int s = 0; s < SLOTS; ++s) {
+      const int j = s * LPR + sub;
+      if (j < a.k && row < a.T) {
+        a.ids[row * a.k + j] = sel_e[s];
+        a.weights[row * a.k + j] = w[s] * inv;
+        if (sel_e[s] >= 0) atomicAdd(&hist[sel_e[s]], 1);
+      }
+    }
+    live_count += __popcll(__builtin_amdgcn_ballot_w64(live && sub == 0));
+  }
+
+  if (lane == 0) live_rows[wave] = live_count;
+  if (a.loss) {
+#pragma unroll
+    for (int c = 0; c < V; ++c) {
+      if constexpr (LPR == 16) {
+        acc[c] += __shfl_xor(acc[c], 16);
+        acc[c] += __shfl_xor(acc[c], 32);
+      }
+      const int e = expert_of<LPR, VEC>(c, sub);
+      if (lane < LPR && e < a.E) sums[wave * a.E + e] = acc[c];
+    }
+  }
+  __syncthreads();
+  int live_total = 0;
+  for (int w = 0; w < kRouteWaves; ++w) live_total += live_rows[w];
+  const bool only = gridDim.x == 1;
+  int32_t *part = a.part + blockIdx.x * part_stride(a.E);
+  float mine = 0.0f;   // this thread's experts: sum of c_e * sum p_e
+  for (int e = tid; e < a.E; e += kRouteThreads) {
+    float s = 0.0f;
+    if (a.loss)
+      for (int w = 0; w < kRouteWaves; ++w) s += sums[w * a.E + e];
+    if (only) {
+      a.counts[e] = hist[e];
+      mine += (float)hist[e] * s;
+    } else {
+      part[e] = hist[e];
+      if (a.loss) part[a.E + 1 + e] = __float_as_int(s);
+    }
+  }
+  if (!only) {
+    if (tid == 0) {
+      part[a.E] = live_total;
+      if (blockIdx.x == 0) *a.ticket = 0;
+    }
+    return;
+  }
+  if (tid == 0) *a.rows = live_total;
+  if (!a.loss) return;
+  __syncthreads();
+  mine = row_sum<64>(mine);
+  if (lane == 0) sums[wave] = mine;
+  __syncthreads();
+  if (tid == 0) {
+    double s = 0.0;
+    for (int w = 0; w < kRouteWaves; ++w) s += (double)sums[w];
+    *a.loss_out = balance(s, a.coef, a.E, a.k, live_total);
+  }
+}
+
+// Adds the workgroups' counts and sums: 16 experts per workgroup, 16 threads
+// an expert.  The last workgroup to finish (an integer ticket; nothing waits
+// for it) adds the experts' terms of the loss in order.
+constexpr int kFinishThreads = 256;
+
+__global__ __launch_bounds__(kFinishThreads) void route_finish_kernel(RouteArgs a, int blocks,
+                                                                      float *terms) {
+  __shared__ int cnt[16][17];
+  __shared__ float sum[16][17];
+  __shared__ int last;
+  const int col = threadIdx.x & 15, sl = threadIdx.x >> 4;
+  const int e = blockIdx.x * 16 + col;
+  const size_t stride = part_stride(a.E);
+  int c = 0;
+  float s = 0.0f;
+  if (e < a.E)
+    for (int b = sl; b < blocks; b += 16) {
+      c += a.part[b * stride + e];
+      if (a.loss) s += __int_as_float(a.part[b * stride + a.E + 1 + e]);
+    }
+  cnt[sl][col] = c;
+  sum[sl][col] = s;
+  __syncthreads();
+  if (sl == 0 && e < a.E) {
+    c = 0;
+    s = 0.0f;
+    for (int i = 0; i < 16; ++i) {
+      c += cnt[i][col];
+      s += sum[i][col];
+    }
+    a.counts[e] = c;
+    if (a.loss)
+      __hip_atomic_store(&terms[e], (float)c * s, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  }
+  __syncthreads();
+  if (threadIdx.x == 0)
+    last = __hip_atomic_fetch_add(a.ticket, 1, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT) ==
+           (int)gridDim.x - 1;
+  __syncthreads();
+  if (!last) return;
+  // live rows and loss, by the first wave
+  if (threadIdx.x >= 64) return;
+  int n = 0;
+  for (int b = threadIdx.x; b < blocks; b += 64) n += a.part[b * stride + a.E];
+#pragma unroll
+  for (int d = 1; d < 64; d *= 2) n += __shfl_xor(n, d);
+  if (threadIdx.x == 0) *a.rows = n;
+  if (!a.loss) return;
+  double t = 0.0;
+  for (int i = threadIdx.x; i < a.E; i += 64)
+    t += (double)__hip_atomic_load(&terms[i], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+#pragma unroll
+  for (int d = 1; d < 64; d *= 2) t += __shfl_xor(t, d);
+  if (threadIdx.x == 0) *a.loss_out = balance(t, a.coef, a.E, a.k, n);
+}
+
+// ---------------------------------------------------------------------------
+// Routing, backward: for a live row, with g_e = dL * coef * E * c_e / (k n^2),
+//   renormalize:  dl = p (g - <p, g>) + [on S] w (dw - <w, dw>)
+//   otherwise:    the same softmax gradient with g_e + [e in S] dw_e, whose
+//                 inner product over S is <w, dw>.
+// The counts carry no gradient.  g enters as c_e minus the mean count: p sums
+// to one, so the constant cancels exactly in dl and not in the rounding.
+// The k values on S reach their lanes through LDS, each wave its own rows.
+struct RouteBackArgs {
+  const void *logits;
+  int64_t T;
+  int E, k, renorm;
+  float coef;
+  const int32_t *ids;
+  const float *weights;
+  const int32_t *counts, *rows;
+  const float *dw;       // [T, k] or NULL
+  const float *dloss;    // one value or NULL
+  void *dlogits;
+};
+
+template <typename T, int LPR, int V, int VEC>
+__global__ __launch_bounds__(kRouteThreads) void route_backward_kernel(RouteBackArgs a) {
+  extern __shared__ float lds[];     // [waves][RPW][E]
+  __shared__ int total_count[kRouteWaves];
+  constexpr int RPW = 64 / LPR;
+  constexpr int SLOTS = (kRouteMaxK + LPR - 1) / LPR;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int sub = lane % LPR;
+  float *mine = lds + (size_t)(wave * RPW + lane / LPR) * a.E;
+  for (int e = sub; e < a.E; e += LPR) mine[e] = 0.0f;
+  const float dl = a.dloss ? *a.dloss : 0.0f;
+
+  float g[V];
+  if (a.dloss) {
+    int part = 0;
+    for (int e = tid; e < a.E; e += kRouteThreads) part += a.counts[e];
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2) part += __shfl_xor(part, d);
+    if (lane == 0) total_count[wave] = part;
+    __syncthreads();
+    int total = 0;
+    for (int w = 0; w < kRouteWaves; ++w) total += total_count[w];
+    const float mean = (float)total / (float)a.E;
+    const float n = (float)max(*a.rows, 1);
+    const float f = dl * (a.coef * (float)a.E / ((float)a.k * n)) / n;
+#pragma unroll
+    for (int c = 0; c < V; ++c) {
+      const int e = expert_of<LPR, VEC>(c, sub);
+      g[c] = e < a.E ? ((float)a.counts[e] - mean) * f : 0.0f;
+    }
+  } else {
+#pragma unroll
+    for (int c = 0; c < V; ++c) g[c] = 0.0f;
+  }
+
+  const int64_t step = (int64_t)gridDim.x * kRouteWaves * RPW;
+  for (int64_t r0 = ((int64_t)blockIdx.x * kRouteWaves + wave) * RPW; r0 < a.T; r0 += step) {
+    const int64_t row = r0 + lane / LPR;
+    const int64_t at = row < a.T ? row : a.T - 1;
+    const bool live = row < a.T && a.ids[at * a.k] >= 0;
+    float v[V], d[V];
+    load_row<T, LPR, V, VEC>(static_cast<const T *>(a.logits) + at * a.E, a.E, sub, live, v);
+    int id[SLOTS];
+    float w[SLOTS], dw[SLOTS], dot = 0.0f;
+#pragma unroll
+    for (int s = 0; s < SLOTS; ++s) {
+      const int j = s * LPR + sub;
+      id[s] = -1;
+      w[s] = dw[s] = 0.0f;
+      if (j < a.k && live && a.dw) {
+        const int i = a.ids[at * a.k + j];
+        if (i >= 0 && i < a.E) {
+          id[s] = i;
+          w[s] = a.weights[at * a.k + j];
+          dw[s] = a.dw[at * a.k + j];
+          dot += w[s] * dw[s];
+        }
+      }
+    }
+    dot = row_sum<LPR>(dot);
+    const float back = a.renorm ? dot : 0.0f;
+#pragma unroll
+    for (int s = 0; s < SLOTS; ++s)
+      if (id[s] >= 0) mine[id[s]] = w[s] * (dw[s] - back);
+    // the wave's own LDS: in order, but the compiler has to keep it so
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+    float peak = kNegInf;
+#pragma unroll
+    for (int c = 0; c < V; ++c) peak = fmaxf(peak, v[c]);
+    peak = row_max<LPR>(peak);
+    float total = 0.0f, inner = 0.0f;
+#pragma unroll
+    for (int c = 0; c < V; ++c) {
+      v[c] = live ? exp_neg(v[c] - peak) : 0.0f;
+      total += v[c];
+      inner += v[c] * g[c];
+    }
+    total = row_sum<LPR>(total);
+    const float inv = live ? 1.0f / total : 0.0f;
+    inner = row_sum<LPR>(inner) * inv + (a.renorm ? 0.0f : dot);
+#pragma unroll
+    for (int c = 0; c < V; ++c) {
+      const int e = expert_of<LPR, VEC>(c, sub);
+      d[c] = v[c] * inv * (g[c] - inner) + (e < a.E ? mine[e] : 0.0f);
+    }
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+#pragma unroll
+    for (int s = 0; s < SLOTS; ++s)
+      if (id[s] >= 0) mine[id[s]] = 0.0f;
+    if (row < a.T)
+      store_row<T, LPR, V, VEC>(static_cast<T *>(a.dlogits) + row * a.E, a.E, sub, d);
+  }
+}
+
+namespace {
+
+// Kernel of a row width: the fewest logits per lane that cover E, in DPP rows
+// of 16 lanes up to 256 experts and in whole waves above; four logits per
+// load where the rows' alignment (E % 4 == 0) allows it.
+template <typename T, template <typename, int, int, int> class L, typename... A>
+hipError_t by_width(int E, A... args) {
+  if (E % 4 == 0) {
+    if (E <= 64) return L<T, 16, 4, 4>::go(args...);
+    if (E <= 128) return L<T, 16, 8, 4>::go(args...);
+    if (E <= 256) return L<T, 16, 16, 4>::go(args...);
+    if (E <= 512) return L<T, 64, 8, 4>::go(args...);
+    return L<T, 64, 16, 4>::go(args...);
+  }
+  if (E <= 64) return L<T, 16, 4, 1>::go(args...);
+  if (E <= 128) return L<T, 16, 8, 1>::go(args...);
+  if (E <= 256) return L<T, 16, 16, 1>::go(args...);
+  if (E <= 512) return L<T, 64, 8, 1>::go(args...);
+  return L<T, 64, 16, 1>::go(args...);
+}
+
+template <typename T, int LPR, int V, int VEC>
+struct RouteLaunch {
+  static hipError_t go(const RouteArgs *a, int blocks, hipStream_t st) {
+    const size_t lds = sizeof(float) * a->E * (1 + (a->loss ? kRouteWaves : 0));
+    route_kernel<T, LPR, V, VEC><<<blocks, kRouteThreads, lds + 64, st>>>(*a);
+    return hipGetLastError();
+  }
+};
+
+template <typename T, int LPR, int V, int VEC>
+struct RouteBackLaunch {
+  static hipError_t go(const RouteBackArgs *a, int blocks, hipStream_t st) {
+    const size_t lds = sizeof(float) * a->E * kRouteWaves * (64 / LPR);
+    route_backward_kernel<T, LPR, V, VEC><<<blocks, kRouteThreads, lds, st>>>(*a);
+    return hipGetLastError();
+  }
+};
+
+int route_rows_per_block(int E) { return kRouteWaves * (E <= 256 ? 4 : 1); }
+
+int route_blocks(int64_t T, int E) {
+  const int64_t per = route_rows_per_block(E);
+  const int64_t need = (T + per - 1) / per;
+  // one workgroup for as many rows as cost less than the second launch
+  if (need <= 2) return 1;
+  return (int)(need < kRouteMaxBlocks ? need : kRouteMaxBlocks);
+}
+
+}  // namespace
+
+size_t route_workspace_bytes(int64_t T, int32_t E) {
+  const int blocks = route_blocks(T, E);
+  if (blocks <= 1) return 0;
+  return sizeof(int32_t) * (blocks * (2 * (size_t)E + 1) + E + 1);
+}
+
+hipError_t launch_route(const void *logits, bool bf16, const uint8_t *mask, int64_t T, int32_t E,
+                        int32_t k, bool renorm, float coef, int32_t *ids, float *weights,
+                        int32_t *counts, int32_t *rows, float *loss, void *work,
+                        hipStream_t stream) {
+  RouteArgs a{};
+  a.logits = logits;
+  a.mask = mask;
+  a.T = T;
+  a.E = E;
+  a.k = k;
+  a.renorm = renorm;
+  a.loss = loss != nullptr;
+  a.coef = coef;
+  a.ids = ids;
+  a.weights = weights;
+  a.counts = counts;
+  a.rows = rows;
+  a.loss_out = loss;
+  const int blocks = route_blocks(T, E);
+  a.part = static_cast<int32_t *>(work);
+  float *terms = nullptr;
+  if (blocks > 1) {
+    terms = reinterpret_cast<float *>(a.part + blocks * (2 * (size_t)E + 1));
+    a.ticket = reinterpret_cast<int32_t *>(terms + E);
+  }
+  hipError_t e = bf16 ? by_width<uint16_t, RouteLaunch>(E, &a, blocks, stream)
+                      : by_width<uint32_t, RouteLaunch>(E, &a, blocks, stream);
+  if (e != hipSuccess || blocks == 1) return e;
+  route_finish_kernel<<<(E + 15) / 16, kFinishThreads, 0, stream>>>(a, blocks, terms);
+  return hipGetLastError();
+}
+
+hipError_t launch_route_backward(const void *logits, bool bf16, int64_t T, int32_t E, int32_t k,
+                                 bool renorm, float coef, const int32_t *ids, const float *weights,
+                                 const int32_t *counts, const int32_t *rows, const float *dw,
+                                 const float *dloss, void *dlogits, hipStream_t stream) {
+  RouteBackArgs a{};
+  a.logits = logits;
+  a.T = T;
+  a.E = E;
+  a.k = k;
+  a.renorm = renorm;
+  a.coef = coef;
+  a.ids = ids;
+  a.weights = weights;
+  a.counts = counts;
+  a.rows = rows;
+  a.dw = dw;
+  a.dloss = dloss;
+  a.dlogits = dlogits;
+  const int64_t per = route_rows_per_block(E);
+  const int64_t need = (T + per - 1) / per;
+  const int blocks = (int)(need < 2 * kRouteMaxBlocks ? need : 2 * kRouteMaxBlocks);
+  return bf16 ? by_width<uint16_t, RouteBackLaunch>(E, &a, blocks, stream)
+              : by_width<uint32_t, RouteBackLaunch>(E, &a, blocks, stream);
+}
+
+// ---------------------------------------------------------------------------
+// Rows by group: a stable counting sort of R group numbers.
+//
+// Each wave counts its own run of rows in LDS; the counts are added up over
+// waves (and workgroups) into each run's first place in its group; then the
+// wave walks its run again, 64 rows at a time: lanes with equal keys find each
+// other with one ballot per key bit, take consecutive places, and the first of
+// them moves the run's counter on.  Rows with a number outside [0, G) count as
+// group G: they are listed last and have position -1.  Only integer counts
+// are added atomically, so the order never varies.
+constexpr int kGroupThreads = 1024;
+constexpr int kGroupWaves = kGroupThreads / 64;
+constexpr int kGroupMaxBlocks = 128;
+// R up to which one workgroup does all of it in one launch.
+constexpr int64_t kGroupOneBlock = 8192;
+
+__device__ __forceinline__ int group_key(int id, int G) { return (unsigned)id < (unsigned)G ? id : G; }
+
+__global__ __launch_bounds__(kGroupThreads) void group_count_kernel(
+    const int32_t *__restrict__ ids, int64_t R, int G, int64_t per_block,
+    int32_t *__restrict__ part) {
+  extern __shared__ int hist[];
+  for (int g = threadIdx.x; g <= G; g += kGroupThreads) hist[g] = 0;
+  __syncthreads();
+  const int64_t lo = blockIdx.x * per_block;
+  const int64_t hi = lo + per_block < R ? lo + per_block : R;
+  for (int64_t i = lo + threadIdx.x; i < hi; i += kGroupThreads)
+    atomicAdd(&hist[group_key(ids[i], G)], 1);
+  __syncthreads();
+  for (int g = threadIdx.x; g <= G; g += kGroupThreads) part[(int64_t)blockIdx.x * (G + 1) + g] = hist[g];
+}
+
+__global__ __launch_bounds__(kGroupThreads) void group_place_kernel(
+    const int32_t *__restrict__ ids, int64_t R, int G, int64_t per_block,
+    const int32_t *__restrict__ part, int32_t *__restrict__ order,
+    int32_t *__restrict__ positions, int32_t *__restrict__ offsets) {
+  extern __shared__ int hist[];          // [waves][G + 1]
+  __shared__ int wave_total[kGroupWaves];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int G1 = G + 1;
+  for (int i = tid; i < kGroupWaves * G1; i += kGroupThreads) hist[i] = 0;
+  __syncthreads();
+  const int64_t per_wave = (per_block / kGroupWaves + 63) / 64 * 64;
+  const int64_t end = (blockIdx.x + 1) * per_block < R ? (blockIdx.x + 1) * per_block : R;
+  const int64_t lo = blockIdx.x * per_block + wave * per_wave;
+  const int64_t hi = lo + per_wave < end ? lo + per_wave : end;
+  int *mine = hist + wave * G1;
+  for (int64_t i = lo + lane; i < hi; i += 64) atomicAdd(&mine[group_key(ids[i], G)], 1);
+  __syncthreads();
+  // groups 2 tid and 2 tid + 1: rows of earlier workgroups, of all, and the
+  // waves' first places within this workgroup's rows
+  int total[2] = {0, 0}, before[2] = {0, 0};
+#pragma unroll
+  for (int q = 0; q < 2; ++q) {
+    const int g = 2 * tid + q;
+    if (g >= G1) continue;
+    if (gridDim.x > 1) {
+      for (int b = 0; b < (int)gridDim.x; ++b) {
+        const int c = part[(int64_t)b * G1 + g];
+        before[q] += b < (int)blockIdx.x ? c : 0;
+        total[q] += c;
+      }
+    } else {
+      for (int w = 0; w < kGroupWaves; ++w) total[q] += hist[w * G1 + g];
+    }
+  }
+  const int pair = total[0] + total[1];
+  int scan = pair;
+#pragma unroll
+  for (int d = 1; d < 64; d *= 2) {
+    const int o = __shfl_up(scan, d);
+    scan += lane >= d ? o : 0;
+  }
+  if (lane == 63) wave_total[wave] = scan;
+  __syncthreads();
+  int first = scan - pair;
+  for (int w = 0; w < wave; ++w) first += wave_total[w];
+#pragma unroll
+  for (int q = 0; q < 2; ++q) {
+    const int g = 2 * tid + q;
+    if (g >= G1) continue;
+    if (blockIdx.x == 0) offsets[g] = first;
+    int at = first + before[q];
+    for (int w = 0; w < kGroupWaves; ++w) {
+      const int c = hist[w * G1 + g];
+      hist[w * G1 + g] = at;
+      at += c;
+    }
+    first += total[q];
+  }
+  __syncthreads();
+  const int bits = 32 - __clz(G);   // keys 0 .. G
+  for (int64_t i0 = lo; i0 < hi; i0 += 64) {
+    const int64_t i = i0 + lane;
+    const bool in = i < hi;
+    const int key = in ? group_key(ids[i], G) : 0;
+    uint64_t same = __builtin_amdgcn_ballot_w64(in);
+    for (int b = 0; b < bits; ++b) {
+      const bool set = (key >> b) & 1;
+      const uint64_t m = __builtin_amdgcn_ballot_w64(set);
+      same &= set ? m : ~m;
+    }
+    if (in) {
+      const uint64_t below = same & ((1ull << lane) - 1);
+      const int leader = __ffsll((unsigned long long)same) - 1;
+      int base = 0;
+      if (lane == leader) base = atomicAdd(&mine[key], (int)__popcll(same));
+      base = __shfl(base, leader);
+      const int at = base + (int)__popcll(below);
+      order[at] = (int)i;
+      positions[i] = key < G ? at : -1;
+    }
+  }
+}
+
+namespace {
+int64_t group_rows_per_block(int64_t R) {
+  if (R <= kGroupOneBlock) return (R + kGroupThreads - 1) / kGroupThreads * kGroupThreads;
+  const int64_t per = (R + kGroupMaxBlocks - 1) / kGroupMaxBlocks;
+  return (per + kGroupThreads - 1) / kGroupThreads * kGroupThreads;
+}
+}  // namespace
+
+size_t group_workspace_bytes(int64_t R, int32_t G) {
+  if (R <= kGroupOneBlock) return 0;
+  const int64_t per = group_rows_per_block(R);
+  return sizeof(int32_t) * (size_t)((R + per - 1) / per) * (G + 1);
+}
+
+hipError_t launch_group_rows(const int32_t *ids, int64_t R, int32_t G, int32_t *order,
+                             int32_t *positions, int32_t *offsets, void *work,
+                             hipStream_t stream) {
+  const int64_t per = R > 0 ? group_rows_per_block(R) : kGroupThreads;
+  const int blocks = R > 0 ? (int)((R + per - 1) / per) : 1;
+  int32_t *part = static_cast<int32_t *>(work);
+  if (blocks > 1) {
+    group_count_kernel<<<blocks, kGroupThreads, sizeof(int) * (G + 1), stream>>>(ids, R, G, per, part);
+    if (hipError_t e = hipGetLastError()) return e;
+  }
+  group_place_kernel<<<blocks, kGroupThreads, sizeof(int) * kGroupWaves * (G + 1), stream>>>(
+      ids, R, G, per, part, order, positions, offsets);
+  return hipGetLastError();
+}
+
+// ---------------------------------------------------------------------------
+// Combine: out[t] = base[t] + sum_j w[t,j] * y[pos[t,j]], fp32 sums in the
+// order of j, one rounding to bf16.  Slots whose position is outside [0, R)
+// add nothing, and their rows of y are not read.
+//
+// HBM-bound (k + 1 rows of N read or written per token).  A wave takes 512
+// columns of one token, 8 per lane, so positions and weights are scalar loads
+// and the k row loads of a lane are independent 16-byte loads.  Rows may start
+// at any even address (odd N): gfx950's global loads take those at 16 bytes
+// a lane too, and the last N % 8 columns go one by one.
+struct __attribute__((packed, aligned(2))) U128 {
+  uint32_t v[4];
+};
+
+namespace {
+
+// Up to 8 bf16 at columns [c, c + 8) of a row of N, as fp32; 0 past N.
+__device__ __forceinline__ void load8(const uint16_t *row, int64_t c, int64_t N, float *f) {
+  if (c + 8 <= N) {
+    const U128 w = *reinterpret_cast<const U128 *>(row + c);
+    unpack8(make_uint4(w.v[0], w.v[1], w.v[2], w.v[3]), f);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[i] = c + i < N ? bf16_lo(row[c + i]) : 0.0f;
+  }
+}
+
+__device__ __forceinline__ void store8(uint16_t *row, int64_t c, int64_t N, const float *f) {
+  if (c + 8 <= N) {
+    U128 w;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w.v[i] = pack_bf16(f[2 * i], f[2 * i + 1]);
+    *reinterpret_cast<U128 *>(row + c) = w;
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (c + i < N) row[c + i] = to_bf16(f[i]);
+  }
+}
+
+}  // namespace
+
+constexpr int kCombineThreads = 256;
+constexpr int kCombineCols = 512;   // columns of a wave
+
+__global__ __launch_bounds__(kCombineThreads) void combine_kernel(
+    const uint16_t *__restrict__ y, int64_t R, const float *__restrict__ weights,
+    const int32_t *__restrict__ positions, const uint16_t *base, int64_t T, int k, int64_t N,
+    uint16_t *out) {   // out may be base: each lane reads its columns first
+  const int lane = threadIdx.x & 63;
+  const int64_t chunks = (N + kCombineCols - 1) / kCombineCols;
+  const int64_t unit = (int64_t)blockIdx.x * (kCombineThreads / 64) +
+                       __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int64_t t = unit / chunks;
+  if (t >= T) return;
+  const int64_t c = (unit - t * chunks) * kCombineCols + lane * 8;
+  if (c >= N) return;
+  float acc[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+  if (base) load8(base + t * N, c, N, acc);
+#pragma unroll 4
+  for (int j = 0; j < k; ++j) {
+    const int p = positions[t * k + j];
+    if (p < 0 || p >= R) continue;
+    const float w = weights[t * k + j];
+    float f[8];
+    load8(y + (int64_t)p * N, c, N, f);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) acc[i] = fmaf(w, f[i], acc[i]);
+  }
+  store8(out + t * N, c, N, acc);
+}
+
+hipError_t launch_combine(const void *y, int64_t R, const float *weights, const int32_t *positions,
+                          const void *base, int64_t T, int32_t k, int64_t N, void *out,
+                          hipStream_t stream) {
+  const int64_t units = T * ((N + kCombineCols - 1) / kCombineCols);
+  const int64_t per = kCombineThreads / 64;
+  combine_kernel<<<(unsigned)((units + per - 1) / per), kCombineThreads, 0, stream>>>(
+      static_cast<const uint16_t *>(y), R, weights, positions, static_cast<const uint16_t *>(base),
+      T, k, N, static_cast<uint16_t *>(out));
+  return hipGetLastError();
+}
+
+// Combine, backward: dy[pos] = bf16(w * d), dw = <d, y[pos]> (fp32, a fixed
+// order), one workgroup per token; each column of d is read once per 8 slots
+// and stays in registers while the slots' rows stream past.  Rows of dy past
+// the last used one (n_used, in device memory) are zeroed.  Dropped slots get
+// dw = 0.
+__global__ __launch_bounds__(kCombineThreads) void combine_backward_kernel(
+    const uint16_t *__restrict__ d_out, const uint16_t *__restrict__ y, int64_t R,
+    const float *__restrict__ weights, const int32_t *__restrict__ positions,
+    const int32_t *__restrict__ n_used, int64_t T, int k, int64_t N, uint16_t *__restrict__ dy,
+    float *__restrict__ dw) {
+  constexpr int J = 8;
+  __shared__ float sums[kCombineThreads / 64][J];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int64_t t = blockIdx.x;
+  if (t < T) {
+    for (int j0 = 0; j0 < k; j0 += J) {
+      float acc[J];
+#pragma unroll
+      for (int j = 0; j < J; ++j) acc[j] = 0.0f;
+      for (int64_t c = tid * 8; c < N; c += kCombineThreads * 8) {
+        float d[8];
+        load8(d_out + t * N, c, N, d);
+#pragma unroll
+        for (int j = 0; j < J; ++j) {
+          if (j0 + j >= k) continue;
+          const int p = positions[t * k + j0 + j];
+          if (p < 0 || p >= R) continue;
+          const float w = weights[t * k + j0 + j];
+          float f[8];
+          load8(y + (int64_t)p * N, c, N, f);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            acc[j] = fmaf(d[i], f[i], acc[j]);
+            f[i] = w * d[i];
+          }
+          store8(dy + (int64_t)p * N, c, N, f);
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < J; ++j) {
+        acc[j] = row_sum<64>(acc[j]);
+        if (lane == 0) sums[wave][j] = acc[j];
+      }
+      __syncthreads();
+      if (tid < J && j0 + tid < k) {
+        float s = 0.0f;
+        for (int w = 0; w < kCombineThreads / 64; ++w) s += sums[w][tid];
+        dw[t * k + j0 + tid] = s;
+      }
+      __syncthreads();
+    }
+  }
+  const int64_t used = max(*n_used, 0);
+  const float zero[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+  for (int64_t p = used + blockIdx.x; p < R; p += gridDim.x)
+    for (int64_t c = tid * 8; c < N; c += kCombineThreads * 8) store8(dy + p * N, c, N, zero);
+}
+
+hipError_t launch_combine_backward(const void *d_out, const void *y, int64_t R,
+                                   const float *weights, const int32_t *positions,
+                                   const int32_t *n_used, int64_t T, int32_t k, int64_t N,
+                                   void *dy, float *dw, hipStream_t stream) {
+  const int64_t blocks = T > 0 ? T : (R < 1024 ? R : 1024);
+  combine_backward_kernel<<<(unsigned)blocks, kCombineThreads, 0, stream>>>(
+      static_cast<const uint16_t *>(d_out), static_cast<const uint16_t *>(y), R, weights,
+      positions, n_used, T, k, N, static_cast<uint16_t *>(dy), dw);
+  return hipGetLastError();
+}
+
+}  // namespace fp8blk

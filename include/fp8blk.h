@@ -389,6 +389,137 @@ FP8BLK_API fp8blk_status fp8_grouped_block_gemm_ue8m0(const void *x_q, const uin
                                                       int64_t total_M, int64_t N, int64_t K,
                                                       void *y_bf16, void *stream);
 
+/* ------------------------------------------------------------------------
+ * Around the expert products and the shared projections: routing with its
+ * balance loss, rows by group, the weighted return of the experts' rows, and
+ * low-rank adapters of many requests.
+ *
+ * Conventions as above, except where an entry says otherwise: fp32 and int32
+ * arrays other than logits need 4-byte alignment, byte masks none; rows of
+ * bf16 matrices may have any width N >= 0 (odd ones too) and start at any
+ * even address, only the base pointers are 16-byte aligned.  Workspaces are
+ * 16-byte aligned device memory of at least the size the _workspace_bytes
+ * function returns (0: may be NULL), overwritten, not initialised by the
+ * caller (missing: FP8BLK_ERR_NULL, too small: FP8BLK_ERR_SHAPE); calls that
+ * share one must be ordered on one stream.  None of these
+ * calls synchronises, and no result depends on the order in which workgroups
+ * run: the same inputs give the same bits. */
+
+#define FP8BLK_F32 0
+#define FP8BLK_BF16 1
+#define FP8BLK_MAX_GROUPS 1024  /* experts, groups or adapters of one call */
+#define FP8BLK_MAX_TOPK 32
+#define FP8BLK_MAX_RANK 256
+
+/* Routing of T tokens to k of E experts each, with the rows each expert gets
+ * and the balance loss.
+ *   logits [T,E] of logits_type (FP8BLK_F32 or FP8BLK_BF16) in
+ *   mask [T] bytes in, or NULL (all set): rows with 0 are not routed, whatever
+ *       their logits hold
+ *   ids [T,k] int32 out: the k largest logits' experts, largest first, equal
+ *       ones by the lowest expert; an expert whose logit is -infinity is never
+ *       chosen, and slots left over hold -1
+ *   weights [T,k] fp32 out: softmax over all experts at the chosen ones, or
+ *       (renormalize != 0) softmax over the chosen ones alone; 0 in slots
+ *       with id -1
+ *   counts [E] int32 out: rows that chose each expert
+ *   rows [1] int32 out: rows routed (mask set and some logit > -infinity) = n
+ *   loss [1] fp32 out, or NULL (not computed):
+ *       loss_coef * sum_e (counts_e * E / (k * n)) * (sum_t p_te / n),
+ *       p the softmax over all experts of the routed rows; 0 if n = 0.
+ * Sums are kept in fp32 in a fixed order.  NaN logits are never chosen and
+ * make their row's weights and the loss unspecified; ids stay in range.
+ * 1 <= E <= FP8BLK_MAX_GROUPS, 1 <= k <= min(E, FP8BLK_MAX_TOPK),
+ * T * k < 2^31.  T = 0 clears counts, rows and loss. */
+FP8BLK_API size_t fp8blk_moe_route_workspace_bytes(int64_t T, int32_t E);
+FP8BLK_API fp8blk_status fp8blk_moe_route(const void *logits, int logits_type, const uint8_t *mask,
+                                          int64_t T, int32_t E, int32_t k, int renormalize,
+                                          float loss_coef, int32_t *ids, float *weights,
+                                          int32_t *counts, int32_t *rows, float *loss,
+                                          void *workspace, size_t workspace_bytes, void *stream);
+
+/* Gradient of the logits, from the gradients of the weights and of the loss
+ * (the choice and the counts carry none).  logits, ids, weights, counts, rows,
+ * renormalize and loss_coef as in and out of fp8blk_moe_route.
+ *   d_weights [T,k] fp32 in, or NULL (zero); those of slots with id -1 are
+ *       not read
+ *   d_loss [1] fp32 in (device memory), or NULL (zero)
+ *   d_logits [T,E] of logits_type out; rows not routed get 0. */
+FP8BLK_API fp8blk_status fp8blk_moe_route_backward(
+    const void *logits, int logits_type, int64_t T, int32_t E, int32_t k, int renormalize,
+    float loss_coef, const int32_t *ids, const float *weights, const int32_t *counts,
+    const int32_t *rows, const float *d_weights, const float *d_loss, void *d_logits,
+    void *stream);
+
+/* R rows listed by group (a stable counting sort), e.g. the slots of a routed
+ * batch by expert (ids of fp8blk_moe_route, R = T * k) or rows by adapter.
+ *   ids [R] int32 in: a row's group in [0, G); rows with any other number
+ *       belong to no group
+ *   order [R] int32 out: the rows group by group, in their own order within a
+ *       group, rows of no group last
+ *   positions [R] int32 out: a row's place in order, -1 for rows of no group
+ *   offsets [G+1] int32 out: group g's rows are order[offsets[g] ..
+ *       offsets[g+1]) -- the expert_offsets of the grouped GEMM.
+ * 1 <= G <= FP8BLK_MAX_GROUPS, R < 2^31. */
+FP8BLK_API size_t fp8blk_group_rows_workspace_bytes(int64_t R, int32_t G);
+FP8BLK_API fp8blk_status fp8blk_group_rows(const int32_t *ids, int64_t R, int32_t G,
+                                           int32_t *order, int32_t *positions, int32_t *offsets,
+                                           void *workspace, size_t workspace_bytes, void *stream);
+
+/* The experts' rows back to their tokens:
+ * out[t] = bf16( base[t] + sum_j weights[t,j] * y[positions[t,j]] ), fp32 sums
+ * in the order of j.
+ *   y_bf16 [R,N], weights [T,k] fp32, positions [T,k] int32 in; a slot whose
+ *       position is outside [0, R) adds nothing, and rows of y that no slot
+ *       names are not read
+ *   base_bf16 [T,N] in, or NULL (zero); out_bf16 [T,N] out, may be base_bf16.
+ * 1 <= k <= FP8BLK_MAX_TOPK, T * k < 2^31. */
+FP8BLK_API fp8blk_status fp8blk_moe_combine(const void *y_bf16, int64_t R, const float *weights,
+                                            const int32_t *positions, const void *base_bf16,
+                                            int64_t T, int32_t k, int64_t N, void *out_bf16,
+                                            void *stream);
+
+/* Gradients of fp8blk_moe_combine (that of base is d_out itself).
+ *   rows_used [1] int32 in (device memory): the rows of y in use come first,
+ *       e.g. offsets[G] of fp8blk_group_rows; positions names each of them
+ *       once
+ *   d_y_bf16 [R,N] out: bf16(weights[t,j] * d_out[t]) at positions[t,j]; rows
+ *       from rows_used on get 0
+ *   d_weights [T,k] fp32 out: <d_out[t], y[positions[t,j]]>, 0 for slots
+ *       without a position. */
+FP8BLK_API fp8blk_status fp8blk_moe_combine_backward(
+    const void *d_out_bf16, const void *y_bf16, int64_t R, const float *weights,
+    const int32_t *positions, const int32_t *rows_used, int64_t T, int32_t k, int64_t N,
+    void *d_y_bf16, float *d_weights, void *stream);
+
+/* Low-rank adapters of many requests at once, beside a shared projection:
+ * out[t] = bf16( base[t] + scale[g] * (x[t] A[g]^T) B[g]^T ), g = ids[t];
+ * rows with ids[t] outside [0, L) have no adapter: out[t] = base[t].
+ * Products accumulate in fp32; x A^T enters the second product with 16
+ * significant bits.
+ *   base_bf16 [T,N], row stride base_stride elements, in, or NULL (zero)
+ *   x_bf16 [T,K], row stride x_stride, in
+ *   a_bf16 [L,r,K], b_bf16 [L,N,r], scale [L] fp32 (or NULL: 1) in.  Adapters
+ *       of a smaller rank are padded with zeros.
+ *   ids [T] int32 in
+ *   order [T], offsets [L+1] int32 in, or both NULL: fp8blk_group_rows of ids,
+ *       which a program with many projections computes once per batch; used
+ *       (and needed inside, in the workspace) only for T > 64
+ *   out_bf16 [T,N], row stride out_stride, out; may be base_bf16 (with the
+ *       same stride), and rows without adapter are then left alone.
+ * K a positive multiple of 128, r a multiple of 8 up to FP8BLK_MAX_RANK,
+ * 1 <= L <= FP8BLK_MAX_GROUPS; strides at least the rows' widths. */
+FP8BLK_API size_t fp8blk_lora_add_workspace_bytes(int64_t T, int64_t K, int32_t r, int32_t L,
+                                                  int listed);
+FP8BLK_API fp8blk_status fp8blk_lora_add(const void *base_bf16, int64_t base_stride,
+                                         const void *x_bf16, int64_t x_stride,
+                                         const void *a_bf16, const void *b_bf16,
+                                         const int32_t *ids, const float *scale,
+                                         const int32_t *order, const int32_t *offsets, int64_t T,
+                                         int64_t K, int64_t N, int32_t r, int32_t L,
+                                         void *out_bf16, int64_t out_stride, void *workspace,
+                                         size_t workspace_bytes, void *stream);
+
 /* Human-readable name of a status code (static storage, never NULL). */
 FP8BLK_API const char *fp8blk_status_string(int status);
 
