@@ -342,11 +342,13 @@ __global__ __launch_bounds__(kFinishThreads) void route_finish_kernel(RouteArgs 
   const size_t stride = part_stride(a.E);
   int c = 0;
   float s = 0.0f;
-  if (e < a.E)
+  if (e < a.E) {
+#pragma unroll 8
     for (int b = sl; b < blocks; b += 16) {
       c += a.part[b * stride + e];
       if (a.loss) s += __int_as_float(a.part[b * stride + a.E + 1 + e]);
     }
+  }
   cnt[sl][col] = c;
   sum[sl][col] = s;
   __syncthreads();
@@ -619,21 +621,26 @@ hipError_t launch_route_backward(const void *logits, bool bf16, int64_t T, int32
 // ---------------------------------------------------------------------------
 // Rows by group: a stable counting sort of R group numbers.
 //
-// Each wave counts its own run of rows in LDS; the counts are added up over
-// waves (and workgroups) into each run's first place in its group; then the
-// wave walks its run again, 64 rows at a time: lanes with equal keys find each
-// other with one ballot per key bit, take consecutive places, and the first of
-// them moves the run's counter on.  Rows with a number outside [0, G) count as
-// group G: they are listed last and have position -1.  Only integer counts
-// are added atomically, so the order never varies.
+// A wave holds a run of up to 16 x 64 consecutive rows, a register per 64.
+// Lanes with equal keys find each other with one ballot per key bit; the first
+// of them takes as many places from the wave's counter of that group (in LDS)
+// as there are lanes, which gives every row its place in its group within the
+// run, and leaves the run's counts.  Added up over waves, workgroups and
+// groups they give each run's first place.  Rows with a number outside [0, G)
+// count as group G: they are listed last and have position -1.  All sums are
+// integers, so the order never varies.
+//
+// Up to 8192 rows one workgroup does all of it.  Beyond, the workgroups' counts
+// come first (group_count_kernel), then their sums over workgroups, a wave per
+// group (group_scan_kernel), then the places: three launches, each of them
+// bound by latency at these sizes (1M rows move 17 MB).
 constexpr int kGroupThreads = 1024;
 constexpr int kGroupWaves = kGroupThreads / 64;
-constexpr int kGroupMaxBlocks = 128;
-// R up to which one workgroup does all of it in one launch.
 constexpr int64_t kGroupOneBlock = 8192;
 
 __device__ __forceinline__ int group_key(int id, int G) { return (unsigned)id < (unsigned)G ? id : G; }
 
+// part[g][b] = rows of group g in workgroup b's rows.
 __global__ __launch_bounds__(kGroupThreads) void group_count_kernel(
     const int32_t *__restrict__ ids, int64_t R, int G, int64_t per_block,
     int32_t *__restrict__ part) {
@@ -642,53 +649,108 @@ __global__ __launch_bounds__(kGroupThreads) void group_count_kernel(
   __syncthreads();
   const int64_t lo = blockIdx.x * per_block;
   const int64_t hi = lo + per_block < R ? lo + per_block : R;
+#pragma unroll 4
   for (int64_t i = lo + threadIdx.x; i < hi; i += kGroupThreads)
     atomicAdd(&hist[group_key(ids[i], G)], 1);
   __syncthreads();
-  for (int g = threadIdx.x; g <= G; g += kGroupThreads) part[(int64_t)blockIdx.x * (G + 1) + g] = hist[g];
+  for (int g = threadIdx.x; g <= G; g += kGroupThreads) part[(int64_t)g * gridDim.x + blockIdx.x] = hist[g];
 }
 
+__device__ __forceinline__ int wave_scan(int v, int lane) {   // inclusive
+#pragma unroll
+  for (int d = 1; d < 64; d *= 2) {
+    const int o = __shfl_up(v, d);
+    v += lane >= d ? o : 0;
+  }
+  return v;
+}
+
+// part[g][b] becomes the rows of group g before workgroup b, total[g] all of
+// them; a wave per group, 256 workgroups a step.
+constexpr int kScanThreads = 256;
+
+__global__ __launch_bounds__(kScanThreads) void group_scan_kernel(int32_t *__restrict__ part,
+                                                                  int blocks, int G1,
+                                                                  int32_t *__restrict__ total) {
+  const int lane = threadIdx.x & 63;
+  const int g = blockIdx.x * (kScanThreads / 64) + (threadIdx.x >> 6);
+  if (g >= G1) return;
+  int32_t *row = part + (int64_t)g * blocks;
+  int before = 0;
+  for (int b0 = 0; b0 < blocks; b0 += 256) {
+    int c[4], sum = 0;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const int b = b0 + lane * 4 + q;
+      c[q] = b < blocks ? row[b] : 0;
+    }
+#pragma unroll
+    for (int q = 0; q < 4; ++q) sum += c[q];
+    const int scan = wave_scan(sum, lane);
+    int at = before + scan - sum;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const int b = b0 + lane * 4 + q;
+      if (b < blocks) row[b] = at;
+      at += c[q];
+    }
+    before += __builtin_amdgcn_readlane(scan, 63);
+  }
+  if (lane == 0) total[g] = before;
+}
+
+template <int STEPS>
 __global__ __launch_bounds__(kGroupThreads) void group_place_kernel(
-    const int32_t *__restrict__ ids, int64_t R, int G, int64_t per_block,
-    const int32_t *__restrict__ part, int32_t *__restrict__ order,
+    const int32_t *__restrict__ ids, int64_t R, int G, const int32_t *__restrict__ part,
+    const int32_t *__restrict__ total, int32_t *__restrict__ order,
     int32_t *__restrict__ positions, int32_t *__restrict__ offsets) {
   extern __shared__ int hist[];          // [waves][G + 1]
   __shared__ int wave_total[kGroupWaves];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int G1 = G + 1;
+  const int64_t lo = ((int64_t)blockIdx.x * kGroupWaves + wave) * (STEPS * 64);
+  int key[STEPS], place[STEPS];
+#pragma unroll
+  for (int s = 0; s < STEPS; ++s) {
+    const int64_t i = lo + s * 64 + lane;
+    key[s] = i < R ? group_key(ids[i], G) : -1;
+  }
   for (int i = tid; i < kGroupWaves * G1; i += kGroupThreads) hist[i] = 0;
   __syncthreads();
-  const int64_t per_wave = (per_block / kGroupWaves + 63) / 64 * 64;
-  const int64_t end = (blockIdx.x + 1) * per_block < R ? (blockIdx.x + 1) * per_block : R;
-  const int64_t lo = blockIdx.x * per_block + wave * per_wave;
-  const int64_t hi = lo + per_wave < end ? lo + per_wave : end;
   int *mine = hist + wave * G1;
-  for (int64_t i = lo + lane; i < hi; i += 64) atomicAdd(&mine[group_key(ids[i], G)], 1);
+  const int bits = 32 - __clz(G);   // keys 0 .. G
+  const uint64_t lower = (1ull << lane) - 1;
+#pragma unroll
+  for (int s = 0; s < STEPS; ++s) {
+    const bool in = key[s] >= 0;
+    uint64_t same = __builtin_amdgcn_ballot_w64(in);
+    for (int b = 0; b < bits; ++b) {
+      const bool set = (key[s] >> b) & 1;
+      const uint64_t m = __builtin_amdgcn_ballot_w64(set);
+      same &= set ? m : ~m;
+    }
+    const int leader = in ? __builtin_ctzll(same) : lane;
+    int base = 0;
+    if (in && lane == leader) base = atomicAdd(&mine[key[s]], (int)__popcll(same));
+    place[s] = __shfl(base, leader) + (int)__popcll(same & lower);
+  }
   __syncthreads();
-  // groups 2 tid and 2 tid + 1: rows of earlier workgroups, of all, and the
-  // waves' first places within this workgroup's rows
-  int total[2] = {0, 0}, before[2] = {0, 0};
+  // groups 2 tid and 2 tid + 1: rows of earlier groups, then the waves' first
+  // places
+  int all[2] = {0, 0};
 #pragma unroll
   for (int q = 0; q < 2; ++q) {
     const int g = 2 * tid + q;
     if (g >= G1) continue;
     if (gridDim.x > 1) {
-      for (int b = 0; b < (int)gridDim.x; ++b) {
-        const int c = part[(int64_t)b * G1 + g];
-        before[q] += b < (int)blockIdx.x ? c : 0;
-        total[q] += c;
-      }
+      all[q] = total[g];
     } else {
-      for (int w = 0; w < kGroupWaves; ++w) total[q] += hist[w * G1 + g];
+#pragma unroll
+      for (int w = 0; w < kGroupWaves; ++w) all[q] += hist[w * G1 + g];
     }
   }
-  const int pair = total[0] + total[1];
-  int scan = pair;
-#pragma unroll
-  for (int d = 1; d < 64; d *= 2) {
-    const int o = __shfl_up(scan, d);
-    scan += lane >= d ? o : 0;
-  }
+  const int pair = all[0] + all[1];
+  const int scan = wave_scan(pair, lane);
   if (lane == 63) wave_total[wave] = scan;
   __syncthreads();
   int first = scan - pair;
@@ -698,65 +760,78 @@ __global__ __launch_bounds__(kGroupThreads) void group_place_kernel(
     const int g = 2 * tid + q;
     if (g >= G1) continue;
     if (blockIdx.x == 0) offsets[g] = first;
-    int at = first + before[q];
+    int at = first + (gridDim.x > 1 ? part[(int64_t)g * gridDim.x + blockIdx.x] : 0);
+#pragma unroll
     for (int w = 0; w < kGroupWaves; ++w) {
       const int c = hist[w * G1 + g];
       hist[w * G1 + g] = at;
       at += c;
     }
-    first += total[q];
+    first += all[q];
   }
   __syncthreads();
-  const int bits = 32 - __clz(G);   // keys 0 .. G
-  for (int64_t i0 = lo; i0 < hi; i0 += 64) {
-    const int64_t i = i0 + lane;
-    const bool in = i < hi;
-    const int key = in ? group_key(ids[i], G) : 0;
-    uint64_t same = __builtin_amdgcn_ballot_w64(in);
-    for (int b = 0; b < bits; ++b) {
-      const bool set = (key >> b) & 1;
-      const uint64_t m = __builtin_amdgcn_ballot_w64(set);
-      same &= set ? m : ~m;
-    }
-    if (in) {
-      const uint64_t below = same & ((1ull << lane) - 1);
-      const int leader = __ffsll((unsigned long long)same) - 1;
-      int base = 0;
-      if (lane == leader) base = atomicAdd(&mine[key], (int)__popcll(same));
-      base = __shfl(base, leader);
-      const int at = base + (int)__popcll(below);
-      order[at] = (int)i;
-      positions[i] = key < G ? at : -1;
-    }
+#pragma unroll
+  for (int s = 0; s < STEPS; ++s) {
+    if (key[s] < 0) continue;
+    const int64_t i = lo + s * 64 + lane;
+    const int at = mine[key[s]] + place[s];
+    order[at] = (int)i;
+    positions[i] = key[s] < G ? at : -1;
   }
 }
 
 namespace {
-int64_t group_rows_per_block(int64_t R) {
-  if (R <= kGroupOneBlock) return (R + kGroupThreads - 1) / kGroupThreads * kGroupThreads;
-  const int64_t per = (R + kGroupMaxBlocks - 1) / kGroupMaxBlocks;
-  return (per + kGroupThreads - 1) / kGroupThreads * kGroupThreads;
+
+// Steps of 64 rows a wave: the fewest that one workgroup needs; 4 beyond
+// (256 workgroups at 1M rows, one per compute unit), 16 past that.
+int group_steps(int64_t R) {
+  if (R <= kGroupOneBlock) {
+    int s = 1;
+    while (s * kGroupThreads < R) s *= 2;
+    return s;
+  }
+  return R <= (int64_t)256 * 4 * kGroupThreads ? 4 : 16;
 }
+
+int64_t group_blocks(int64_t R) {
+  const int64_t per = (int64_t)group_steps(R) * kGroupThreads;
+  return R > 0 ? (R + per - 1) / per : 1;
+}
+
 }  // namespace
 
 size_t group_workspace_bytes(int64_t R, int32_t G) {
   if (R <= kGroupOneBlock) return 0;
-  const int64_t per = group_rows_per_block(R);
-  return sizeof(int32_t) * (size_t)((R + per - 1) / per) * (G + 1);
+  return sizeof(int32_t) * (size_t)(group_blocks(R) + 1) * (G + 1);
 }
 
 hipError_t launch_group_rows(const int32_t *ids, int64_t R, int32_t G, int32_t *order,
                              int32_t *positions, int32_t *offsets, void *work,
                              hipStream_t stream) {
-  const int64_t per = R > 0 ? group_rows_per_block(R) : kGroupThreads;
-  const int blocks = R > 0 ? (int)((R + per - 1) / per) : 1;
-  int32_t *part = static_cast<int32_t *>(work);
+  const int steps = group_steps(R);
+  const int blocks = (int)group_blocks(R);
+  int32_t *total = static_cast<int32_t *>(work);
+  int32_t *part = blocks > 1 ? total + G + 1 : nullptr;
   if (blocks > 1) {
-    group_count_kernel<<<blocks, kGroupThreads, sizeof(int) * (G + 1), stream>>>(ids, R, G, per, part);
+    group_count_kernel<<<blocks, kGroupThreads, sizeof(int) * (G + 1), stream>>>(
+        ids, R, G, (int64_t)steps * kGroupThreads, part);
+    if (hipError_t e = hipGetLastError()) return e;
+    constexpr int per = kScanThreads / 64;
+    group_scan_kernel<<<(G + per) / per, kScanThreads, 0, stream>>>(part, blocks, G + 1, total);
     if (hipError_t e = hipGetLastError()) return e;
   }
-  group_place_kernel<<<blocks, kGroupThreads, sizeof(int) * kGroupWaves * (G + 1), stream>>>(
-      ids, R, G, per, part, order, positions, offsets);
+  const size_t lds = sizeof(int) * kGroupWaves * (G + 1);
+#define FP8BLK_PLACE(S)                                                                       \
+  group_place_kernel<S><<<blocks, kGroupThreads, lds, stream>>>(ids, R, G, part, total, order, \
+                                                                positions, offsets)
+  switch (steps) {
+    case 1: FP8BLK_PLACE(1); break;
+    case 2: FP8BLK_PLACE(2); break;
+    case 4: FP8BLK_PLACE(4); break;
+    case 8: FP8BLK_PLACE(8); break;
+    default: FP8BLK_PLACE(16); break;
+  }
+#undef FP8BLK_PLACE
   return hipGetLastError();
 }
 
