@@ -188,8 +188,15 @@ def _ptr(t):
     return ctypes.c_void_p(t.data_ptr()) if t is not None else ctypes.c_void_p(0)
 
 
+# The current stream's handle without a Stream object around it: 0.3 us a call
+# against 2.9 us (host-bound decode steps make several).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream():
-    return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+    if _raw_stream is not None:
+        return _raw_stream(torch.cuda.current_device())
+    return torch.cuda.current_stream().cuda_stream
 
 
 def _need(t: torch.Tensor, name: str, dtypes, ndim: int | None = None):
@@ -627,7 +634,7 @@ class Routing(NamedTuple):
     ids: torch.Tensor        # [T,k] int32, -1 in unused slots
     weights: torch.Tensor    # [T,k] fp32
     counts: torch.Tensor     # [E] int32
-    rows: torch.Tensor       # [1] int32: rows routed
+    rows: torch.Tensor | None   # [1] int32: rows routed (with the loss)
     loss: torch.Tensor | None   # fp32 scalar
     loss_coef: float
     renormalize: bool
@@ -673,6 +680,10 @@ def _same_device(first, *others):
         raise ValueError(f"the tensors are on cuda:{d}, which is not the current device")
 
 
+def _at(t):
+    return t.data_ptr() if t is not None else None
+
+
 def _work(need, device):
     return torch.empty(need, dtype=torch.uint8, device=device) if need else None
 
@@ -684,27 +695,28 @@ def _bytes(t):
 def fp8blk_moe_route(logits, mask, renormalize, loss_coef, ids, weights, counts, rows, loss,
                      workspace=None):
     """Routing into preallocated outputs; k is ids' width, ``mask`` (uint8 or
-    bool [T]) and ``loss`` (fp32, one value) may be None, ``workspace`` holds
-    fp8blk_moe_route_workspace_bytes(T, E) bytes."""
+    bool [T]), ``rows`` (int32) and ``loss`` (fp32, one value each) may be None,
+    ``workspace`` holds fp8blk_moe_route_workspace_bytes(T, E) bytes."""
     _need(logits, "logits", tuple(_LOGITS), 2)
     T, E = logits.shape
     _need(ids, "ids", _I32, 2); _need(weights, "weights", _F32, 2)
-    _need(counts, "counts", _I32, 1); _need(rows, "rows", _I32)
+    _need(counts, "counts", _I32, 1)
     k = ids.shape[1]
     _shape_eq(ids, (T, k), "ids"); _shape_eq(weights, (T, k), "weights")
     _shape_eq(counts, (E,), "counts")
-    if rows.numel() != 1 or (loss is not None and loss.numel() != 1):
-        raise ValueError("rows and loss hold one value each")
+    for t, name, dtype in ((rows, "rows", _I32), (loss, "loss", _F32)):
+        if t is not None:
+            _need(t, name, dtype)
+            if t.numel() != 1:
+                raise ValueError(f"{name} holds one value")
     if mask is not None:
         _need(mask, "mask", (torch.bool, torch.uint8), 1)
         _shape_eq(mask, (T,), "mask")
-    if loss is not None:
-        _need(loss, "loss", _F32)
     _same_device(logits, mask, ids, weights, counts, rows, loss, workspace)
     _check(load_library().fp8blk_moe_route(
-        logits.data_ptr(), _LOGITS[logits.dtype], _ptr(mask), T, E, k, int(renormalize), loss_coef,
-        ids.data_ptr(), weights.data_ptr(), counts.data_ptr(), rows.data_ptr(), _ptr(loss),
-        _ptr(workspace), _bytes(workspace), _stream()), "fp8blk_moe_route")
+        logits.data_ptr(), _LOGITS[logits.dtype], _at(mask), T, E, k, int(renormalize), loss_coef,
+        ids.data_ptr(), weights.data_ptr(), counts.data_ptr(), _at(rows), _at(loss),
+        _at(workspace), _bytes(workspace), _stream()), "fp8blk_moe_route")
 
 
 def fp8blk_moe_route_backward(logits, routing, d_weights, d_loss, d_logits):
@@ -723,11 +735,13 @@ def fp8blk_moe_route_backward(logits, routing, d_weights, d_loss, d_logits):
         _need(d_loss, "d_loss", _F32)
         if d_loss.numel() != 1:
             raise ValueError("d_loss holds one value")
+        if routing.rows is None:
+            raise ValueError("d_loss needs a routing that computed the loss")
     _same_device(logits, routing.ids, d_weights, d_loss, d_logits)
     _check(load_library().fp8blk_moe_route_backward(
         logits.data_ptr(), _LOGITS[logits.dtype], T, E, k, int(routing.renormalize),
         routing.loss_coef, routing.ids.data_ptr(), routing.weights.data_ptr(),
-        routing.counts.data_ptr(), routing.rows.data_ptr(), _ptr(d_weights), _ptr(d_loss),
+        routing.counts.data_ptr(), _at(routing.rows), _at(d_weights), _at(d_loss),
         d_logits.data_ptr(), _stream()), "fp8blk_moe_route_backward")
 
 
@@ -742,7 +756,7 @@ def fp8blk_group_rows(ids, order, positions, offsets, workspace=None):
     _same_device(ids, order, positions, offsets, workspace)
     _check(load_library().fp8blk_group_rows(
         ids.data_ptr(), R, offsets.numel() - 1, order.data_ptr(), positions.data_ptr(),
-        offsets.data_ptr(), _ptr(workspace), _bytes(workspace), _stream()), "fp8blk_group_rows")
+        offsets.data_ptr(), _at(workspace), _bytes(workspace), _stream()), "fp8blk_group_rows")
 
 
 def fp8blk_moe_combine(y, weights, positions, base, out):
@@ -757,7 +771,7 @@ def fp8blk_moe_combine(y, weights, positions, base, out):
         _shape_eq(base, (T, N), "base")
     _same_device(y, weights, positions, base, out)
     _check(load_library().fp8blk_moe_combine(
-        y.data_ptr(), R, weights.data_ptr(), positions.data_ptr(), _ptr(base), T, k, N,
+        y.data_ptr(), R, weights.data_ptr(), positions.data_ptr(), _at(base), T, k, N,
         out.data_ptr(), _stream()), "fp8blk_moe_combine")
 
 
@@ -808,9 +822,9 @@ def fp8blk_lora_add(base, x, a, b, ids, scale, groups, out, workspace):
         _shape_eq(order, (T,), "groups.order"); _shape_eq(offsets, (L + 1,), "groups.offsets")
     _same_device(x, base, a, b, ids, scale, order, out, workspace)
     _check(load_library().fp8blk_lora_add(
-        _ptr(base), ldb, x.data_ptr(), ldx, a.data_ptr(), b.data_ptr(), ids.data_ptr(),
-        _ptr(scale), _ptr(order), _ptr(offsets), T, K, N, r, L, out.data_ptr(), ldo,
-        _ptr(workspace), _bytes(workspace), _stream()), "fp8blk_lora_add")
+        _at(base), ldb, x.data_ptr(), ldx, a.data_ptr(), b.data_ptr(), ids.data_ptr(),
+        _at(scale), _at(order), _at(offsets), T, K, N, r, L, out.data_ptr(), ldo,
+        _at(workspace), _bytes(workspace), _stream()), "fp8blk_lora_add")
 
 
 def moe_route(logits, k, mask=None, renormalize=True, loss_coef=None):
@@ -823,15 +837,16 @@ def moe_route(logits, k, mask=None, renormalize=True, loss_coef=None):
     T, E = logits.shape
     if not 1 <= k <= E:
         raise ValueError(f"k must be between 1 and the number of experts, got {k}")
-    dev = logits.device
-    ids = torch.empty((T, k), dtype=torch.int32, device=dev)
-    weights = torch.empty((T, k), dtype=torch.float32, device=dev)
-    counts = torch.empty((E,), dtype=torch.int32, device=dev)
-    rows = torch.empty((1,), dtype=torch.int32, device=dev)
-    loss = torch.empty((), dtype=torch.float32, device=dev) if loss_coef is not None else None
+    ids = logits.new_empty((T, k), dtype=torch.int32)
+    weights = logits.new_empty((T, k), dtype=torch.float32)
+    counts = logits.new_empty((E,), dtype=torch.int32)
+    rows = loss = None
+    if loss_coef is not None:
+        rows = logits.new_empty((1,), dtype=torch.int32)
+        loss = logits.new_empty((), dtype=torch.float32)
     coef = float(loss_coef or 0.0)
     fp8blk_moe_route(logits, mask, renormalize, coef, ids, weights, counts, rows, loss,
-                     _work(load_library().fp8blk_moe_route_workspace_bytes(T, E), dev))
+                     _work(load_library().fp8blk_moe_route_workspace_bytes(T, E), logits.device))
     return Routing(ids, weights, counts, rows, loss, coef, bool(renormalize))
 
 
@@ -847,19 +862,18 @@ def group_rows(ids, groups):
     """Rows (entries of ids, any shape) listed by group, in their own order
     within a group; entries outside [0, groups) belong to none and come last."""
     _need(ids, "ids", _I32)
-    R, dev = ids.numel(), ids.device
-    order = torch.empty((R,), dtype=torch.int32, device=dev)
-    positions = torch.empty_like(ids)
-    offsets = torch.empty((groups + 1,), dtype=torch.int32, device=dev)
+    R = ids.numel()
+    order, positions = ids.new_empty((R,)), torch.empty_like(ids)
+    offsets = ids.new_empty((groups + 1,))
     fp8blk_group_rows(ids, order, positions, offsets,
-                      _work(load_library().fp8blk_group_rows_workspace_bytes(R, groups), dev))
+                      _work(load_library().fp8blk_group_rows_workspace_bytes(R, groups), ids.device))
     return RowGroups(order, positions, offsets)
 
 
 def moe_combine(y, weights, positions, base=None):
     """out[t] = base[t] + sum_j weights[t,j] * y[positions[t,j]] in bf16;
     slots with position -1 add nothing."""
-    out = torch.empty((weights.shape[0], y.shape[1]), dtype=torch.bfloat16, device=y.device)
+    out = y.new_empty((weights.shape[0], y.shape[1]))
     fp8blk_moe_combine(y, weights, positions, base, out)
     return out
 
@@ -879,7 +893,7 @@ def lora_add(base, x, a, b, ids, scale=None, groups=None, out=None):
     T, K = x.shape
     L, r = a.shape[0], a.shape[1]
     if out is None:
-        out = torch.empty((T, b.shape[1]), dtype=torch.bfloat16, device=x.device)
+        out = x.new_empty((T, b.shape[1]))
     need = load_library().fp8blk_lora_add_workspace_bytes(T, K, r, L, groups is not None)
     fp8blk_lora_add(base, x, a, b, ids, scale, groups, out, _work(need, x.device))
     return out

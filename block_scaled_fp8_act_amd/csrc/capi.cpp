@@ -413,7 +413,7 @@ fp8blk_status fp8blk_moe_route(const void *logits, int logits_type, const uint8_
                                int32_t *ids, float *weights, int32_t *counts, int32_t *rows,
                                float *loss, void *workspace, size_t workspace_bytes,
                                void *stream) {
-  if (!counts || !rows || (T > 0 && (!logits || !ids || !weights))) return FP8BLK_ERR_NULL;
+  if (!counts || (T > 0 && (!logits || !ids || !weights))) return FP8BLK_ERR_NULL;
   if (bad_route(logits_type, T, E, k)) return FP8BLK_ERR_SHAPE;
   const size_t need = fp8blk::route_workspace_bytes(T, E);
   if (need > 0 && workspace == nullptr) return FP8BLK_ERR_NULL;
@@ -433,7 +433,7 @@ fp8blk_status fp8blk_moe_route_backward(const void *logits, int logits_type, int
                                         const int32_t *counts, const int32_t *rows,
                                         const float *d_weights, const float *d_loss,
                                         void *d_logits, void *stream) {
-  if (T > 0 && (!logits || !ids || !weights || !counts || !rows || !d_logits))
+  if (T > 0 && (!logits || !ids || !weights || !counts || !d_logits || (d_loss && !rows)))
     return FP8BLK_ERR_NULL;
   if (bad_route(logits_type, T, E, k)) return FP8BLK_ERR_SHAPE;
   if (T > 0 && (any_misaligned({logits, d_logits}, 16) ||

@@ -152,9 +152,9 @@ __device__ __forceinline__ void store_row(T *row, int E, int sub, const float *v
 // workgroups in a fixed order, so results do not vary between runs; counts
 // are integer LDS atomics.  The workgroup's sums go to `part` and
 // route_finish_kernel adds them, except when one workgroup does all rows.
-constexpr int kRouteThreads = 512;
-constexpr int kRouteWaves = kRouteThreads / 64;
-constexpr int kRouteMaxBlocks = 512;
+constexpr int kRouteMaxThreads = 1024;
+constexpr int kRouteMaxWaves = kRouteMaxThreads / 64;
+constexpr int kRouteMaxBlocks = 256;
 constexpr int kRouteMaxK = 32;
 
 struct RouteArgs {
@@ -180,16 +180,17 @@ __device__ __forceinline__ float balance(double sum, float coef, int E, int k, i
 }
 
 template <typename T, int LPR, int V, int VEC>
-__global__ __launch_bounds__(kRouteThreads) void route_kernel(RouteArgs a) {
+__global__ __launch_bounds__(kRouteMaxThreads) void route_kernel(RouteArgs a) {
   extern __shared__ float lds[];          // [E] counts, [waves][E] sums
-  __shared__ int live_rows[kRouteWaves];
+  __shared__ int live_rows[kRouteMaxWaves];
+  const int threads = blockDim.x, waves = threads / 64;
   constexpr int RPW = 64 / LPR;
   constexpr int SLOTS = (kRouteMaxK + LPR - 1) / LPR;
   int *hist = reinterpret_cast<int *>(lds);
   float *sums = lds + a.E;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int sub = lane % LPR;
-  for (int e = tid; e < a.E; e += kRouteThreads) hist[e] = 0;
+  for (int e = tid; e < a.E; e += threads) hist[e] = 0;
   __syncthreads();
 
   float acc[V];
@@ -197,8 +198,8 @@ __global__ __launch_bounds__(kRouteThreads) void route_kernel(RouteArgs a) {
   for (int c = 0; c < V; ++c) acc[c] = 0.0f;
   int live_count = 0;
   const bool all = a.loss || !a.renorm;   // probabilities over every expert
-  const int64_t step = (int64_t)gridDim.x * kRouteWaves * RPW;
-  const int64_t first = ((int64_t)blockIdx.x * kRouteWaves + wave) * RPW;
+  const int64_t step = (int64_t)gridDim.x * waves * RPW;
+  const int64_t first = ((int64_t)blockIdx.x * waves + wave) * RPW;
   for (int64_t r0 = first; r0 < a.T; r0 += step) {
     const int64_t row = r0 + lane / LPR;
     const bool in = row < a.T && (!a.mask || a.mask[row]);
@@ -291,14 +292,14 @@ __global__ __launch_bounds__(kRouteThreads) void route_kernel(RouteArgs a) {
   }
   __syncthreads();
   int live_total = 0;
-  for (int w = 0; w < kRouteWaves; ++w) live_total += live_rows[w];
+  for (int w = 0; w < waves; ++w) live_total += live_rows[w];
   const bool only = gridDim.x == 1;
   int32_t *part = a.part + blockIdx.x * part_stride(a.E);
   float mine = 0.0f;   // this thread's experts: sum of c_e * sum p_e
-  for (int e = tid; e < a.E; e += kRouteThreads) {
+  for (int e = tid; e < a.E; e += threads) {
     float s = 0.0f;
     if (a.loss)
-      for (int w = 0; w < kRouteWaves; ++w) s += sums[w * a.E + e];
+      for (int w = 0; w < waves; ++w) s += sums[w * a.E + e];
     if (only) {
       a.counts[e] = hist[e];
       mine += (float)hist[e] * s;
@@ -314,7 +315,7 @@ __global__ __launch_bounds__(kRouteThreads) void route_kernel(RouteArgs a) {
     }
     return;
   }
-  if (tid == 0) *a.rows = live_total;
+  if (tid == 0 && a.rows) *a.rows = live_total;
   if (!a.loss) return;
   __syncthreads();
   mine = row_sum<64>(mine);
@@ -322,68 +323,87 @@ __global__ __launch_bounds__(kRouteThreads) void route_kernel(RouteArgs a) {
   __syncthreads();
   if (tid == 0) {
     double s = 0.0;
-    for (int w = 0; w < kRouteWaves; ++w) s += (double)sums[w];
+    for (int w = 0; w < waves; ++w) s += (double)sums[w];
     *a.loss_out = balance(s, a.coef, a.E, a.k, live_total);
   }
 }
 
-// Adds the workgroups' counts and sums: 16 experts per workgroup, 16 threads
-// an expert.  The last workgroup to finish (an integer ticket; nothing waits
-// for it) adds the experts' terms of the loss in order.
-constexpr int kFinishThreads = 256;
+// Adds the workgroups' counts and sums: COLS experts per workgroup, the other
+// threads share the workgroups' entries.  Up to 64 experts one workgroup does
+// all of them; beyond, the last one to finish (an integer ticket; nothing
+// waits for it) adds the experts' terms of the loss in order.
+constexpr int kFinishThreads = 1024;
 
+template <int COLS>
 __global__ __launch_bounds__(kFinishThreads) void route_finish_kernel(RouteArgs a, int blocks,
                                                                       float *terms) {
-  __shared__ int cnt[16][17];
-  __shared__ float sum[16][17];
+  constexpr int SL = kFinishThreads / COLS;      // slices of the workgroups
+  constexpr int WAVES = kFinishThreads / 64;
+  __shared__ int cnt[SL][COLS + 1];
+  __shared__ float sum[SL][COLS + 1];
+  __shared__ int live[WAVES];
+  __shared__ double part_sum[WAVES];
   __shared__ int last;
-  const int col = threadIdx.x & 15, sl = threadIdx.x >> 4;
-  const int e = blockIdx.x * 16 + col;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int col = tid % COLS, sl = tid / COLS;
+  const int e = blockIdx.x * COLS + col;
   const size_t stride = part_stride(a.E);
-  int c = 0;
+  int c = 0, n = tid < blocks ? a.part[tid * stride + a.E] : 0;   // (at most 256 workgroups)
   float s = 0.0f;
   if (e < a.E) {
 #pragma unroll 8
-    for (int b = sl; b < blocks; b += 16) {
+    for (int b = sl; b < blocks; b += SL) {
       c += a.part[b * stride + e];
       if (a.loss) s += __int_as_float(a.part[b * stride + a.E + 1 + e]);
     }
   }
   cnt[sl][col] = c;
   sum[sl][col] = s;
+#pragma unroll
+  for (int d = 1; d < 64; d *= 2) n += __shfl_xor(n, d);
+  if (lane == 0) live[wave] = n;
   __syncthreads();
+  n = 0;
+#pragma unroll
+  for (int w = 0; w < WAVES; ++w) n += live[w];
+  double t = 0.0;
   if (sl == 0 && e < a.E) {
     c = 0;
     s = 0.0f;
-    for (int i = 0; i < 16; ++i) {
+#pragma unroll 16
+    for (int i = 0; i < SL; ++i) {
       c += cnt[i][col];
       s += sum[i][col];
     }
     a.counts[e] = c;
-    if (a.loss)
+    t = (double)((float)c * s);
+    if (a.loss && gridDim.x > 1)
       __hip_atomic_store(&terms[e], (float)c * s, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
   }
-  __syncthreads();
-  if (threadIdx.x == 0)
-    last = __hip_atomic_fetch_add(a.ticket, 1, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT) ==
-           (int)gridDim.x - 1;
-  __syncthreads();
-  if (!last) return;
-  // live rows and loss, by the first wave
-  if (threadIdx.x >= 64) return;
-  int n = 0;
-  for (int b = threadIdx.x; b < blocks; b += 64) n += a.part[b * stride + a.E];
-#pragma unroll
-  for (int d = 1; d < 64; d *= 2) n += __shfl_xor(n, d);
-  if (threadIdx.x == 0) *a.rows = n;
+  if (blockIdx.x == 0 && tid == 0 && a.rows) *a.rows = n;
   if (!a.loss) return;
-  double t = 0.0;
-  for (int i = threadIdx.x; i < a.E; i += 64)
-    t += (double)__hip_atomic_load(&terms[i], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  if (gridDim.x > 1) {
+    __syncthreads();
+    if (tid == 0)
+      last = __hip_atomic_fetch_add(a.ticket, 1, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT) ==
+             (int)gridDim.x - 1;
+    __syncthreads();
+    if (!last) return;
+    t = tid < a.E
+            ? (double)__hip_atomic_load(&terms[tid], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT)
+            : 0.0;
+  }
 #pragma unroll
   for (int d = 1; d < 64; d *= 2) t += __shfl_xor(t, d);
-  if (threadIdx.x == 0) *a.loss_out = balance(t, a.coef, a.E, a.k, n);
+  if (lane == 0) part_sum[wave] = t;
+  __syncthreads();
+  if (tid == 0) {
+    t = 0.0;
+    for (int w = 0; w < WAVES; ++w) t += part_sum[w];
+    *a.loss_out = balance(t, a.coef, a.E, a.k, n);
+  }
 }
+static_assert(kRouteMaxBlocks <= kFinishThreads, "one entry of live rows a thread");
 
 // ---------------------------------------------------------------------------
 // Routing, backward: for a live row, with g_e = dL * coef * E * c_e / (k n^2),
@@ -406,10 +426,14 @@ struct RouteBackArgs {
   void *dlogits;
 };
 
+constexpr int kBackThreads = 512;
+constexpr int kBackWaves = kBackThreads / 64;
+constexpr int kBackMaxBlocks = 1024;
+
 template <typename T, int LPR, int V, int VEC>
-__global__ __launch_bounds__(kRouteThreads) void route_backward_kernel(RouteBackArgs a) {
+__global__ __launch_bounds__(kBackThreads) void route_backward_kernel(RouteBackArgs a) {
   extern __shared__ float lds[];     // [waves][RPW][E]
-  __shared__ int total_count[kRouteWaves];
+  __shared__ int total_count[kBackWaves];
   constexpr int RPW = 64 / LPR;
   constexpr int SLOTS = (kRouteMaxK + LPR - 1) / LPR;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
@@ -421,13 +445,13 @@ __global__ __launch_bounds__(kRouteThreads) void route_backward_kernel(RouteBack
   float g[V];
   if (a.dloss) {
     int part = 0;
-    for (int e = tid; e < a.E; e += kRouteThreads) part += a.counts[e];
+    for (int e = tid; e < a.E; e += kBackThreads) part += a.counts[e];
 #pragma unroll
     for (int d = 1; d < 64; d *= 2) part += __shfl_xor(part, d);
     if (lane == 0) total_count[wave] = part;
     __syncthreads();
     int total = 0;
-    for (int w = 0; w < kRouteWaves; ++w) total += total_count[w];
+    for (int w = 0; w < kBackWaves; ++w) total += total_count[w];
     const float mean = (float)total / (float)a.E;
     const float n = (float)max(*a.rows, 1);
     const float f = dl * (a.coef * (float)a.E / ((float)a.k * n)) / n;
@@ -441,8 +465,8 @@ __global__ __launch_bounds__(kRouteThreads) void route_backward_kernel(RouteBack
     for (int c = 0; c < V; ++c) g[c] = 0.0f;
   }
 
-  const int64_t step = (int64_t)gridDim.x * kRouteWaves * RPW;
-  for (int64_t r0 = ((int64_t)blockIdx.x * kRouteWaves + wave) * RPW; r0 < a.T; r0 += step) {
+  const int64_t step = (int64_t)gridDim.x * kBackWaves * RPW;
+  for (int64_t r0 = ((int64_t)blockIdx.x * kBackWaves + wave) * RPW; r0 < a.T; r0 += step) {
     const int64_t row = r0 + lane / LPR;
     const int64_t at = row < a.T ? row : a.T - 1;
     const bool live = row < a.T && a.ids[at * a.k] >= 0;
@@ -527,9 +551,9 @@ hipError_t by_width(int E, A... args) {
 
 template <typename T, int LPR, int V, int VEC>
 struct RouteLaunch {
-  static hipError_t go(const RouteArgs *a, int blocks, hipStream_t st) {
-    const size_t lds = sizeof(float) * a->E * (1 + (a->loss ? kRouteWaves : 0));
-    route_kernel<T, LPR, V, VEC><<<blocks, kRouteThreads, lds + 64, st>>>(*a);
+  static hipError_t go(const RouteArgs *a, int blocks, int threads, hipStream_t st) {
+    const size_t lds = sizeof(float) * a->E * (1 + (a->loss ? threads / 64 : 0));
+    route_kernel<T, LPR, V, VEC><<<blocks, threads, lds + 64, st>>>(*a);
     return hipGetLastError();
   }
 };
@@ -537,26 +561,32 @@ struct RouteLaunch {
 template <typename T, int LPR, int V, int VEC>
 struct RouteBackLaunch {
   static hipError_t go(const RouteBackArgs *a, int blocks, hipStream_t st) {
-    const size_t lds = sizeof(float) * a->E * kRouteWaves * (64 / LPR);
-    route_backward_kernel<T, LPR, V, VEC><<<blocks, kRouteThreads, lds, st>>>(*a);
+    const size_t lds = sizeof(float) * a->E * kBackWaves * (64 / LPR);
+    route_backward_kernel<T, LPR, V, VEC><<<blocks, kBackThreads, lds, st>>>(*a);
     return hipGetLastError();
   }
 };
 
-int route_rows_per_block(int E) { return kRouteWaves * (E <= 256 ? 4 : 1); }
+int route_rows_per_wave(int E) { return E <= 256 ? 4 : 1; }
 
-int route_blocks(int64_t T, int E) {
-  const int64_t per = route_rows_per_block(E);
-  const int64_t need = (T + per - 1) / per;
-  // one workgroup for as many rows as cost less than the second launch
-  if (need <= 2) return 1;
-  return (int)(need < kRouteMaxBlocks ? need : kRouteMaxBlocks);
+// One workgroup for as many rows as cost less than the second launch, spread
+// over its waves; else up to 256, of 8 waves while that leaves a wave one
+// group of rows and of 16 beyond (fewer sums to add up).
+struct RoutePlan {
+  int blocks, threads;
+};
+RoutePlan route_plan(int64_t T, int E) {
+  const int64_t waves = (T + route_rows_per_wave(E) - 1) / route_rows_per_wave(E);
+  if (waves <= kRouteMaxWaves) return {1, waves <= 4 ? 256 : kRouteMaxThreads};
+  const int per = waves <= 8 * kRouteMaxBlocks ? 8 : kRouteMaxWaves;
+  const int64_t need = (waves + per - 1) / per;
+  return {(int)(need < kRouteMaxBlocks ? need : kRouteMaxBlocks), per * 64};
 }
 
 }  // namespace
 
 size_t route_workspace_bytes(int64_t T, int32_t E) {
-  const int blocks = route_blocks(T, E);
+  const int blocks = route_plan(T, E).blocks;
   if (blocks <= 1) return 0;
   return sizeof(int32_t) * (blocks * (2 * (size_t)E + 1) + E + 1);
 }
@@ -579,17 +609,20 @@ hipError_t launch_route(const void *logits, bool bf16, const uint8_t *mask, int6
   a.counts = counts;
   a.rows = rows;
   a.loss_out = loss;
-  const int blocks = route_blocks(T, E);
+  const RoutePlan plan = route_plan(T, E);
+  const int blocks = plan.blocks;
   a.part = static_cast<int32_t *>(work);
   float *terms = nullptr;
   if (blocks > 1) {
     terms = reinterpret_cast<float *>(a.part + blocks * (2 * (size_t)E + 1));
     a.ticket = reinterpret_cast<int32_t *>(terms + E);
   }
-  hipError_t e = bf16 ? by_width<uint16_t, RouteLaunch>(E, &a, blocks, stream)
-                      : by_width<uint32_t, RouteLaunch>(E, &a, blocks, stream);
+  hipError_t e = bf16 ? by_width<uint16_t, RouteLaunch>(E, &a, blocks, plan.threads, stream)
+                      : by_width<uint32_t, RouteLaunch>(E, &a, blocks, plan.threads, stream);
   if (e != hipSuccess || blocks == 1) return e;
-  route_finish_kernel<<<(E + 15) / 16, kFinishThreads, 0, stream>>>(a, blocks, terms);
+  if (E <= 32) route_finish_kernel<32><<<1, kFinishThreads, 0, stream>>>(a, blocks, terms);
+  else if (E <= 64) route_finish_kernel<64><<<1, kFinishThreads, 0, stream>>>(a, blocks, terms);
+  else route_finish_kernel<16><<<(E + 15) / 16, kFinishThreads, 0, stream>>>(a, blocks, terms);
   return hipGetLastError();
 }
 
@@ -611,9 +644,9 @@ hipError_t launch_route_backward(const void *logits, bool bf16, int64_t T, int32
   a.dw = dw;
   a.dloss = dloss;
   a.dlogits = dlogits;
-  const int64_t per = route_rows_per_block(E);
+  const int64_t per = route_rows_per_wave(E) * kBackWaves;
   const int64_t need = (T + per - 1) / per;
-  const int blocks = (int)(need < 2 * kRouteMaxBlocks ? need : 2 * kRouteMaxBlocks);
+  const int blocks = (int)(need < kBackMaxBlocks ? need : kBackMaxBlocks);
   return bf16 ? by_width<uint16_t, RouteBackLaunch>(E, &a, blocks, stream)
               : by_width<uint32_t, RouteBackLaunch>(E, &a, blocks, stream);
 }

@@ -423,7 +423,8 @@ FP8BLK_API fp8blk_status fp8_grouped_block_gemm_ue8m0(const void *x_q, const uin
  *       (renormalize != 0) softmax over the chosen ones alone; 0 in slots
  *       with id -1
  *   counts [E] int32 out: rows that chose each expert
- *   rows [1] int32 out: rows routed (mask set and some logit > -infinity) = n
+ *   rows [1] int32 out, or NULL (not wanted): rows routed (mask set and some
+ *       logit > -infinity) = n
  *   loss [1] fp32 out, or NULL (not computed):
  *       loss_coef * sum_e (counts_e * E / (k * n)) * (sum_t p_te / n),
  *       p the softmax over all experts of the routed rows; 0 if n = 0.
@@ -440,7 +441,8 @@ FP8BLK_API fp8blk_status fp8blk_moe_route(const void *logits, int logits_type, c
 
 /* Gradient of the logits, from the gradients of the weights and of the loss
  * (the choice and the counts carry none).  logits, ids, weights, counts, rows,
- * renormalize and loss_coef as in and out of fp8blk_moe_route.
+ * renormalize and loss_coef as in and out of fp8blk_moe_route; counts and rows
+ * are read only with d_loss (rows may be NULL without it).
  *   d_weights [T,k] fp32 in, or NULL (zero); those of slots with id -1 are
  *       not read
  *   d_loss [1] fp32 in (device memory), or NULL (zero)

@@ -136,8 +136,8 @@ def test_route_without_loss_and_its_repeats():
         a = fb.moe_route(x, 8, mask=m, loss_coef=0.01)
         b = fb.moe_route(x, 8, mask=m)
         c = fb.moe_route(x, 8, mask=m, loss_coef=0.01)
-        assert b.loss is None
-        for f in ("ids", "weights", "counts", "rows"):
+        assert b.loss is None and b.rows is None
+        for f in ("ids", "weights", "counts"):
             assert torch.equal(getattr(a, f), getattr(b, f)), f
         assert torch.equal(a.loss, c.loss)
 
@@ -229,3 +229,5 @@ def test_route_refusals():
         fb.moe_route_backward(x, r, torch.zeros(4, 3, device=dev()))
     with pytest.raises(ValueError):
         fb.moe_route_backward(torch.zeros(4, 9, device=dev()), r)
+    with pytest.raises(ValueError):
+        fb.moe_route_backward(x, r, d_loss=torch.ones(1, device=dev()))   # routed without the loss
