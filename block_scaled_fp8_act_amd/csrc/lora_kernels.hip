@@ -21,17 +21,18 @@ typedef unsigned v4u __attribute__((ext_vector_type(4)));
 
 namespace {
 
-constexpr int kTileRows = 16;
+constexpr int kTileRows = 16;   // rows of a matrix instruction, and of a small batch's tile
 constexpr int kLoraThreads = 256;
 constexpr int kLoraWaves = kLoraThreads / 64;
 // Batches up to a wave's width find their rows from the adapter numbers
-// directly; larger ones through a listing by adapter (order, offsets).
+// directly and take tiles of 16 rows; larger ones go by a listing by adapter
+// (order, offsets) in tiles of 64.  16-row tiles past 64 rows measured 16-20 %
+// faster with an adapter per row (128 rows, 4096 x 4096, r = 16: 22 against
+// 27 us) and up to three times slower with shared ones (400 rows of 20
+// adapters, r = 128: 90 against 31 us).
 constexpr int kDirectRows = 64;
 constexpr int kWideRows = 64;
-// Batches from here on take the kernels with 64-row tiles (measured at 515
-// rows of 32 adapters, 7168 -> 1536, r = 64: 26 us against 36 us).
-constexpr int64_t kWideBatch = 512;
-constexpr int kMaxSplit = 16;
+constexpr int kMaxSplit = 8;
 
 struct LoraArgs {
   const uint16_t *x, *a, *b, *base;
@@ -127,22 +128,6 @@ __device__ __forceinline__ bool find_listed(const LoraArgs &p, int index, Listed
   return false;
 }
 
-__device__ __forceinline__ bool find_tile_listed(const LoraArgs &p, int index, Tile *t) {
-  ListedTile lt;
-  if (!find_listed<kTileRows>(p, index, &lt)) return false;
-  t->g = lt.g;
-  const int slot = threadIdx.x & 15;
-  const int row = slot < lt.rows ? p.order[lt.start + slot] : -1;
-  t->row = row < p.T ? row : -1;
-  return true;
-}
-
-template <bool DIRECT>
-__device__ __forceinline__ bool find_tile(const LoraArgs &p, int index, Tile *t) {
-  if constexpr (DIRECT) return find_tile_direct(p, index, t);
-  else return find_tile_listed(p, index, t);
-}
-
 __device__ __forceinline__ v8bf as_bf(const uint4 &v) { return __builtin_bit_cast(v8bf, v); }
 
 struct __attribute__((packed, aligned(2))) U128 {
@@ -165,151 +150,224 @@ __device__ __forceinline__ uint16_t bf_bits(float f) {
 
 }  // namespace
 
-// h[s][row][:] = the part of x[row] A[g]^T over K range s.  The instruction's
-// rows are ranks (A) and its columns the tile's rows (x): both operands are
-// 16-byte loads along K, and a lane ends with four consecutive ranks of one
-// row.  The four waves take every fourth 32 of K and add up through LDS.
-template <bool DIRECT, int NT>
+// ---------------------------------------------------------------------------
+// Batches of up to 64 rows: a tile of up to 16 rows of one adapter.
+//
+// Latency counts here: the adapters in use are read once each from HBM (A and B
+// of 16 requests at 4096 x 4096, r = 16: 4 MB, 1 us) by as many workgroups as
+// the chip holds, in two launches.
+//
+// Chunk swizzle of 128-byte LDS rows: 16-byte chunk c of row r is kept at
+// c ^ f(r), so that 16 lanes reading one chunk of 16 consecutive rows meet no
+// bank twice.
+__device__ __forceinline__ int swz_f(int row) { return ((row & 3) << 1) | ((row >> 2) & 1); }
+
+// Barrier for data passed through LDS alone: unlike __syncthreads() it leaves
+// global loads and stores in flight.
+__device__ __forceinline__ void lds_barrier() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
+  __builtin_amdgcn_s_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
+}
+
+// h[s][row][16 ranks] = the part of x[row] A[g]^T over K range s, a workgroup
+// per tile, 16 ranks and range.  A lane of a matrix instruction holds 16 bytes
+// of one row and its neighbours other rows; loaded that way every lane's 16
+// bytes are a request of their own.  So 256 of K at a time pass through LDS,
+// loaded with 32 neighbouring lanes on a row's 512 bytes, one stage ahead in
+// registers; each wave takes 64 of them, and the waves' sums add up through
+// LDS.  The instruction's rows are ranks, its columns the tile's rows.
+constexpr int kSmallK = 256;
+
 __global__ __launch_bounds__(kLoraThreads) void lora_shrink_kernel(LoraArgs p) {
-  __shared__ float part[kLoraWaves][NT * 256];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int s = blockIdx.x % p.S;
+  __shared__ __align__(16) uint8_t lds[kLoraWaves][32 * 128];   // 64 of K: 16 rows of x, 16 of A
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int pieces = (p.r + 15) / 16;
+  const int s = blockIdx.x % p.S, piece = blockIdx.x / p.S % pieces;
   Tile t;
-  if (!find_tile<DIRECT>(p, blockIdx.x / p.S, &t) || t.g >= p.L) return;
-  const int KB = (int)(p.K / kBlock);
+  if (!find_tile_direct(p, blockIdx.x / p.S / pieces, &t) || t.g >= p.L) return;
+  const int KB = (int)((p.K + kSmallK - 1) / kSmallK);
   const int kb0 = (int)((int64_t)KB * s / p.S), kb1 = (int)((int64_t)KB * (s + 1) / p.S);
-  const int koff = wave * 32 + (lane >> 4) * 8;
-  // slots past the tile's rows repeat slot 0's row (a tile has one at least)
+  // thread: rows tid / 32 and + 8 of x (slots past the tile's rows repeat the
+  // first) and of A, 16 bytes at column tid % 32 * 8 of the stage
+  const int r8 = tid >> 5, c32 = tid & 31;
   const int row0 = __builtin_amdgcn_readlane(t.row, 0);
-  const int row = max(t.row >= 0 ? t.row : row0, 0);
-  const uint16_t *xr = p.x + (int64_t)row * p.ldx + koff;
-  const uint16_t *ar[NT];
+  const uint16_t *src[4];
 #pragma unroll
-  for (int f = 0; f < NT; ++f)
-    ar[f] = p.a + ((int64_t)t.g * p.r + min(f * 16 + (lane & 15), p.r - 1)) * p.K + koff;
-  v4f acc[NT];
+  for (int j = 0; j < 2; ++j) {
+    const int slot = r8 + 8 * j;
+    const int row = __shfl(t.row, slot);
+    src[j] = p.x + (int64_t)(row >= 0 ? row : row0) * p.ldx + c32 * 8;
+    src[2 + j] = p.a + ((int64_t)t.g * p.r + min(piece * 16 + slot, p.r - 1)) * p.K + c32 * 8;
+  }
+  const int dst = r8 * 128 + (((c32 & 7) ^ swz_f(r8)) << 4);   // (row + 8: the same swizzle)
+  v4u v[4];
+  auto load = [&](int kb) {
+    const int64_t k = (int64_t)min(kb, kb1 - 1) * kSmallK;
+    const bool in = k + c32 * 8 < p.K;    // (K is a multiple of 128)
 #pragma unroll
-  for (int f = 0; f < NT; ++f) acc[f] = v4f{0, 0, 0, 0};
-#pragma unroll 4
+    for (int j = 0; j < 4; ++j) v[j] = in ? load16v(src[j] + k) : v4u{0, 0, 0, 0};
+  };
+  v4f acc = v4f{0, 0, 0, 0};
+  load(kb0);
   for (int kb = kb0; kb < kb1; ++kb) {
-    const int64_t k = (int64_t)kb * kBlock;
-    const v8bf xv = as_bf(load16(xr + k));
+    lds_barrier();
 #pragma unroll
-    for (int f = 0; f < NT; ++f) {
-      if (f * 16 < p.r)
-        acc[f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-            as_bf(*reinterpret_cast<const uint4 *>(ar[f] + k)), xv, acc[f], 0, 0, 0);
+    for (int j = 0; j < 4; ++j)
+      *reinterpret_cast<v4u *>(&lds[c32 >> 3][dst + j * 8 * 128]) = v[j];
+    load(kb + 1);
+    lds_barrier();
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int r = lane & 15;
+      const int at = r * 128 + (((h * 4 + (lane >> 4)) ^ swz_f(r)) << 4);
+      const v8bf xv = *reinterpret_cast<const v8bf *>(&lds[wave][at]);
+      const v8bf av = *reinterpret_cast<const v8bf *>(&lds[wave][16 * 128 + at]);
+      acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(av, xv, acc, 0, 0, 0);
     }
   }
+  lds_barrier();
+  v4f *part = reinterpret_cast<v4f *>(&lds[0][0]);
+  part[wave * 64 + lane] = acc;
+  lds_barrier();
+  if (wave) return;
 #pragma unroll
-  for (int f = 0; f < NT; ++f)
-    *reinterpret_cast<v4f *>(&part[wave][f * 256 + lane * 4]) = acc[f];
-  __syncthreads();
-  // wave w stores fragments w, w + 4, ...
-  for (int f = wave; f * 16 < p.r; f += kLoraWaves) {
-    v4f v = v4f{0, 0, 0, 0};
+  for (int w = 1; w < kLoraWaves; ++w) acc += part[w * 64 + lane];
+  const int rank = piece * 16 + (lane >> 4) * 4;
+  if (t.row >= 0 && rank < p.r)
+    *reinterpret_cast<v4f *>(p.h + ((int64_t)s * p.T + t.row) * p.r + rank) = acc;
+}
+
+// v as upper half and rest (an infinite or NaN value has no rest).
+__device__ __forceinline__ void split_bf16(float v, uint16_t *hi, uint16_t *lo) {
+  const uint32_t u = __float_as_uint(v) & 0xffff0000u;
+  *hi = (uint16_t)(u >> 16);
+  *lo = bf_bits(__builtin_isfinite(v) ? v - __uint_as_float(u) : 0.0f);
+}
+
+// scale times the sum of h's parts at hp (8 ranks), split: the upper halves,
+// then the rests.
+__device__ __forceinline__ void join_parts(const LoraArgs &p, const float *hp, float scale,
+                                           v4u *hi, v4u *lo) {
+  const int64_t step = p.T * p.r;
+  v4f h[2] = {v4f{0, 0, 0, 0}, v4f{0, 0, 0, 0}};
+  for (int s0 = 0; s0 < p.S; s0 += 8) {   // 8 parts' loads in flight
+    v4f u[8][2];
 #pragma unroll
-    for (int w = 0; w < kLoraWaves; ++w)
-      v += *reinterpret_cast<const v4f *>(&part[w][f * 256 + lane * 4]);
-    const int rank = f * 16 + (lane >> 4) * 4;
-    if (t.row >= 0 && rank < p.r)
-      *reinterpret_cast<v4f *>(p.h + ((int64_t)s * p.T + t.row) * p.r + rank) = v;
+    for (int j = 0; j < 8; ++j) {
+      const float *q = hp + min(s0 + j, p.S - 1) * step;
+      u[j][0] = *reinterpret_cast<const v4f *>(q);
+      u[j][1] = *reinterpret_cast<const v4f *>(q + 4);
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (s0 + j < p.S) {
+        h[0] += u[j][0];
+        h[1] += u[j][1];
+      }
+  }
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    uint16_t a, b, c, d;
+    split_bf16(h[j >> 1][2 * j & 3] * scale, &a, &b);
+    split_bf16(h[j >> 1][(2 * j & 3) + 1] * scale, &c, &d);
+    (*hi)[j] = a | ((uint32_t)c << 16);
+    (*lo)[j] = b | ((uint32_t)d << 16);
   }
 }
 
-// out = base + (scale * sum of h's parts) B^T for 16 rows and 64 columns a
+// out = base + (scale * sum of h's parts) B^T for a tile and 128 columns, 32 a
 // wave.  h enters the product as the sum of two bf16 values, its upper half
 // and the rest, which keeps 16 significant bits of it (2^-17, far below the
 // output's rounding): the instruction's 32 values of K hold 16 ranks' upper
-// halves and rests, against B's ranks twice.  The instruction's rows are
-// columns of the output, mapped so that a lane ends with two runs of 8
-// consecutive columns of one row, the four lanes of a row side by side: base
-// and out move 16 bytes a lane, 64 together.
-template <bool DIRECT, int NS>
+// halves and rests, against B's ranks twice.  B's 128 rows are contiguous in
+// memory and pass through LDS for the reason above, with an odd number of
+// 16-byte chunks between rows so that 16 rows' chunks spread over the banks.
+constexpr int kSmallCols = 128;
+
 __global__ __launch_bounds__(kLoraThreads) void lora_expand_kernel(LoraArgs p) {
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int blocks_n = (int)((p.N + 255) / 256);
+  extern __shared__ __align__(16) uint8_t lds[];   // h's fragments, then B's rows [2][64]
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int runs = (int)((p.N + kSmallCols - 1) / kSmallCols);
   Tile t;
-  if (!find_tile<DIRECT>(p, blockIdx.x / blocks_n, &t)) return;
-  const int64_t n0 = (int64_t)(blockIdx.x % blocks_n) * 256 + wave * 64;
-  if (n0 >= p.N) return;
-  v4f acc[4];
+  if (!find_tile_direct(p, blockIdx.x / runs, &t)) return;
+  const int64_t n0 = (int64_t)(blockIdx.x % runs) * kSmallCols;
+  const int i16 = lane & 15, g16 = lane >> 4;
+  const int chunks = p.r / 8, steps = (p.r + 15) / 16;
+  const int pitch = (chunks | 1) * 16;
+  uint8_t *lb = lds + steps * 1024;
+  const bool worn = t.g < p.L;
+  // base of rows g16 * 4 + q, columns c0 and c0 + 1
+  const int64_t c0 = n0 + wave * 32 + i16 * 2;
+  int row[4];
+  uint32_t bs[4];
 #pragma unroll
-  for (int f = 0; f < 4; ++f) acc[f] = v4f{0, 0, 0, 0};
-  if (t.g < p.L) {
+  for (int q = 0; q < 4; ++q) {
+    row[q] = __shfl(t.row, g16 * 4 + q);
+    bs[q] = 0;
+    if (p.base && row[q] >= 0) {
+      const uint16_t *b = p.base + (int64_t)row[q] * p.ldb + c0;
+      if (c0 < p.N) bs[q] = b[0];
+      if (c0 + 1 < p.N) bs[q] |= (uint32_t)b[1] << 16;
+    }
+  }
+  v4f acc[2] = {v4f{0, 0, 0, 0}, v4f{0, 0, 0, 0}};
+  if (worn) {
+    // B's chunks: the first kHeld of a thread are loaded here and written below,
+    // so that their latency and that of h's parts pass together
+    constexpr int kHeld = 4;
+    const uint16_t *bg = p.b + (int64_t)t.g * p.N * p.r;
+    v4u held[kHeld];
+    int at[kHeld];
+    auto fetch = [&](int c, v4u *v, int *dst) {
+      const int n = c / chunks, ch = c - n * chunks;
+      // column n = 2 i + f is row i of half f; columns past N repeat the last one
+      *dst = ((n & 1) * 64 + (n >> 1)) * pitch + ch * 16;
+      *v = *reinterpret_cast<const v4u *>(bg + min(n0 + n, p.N - 1) * p.r + ch * 8);
+    };
+    const int total = kSmallCols * chunks;
+#pragma unroll
+    for (int j = 0; j < kHeld; ++j) fetch(min(tid + j * kLoraThreads, total - 1), &held[j], &at[j]);
     const float scale = p.scale ? p.scale[t.g] : 1.0f;
-    const bool rest = (lane >> 4) & 1;
-    const int m = lane & 15;
-    const uint16_t *br[4];
-#pragma unroll
-    for (int f = 0; f < 4; ++f) {
-      const int64_t n = n0 + (f >> 1) * 32 + (m >> 2) * 8 + (f & 1) * 4 + (m & 3);
-      br[f] = p.b + ((int64_t)t.g * p.N + (n < p.N ? n : p.N - 1)) * p.r;
+    for (int c = tid; c < 32 * steps; c += kLoraThreads) {
+      const int slot = c & 15, ch = c >> 4;
+      const int r = __shfl(t.row, slot);            // (lane & 15 == slot)
+      v4u hi = v4u{0, 0, 0, 0}, lo = hi;
+      if (r >= 0 && ch < chunks)
+        join_parts(p, p.h + (int64_t)r * p.r + ch * 8, scale, &hi, &lo);
+      v4u *f = reinterpret_cast<v4u *>(lds + (ch >> 1) * 1024) + (ch & 1) * 32 + slot;
+      f[0] = hi;
+      f[16] = lo;
     }
 #pragma unroll
-    for (int st = 0; st < NS; ++st) {
-      if (st * 16 >= p.r) break;
-      const int rank = st * 16 + (lane >> 5) * 8;
-      const bool in = rank < p.r;
-      float h[8];
+    for (int j = 0; j < kHeld; ++j) *reinterpret_cast<v4u *>(&lb[at[j]]) = held[j];
+    for (int c = tid + kHeld * kLoraThreads; c < total; c += kHeld * kLoraThreads) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) h[i] = 0.0f;
-      if (in && t.row >= 0) {
-        const float *hp = p.h + (int64_t)t.row * p.r + rank;
-        for (int s = 0; s < p.S; ++s) {
-          const float4 u = *reinterpret_cast<const float4 *>(hp + (int64_t)s * p.T * p.r);
-          const float4 v = *reinterpret_cast<const float4 *>(hp + (int64_t)s * p.T * p.r + 4);
-          h[0] += u.x; h[1] += u.y; h[2] += u.z; h[3] += u.w;
-          h[4] += v.x; h[5] += v.y; h[6] += v.z; h[7] += v.w;
-        }
-      }
-      uint32_t w[4];
+      for (int j = 0; j < kHeld; ++j)
+        fetch(min(c + j * kLoraThreads, total - 1), &held[j], &at[j]);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        uint32_t q[2];
+      for (int j = 0; j < kHeld; ++j) *reinterpret_cast<v4u *>(&lb[at[j]]) = held[j];
+    }
+    lds_barrier();
+#pragma unroll 2
+    for (int st = 0; st < steps; ++st) {
+      // past the rank h is zero, and B's last chunk stands in
+      const int chunk = min(st * 2 + (g16 >> 1), chunks - 1);
+      const v8bf hv = *reinterpret_cast<const v8bf *>(lds + st * 1024 + lane * 16);
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const float v = h[2 * i + j] * scale;
-          const float hi = __uint_as_float(__float_as_uint(v) & 0xffff0000u);
-          // an infinite or NaN value has no rest
-          const float lo = __builtin_isfinite(v) ? v - hi : 0.0f;
-          q[j] = rest ? bf_bits(lo) : __float_as_uint(hi) >> 16;
-        }
-        w[i] = q[0] | (q[1] << 16);
-      }
-      const v8bf hv = as_bf(make_uint4(w[0], w[1], w[2], w[3]));
-#pragma unroll
-      for (int f = 0; f < 4; ++f) {
-        const uint4 bv = in ? *reinterpret_cast<const uint4 *>(br[f] + rank) : make_uint4(0, 0, 0, 0);
-        acc[f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf(bv), hv, acc[f], 0, 0, 0);
+      for (int f = 0; f < 2; ++f) {
+        const v8bf bv = *reinterpret_cast<const v8bf *>(
+            &lb[(f * 64 + wave * 16 + i16) * pitch + chunk * 16]);
+        acc[f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(hv, bv, acc[f], 0, 0, 0);
       }
     }
   }
-  if (t.row < 0) return;
-  uint16_t *o = p.out + (int64_t)t.row * p.ldo;
-  const uint16_t *bs = p.base ? p.base + (int64_t)t.row * p.ldb : nullptr;
 #pragma unroll
-  for (int q = 0; q < 2; ++q) {
-    const int64_t c = n0 + q * 32 + (lane >> 4) * 8;
-    if (c + 8 <= p.N) {
-      float f[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-      if (bs) unpack8(load16(bs + c), f);
-      U128 w;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const v4f v = acc[q * 2 + i / 2];
-        w.v[i] = (uint32_t)bf_bits(f[2 * i] + v[(2 * i) & 3]) |
-                 ((uint32_t)bf_bits(f[2 * i + 1] + v[(2 * i + 1) & 3]) << 16);
-      }
-      *reinterpret_cast<U128 *>(o + c) = w;
-    } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (c + i < p.N) {
-          const float f = bs ? bf16_lo(bs[c + i]) : 0.0f;
-          o[c + i] = bf_bits(f + acc[q * 2 + i / 4][i & 3]);
-        }
-    }
+  for (int q = 0; q < 4; ++q) {
+    if (row[q] < 0) continue;
+    uint16_t *o = p.out + (int64_t)row[q] * p.ldo + c0;
+    if (c0 < p.N) o[0] = bf_bits(bf16_lo(bs[q]) + acc[0][q]);
+    if (c0 + 1 < p.N) o[1] = bf_bits(bf16_hi(bs[q]) + acc[1][q]);
   }
 }
 
@@ -320,26 +378,6 @@ __global__ __launch_bounds__(kLoraThreads) void lora_expand_kernel(LoraArgs p) {
 // the only HBM traffic of weight.  h is kept as the second product takes it:
 // per row and 8 ranks, the 8 upper halves and then the 8 rests in bf16.
 
-
-// v as upper half and rest (an infinite or NaN value has no rest).
-__device__ __forceinline__ void split_bf16(float v, uint16_t *hi, uint16_t *lo) {
-  const uint32_t u = __float_as_uint(v) & 0xffff0000u;
-  *hi = (uint16_t)(u >> 16);
-  *lo = bf_bits(__builtin_isfinite(v) ? v - __uint_as_float(u) : 0.0f);
-}
-
-// Chunk swizzle of 128-byte LDS rows: 16-byte chunk c of row r is kept at
-// c ^ f(r), so that 16 lanes reading one chunk of 16 consecutive rows meet no
-// bank twice.
-__device__ __forceinline__ int swz_f(int row) { return ((row & 3) << 1) | ((row >> 2) & 1); }
-
-// Barrier for data passed through LDS alone: unlike __syncthreads() it leaves
-// global loads and stores in flight (waiting for them cost 5 us a stage).
-__device__ __forceinline__ void lds_barrier() {
-  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
-  __builtin_amdgcn_s_barrier();
-  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
-}
 
 // A lane of a matrix instruction holds 16 bytes of one row, and neighbouring
 // lanes hold different rows: loaded that way every lane's 16 bytes are a
@@ -460,24 +498,8 @@ __global__ __launch_bounds__(kLoraThreads) void lora_join_kernel(LoraArgs p) {
   const int64_t row = i / chunks;
   const int g = p.ids[row];
   if ((unsigned)g >= (unsigned)p.L) return;
-  const float *hp = p.h + row * p.r + (i - row * chunks) * 8;
-  float h[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-  for (int s = 0; s < p.S; ++s) {
-    const float4 u = *reinterpret_cast<const float4 *>(hp + (int64_t)s * p.T * p.r);
-    const float4 v = *reinterpret_cast<const float4 *>(hp + (int64_t)s * p.T * p.r + 4);
-    h[0] += u.x; h[1] += u.y; h[2] += u.z; h[3] += u.w;
-    h[4] += v.x; h[5] += v.y; h[6] += v.z; h[7] += v.w;
-  }
-  const float scale = p.scale ? p.scale[g] : 1.0f;
-  uint16_t q[16];
-#pragma unroll
-  for (int j = 0; j < 8; ++j) split_bf16(h[j] * scale, &q[j], &q[8 + j]);
-  uint32_t w[8];
-#pragma unroll
-  for (int j = 0; j < 8; ++j) w[j] = q[2 * j] | ((uint32_t)q[2 * j + 1] << 16);
-  uint4 *o = reinterpret_cast<uint4 *>(p.hs + i * 16);
-  o[0] = make_uint4(w[0], w[1], w[2], w[3]);
-  o[1] = make_uint4(w[4], w[5], w[6], w[7]);
+  v4u *o = reinterpret_cast<v4u *>(p.hs + i * 16);
+  join_parts(p, p.h + row * p.r + (i - row * chunks) * 8, p.scale ? p.scale[g] : 1.0f, &o[0], &o[1]);
 }
 
 // out for a tile's 64 rows and CT runs of 128 columns, 16 rows a wave.  Rows
@@ -591,20 +613,19 @@ __global__ __launch_bounds__(kLoraThreads) void lora_expand_wide_kernel(LoraArgs
 }
 
 namespace {
-bool is_wide(int64_t T) { return T >= kWideBatch; }
-
 // Tiles a batch can have at most: full ones, and one more per adapter (and
 // for the rows without one).
 int64_t max_tiles(int64_t T, int L) {
   if (T <= kDirectRows) return T;
   const int64_t groups = (int64_t)L + 1 < T ? (int64_t)L + 1 : T;
-  return T / (is_wide(T) ? kWideRows : kTileRows) + groups;
+  return T / kWideRows + groups;
 }
 
-// K ranges: enough workgroups to fill the chip, at least 256 of K each.
-int split_of(int64_t T, int64_t K, int L) {
-  const int64_t tiles = max_tiles(T, L);
-  int64_t s = 512 / tiles;
+// K ranges: enough workgroups to fill the chip twice, at least 256 of K each.
+int split_of(int64_t T, int64_t K, int32_t r, int L) {
+  int64_t units = max_tiles(T, L);
+  if (T <= kDirectRows) units = (units < L ? units : L) * ((r + 15) / 16);
+  int64_t s = 512 / units;
   if (s > K / 256) s = K / 256;
   if (s > kMaxSplit) s = kMaxSplit;
   return s < 1 ? 1 : (int)s;
@@ -615,8 +636,8 @@ size_t align256(size_t n) { return (n + 255) / 256 * 256; }
 }  // namespace
 
 size_t lora_workspace_bytes(int64_t T, int64_t K, int32_t r, int32_t L, bool listed) {
-  size_t n = align256(sizeof(float) * (size_t)split_of(T, K, L) * T * r);
-  if (is_wide(T)) n += align256(sizeof(float) * (size_t)T * r);
+  size_t n = align256(sizeof(float) * (size_t)split_of(T, K, r, L) * T * r);
+  if (T > kDirectRows) n += align256(sizeof(float) * (size_t)T * r);
   if (T > kDirectRows && !listed)
     n += align256(sizeof(int32_t) * (size_t)T) * 2 + align256(sizeof(int32_t) * ((size_t)L + 1)) +
          group_workspace_bytes(T, L);
@@ -646,18 +667,24 @@ hipError_t launch_lora_add(const void *base, int64_t ldb, const void *x, int64_t
   p.N = N;
   p.L = L;
   p.r = r;
-  p.S = split_of(T, K, L);
+  p.S = split_of(T, K, r, L);
   p.copy_bare = base != out;
   char *w = static_cast<char *>(work);
   p.h = reinterpret_cast<float *>(w);
   w += align256(sizeof(float) * (size_t)p.S * T * r);
-  const bool direct = T <= kDirectRows;
-  const bool wide = is_wide(T);
-  if (wide) {
-    p.hs = reinterpret_cast<uint16_t *>(w);
-    w += align256(sizeof(float) * (size_t)T * r);
+  const int64_t tiles = max_tiles(T, L);
+  if (T <= kDirectRows) {
+    const int steps = (r + 15) / 16;
+    lora_shrink_kernel<<<(unsigned)(tiles * steps * p.S), kLoraThreads, 0, stream>>>(p);
+    if (hipError_t e = hipGetLastError()) return e;
+    const size_t lds = (size_t)steps * 1024 + (size_t)kSmallCols * ((r / 8) | 1) * 16;
+    lora_expand_kernel<<<(unsigned)(tiles * ((N + kSmallCols - 1) / kSmallCols)), kLoraThreads,
+                         lds, stream>>>(p);
+    return hipGetLastError();
   }
-  if (!direct && !order) {
+  p.hs = reinterpret_cast<uint16_t *>(w);
+  w += align256(sizeof(float) * (size_t)T * r);
+  if (!order) {
     int32_t *ord = reinterpret_cast<int32_t *>(w);
     w += align256(sizeof(int32_t) * (size_t)T);
     int32_t *pos = reinterpret_cast<int32_t *>(w);
@@ -668,52 +695,29 @@ hipError_t launch_lora_add(const void *base, int64_t ldb, const void *x, int64_t
     p.order = ord;
     p.offsets = off;
   }
-  const int64_t tiles = max_tiles(T, L);
   const unsigned gs = (unsigned)(tiles * p.S);
-  const unsigned ge = (unsigned)(tiles * ((N + 255) / 256));
-  if (wide) {
-    if (r <= 16) lora_shrink_wide_kernel<4, 1, 1, 1><<<gs, kLoraThreads, 0, stream>>>(p);
-    else if (r <= 32) lora_shrink_wide_kernel<4, 1, 1, 2><<<gs, kLoraThreads, 0, stream>>>(p);
-    else if (r <= 64) lora_shrink_wide_kernel<2, 2, 2, 2><<<gs, kLoraThreads, 0, stream>>>(p);
-    else if (r <= 128) lora_shrink_wide_kernel<2, 2, 2, 4><<<gs, kLoraThreads, 0, stream>>>(p);
-    else lora_shrink_wide_kernel<2, 2, 2, 8><<<gs, kLoraThreads, 0, stream>>>(p);
-    if (hipError_t e = hipGetLastError()) return e;
-    const int64_t pieces = T * (r / 8);
-    lora_join_kernel<<<(unsigned)((pieces + kLoraThreads - 1) / kLoraThreads), kLoraThreads, 0,
-                       stream>>>(p);
-    if (hipError_t e = hipGetLastError()) return e;
-    // several runs of columns a workgroup where that leaves enough of them
-    const int64_t runs = (N + kExpandCols - 1) / kExpandCols;
-    int64_t ct = tiles * runs / 1024;
-    ct = ct < 1 ? 1 : ct > 4 ? 4 : ct;
-    const unsigned gw = (unsigned)(tiles * ((runs + ct - 1) / ct));
-    const size_t lds = (size_t)kExpandCols * ((r / 8) | 1) * 16;
-    if (r <= 16) lora_expand_wide_kernel<1><<<gw, kLoraThreads, lds, stream>>>(p, (int)ct);
-    else if (r <= 32) lora_expand_wide_kernel<2><<<gw, kLoraThreads, lds, stream>>>(p, (int)ct);
-    else if (r <= 64) lora_expand_wide_kernel<4><<<gw, kLoraThreads, lds, stream>>>(p, (int)ct);
-    else if (r <= 128) lora_expand_wide_kernel<8><<<gw, kLoraThreads, lds, stream>>>(p, (int)ct);
-    else lora_expand_wide_kernel<16><<<gw, kLoraThreads, lds, stream>>>(p, (int)ct);
-    return hipGetLastError();
-  }
-#define FP8BLK_LORA(D, NT)                                                  \
-  do {                                                                      \
-    lora_shrink_kernel<D, NT><<<gs, kLoraThreads, 0, stream>>>(p);          \
-    if (hipError_t e = hipGetLastError()) return e;                         \
-    lora_expand_kernel<D, NT><<<ge, kLoraThreads, 0, stream>>>(p);          \
-    return hipGetLastError();                                               \
-  } while (0)
-#define FP8BLK_LORA_RANK(D)                                                 \
-  do {                                                                      \
-    if (r <= 16) FP8BLK_LORA(D, 1);                                         \
-    if (r <= 32) FP8BLK_LORA(D, 2);                                         \
-    if (r <= 64) FP8BLK_LORA(D, 4);                                         \
-    if (r <= 128) FP8BLK_LORA(D, 8);                                        \
-    FP8BLK_LORA(D, 16);                                                     \
-  } while (0)
-  if (direct) FP8BLK_LORA_RANK(true);
-  FP8BLK_LORA_RANK(false);
-#undef FP8BLK_LORA_RANK
-#undef FP8BLK_LORA
+  if (r <= 16) lora_shrink_wide_kernel<4, 1, 1, 1><<<gs, kLoraThreads, 0, stream>>>(p);
+  else if (r <= 32) lora_shrink_wide_kernel<4, 1, 1, 2><<<gs, kLoraThreads, 0, stream>>>(p);
+  else if (r <= 64) lora_shrink_wide_kernel<2, 2, 2, 2><<<gs, kLoraThreads, 0, stream>>>(p);
+  else if (r <= 128) lora_shrink_wide_kernel<2, 2, 2, 4><<<gs, kLoraThreads, 0, stream>>>(p);
+  else lora_shrink_wide_kernel<2, 2, 2, 8><<<gs, kLoraThreads, 0, stream>>>(p);
+  if (hipError_t e = hipGetLastError()) return e;
+  const int64_t pieces = T * (r / 8);
+  lora_join_kernel<<<(unsigned)((pieces + kLoraThreads - 1) / kLoraThreads), kLoraThreads, 0,
+                     stream>>>(p);
+  if (hipError_t e = hipGetLastError()) return e;
+  // several runs of columns a workgroup where that leaves enough of them
+  const int64_t runs = (N + kExpandCols - 1) / kExpandCols;
+  int64_t ct = tiles * runs / 1024;
+  ct = ct < 1 ? 1 : ct > 4 ? 4 : ct;
+  const unsigned gw = (unsigned)(tiles * ((runs + ct - 1) / ct));
+  const size_t lds = (size_t)kExpandCols * ((r / 8) | 1) * 16;
+  if (r <= 16) lora_expand_wide_kernel<1><<<gw, kLoraThreads, lds, stream>>>(p, (int)ct);
+  else if (r <= 32) lora_expand_wide_kernel<2><<<gw, kLoraThreads, lds, stream>>>(p, (int)ct);
+  else if (r <= 64) lora_expand_wide_kernel<4><<<gw, kLoraThreads, lds, stream>>>(p, (int)ct);
+  else if (r <= 128) lora_expand_wide_kernel<8><<<gw, kLoraThreads, lds, stream>>>(p, (int)ct);
+  else lora_expand_wide_kernel<16><<<gw, kLoraThreads, lds, stream>>>(p, (int)ct);
+  return hipGetLastError();
 }
 
 }  // namespace fp8blk
