@@ -650,6 +650,7 @@ class RowGroups(NamedTuple):
 _LOGITS = {torch.float32: 0, torch.bfloat16: 1}    # FP8BLK_F32, FP8BLK_BF16
 _I32 = (torch.int32,)
 _BF16 = (torch.bfloat16,)
+_MASK = (torch.bool, torch.uint8)
 
 
 def _rows_2d(t, name):
@@ -660,6 +661,8 @@ def _rows_2d(t, name):
         raise ValueError(f"{name} must be a device (cuda/hip) tensor")
     if t.dim() != 2:
         raise ValueError(f"{name} must have 2 dimensions, got {t.dim()}")
+    if t.is_contiguous():
+        return t.shape[1]
     rows, cols = t.shape
     if rows <= 1 or cols == 0:
         if cols > 1 and t.stride(1) != 1:
@@ -684,12 +687,30 @@ def _at(t):
     return t.data_ptr() if t is not None else None
 
 
-def _work(need, device):
-    return torch.empty(need, dtype=torch.uint8, device=device) if need else None
+def _work(need, like):
+    return like.new_empty((need,), dtype=torch.uint8) if need else None
 
 
 def _bytes(t):
     return t.numel() * t.element_size() if t is not None else 0
+
+
+# Each operator's call of the library, its arguments checked: the low-level entry
+# points check every buffer, the wrappers what the caller gave them.
+
+def _route_in(logits, mask):
+    _need(logits, "logits", tuple(_LOGITS), 2)
+    if mask is not None:
+        _need(mask, "mask", _MASK, 1)
+        _shape_eq(mask, (logits.shape[0],), "mask")
+
+
+def _route_call(logits, mask, k, renormalize, coef, ids, weights, counts, rows, loss, workspace):
+    T, E = logits.shape
+    _check(load_library().fp8blk_moe_route(
+        logits.data_ptr(), _LOGITS[logits.dtype], _at(mask), T, E, k, renormalize, coef,
+        ids.data_ptr(), weights.data_ptr(), counts.data_ptr(), _at(rows), _at(loss),
+        _at(workspace), _bytes(workspace), _stream()), "fp8blk_moe_route")
 
 
 def fp8blk_moe_route(logits, mask, renormalize, loss_coef, ids, weights, counts, rows, loss,
@@ -697,7 +718,7 @@ def fp8blk_moe_route(logits, mask, renormalize, loss_coef, ids, weights, counts,
     """Routing into preallocated outputs; k is ids' width, ``mask`` (uint8 or
     bool [T]), ``rows`` (int32) and ``loss`` (fp32, one value each) may be None,
     ``workspace`` holds fp8blk_moe_route_workspace_bytes(T, E) bytes."""
-    _need(logits, "logits", tuple(_LOGITS), 2)
+    _route_in(logits, mask)
     T, E = logits.shape
     _need(ids, "ids", _I32, 2); _need(weights, "weights", _F32, 2)
     _need(counts, "counts", _I32, 1)
@@ -709,25 +730,20 @@ def fp8blk_moe_route(logits, mask, renormalize, loss_coef, ids, weights, counts,
             _need(t, name, dtype)
             if t.numel() != 1:
                 raise ValueError(f"{name} holds one value")
-    if mask is not None:
-        _need(mask, "mask", (torch.bool, torch.uint8), 1)
-        _shape_eq(mask, (T,), "mask")
     _same_device(logits, mask, ids, weights, counts, rows, loss, workspace)
-    _check(load_library().fp8blk_moe_route(
-        logits.data_ptr(), _LOGITS[logits.dtype], _at(mask), T, E, k, int(renormalize), loss_coef,
-        ids.data_ptr(), weights.data_ptr(), counts.data_ptr(), _at(rows), _at(loss),
-        _at(workspace), _bytes(workspace), _stream()), "fp8blk_moe_route")
+    _route_call(logits, mask, k, bool(renormalize), loss_coef, ids, weights, counts, rows, loss,
+                workspace)
 
 
-def fp8blk_moe_route_backward(logits, routing, d_weights, d_loss, d_logits):
-    """Gradient of the logits into d_logits; d_weights [T,k] or d_loss (one
-    value) may be None."""
-    _need(logits, "logits", tuple(_LOGITS), 2); _need(d_logits, "d_logits", (logits.dtype,), 2)
+def _route_back_in(logits, routing, d_weights, d_loss):
+    _need(logits, "logits", tuple(_LOGITS), 2)
     T, E = logits.shape
-    k = routing.ids.shape[1]
-    _shape_eq(routing.ids, (T, k), "routing.ids")
-    _shape_eq(routing.counts, (E,), "routing.counts")
-    _shape_eq(d_logits, (T, E), "d_logits")
+    ids, weights, counts = routing.ids, routing.weights, routing.counts
+    _need(ids, "routing.ids", _I32, 2); _need(weights, "routing.weights", _F32, 2)
+    _need(counts, "routing.counts", _I32, 1)
+    k = ids.shape[1]
+    _shape_eq(ids, (T, k), "routing.ids"); _shape_eq(weights, (T, k), "routing.weights")
+    _shape_eq(counts, (E,), "routing.counts")
     if d_weights is not None:
         _need(d_weights, "d_weights", _F32, 2)
         _shape_eq(d_weights, (T, k), "d_weights")
@@ -737,12 +753,33 @@ def fp8blk_moe_route_backward(logits, routing, d_weights, d_loss, d_logits):
             raise ValueError("d_loss holds one value")
         if routing.rows is None:
             raise ValueError("d_loss needs a routing that computed the loss")
-    _same_device(logits, routing.ids, d_weights, d_loss, d_logits)
+        _need(routing.rows, "routing.rows", _I32)
+
+
+def _route_back_call(logits, routing, d_weights, d_loss, d_logits):
+    T, E = logits.shape
     _check(load_library().fp8blk_moe_route_backward(
-        logits.data_ptr(), _LOGITS[logits.dtype], T, E, k, int(routing.renormalize),
+        logits.data_ptr(), _LOGITS[logits.dtype], T, E, routing.ids.shape[1], routing.renormalize,
         routing.loss_coef, routing.ids.data_ptr(), routing.weights.data_ptr(),
         routing.counts.data_ptr(), _at(routing.rows), _at(d_weights), _at(d_loss),
         d_logits.data_ptr(), _stream()), "fp8blk_moe_route_backward")
+
+
+def fp8blk_moe_route_backward(logits, routing, d_weights, d_loss, d_logits):
+    """Gradient of the logits into d_logits; d_weights [T,k] or d_loss (one
+    value) may be None."""
+    _route_back_in(logits, routing, d_weights, d_loss)
+    _need(d_logits, "d_logits", (logits.dtype,), 2)
+    _shape_eq(d_logits, logits.shape, "d_logits")
+    _same_device(logits, routing.ids, routing.weights, routing.counts, routing.rows, d_weights,
+                 d_loss, d_logits)
+    _route_back_call(logits, routing, d_weights, d_loss, d_logits)
+
+
+def _group_call(ids, groups, order, positions, offsets, workspace):
+    _check(load_library().fp8blk_group_rows(
+        ids.data_ptr(), ids.numel(), groups, order.data_ptr(), positions.data_ptr(),
+        offsets.data_ptr(), _at(workspace), _bytes(workspace), _stream()), "fp8blk_group_rows")
 
 
 def fp8blk_group_rows(ids, order, positions, offsets, workspace=None):
@@ -754,45 +791,60 @@ def fp8blk_group_rows(ids, order, positions, offsets, workspace=None):
     if order.numel() != R or positions.numel() != R:
         raise ValueError("order and positions have an entry per row")
     _same_device(ids, order, positions, offsets, workspace)
-    _check(load_library().fp8blk_group_rows(
-        ids.data_ptr(), R, offsets.numel() - 1, order.data_ptr(), positions.data_ptr(),
-        offsets.data_ptr(), _at(workspace), _bytes(workspace), _stream()), "fp8blk_group_rows")
+    _group_call(ids, offsets.numel() - 1, order, positions, offsets, workspace)
 
 
-def fp8blk_moe_combine(y, weights, positions, base, out):
-    """Weighted sums of y's rows into out; base may be None or out itself."""
+def _combine_in(y, weights, positions, base):
     _need(y, "y", _BF16, 2); _need(weights, "weights", _F32, 2)
-    _need(positions, "positions", _I32, 2); _need(out, "out", _BF16, 2)
-    T, k = weights.shape
-    R, N = y.shape
-    _shape_eq(positions, (T, k), "positions"); _shape_eq(out, (T, N), "out")
+    _need(positions, "positions", _I32, 2)
+    _shape_eq(positions, weights.shape, "positions")
     if base is not None:
         _need(base, "base", _BF16, 2)
-        _shape_eq(base, (T, N), "base")
-    _same_device(y, weights, positions, base, out)
+        _shape_eq(base, (weights.shape[0], y.shape[1]), "base")
+
+
+def _combine_call(y, weights, positions, base, out):
+    T, k = weights.shape
+    R, N = y.shape
     _check(load_library().fp8blk_moe_combine(
         y.data_ptr(), R, weights.data_ptr(), positions.data_ptr(), _at(base), T, k, N,
         out.data_ptr(), _stream()), "fp8blk_moe_combine")
 
 
-def fp8blk_moe_combine_backward(d_out, y, weights, positions, rows_used, d_y, d_weights):
-    """Gradients into d_y and d_weights; the last entry of ``rows_used`` (an
-    int32 tensor, e.g. RowGroups.offsets) is the number of y's rows in use."""
-    _need(d_out, "d_out", _BF16, 2); _need(y, "y", _BF16, 2)
-    _need(weights, "weights", _F32, 2); _need(positions, "positions", _I32, 2)
-    _need(rows_used, "rows_used", _I32)
-    _need(d_y, "d_y", _BF16, 2); _need(d_weights, "d_weights", _F32, 2)
-    T, k = weights.shape
-    R, N = y.shape
-    _shape_eq(d_out, (T, N), "d_out"); _shape_eq(positions, (T, k), "positions")
-    _shape_eq(d_y, (R, N), "d_y"); _shape_eq(d_weights, (T, k), "d_weights")
+def fp8blk_moe_combine(y, weights, positions, base, out):
+    """Weighted sums of y's rows into out; base may be None or out itself."""
+    _combine_in(y, weights, positions, base)
+    _need(out, "out", _BF16, 2)
+    _shape_eq(out, (weights.shape[0], y.shape[1]), "out")
+    _same_device(y, weights, positions, base, out)
+    _combine_call(y, weights, positions, base, out)
+
+
+def _combine_back_in(d_out, y, weights, positions, rows_used):
+    _combine_in(y, weights, positions, None)
+    _need(d_out, "d_out", _BF16, 2); _need(rows_used, "rows_used", _I32)
+    _shape_eq(d_out, (weights.shape[0], y.shape[1]), "d_out")
     if rows_used.numel() < 1:
         raise ValueError("rows_used holds one value at least")
-    _same_device(d_out, y, weights, positions, rows_used, d_y, d_weights)
+
+
+def _combine_back_call(d_out, y, weights, positions, rows_used, d_y, d_weights):
+    T, k = weights.shape
+    R, N = y.shape
     _check(load_library().fp8blk_moe_combine_backward(
         d_out.data_ptr(), y.data_ptr(), R, weights.data_ptr(), positions.data_ptr(),
         rows_used.data_ptr() + 4 * (rows_used.numel() - 1), T, k, N, d_y.data_ptr(),
         d_weights.data_ptr(), _stream()), "fp8blk_moe_combine_backward")
+
+
+def fp8blk_moe_combine_backward(d_out, y, weights, positions, rows_used, d_y, d_weights):
+    """Gradients into d_y and d_weights; the last entry of ``rows_used`` (an
+    int32 tensor, e.g. RowGroups.offsets) is the number of y's rows in use."""
+    _combine_back_in(d_out, y, weights, positions, rows_used)
+    _need(d_y, "d_y", _BF16, 2); _need(d_weights, "d_weights", _F32, 2)
+    _shape_eq(d_y, y.shape, "d_y"); _shape_eq(d_weights, weights.shape, "d_weights")
+    _same_device(d_out, y, weights, positions, rows_used, d_y, d_weights)
+    _combine_back_call(d_out, y, weights, positions, rows_used, d_y, d_weights)
 
 
 def fp8blk_lora_add(base, x, a, b, ids, scale, groups, out, workspace):
@@ -809,7 +861,9 @@ def fp8blk_lora_add(base, x, a, b, ids, scale, groups, out, workspace):
     _shape_eq(b, (L, N, r), "b"); _shape_eq(ids, (T,), "ids")
     _shape_eq(out, (T, N), "out")
     ldb = 0
-    if base is not None:
+    if base is out:
+        ldb = ldo
+    elif base is not None:
         ldb = _rows_2d(base, "base")
         _shape_eq(base, (T, N), "base")
     if scale is not None:
@@ -820,7 +874,7 @@ def fp8blk_lora_add(base, x, a, b, ids, scale, groups, out, workspace):
         order, offsets = groups.order, groups.offsets
         _need(order, "groups.order", _I32, 1); _need(offsets, "groups.offsets", _I32, 1)
         _shape_eq(order, (T,), "groups.order"); _shape_eq(offsets, (L + 1,), "groups.offsets")
-    _same_device(x, base, a, b, ids, scale, order, out, workspace)
+    _same_device(x, base, a, b, ids, scale, order, offsets, out, workspace)
     _check(load_library().fp8blk_lora_add(
         _at(base), ldb, x.data_ptr(), ldx, a.data_ptr(), b.data_ptr(), ids.data_ptr(),
         _at(scale), _at(order), _at(offsets), T, K, N, r, L, out.data_ptr(), ldo,
@@ -833,7 +887,8 @@ def moe_route(logits, k, mask=None, renormalize=True, loss_coef=None):
     loss_coef * sum_e (counts_e E / (k n)) * mean_t p_te.  Rows with mask 0,
     and experts with logit -inf, are left out; unused slots have id -1 and
     weight 0."""
-    _need(logits, "logits", tuple(_LOGITS), 2)
+    _route_in(logits, mask)
+    _same_device(logits, mask)
     T, E = logits.shape
     if not 1 <= k <= E:
         raise ValueError(f"k must be between 1 and the number of experts, got {k}")
@@ -844,17 +899,19 @@ def moe_route(logits, k, mask=None, renormalize=True, loss_coef=None):
     if loss_coef is not None:
         rows = logits.new_empty((1,), dtype=torch.int32)
         loss = logits.new_empty((), dtype=torch.float32)
-    coef = float(loss_coef or 0.0)
-    fp8blk_moe_route(logits, mask, renormalize, coef, ids, weights, counts, rows, loss,
-                     _work(load_library().fp8blk_moe_route_workspace_bytes(T, E), logits.device))
-    return Routing(ids, weights, counts, rows, loss, coef, bool(renormalize))
+    coef, renormalize = float(loss_coef or 0.0), bool(renormalize)
+    _route_call(logits, mask, k, renormalize, coef, ids, weights, counts, rows, loss,
+                _work(load_library().fp8blk_moe_route_workspace_bytes(T, E), logits))
+    return Routing(ids, weights, counts, rows, loss, coef, renormalize)
 
 
 def moe_route_backward(logits, routing, d_weights=None, d_loss=None):
     """Gradient of the logits (in their type) from those of the weights and of
     the loss; the choice itself has none."""
+    _route_back_in(logits, routing, d_weights, d_loss)
+    _same_device(logits, routing.ids, routing.weights, routing.counts, routing.rows, d_weights, d_loss)
     d_logits = torch.empty_like(logits)
-    fp8blk_moe_route_backward(logits, routing, d_weights, d_loss, d_logits)
+    _route_back_call(logits, routing, d_weights, d_loss, d_logits)
     return d_logits
 
 
@@ -862,27 +919,32 @@ def group_rows(ids, groups):
     """Rows (entries of ids, any shape) listed by group, in their own order
     within a group; entries outside [0, groups) belong to none and come last."""
     _need(ids, "ids", _I32)
+    _same_device(ids)
     R = ids.numel()
     order, positions = ids.new_empty((R,)), torch.empty_like(ids)
     offsets = ids.new_empty((groups + 1,))
-    fp8blk_group_rows(ids, order, positions, offsets,
-                      _work(load_library().fp8blk_group_rows_workspace_bytes(R, groups), ids.device))
+    _group_call(ids, groups, order, positions, offsets,
+                _work(load_library().fp8blk_group_rows_workspace_bytes(R, groups), ids))
     return RowGroups(order, positions, offsets)
 
 
 def moe_combine(y, weights, positions, base=None):
     """out[t] = base[t] + sum_j weights[t,j] * y[positions[t,j]] in bf16;
     slots with position -1 add nothing."""
+    _combine_in(y, weights, positions, base)
+    _same_device(y, weights, positions, base)
     out = y.new_empty((weights.shape[0], y.shape[1]))
-    fp8blk_moe_combine(y, weights, positions, base, out)
+    _combine_call(y, weights, positions, base, out)
     return out
 
 
 def moe_combine_backward(d_out, y, weights, positions, offsets):
     """(d_y, d_weights) of moe_combine; the last entry of offsets is the number
     of y's rows in use (rows past it get 0)."""
+    _combine_back_in(d_out, y, weights, positions, offsets)
+    _same_device(d_out, y, weights, positions, offsets)
     d_y, d_weights = torch.empty_like(y), torch.empty_like(weights)
-    fp8blk_moe_combine_backward(d_out, y, weights, positions, offsets, d_y, d_weights)
+    _combine_back_call(d_out, y, weights, positions, offsets, d_y, d_weights)
     return d_y, d_weights
 
 
@@ -895,7 +957,7 @@ def lora_add(base, x, a, b, ids, scale=None, groups=None, out=None):
     if out is None:
         out = x.new_empty((T, b.shape[1]))
     need = load_library().fp8blk_lora_add_workspace_bytes(T, K, r, L, groups is not None)
-    fp8blk_lora_add(base, x, a, b, ids, scale, groups, out, _work(need, x.device))
+    fp8blk_lora_add(base, x, a, b, ids, scale, groups, out, _work(need, x))
     return out
 
 

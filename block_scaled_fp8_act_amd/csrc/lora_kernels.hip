@@ -128,20 +128,19 @@ __device__ __forceinline__ bool find_listed(const LoraArgs &p, int index, Listed
   return false;
 }
 
-__device__ __forceinline__ v8bf as_bf(const uint4 &v) { return __builtin_bit_cast(v8bf, v); }
-
-struct __attribute__((packed, aligned(2))) U128 {
-  uint32_t v[4];
-};
-
-__device__ __forceinline__ uint4 load16(const uint16_t *p) {
-  const U128 w = *reinterpret_cast<const U128 *>(p);
-  return make_uint4(w.v[0], w.v[1], w.v[2], w.v[3]);
-}
+// 16 bytes at any even address (gfx950's global loads and stores take those);
+// the _once forms for what is read or written once: non-temporal, so that it
+// does not displace the adapters in L2.
+typedef unsigned v4u_any __attribute__((ext_vector_type(4), aligned(2)));
 
 __device__ __forceinline__ v4u load16v(const uint16_t *p) {
-  typedef unsigned v4u_any __attribute__((ext_vector_type(4), aligned(2)));
   return *reinterpret_cast<const v4u_any *>(p);
+}
+__device__ __forceinline__ v4u load16_once(const uint16_t *p) {
+  return __builtin_nontemporal_load(reinterpret_cast<const v4u_any *>(p));
+}
+__device__ __forceinline__ void store16_once(uint16_t *p, v4u v) {
+  __builtin_nontemporal_store(v, reinterpret_cast<v4u_any *>(p));
 }
 
 __device__ __forceinline__ uint16_t bf_bits(float f) {
@@ -452,13 +451,13 @@ __global__ __launch_bounds__(kLoraThreads) void lora_shrink_wide_kernel(LoraArgs
 #pragma unroll
       for (int q = 0; q < MR; ++q) {
         const int r = first + q * 16 + (lane & 15);
-        xv[q] = as_bf(*reinterpret_cast<const uint4 *>(&lds[b][r * 128 + ((chunk ^ swz_f(r)) << 4)]));
+        xv[q] = *reinterpret_cast<const v8bf *>(&lds[b][r * 128 + ((chunk ^ swz_f(r)) << 4)]);
       }
 #pragma unroll
       for (int f = 0; f < NR; ++f) {
         const int r = rank0 + f * 16 + (lane & 15);
-        av[f] = as_bf(*reinterpret_cast<const uint4 *>(
-            &lds[b][(kWideRows + r) * 128 + ((chunk ^ swz_f(r)) << 4)]));
+        av[f] = *reinterpret_cast<const v8bf *>(
+            &lds[b][(kWideRows + r) * 128 + ((chunk ^ swz_f(r)) << 4)]);
       }
 #pragma unroll
       for (int q = 0; q < MR; ++q)
@@ -559,12 +558,12 @@ __global__ __launch_bounds__(kLoraThreads) void lora_expand_wide_kernel(LoraArgs
   if (worn) load_b(run0);
   for (int run = run0; run < run1; ++run) {
     const int64_t c0 = (int64_t)run * kExpandCols + i16 * 8;
-    uint4 bs[4];
+    v4u bs[4];
 #pragma unroll
     for (int q = 0; q < 4; ++q)
       bs[q] = p.base && c0 + 8 <= p.N
-                  ? load16(p.base + (int64_t)rows[wave * 16 + g16 * 4 + q] * p.ldb + c0)
-                  : make_uint4(0, 0, 0, 0);
+                  ? load16_once(p.base + (int64_t)rows[wave * 16 + g16 * 4 + q] * p.ldb + c0)
+                  : v4u{0, 0, 0, 0};
     v4f acc[8];
 #pragma unroll
     for (int f = 0; f < 8; ++f) acc[f] = v4f{0, 0, 0, 0};
@@ -593,13 +592,13 @@ __global__ __launch_bounds__(kLoraThreads) void lora_expand_wide_kernel(LoraArgs
       uint16_t *o = p.out + (int64_t)rows[slot] * p.ldo;
       if (c0 + 8 <= p.N) {
         float f[8];
-        unpack8(bs[q], f);
-        U128 w;
+        unpack8(make_uint4(bs[q][0], bs[q][1], bs[q][2], bs[q][3]), f);
+        v4u w;
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-          w.v[j] = (uint32_t)bf_bits(f[2 * j] + acc[2 * j][q]) |
-                   ((uint32_t)bf_bits(f[2 * j + 1] + acc[2 * j + 1][q]) << 16);
-        *reinterpret_cast<U128 *>(o + c0) = w;
+          w[j] = (uint32_t)bf_bits(f[2 * j] + acc[2 * j][q]) |
+                 ((uint32_t)bf_bits(f[2 * j + 1] + acc[2 * j + 1][q]) << 16);
+        store16_once(o + c0, w);
       } else {
 #pragma unroll
         for (int j = 0; j < 8; ++j)
