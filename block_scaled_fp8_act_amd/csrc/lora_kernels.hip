@@ -41,7 +41,9 @@ struct LoraArgs {
   const int32_t *order, *offsets; // [T], [L + 1], T > kDirectRows
   const float *scale;             // [L] or NULL (1)
   float *h;                       // [S][T][r]
-  uint16_t *hs;                   // [T][r / 8][16]: h split, for large batches
+  // larger batches: per tile of 64 rows its adapter, its rows and its h, split
+  int32_t *tile_adapter, *tile_rows;
+  uint16_t *hs;
   uint16_t *out;
   int64_t T, K, N;
   int L, r, S, copy_bare;         // copy_bare: rows without adapter: out = base
@@ -386,17 +388,17 @@ __global__ __launch_bounds__(kLoraThreads) void lora_expand_kernel(LoraArgs p) {
 // stages ahead in registers.  WR x WN waves take MR row fragments and NR rank
 // fragments each.  h goes out in fp32 parts, one per K range.
 template <int WR, int WN, int MR, int NR>
-__global__ __launch_bounds__(kLoraThreads) void lora_shrink_wide_kernel(LoraArgs p) {
-  static_assert(WR * WN == kLoraWaves && WR * MR * 16 == kWideRows, "tile shape");
+__global__ __launch_bounds__(WR * WN * 64) void lora_shrink_wide_kernel(LoraArgs p) {
+  constexpr int ROWS = WR * MR * 16, THREADS = WR * WN * 64;
   constexpr int RA = WN * NR * 16;                      // rows of A in a stage
-  constexpr int NX = kWideRows * 8 / kLoraThreads;      // 16-byte chunks a thread loads
-  constexpr int NA = (RA * 8 + kLoraThreads - 1) / kLoraThreads;
-  constexpr int kStage = (kWideRows + RA) * 128;
+  constexpr int NX = ROWS * 8 / THREADS;      // 16-byte chunks a thread loads
+  constexpr int NA = (RA * 8 + THREADS - 1) / THREADS;
+  constexpr int kStage = (ROWS + RA) * 128;
   __shared__ __align__(16) uint8_t lds[2][kStage];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int s = blockIdx.x % p.S;
   ListedTile t;
-  if (!find_listed<kWideRows>(p, blockIdx.x / p.S, &t) || t.g >= p.L) return;
+  if (!find_listed<ROWS>(p, blockIdx.x / p.S, &t) || t.g >= p.L) return;
   const int KB = (int)(p.K / 64);
   const int kb0 = (int)((int64_t)KB * s / p.S), n = (int)((int64_t)KB * (s + 1) / p.S) - kb0;
   auto row_of = [&](int slot) {   // slots past the tile's rows repeat its last row
@@ -407,15 +409,15 @@ __global__ __launch_bounds__(kLoraThreads) void lora_shrink_wide_kernel(LoraArgs
   int xo[NX], ao[NA];
 #pragma unroll
   for (int j = 0; j < NX; ++j) {
-    const int c = tid + j * kLoraThreads, r = c >> 3;
+    const int c = tid + j * THREADS, r = c >> 3;
     xp[j] = p.x + (int64_t)row_of(r) * p.ldx + (int64_t)kb0 * 64 + (c & 7) * 8;
     xo[j] = r * 128 + (((c & 7) ^ swz_f(r)) << 4);
   }
 #pragma unroll
   for (int j = 0; j < NA; ++j) {
-    const int c = min(tid + j * kLoraThreads, RA * 8 - 1), r = c >> 3;
+    const int c = min(tid + j * THREADS, RA * 8 - 1), r = c >> 3;
     ap[j] = p.a + ((int64_t)t.g * p.r + min(r, p.r - 1)) * p.K + (int64_t)kb0 * 64 + (c & 7) * 8;
-    ao[j] = (kWideRows + r) * 128 + (((c & 7) ^ swz_f(r)) << 4);
+    ao[j] = (ROWS + r) * 128 + (((c & 7) ^ swz_f(r)) << 4);
   }
   v4f acc[MR][NR];
 #pragma unroll
@@ -439,7 +441,7 @@ __global__ __launch_bounds__(kLoraThreads) void lora_shrink_wide_kernel(LoraArgs
     for (int j = 0; j < NX; ++j) *reinterpret_cast<v4u *>(&lds[b][xo[j]]) = x[j];
 #pragma unroll
     for (int j = 0; j < NA; ++j)
-      if (RA * 8 % kLoraThreads == 0 || tid + j * kLoraThreads < RA * 8)
+      if (RA * 8 % THREADS == 0 || tid + j * THREADS < RA * 8)
         *reinterpret_cast<v4u *>(&lds[b][ao[j]]) = w[j];
     load(x, w, i + 2);
     lds_barrier();
@@ -457,7 +459,7 @@ __global__ __launch_bounds__(kLoraThreads) void lora_shrink_wide_kernel(LoraArgs
       for (int f = 0; f < NR; ++f) {
         const int r = rank0 + f * 16 + (lane & 15);
         av[f] = *reinterpret_cast<const v8bf *>(
-            &lds[b][(kWideRows + r) * 128 + ((chunk ^ swz_f(r)) << 4)]);
+            &lds[b][(ROWS + r) * 128 + ((chunk ^ swz_f(r)) << 4)]);
       }
 #pragma unroll
       for (int q = 0; q < MR; ++q)
@@ -489,88 +491,108 @@ __global__ __launch_bounds__(kLoraThreads) void lora_shrink_wide_kernel(LoraArgs
   }
 }
 
-// Adds the parts of h, scales and splits them: a thread takes 8 ranks of a row.
+// A tile's rows and adapter for the expand kernel, and its h: the parts added,
+// scaled, split, in the order in which the matrix instruction takes them (per
+// 16 rows and 16 ranks 64 lanes' 16 bytes), so that the many workgroups of the
+// expand kernel find all of it by the tile's number alone.  A workgroup takes
+// 4 runs of 8 ranks of a tile.
+constexpr int kJoinChunks = kLoraThreads / kWideRows;
+
 __global__ __launch_bounds__(kLoraThreads) void lora_join_kernel(LoraArgs p) {
-  const int chunks = p.r / 8;
-  const int64_t i = (int64_t)blockIdx.x * kLoraThreads + threadIdx.x;
-  if (i >= p.T * chunks) return;
-  const int64_t row = i / chunks;
-  const int g = p.ids[row];
-  if ((unsigned)g >= (unsigned)p.L) return;
-  v4u *o = reinterpret_cast<v4u *>(p.hs + i * 16);
-  join_parts(p, p.h + row * p.r + (i - row * chunks) * 8, p.scale ? p.scale[g] : 1.0f, &o[0], &o[1]);
+  const int chunks = p.r / 8, steps = (p.r + 15) / 16;
+  const int blocks = (2 * steps + kJoinChunks - 1) / kJoinChunks;
+  const int tile = blockIdx.x / blocks, part = blockIdx.x % blocks;
+  ListedTile t;
+  const bool found = find_listed<kWideRows>(p, tile, &t);
+  if (part == 0 && threadIdx.x == 0) p.tile_adapter[tile] = found ? t.g : -1;
+  if (!found) return;
+  const int slot = threadIdx.x % kWideRows;
+  int row = slot < t.rows ? p.order[t.start + slot] : -1;
+  row = row < p.T ? row : -1;
+  if (part == 0 && threadIdx.x < kWideRows) p.tile_rows[(int64_t)tile * kWideRows + slot] = row;
+  if (t.g >= p.L || row < 0) return;
+  const float scale = p.scale ? p.scale[t.g] : 1.0f;
+  const int ch = part * kJoinChunks + threadIdx.x / kWideRows;
+  if (ch >= 2 * steps) return;
+  v4u hi = v4u{0, 0, 0, 0}, lo = hi;   // (past a rank that is not a multiple of 16)
+  if (ch < chunks) join_parts(p, p.h + (int64_t)row * p.r + ch * 8, scale, &hi, &lo);
+  v4u *o = reinterpret_cast<v4u *>(p.hs) +
+           (((int64_t)tile * 4 + (slot >> 4)) * steps + (ch >> 1)) * 64 + (ch & 1) * 32 + (slot & 15);
+  o[0] = hi;
+  o[16] = lo;
 }
 
-// out for a tile's 64 rows and CT runs of 128 columns, 16 rows a wave.  Rows
+// out for a tile's 64 rows and ct runs of 16 F columns, 16 rows a wave.  Rows
 // of the instruction are rows of the batch, its columns columns of out, and a
-// lane's eight fragments are eight consecutive columns: base and out move as
-// 256 contiguous bytes of a row per 16 lanes.  h stays in registers for all CT
+// lane's F fragments are F consecutive columns: base and out move as 32 F
+// contiguous bytes of a row per 16 lanes.  h stays in registers for all ct
 // runs; B's run goes through LDS (it is contiguous in memory, but a fragment
 // takes a row per lane), loaded one run ahead in registers, with an odd number
-// of 16-byte chunks between rows so that 16 rows' chunks meet no bank twice.
-constexpr int kExpandCols = 128;
-
-template <int NS>
+// of 16-byte chunks between rows so that 16 rows' chunks spread over the banks.
+// F = 8 up to rank 32, where base and out are all that counts, and 4 above,
+// where its fewer registers let more workgroups overlap (8192 rows, N = 18432,
+// r = 32: 117 us with 8, 127 with 4; 4099 rows, N = 4096, r = 128: 29 and 27).
+template <int NS, int F>
 __global__ __launch_bounds__(kLoraThreads) void lora_expand_wide_kernel(LoraArgs p, int ct) {
   extern __shared__ __align__(16) uint8_t lds[];   // B's run: [fragment][16] rows
-  __shared__ int rows[kWideRows];
+  constexpr int COLS = 16 * F;
+  constexpr int NB = F * NS / 8;   // 16-byte chunks a thread loads of a run
+  typedef unsigned piece __attribute__((ext_vector_type(F / 2), aligned(2)));   // F columns
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int runs = (int)((p.N + kExpandCols - 1) / kExpandCols);
+  const int runs = (int)((p.N + COLS - 1) / COLS);
   const int groups = (runs + ct - 1) / ct;
-  ListedTile t;
-  if (!find_listed<kWideRows>(p, blockIdx.x / groups, &t)) return;
+  const int tile = blockIdx.x / groups;
   const int run0 = (int)(blockIdx.x % groups) * ct;
   const int run1 = min(run0 + ct, runs);
-  if (tid < kWideRows)
-    rows[tid] = min(max(p.order[t.start + min(tid, t.rows - 1)], 0), (int)p.T - 1);
-  lds_barrier();
-  const bool worn = t.g < p.L;
   const int i16 = lane & 15, g16 = lane >> 4;
+  const int g = p.tile_adapter[tile];
+  // rows g16 * 4 + q of the wave's 16, -1 past the tile's
+  const int4 row4 = reinterpret_cast<const int4 *>(p.tile_rows)[(int64_t)tile * 16 + wave * 4 + g16];
+  const int row[4] = {row4.x, row4.y, row4.z, row4.w};
   const int chunks = p.r / 8;                 // 16-byte chunks of a row of B
+  const int steps = (p.r + 15) / 16;
   const int pitch = (chunks | 1) * 16;
-  constexpr int NB = NS;                      // chunks a thread loads: 128 * r / 8 / 256 = r / 16
   v4u hv[NS], br[NB];
-  const uint16_t *hr = p.hs + (int64_t)rows[wave * 16 + i16] * p.r * 2 + g16 * 8;
-  if (worn) {
+  const v4u *hr = reinterpret_cast<const v4u *>(p.hs) + ((int64_t)tile * 4 + wave) * steps * 64 + lane;
 #pragma unroll
-    for (int st = 0; st < NS; ++st)
-      hv[st] = st * 16 + (g16 >> 1) * 8 < p.r ? *reinterpret_cast<const v4u *>(hr + st * 32)
-                                              : v4u{0, 0, 0, 0};
-  }
-  // chunk c of a run is row (column of out) c / chunks of it; column n = 8 i + f
-  // is row i of fragment f.  Columns past N repeat the last one.
-  int bn[NB], bc[NB], bo[NB];
+  for (int st = 0; st < NS; ++st) hv[st] = st < steps ? hr[st * 64] : v4u{0, 0, 0, 0};
+  if (g < 0) return;
+  const bool worn = g < p.L;
+  // chunk c of a run is row (column of out) n = c / chunks of it, and n = F i + f
+  // is row i of fragment f.  Columns past N read as zeros.
+  int off[NB], dst[NB];
 #pragma unroll
   for (int j = 0; j < NB; ++j) {
-    const int c = min(tid + j * kLoraThreads, kExpandCols * chunks - 1);
-    bn[j] = c / chunks;
-    bc[j] = c - bn[j] * chunks;
-    bo[j] = ((bn[j] & 7) * 16 + (bn[j] >> 3)) * pitch + bc[j] * 16;
+    const int c = min(tid + j * kLoraThreads, COLS * chunks - 1);
+    const int n = c / chunks, ch = c - n * chunks;
+    off[j] = n * p.r + ch * 8;
+    dst[j] = ((n % F) * 16 + n / F) * pitch + ch * 16;
   }
-  const uint16_t *bg = p.b + (worn ? (int64_t)t.g * p.N * p.r : 0);
+  const uint16_t *bg = p.b + (worn ? (int64_t)g * p.N * p.r : 0);
   auto load_b = [&](int run) {
+    const int64_t left = (p.N - (int64_t)run * COLS) * p.r;
 #pragma unroll
-    for (int j = 0; j < NB; ++j) {
-      const int64_t col = min((int64_t)run * kExpandCols + bn[j], p.N - 1);
-      br[j] = *reinterpret_cast<const v4u *>(bg + col * p.r + bc[j] * 8);
-    }
+    for (int j = 0; j < NB; ++j)
+      br[j] = off[j] < left ? *reinterpret_cast<const v4u *>(bg + (int64_t)run * COLS * p.r + off[j])
+                            : v4u{0, 0, 0, 0};
   };
   if (worn) load_b(run0);
   for (int run = run0; run < run1; ++run) {
-    const int64_t c0 = (int64_t)run * kExpandCols + i16 * 8;
-    v4u bs[4];
+    const int64_t c0 = (int64_t)run * COLS + i16 * F;
+    piece bs[4];
 #pragma unroll
     for (int q = 0; q < 4; ++q)
-      bs[q] = p.base && c0 + 8 <= p.N
-                  ? load16_once(p.base + (int64_t)rows[wave * 16 + g16 * 4 + q] * p.ldb + c0)
-                  : v4u{0, 0, 0, 0};
-    v4f acc[8];
+      bs[q] = p.base && row[q] >= 0 && c0 + F <= p.N
+                  ? __builtin_nontemporal_load(reinterpret_cast<const piece *>(
+                        p.base + (int64_t)row[q] * p.ldb + c0))
+                  : piece(0);
+    v4f acc[F];
 #pragma unroll
-    for (int f = 0; f < 8; ++f) acc[f] = v4f{0, 0, 0, 0};
+    for (int f = 0; f < F; ++f) acc[f] = v4f{0, 0, 0, 0};
     if (worn) {
       lds_barrier();   // the run before has been read
 #pragma unroll
-      for (int j = 0; j < NB; ++j) *reinterpret_cast<v4u *>(&lds[bo[j]]) = br[j];
+      for (int j = 0; j < NB; ++j) *reinterpret_cast<v4u *>(&lds[dst[j]]) = br[j];
       lds_barrier();
       load_b(min(run + 1, run1 - 1));
 #pragma unroll
@@ -578,7 +600,7 @@ __global__ __launch_bounds__(kLoraThreads) void lora_expand_wide_kernel(LoraArgs
         // past the rank h is zero, and B's last chunk stands in
         const int chunk = min(st * 2 + (g16 >> 1), chunks - 1);
 #pragma unroll
-        for (int f = 0; f < 8; ++f) {
+        for (int f = 0; f < F; ++f) {
           const v8bf bv = *reinterpret_cast<const v8bf *>(&lds[(f * 16 + i16) * pitch + chunk * 16]);
           acc[f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8bf, hv[st]), bv,
                                                            acc[f], 0, 0, 0);
@@ -587,23 +609,20 @@ __global__ __launch_bounds__(kLoraThreads) void lora_expand_wide_kernel(LoraArgs
     }
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
-      const int slot = wave * 16 + g16 * 4 + q;
-      if (slot >= t.rows) continue;
-      uint16_t *o = p.out + (int64_t)rows[slot] * p.ldo;
-      if (c0 + 8 <= p.N) {
-        float f[8];
-        unpack8(make_uint4(bs[q][0], bs[q][1], bs[q][2], bs[q][3]), f);
-        v4u w;
+      if (row[q] < 0) continue;
+      uint16_t *o = p.out + (int64_t)row[q] * p.ldo;
+      if (c0 + F <= p.N) {
+        piece w;
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-          w[j] = (uint32_t)bf_bits(f[2 * j] + acc[2 * j][q]) |
-                 ((uint32_t)bf_bits(f[2 * j + 1] + acc[2 * j + 1][q]) << 16);
-        store16_once(o + c0, w);
+        for (int j = 0; j < F / 2; ++j)
+          w[j] = (uint32_t)bf_bits(bf16_lo(bs[q][j]) + acc[2 * j][q]) |
+                 ((uint32_t)bf_bits(bf16_hi(bs[q][j]) + acc[2 * j + 1][q]) << 16);
+        __builtin_nontemporal_store(w, reinterpret_cast<piece *>(o + c0));
       } else {
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
+        for (int j = 0; j < F; ++j)
           if (c0 + j < p.N) {
-            const float f = p.base ? bf16_lo(p.base[(int64_t)rows[slot] * p.ldb + c0 + j]) : 0.0f;
+            const float f = p.base ? bf16_lo(p.base[(int64_t)row[q] * p.ldb + c0 + j]) : 0.0f;
             o[c0 + j] = bf_bits(f + acc[j][q]);
           }
       }
@@ -612,19 +631,26 @@ __global__ __launch_bounds__(kLoraThreads) void lora_expand_wide_kernel(LoraArgs
 }
 
 namespace {
+// Rows of a shrink tile of a larger batch.  From kBigBatch rows on 128, with
+// eight waves: A is read from L2 once per 128 rows, which is what bounds the
+// kernel there (4099 rows, K = 14336, r = 128: 45 -> 36 us).
+constexpr int64_t kBigBatch = 2048;
+int shrink_rows(int64_t T) { return T >= kBigBatch ? 128 : kWideRows; }
+
 // Tiles a batch can have at most: full ones, and one more per adapter (and
 // for the rows without one).
-int64_t max_tiles(int64_t T, int L) {
-  if (T <= kDirectRows) return T;
+int64_t max_tiles(int64_t T, int L, int rows) {
   const int64_t groups = (int64_t)L + 1 < T ? (int64_t)L + 1 : T;
-  return T / kWideRows + groups;
+  return T / rows + groups;
 }
 
-// K ranges: enough workgroups to fill the chip twice, at least 256 of K each.
+// K ranges, each at least 256 of K, that give two workgroups of four waves or
+// one of eight per compute unit (more of either measured slower: 36 -> 43 us
+// at the sizes above).
 int split_of(int64_t T, int64_t K, int32_t r, int L) {
-  int64_t units = max_tiles(T, L);
-  if (T <= kDirectRows) units = (units < L ? units : L) * ((r + 15) / 16);
-  int64_t s = 512 / units;
+  int64_t units = T <= kDirectRows ? (T < L ? T : L) * ((r + 15) / 16)
+                                   : max_tiles(T, L, shrink_rows(T));
+  int64_t s = (T >= kBigBatch ? 256 : 512) / units;
   if (s > K / 256) s = K / 256;
   if (s > kMaxSplit) s = kMaxSplit;
   return s < 1 ? 1 : (int)s;
@@ -632,11 +658,17 @@ int split_of(int64_t T, int64_t K, int32_t r, int L) {
 
 size_t align256(size_t n) { return (n + 255) / 256 * 256; }
 
+// h of the tiles, split: 64 lanes' 16 bytes per 16 rows and 16 ranks.
+size_t split_bytes(int64_t tiles, int32_t r) { return (size_t)tiles * 4 * ((r + 15) / 16) * 1024; }
+
 }  // namespace
 
 size_t lora_workspace_bytes(int64_t T, int64_t K, int32_t r, int32_t L, bool listed) {
   size_t n = align256(sizeof(float) * (size_t)split_of(T, K, r, L) * T * r);
-  if (T > kDirectRows) n += align256(sizeof(float) * (size_t)T * r);
+  const int64_t tiles = max_tiles(T, L, kWideRows);
+  if (T > kDirectRows)
+    n += split_bytes(tiles, r) + sizeof(int32_t) * (size_t)tiles * kWideRows +
+         align256(sizeof(int32_t) * (size_t)tiles);
   if (T > kDirectRows && !listed)
     n += align256(sizeof(int32_t) * (size_t)T) * 2 + align256(sizeof(int32_t) * ((size_t)L + 1)) +
          group_workspace_bytes(T, L);
@@ -671,8 +703,8 @@ hipError_t launch_lora_add(const void *base, int64_t ldb, const void *x, int64_t
   char *w = static_cast<char *>(work);
   p.h = reinterpret_cast<float *>(w);
   w += align256(sizeof(float) * (size_t)p.S * T * r);
-  const int64_t tiles = max_tiles(T, L);
   if (T <= kDirectRows) {
+    const int64_t tiles = T;   // at most: a row each
     const int steps = (r + 15) / 16;
     lora_shrink_kernel<<<(unsigned)(tiles * steps * p.S), kLoraThreads, 0, stream>>>(p);
     if (hipError_t e = hipGetLastError()) return e;
@@ -681,8 +713,13 @@ hipError_t launch_lora_add(const void *base, int64_t ldb, const void *x, int64_t
                          lds, stream>>>(p);
     return hipGetLastError();
   }
+  const int64_t tiles = max_tiles(T, L, kWideRows);
   p.hs = reinterpret_cast<uint16_t *>(w);
-  w += align256(sizeof(float) * (size_t)T * r);
+  w += split_bytes(tiles, r);
+  p.tile_rows = reinterpret_cast<int32_t *>(w);
+  w += sizeof(int32_t) * (size_t)tiles * kWideRows;
+  p.tile_adapter = reinterpret_cast<int32_t *>(w);
+  w += align256(sizeof(int32_t) * (size_t)tiles);
   if (!order) {
     int32_t *ord = reinterpret_cast<int32_t *>(w);
     w += align256(sizeof(int32_t) * (size_t)T);
@@ -694,29 +731,38 @@ hipError_t launch_lora_add(const void *base, int64_t ldb, const void *x, int64_t
     p.order = ord;
     p.offsets = off;
   }
-  const unsigned gs = (unsigned)(tiles * p.S);
-  if (r <= 16) lora_shrink_wide_kernel<4, 1, 1, 1><<<gs, kLoraThreads, 0, stream>>>(p);
-  else if (r <= 32) lora_shrink_wide_kernel<4, 1, 1, 2><<<gs, kLoraThreads, 0, stream>>>(p);
-  else if (r <= 64) lora_shrink_wide_kernel<2, 2, 2, 2><<<gs, kLoraThreads, 0, stream>>>(p);
-  else if (r <= 128) lora_shrink_wide_kernel<2, 2, 2, 4><<<gs, kLoraThreads, 0, stream>>>(p);
-  else lora_shrink_wide_kernel<2, 2, 2, 8><<<gs, kLoraThreads, 0, stream>>>(p);
+  const unsigned gs = (unsigned)(max_tiles(T, L, shrink_rows(T)) * p.S);
+#define FP8BLK_SHRINK(W, NR)                                                                 \
+  (shrink_rows(T) == kWideRows                                                               \
+       ? (lora_shrink_wide_kernel<4 / W, W, W, NR><<<gs, 256, 0, stream>>>(p), hipSuccess)   \
+       : (lora_shrink_wide_kernel<8 / W, W, W, NR><<<gs, 512, 0, stream>>>(p), hipSuccess))
+  if (r <= 16) FP8BLK_SHRINK(1, 1);
+  else if (r <= 32) FP8BLK_SHRINK(1, 2);
+  else if (r <= 64) FP8BLK_SHRINK(2, 2);
+  else if (r <= 128) FP8BLK_SHRINK(2, 4);
+  else FP8BLK_SHRINK(2, 8);
+#undef FP8BLK_SHRINK
   if (hipError_t e = hipGetLastError()) return e;
-  const int64_t pieces = T * (r / 8);
-  lora_join_kernel<<<(unsigned)((pieces + kLoraThreads - 1) / kLoraThreads), kLoraThreads, 0,
-                     stream>>>(p);
+  const int join_blocks = (2 * ((r + 15) / 16) + kJoinChunks - 1) / kJoinChunks;
+  lora_join_kernel<<<(unsigned)(tiles * join_blocks), kLoraThreads, 0, stream>>>(p);
   if (hipError_t e = hipGetLastError()) return e;
-  // several runs of columns a workgroup where that leaves enough of them
-  const int64_t runs = (N + kExpandCols - 1) / kExpandCols;
-  int64_t ct = tiles * runs / 1024;
-  ct = ct < 1 ? 1 : ct > 4 ? 4 : ct;
-  const unsigned gw = (unsigned)(tiles * ((runs + ct - 1) / ct));
-  const size_t lds = (size_t)kExpandCols * ((r / 8) | 1) * 16;
-  if (r <= 16) lora_expand_wide_kernel<1><<<gw, kLoraThreads, lds, stream>>>(p, (int)ct);
-  else if (r <= 32) lora_expand_wide_kernel<2><<<gw, kLoraThreads, lds, stream>>>(p, (int)ct);
-  else if (r <= 64) lora_expand_wide_kernel<4><<<gw, kLoraThreads, lds, stream>>>(p, (int)ct);
-  else if (r <= 128) lora_expand_wide_kernel<8><<<gw, kLoraThreads, lds, stream>>>(p, (int)ct);
-  else lora_expand_wide_kernel<16><<<gw, kLoraThreads, lds, stream>>>(p, (int)ct);
-  return hipGetLastError();
+#define FP8BLK_EXPAND(NS, F)                                                              \
+  do {                                                                                   \
+    const int64_t runs = (N + 16 * F - 1) / (16 * F);                                    \
+    /* several runs of columns a workgroup where that leaves enough of them */           \
+    int64_t ct = tiles * runs / 1024;                                                    \
+    ct = ct < 1 ? 1 : ct > 4 ? 4 : ct;                                                   \
+    const size_t lds = (size_t)16 * F * ((r / 8) | 1) * 16;                              \
+    lora_expand_wide_kernel<NS, F><<<(unsigned)(tiles * ((runs + ct - 1) / ct)),         \
+                                     kLoraThreads, lds, stream>>>(p, (int)ct);           \
+    return hipGetLastError();                                                            \
+  } while (0)
+  if (r <= 16) FP8BLK_EXPAND(1, 8);
+  if (r <= 32) FP8BLK_EXPAND(2, 8);
+  if (r <= 64) FP8BLK_EXPAND(4, 4);
+  if (r <= 128) FP8BLK_EXPAND(8, 4);
+  FP8BLK_EXPAND(16, 4);
+#undef FP8BLK_EXPAND
 }
 
 }  // namespace fp8blk
