@@ -506,13 +506,14 @@ __global__ __launch_bounds__(kLoraThreads) void lora_join_kernel(LoraArgs p) {
   const bool found = find_listed<kWideRows>(p, tile, &t);
   if (part == 0 && threadIdx.x == 0) p.tile_adapter[tile] = found ? t.g : -1;
   if (!found) return;
-  const int slot = threadIdx.x % kWideRows;
+  // neighbouring threads take neighbouring runs of a row
+  const int slot = threadIdx.x / kJoinChunks;
   int row = slot < t.rows ? p.order[t.start + slot] : -1;
   row = row < p.T ? row : -1;
-  if (part == 0 && threadIdx.x < kWideRows) p.tile_rows[(int64_t)tile * kWideRows + slot] = row;
+  if (part == 0 && threadIdx.x % kJoinChunks == 0) p.tile_rows[(int64_t)tile * kWideRows + slot] = row;
   if (t.g >= p.L || row < 0) return;
   const float scale = p.scale ? p.scale[t.g] : 1.0f;
-  const int ch = part * kJoinChunks + threadIdx.x / kWideRows;
+  const int ch = part * kJoinChunks + threadIdx.x % kJoinChunks;
   if (ch >= 2 * steps) return;
   v4u hi = v4u{0, 0, 0, 0}, lo = hi;   // (past a rank that is not a multiple of 16)
   if (ch < chunks) join_parts(p, p.h + (int64_t)row * p.r + ch * 8, scale, &hi, &lo);
@@ -641,14 +642,15 @@ int shrink_rows(int64_t T) { return T >= kBigBatch ? 128 : kWideRows; }
 // for the rows without one).
 int64_t max_tiles(int64_t T, int L, int rows) {
   const int64_t groups = (int64_t)L + 1 < T ? (int64_t)L + 1 : T;
-  return T / rows + groups;
+  const int64_t tiles = T / rows + groups;
+  return tiles < T ? tiles : T;
 }
 
 // K ranges, each at least 256 of K, that give two workgroups of four waves or
 // one of eight per compute unit (more of either measured slower: 36 -> 43 us
 // at the sizes above).
 int split_of(int64_t T, int64_t K, int32_t r, int L) {
-  int64_t units = T <= kDirectRows ? (T < L ? T : L) * ((r + 15) / 16)
+  int64_t units = T <= kDirectRows ? max_tiles(T, L, kTileRows) * ((r + 15) / 16)
                                    : max_tiles(T, L, shrink_rows(T));
   int64_t s = (T >= kBigBatch ? 256 : 512) / units;
   if (s > K / 256) s = K / 256;
@@ -704,7 +706,7 @@ hipError_t launch_lora_add(const void *base, int64_t ldb, const void *x, int64_t
   p.h = reinterpret_cast<float *>(w);
   w += align256(sizeof(float) * (size_t)p.S * T * r);
   if (T <= kDirectRows) {
-    const int64_t tiles = T;   // at most: a row each
+    const int64_t tiles = max_tiles(T, L, kTileRows);
     const int steps = (r + 15) / 16;
     lora_shrink_kernel<<<(unsigned)(tiles * steps * p.S), kLoraThreads, 0, stream>>>(p);
     if (hipError_t e = hipGetLastError()) return e;
