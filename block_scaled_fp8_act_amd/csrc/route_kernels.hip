@@ -9,6 +9,7 @@
 #include "fp8blk_device.h"
 #include "fp8blk_launch.h"
 
+#include <float.h>
 #include <math.h>
 
 namespace fp8blk {
@@ -61,14 +62,32 @@ __device__ __forceinline__ int row_min(int v) {
   return v;
 }
 
+// How many of the other 15 lanes of a DPP row come before this one: a larger
+// value, or an equal one with a lower index (LANES 15 .. 1, by rotation); and
+// how many have a larger value.
+template <int N = 15>
+__device__ __forceinline__ int row_rank(float v, int e) {
+  const float ov = dpp_f<0x120 + N>(v);   // row_ror:N
+  const int oe = dpp_i<0x120 + N>(e);
+  const int before = ov > v || (ov == v && oe < e) ? 1 : 0;
+  if constexpr (N > 1) return before + row_rank<N - 1>(v, e);
+  else return before;
+}
+template <int N = 15>
+__device__ __forceinline__ int row_larger(float v) {
+  const int before = dpp_f<0x120 + N>(v) > v ? 1 : 0;
+  if constexpr (N > 1) return before + row_larger<N - 1>(v);
+  else return before;
+}
+
 // e^x for x <= 0 (or NaN): 2^(x log2 e) with the product's rounding error
 // added back to first order, so the relative error stays near that of the
 // hardware exponential (1 ulp) down to the underflow, not |x| times it.
 __device__ __forceinline__ float exp_neg(float x) {
   constexpr float kL = 0x1.715476p+0f, kLlo = 0x1.4ae0bep-26f;   // log2 e = kL + kLlo
+  x = x < -200.0f ? -200.0f : x;   // e^-200 is 0 in fp32; keeps NaN
   const float t = x * kL;
-  // (x = -inf: t = -inf and the correction is NaN, so it is not applied)
-  const float r = t > -200.0f ? fmaf(x, kL, -t) + x * kLlo : 0.0f;
+  const float r = fmaf(x, kLlo, fmaf(x, kL, -t));
   const float p = __builtin_amdgcn_exp2f(t);
   return fmaf(p, r * 0x1.62e43p-1f, p);
 }
@@ -183,6 +202,7 @@ template <typename T, int LPR, int V, int VEC>
 __global__ __launch_bounds__(kRouteMaxThreads) void route_kernel(RouteArgs a) {
   extern __shared__ float lds[];          // [E] counts, [waves][E] sums
   __shared__ int live_rows[kRouteMaxWaves];
+  __shared__ float2 found[LPR == 16 ? kRouteMaxWaves : 1][4][16];
   const int threads = blockDim.x, waves = threads / 64;
   constexpr int RPW = 64 / LPR;
   constexpr int SLOTS = (kRouteMaxK + LPR - 1) / LPR;
@@ -214,12 +234,13 @@ __global__ __launch_bounds__(kRouteMaxThreads) void route_kernel(RouteArgs a) {
     for (int c = V - 1; c >= 0; --c) bestc = v[c] == bestv ? c : bestc;
     const float peak = row_max<LPR>(bestv);
     const bool live = peak > kNegInf;
+    const float top = live ? peak : 0.0f;
     float inv = 0.0f;
     if (all) {
       float ex[V], total = 0.0f;
 #pragma unroll
       for (int c = 0; c < V; ++c) {
-        ex[c] = live ? exp_neg(v[c] - peak) : 0.0f;
+        ex[c] = exp_neg(v[c] - top);
         total += ex[c];
       }
       total = row_sum<LPR>(total);
@@ -227,52 +248,103 @@ __global__ __launch_bounds__(kRouteMaxThreads) void route_kernel(RouteArgs a) {
 #pragma unroll
       for (int c = 0; c < V; ++c) acc[c] += ex[c] * inv;
     }
-    float sel_v[SLOTS];
-    int sel_e[SLOTS];
+    bool done = false;
+    if constexpr (LPR == 16) {
+      // The k-th largest of the 16 lanes' bests bounds the k-th largest logit
+      // from below, and few logits reach it (11 of 256 on average at k = 8).
+      // Up to 16 of them are laid out one a lane, where a row's order is 15
+      // rotations; with more (ties, or few experts open) the rounds below.
+      if (a.k <= 16) {
+        const float bound = fmaxf(
+            -row_max<LPR>(row_larger(bestv) < a.k ? -bestv : kNegInf), -FLT_MAX);
+        int n = 0;
 #pragma unroll
-    for (int s = 0; s < SLOTS; ++s) {
-      sel_v[s] = kNegInf;
-      sel_e[s] = -1;
-    }
-    for (int j = 0; j < a.k; ++j) {
-      const float m = j ? row_max<LPR>(bestv) : peak;
-      const int mine = expert_of<LPR, VEC>(bestc, sub);
-      const int e = row_min<LPR>(m > kNegInf && bestv == m ? mine : INT32_MAX);
+        for (int c = 0; c < V; ++c) n += v[c] >= bound ? 1 : 0;
+        int at = n;   // inclusive sum over the row's lanes
+        at += dpp_i<0x111>(at);   // row_shr:1, 2, 4, 8
+        at += dpp_i<0x112>(at);
+        at += dpp_i<0x114>(at);
+        at += dpp_i<0x118>(at);
+        done = __builtin_amdgcn_ballot_w64(at > 16) == 0;
+        if (done) {
+          float2 *mine = found[wave][lane / LPR];
+          mine[sub] = make_float2(kNegInf, 0.0f);
+          at -= n;
 #pragma unroll
-      for (int s = 0; s < SLOTS; ++s) {
-        if (j == s * LPR + sub && e != INT32_MAX) {
-          sel_v[s] = m;
-          sel_e[s] = e;
+          for (int c = 0; c < V; ++c)
+            if (v[c] >= bound)
+              mine[at++] = make_float2(v[c], __int_as_float(expert_of<LPR, VEC>(c, sub)));
+          // the wave's own LDS: in order, but the compiler has to keep it so
+          __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+          __builtin_amdgcn_wave_barrier();
+          __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+          const float2 f = mine[sub];
+          const int e = __float_as_int(f.y);
+          const int rank = row_rank(f.x, e);
+          const bool chosen = f.x > kNegInf && rank < a.k;
+          const float w = chosen ? exp_neg(f.x - peak) : 0.0f;
+          if (a.renorm) {
+            const float total = row_sum<LPR>(w);
+            inv = live ? 1.0f / total : 0.0f;
+          }
+          // lanes past the candidates fill the slots left over
+          const int j = chosen ? rank : f.x > kNegInf ? a.k : sub;
+          if (j < a.k && row < a.T) {
+            a.ids[row * a.k + j] = chosen ? e : -1;
+            a.weights[row * a.k + j] = w * inv;
+            if (chosen) atomicAdd(&hist[e], 1);
+          }
         }
       }
-      if (j + 1 == a.k) break;
-      const int drop = mine == e ? bestc : -1;
-      bestv = kNegInf;
+    }
+    if (!done) {
+      float sel_v[SLOTS];
+      int sel_e[SLOTS];
 #pragma unroll
-      for (int c = 0; c < V; ++c) {
-        v[c] = c == drop ? kNegInf : v[c];
-        bestv = fmaxf(bestv, v[c]);
+      for (int s = 0; s < SLOTS; ++s) {
+        sel_v[s] = kNegInf;
+        sel_e[s] = -1;
+      }
+      for (int j = 0; j < a.k; ++j) {
+        const float m = j ? row_max<LPR>(bestv) : peak;
+        const int mine = expert_of<LPR, VEC>(bestc, sub);
+        const int e = row_min<LPR>(m > kNegInf && bestv == m ? mine : INT32_MAX);
+#pragma unroll
+        for (int s = 0; s < SLOTS; ++s) {
+          if (j == s * LPR + sub && e != INT32_MAX) {
+            sel_v[s] = m;
+            sel_e[s] = e;
+          }
+        }
+        if (j + 1 == a.k) break;
+        const int drop = mine == e ? bestc : -1;
+        bestv = kNegInf;
+#pragma unroll
+        for (int c = 0; c < V; ++c) {
+          v[c] = c == drop ? kNegInf : v[c];
+          bestv = fmaxf(bestv, v[c]);
+        }
+#pragma unroll
+        for (int c = V - 1; c >= 0; --c) bestc = v[c] == bestv ? c : bestc;
+      }
+      float w[SLOTS], total = 0.0f;
+#pragma unroll
+      for (int s = 0; s < SLOTS; ++s) {
+        w[s] = sel_e[s] >= 0 ? exp_neg(sel_v[s] - peak) : 0.0f;
+        total += w[s];
+      }
+      if (a.renorm) {
+        total = row_sum<LPR>(total);
+        inv = live ? 1.0f / total : 0.0f;
       }
 #pragma unroll
-      for (int c = V - 1; c >= 0; --c) bestc = v[c] == bestv ? c : bestc;
-    }
-    float w[SLOTS], total = 0.0f;
-#pragma unroll
-    for (int s = 0; s < SLOTS; ++s) {
-      w[s] = sel_e[s] >= 0 ? exp_neg(sel_v[s] - peak) : 0.0f;
-      total += w[s];
-    }
-    if (a.renorm) {
-      total = row_sum<LPR>(total);
-      inv = live ? 1.0f / total : 0.0f;
-    }
-#pragma unroll
-    for (int s = 0; s < SLOTS; ++s) {
-      const int j = s * LPR + sub;
-      if (j < a.k && row < a.T) {
-        a.ids[row * a.k + j] = sel_e[s];
-        a.weights[row * a.k + j] = w[s] * inv;
-        if (sel_e[s] >= 0) atomicAdd(&hist[sel_e[s]], 1);
+      for (int s = 0; s < SLOTS; ++s) {
+        const int j = s * LPR + sub;
+        if (j < a.k && row < a.T) {
+          a.ids[row * a.k + j] = sel_e[s];
+          a.weights[row * a.k + j] = w[s] * inv;
+          if (sel_e[s] >= 0) atomicAdd(&hist[sel_e[s]], 1);
+        }
       }
     }
     live_count += __popcll(__builtin_amdgcn_ballot_w64(live && sub == 0));
@@ -501,11 +573,11 @@ __global__ __launch_bounds__(kBackThreads) void route_backward_kernel(RouteBackA
     float peak = kNegInf;
 #pragma unroll
     for (int c = 0; c < V; ++c) peak = fmaxf(peak, v[c]);
-    peak = row_max<LPR>(peak);
+    peak = live ? row_max<LPR>(peak) : 0.0f;
     float total = 0.0f, inner = 0.0f;
 #pragma unroll
     for (int c = 0; c < V; ++c) {
-      v[c] = live ? exp_neg(v[c] - peak) : 0.0f;
+      v[c] = exp_neg(v[c] - peak);
       total += v[c];
       inner += v[c] * g[c];
     }
@@ -532,17 +604,18 @@ namespace {
 
 // Kernel of a row width: the fewest logits per lane that cover E, in DPP rows
 // of 16 lanes up to 256 experts and in whole waves above; four logits per
-// load where the rows' alignment (E % 4 == 0) allows it.
+// load where the rows' alignment (E % 4 == 0) allows it, except that up to 64
+// experts are spread over all lanes (a lane's best then says more).
 template <typename T, template <typename, int, int, int> class L, typename... A>
 hipError_t by_width(int E, A... args) {
+  if (E <= 32) return L<T, 16, 2, 1>::go(args...);
+  if (E <= 64) return L<T, 16, 4, 1>::go(args...);
   if (E % 4 == 0) {
-    if (E <= 64) return L<T, 16, 4, 4>::go(args...);
     if (E <= 128) return L<T, 16, 8, 4>::go(args...);
     if (E <= 256) return L<T, 16, 16, 4>::go(args...);
     if (E <= 512) return L<T, 64, 8, 4>::go(args...);
     return L<T, 64, 16, 4>::go(args...);
   }
-  if (E <= 64) return L<T, 16, 4, 1>::go(args...);
   if (E <= 128) return L<T, 16, 8, 1>::go(args...);
   if (E <= 256) return L<T, 16, 16, 1>::go(args...);
   if (E <= 512) return L<T, 64, 8, 1>::go(args...);
