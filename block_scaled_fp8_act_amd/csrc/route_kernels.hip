@@ -80,16 +80,12 @@ __device__ __forceinline__ int row_larger(float v) {
   else return before;
 }
 
-// e^x for x <= 0 (or NaN): 2^(x log2 e) with the product's rounding error
-// added back to first order, so the relative error stays near that of the
-// hardware exponential (1 ulp) down to the underflow, not |x| times it.
-__device__ __forceinline__ float exp_neg(float x) {
-  constexpr float kL = 0x1.715476p+0f, kLlo = 0x1.4ae0bep-26f;   // log2 e = kL + kLlo
-  x = x < -200.0f ? -200.0f : x;   // e^-200 is 0 in fp32; keeps NaN
-  const float t = x * kL;
-  const float r = fmaf(x, kLlo, fmaf(x, kL, -t));
-  const float p = __builtin_amdgcn_exp2f(t);
-  return fmaf(p, r * 0x1.62e43p-1f, p);
+// e^(v - peak) for v <= peak: the difference first, so that logits of any size
+// (a row of the type's lowest value among them) leave it small, then one product
+// and the hardware exponential: 2 |v - peak| 2^-24 of the term and 1 ulp.
+// v = -inf gives 0.
+__device__ __forceinline__ float exp_from(float v, float peak) {
+  return __builtin_amdgcn_exp2f((v - peak) * 0x1.715476p+0f);   // log2 e
 }
 
 // Element c of lane `sub` of a row: VEC consecutive experts per load.
@@ -98,31 +94,46 @@ __device__ __forceinline__ int expert_of(int c, int sub) {
   return ((c / VEC) * LPR + sub) * VEC + c % VEC;
 }
 
+// A lane's logits of a row.  Slots past E load the row's start, so that no load
+// waits for a condition, and become -inf, like all of a row that is not live.
+// (Loading the next rows ahead of the present ones' work measured no faster:
+// the vector ALU is the bound.)
 template <typename T, int LPR, int V, int VEC>
-__device__ __forceinline__ void load_row(const T *row, int E, int sub, bool live, float *v) {
+struct RowLoad {
+  static_assert(VEC == 1 || VEC == 4, "one element or four per load");
+  static constexpr int W = VEC * sizeof(T) <= 4 ? 1 : VEC * sizeof(T) / 4;   // dwords a load
+  uint32_t w[V / VEC][W];
+
+  __device__ __forceinline__ void load(const T *row, int E, int sub) {
 #pragma unroll
-  for (int c = 0; c < V; c += VEC) {
-    const int e = expert_of<LPR, VEC>(c, sub);
-    const bool in = live && e < E;
-    if constexpr (sizeof(T) == 4 && VEC == 4) {
-      const uint4 w = in ? *reinterpret_cast<const uint4 *>(row + e) : make_uint4(0, 0, 0, 0);
-      v[c] = in ? __uint_as_float(w.x) : kNegInf;
-      v[c + 1] = in ? __uint_as_float(w.y) : kNegInf;
-      v[c + 2] = in ? __uint_as_float(w.z) : kNegInf;
-      v[c + 3] = in ? __uint_as_float(w.w) : kNegInf;
-    } else if constexpr (sizeof(T) == 2 && VEC == 4) {
-      const uint2 w = in ? *reinterpret_cast<const uint2 *>(row + e) : make_uint2(0, 0);
-      v[c] = in ? bf16_lo(w.x) : kNegInf;
-      v[c + 1] = in ? bf16_hi(w.x) : kNegInf;
-      v[c + 2] = in ? bf16_lo(w.y) : kNegInf;
-      v[c + 3] = in ? bf16_hi(w.y) : kNegInf;
-    } else {
-      static_assert(VEC == 1, "one element or four per load");
-      if constexpr (sizeof(T) == 4) v[c] = in ? __uint_as_float(row[e]) : kNegInf;
-      else v[c] = in ? bf16_lo(row[e]) : kNegInf;
+    for (int i = 0; i < V / VEC; ++i) {
+      const int e = expert_of<LPR, VEC>(i * VEC, sub);
+      const T *p = row + (e < E ? e : 0);
+      if constexpr (W == 4) {
+        const uint4 q = *reinterpret_cast<const uint4 *>(p);
+        w[i][0] = q.x; w[i][1] = q.y; w[i][2] = q.z; w[i][3] = q.w;
+      } else if constexpr (W == 2) {
+        const uint2 q = *reinterpret_cast<const uint2 *>(p);
+        w[i][0] = q.x; w[i][1] = q.y;
+      } else {
+        w[i][0] = *p;
+      }
     }
   }
-}
+  __device__ __forceinline__ void unpack(int E, int sub, bool live, float *v) const {
+#pragma unroll
+    for (int i = 0; i < V / VEC; ++i) {
+      const bool in = live && expert_of<LPR, VEC>(i * VEC, sub) < E;
+#pragma unroll
+      for (int j = 0; j < VEC; ++j) {
+        float f;
+        if constexpr (sizeof(T) == 4) f = __uint_as_float(w[i][j]);
+        else f = j & 1 ? bf16_hi(w[i][j / 2]) : bf16_lo(w[i][j / 2]);
+        v[i * VEC + j] = in ? f : kNegInf;
+      }
+    }
+  }
+};
 
 // fp32 -> bf16 bits with the hardware's rounding (nearest even, NaN kept).
 __device__ __forceinline__ uint16_t to_bf16(float f) {
@@ -222,10 +233,11 @@ __global__ __launch_bounds__(kRouteMaxThreads) void route_kernel(RouteArgs a) {
   const int64_t first = ((int64_t)blockIdx.x * waves + wave) * RPW;
   for (int64_t r0 = first; r0 < a.T; r0 += step) {
     const int64_t row = r0 + lane / LPR;
-    const bool in = row < a.T && (!a.mask || a.mask[row]);
+    const int64_t r = row < a.T ? row : a.T - 1;
     float v[V];
-    load_row<T, LPR, V, VEC>(static_cast<const T *>(a.logits) + (row < a.T ? row : 0) * a.E, a.E,
-                             sub, in, v);
+    RowLoad<T, LPR, V, VEC> in;
+    in.load(static_cast<const T *>(a.logits) + r * a.E, a.E, sub);
+    in.unpack(a.E, sub, row < a.T && (!a.mask || a.mask[r]), v);
     float bestv = kNegInf;
     int bestc = 0;
 #pragma unroll
@@ -240,7 +252,7 @@ __global__ __launch_bounds__(kRouteMaxThreads) void route_kernel(RouteArgs a) {
       float ex[V], total = 0.0f;
 #pragma unroll
       for (int c = 0; c < V; ++c) {
-        ex[c] = exp_neg(v[c] - top);
+        ex[c] = exp_from(v[c], top);
         total += ex[c];
       }
       total = row_sum<LPR>(total);
@@ -282,7 +294,7 @@ __global__ __launch_bounds__(kRouteMaxThreads) void route_kernel(RouteArgs a) {
           const int e = __float_as_int(f.y);
           const int rank = row_rank(f.x, e);
           const bool chosen = f.x > kNegInf && rank < a.k;
-          const float w = chosen ? exp_neg(f.x - peak) : 0.0f;
+          const float w = chosen ? exp_from(f.x, top) : 0.0f;
           if (a.renorm) {
             const float total = row_sum<LPR>(w);
             inv = live ? 1.0f / total : 0.0f;
@@ -330,7 +342,7 @@ __global__ __launch_bounds__(kRouteMaxThreads) void route_kernel(RouteArgs a) {
       float w[SLOTS], total = 0.0f;
 #pragma unroll
       for (int s = 0; s < SLOTS; ++s) {
-        w[s] = sel_e[s] >= 0 ? exp_neg(sel_v[s] - peak) : 0.0f;
+        w[s] = sel_e[s] >= 0 ? exp_from(sel_v[s], top) : 0.0f;
         total += w[s];
       }
       if (a.renorm) {
@@ -543,7 +555,9 @@ __global__ __launch_bounds__(kBackThreads) void route_backward_kernel(RouteBackA
     const int64_t at = row < a.T ? row : a.T - 1;
     const bool live = row < a.T && a.ids[at * a.k] >= 0;
     float v[V], d[V];
-    load_row<T, LPR, V, VEC>(static_cast<const T *>(a.logits) + at * a.E, a.E, sub, live, v);
+    RowLoad<T, LPR, V, VEC> in;
+    in.load(static_cast<const T *>(a.logits) + at * a.E, a.E, sub);
+    in.unpack(a.E, sub, live, v);
     int id[SLOTS];
     float w[SLOTS], dw[SLOTS], dot = 0.0f;
 #pragma unroll
@@ -577,7 +591,7 @@ __global__ __launch_bounds__(kBackThreads) void route_backward_kernel(RouteBackA
     float total = 0.0f, inner = 0.0f;
 #pragma unroll
     for (int c = 0; c < V; ++c) {
-      v[c] = exp_neg(v[c] - peak);
+      v[c] = exp_from(v[c], peak);
       total += v[c];
       inner += v[c] * g[c];
     }
