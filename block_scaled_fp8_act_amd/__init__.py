@@ -216,7 +216,7 @@ _CODES = (torch.uint8, torch.float8_e4m3fn)
 
 
 def _shape_eq(t, shape, name):
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
 
 
@@ -648,6 +648,7 @@ class RowGroups(NamedTuple):
 
 
 _LOGITS = {torch.float32: 0, torch.bfloat16: 1}    # FP8BLK_F32, FP8BLK_BF16
+_LOGIT_TYPES = tuple(_LOGITS)
 _I32 = (torch.int32,)
 _BF16 = (torch.bfloat16,)
 _MASK = (torch.bool, torch.uint8)
@@ -699,7 +700,7 @@ def _bytes(t):
 # points check every buffer, the wrappers what the caller gave them.
 
 def _route_in(logits, mask):
-    _need(logits, "logits", tuple(_LOGITS), 2)
+    _need(logits, "logits", _LOGIT_TYPES, 2)
     if mask is not None:
         _need(mask, "mask", _MASK, 1)
         _shape_eq(mask, (logits.shape[0],), "mask")
@@ -736,7 +737,7 @@ def fp8blk_moe_route(logits, mask, renormalize, loss_coef, ids, weights, counts,
 
 
 def _route_back_in(logits, routing, d_weights, d_loss):
-    _need(logits, "logits", tuple(_LOGITS), 2)
+    _need(logits, "logits", _LOGIT_TYPES, 2)
     T, E = logits.shape
     ids, weights, counts = routing.ids, routing.weights, routing.counts
     _need(ids, "routing.ids", _I32, 2); _need(weights, "routing.weights", _F32, 2)
