@@ -684,6 +684,17 @@ def _same_device(first, *others):
         raise ValueError(f"the tensors are on cuda:{d}, which is not the current device")
 
 
+def _plain(device, *specs):
+    """Whether every (tensor, dtype, shape) is just that, contiguous and on the
+    device: the one quick look that most calls need; where it is not so, the
+    checks one by one accept it or say what is wrong."""
+    for t, dtype, shape in specs:
+        if (t is not None and (t.dtype is not dtype or t.shape != shape or t.get_device() != device
+                               or not t.is_contiguous())):
+            return False
+    return device == torch.cuda.current_device()
+
+
 def _at(t):
     return t.data_ptr() if t is not None else None
 
@@ -848,10 +859,8 @@ def fp8blk_moe_combine_backward(d_out, y, weights, positions, rows_used, d_y, d_
     _combine_back_call(d_out, y, weights, positions, rows_used, d_y, d_weights)
 
 
-def fp8blk_lora_add(base, x, a, b, ids, scale, groups, out, workspace):
-    """Adapters into out; base, scale and groups may be None; base and out, and
-    x, may be column slices of wider matrices.  ``workspace`` holds
-    fp8blk_lora_add_workspace_bytes(T, K, r, L, listed) bytes."""
+def _lora_in(base, x, a, b, ids, scale, groups, out):
+    """Row strides of base, x and out."""
     ldx, ldo = _rows_2d(x, "x"), _rows_2d(out, "out")
     _need(a, "a", _BF16, 3); _need(b, "b", _BF16, 3); _need(ids, "ids", _I32, 1)
     T, K = x.shape
@@ -862,9 +871,7 @@ def fp8blk_lora_add(base, x, a, b, ids, scale, groups, out, workspace):
     _shape_eq(b, (L, N, r), "b"); _shape_eq(ids, (T,), "ids")
     _shape_eq(out, (T, N), "out")
     ldb = 0
-    if base is out:
-        ldb = ldo
-    elif base is not None:
+    if base is not None:
         ldb = _rows_2d(base, "base")
         _shape_eq(base, (T, N), "base")
     if scale is not None:
@@ -875,11 +882,28 @@ def fp8blk_lora_add(base, x, a, b, ids, scale, groups, out, workspace):
         order, offsets = groups.order, groups.offsets
         _need(order, "groups.order", _I32, 1); _need(offsets, "groups.offsets", _I32, 1)
         _shape_eq(order, (T,), "groups.order"); _shape_eq(offsets, (L + 1,), "groups.offsets")
-    _same_device(x, base, a, b, ids, scale, order, offsets, out, workspace)
+    _same_device(x, base, a, b, ids, scale, order, offsets, out)
+    return ldb, ldx, ldo
+
+
+def _lora_call(base, x, a, b, ids, scale, groups, out, workspace, strides):
+    T, K = x.shape
+    L, r = a.shape[:2]
+    order, offsets = (groups.order, groups.offsets) if groups is not None else (None, None)
     _check(load_library().fp8blk_lora_add(
-        _at(base), ldb, x.data_ptr(), ldx, a.data_ptr(), b.data_ptr(), ids.data_ptr(),
-        _at(scale), _at(order), _at(offsets), T, K, N, r, L, out.data_ptr(), ldo,
-        _at(workspace), _bytes(workspace), _stream()), "fp8blk_lora_add")
+        _at(base), strides[0], x.data_ptr(), strides[1], a.data_ptr(), b.data_ptr(),
+        ids.data_ptr(), _at(scale), _at(order), _at(offsets), T, K, out.shape[1], r, L,
+        out.data_ptr(), strides[2], _at(workspace), _bytes(workspace), _stream()),
+        "fp8blk_lora_add")
+
+
+def fp8blk_lora_add(base, x, a, b, ids, scale, groups, out, workspace):
+    """Adapters into out; base, scale and groups may be None; base and out, and
+    x, may be column slices of wider matrices.  ``workspace`` holds
+    fp8blk_lora_add_workspace_bytes(T, K, r, L, listed) bytes."""
+    strides = _lora_in(base, x, a, b, ids, scale, groups, out)
+    _same_device(x, workspace)
+    _lora_call(base, x, a, b, ids, scale, groups, out, workspace, strides)
 
 
 def moe_route(logits, k, mask=None, renormalize=True, loss_coef=None):
@@ -909,8 +933,16 @@ def moe_route(logits, k, mask=None, renormalize=True, loss_coef=None):
 def moe_route_backward(logits, routing, d_weights=None, d_loss=None):
     """Gradient of the logits (in their type) from those of the weights and of
     the loss; the choice itself has none."""
-    _route_back_in(logits, routing, d_weights, d_loss)
-    _same_device(logits, routing.ids, routing.weights, routing.counts, routing.rows, d_weights, d_loss)
+    T, E = logits.shape
+    slots = (T, routing.ids.shape[1])
+    if not (logits.dtype in _LOGITS and (d_loss is None or d_loss.dim() == 0) and routing.rows is not None
+            and _plain(logits.get_device(), (logits, logits.dtype, (T, E)),
+                       (routing.ids, torch.int32, slots), (routing.weights, torch.float32, slots),
+                       (routing.counts, torch.int32, (E,)), (routing.rows, torch.int32, (1,)),
+                       (d_weights, torch.float32, slots), (d_loss, torch.float32, ()))):
+        _route_back_in(logits, routing, d_weights, d_loss)
+        _same_device(logits, routing.ids, routing.weights, routing.counts, routing.rows, d_weights,
+                     d_loss)
     d_logits = torch.empty_like(logits)
     _route_back_call(logits, routing, d_weights, d_loss, d_logits)
     return d_logits
@@ -932,8 +964,12 @@ def group_rows(ids, groups):
 def moe_combine(y, weights, positions, base=None):
     """out[t] = base[t] + sum_j weights[t,j] * y[positions[t,j]] in bf16;
     slots with position -1 add nothing."""
-    _combine_in(y, weights, positions, base)
-    _same_device(y, weights, positions, base)
+    slots = weights.shape
+    if not (len(slots) == 2 and y.dim() == 2 and
+            _plain(y.get_device(), (y, torch.bfloat16, y.shape), (weights, torch.float32, slots),
+                   (positions, torch.int32, slots), (base, torch.bfloat16, (slots[0], y.shape[1])))):
+        _combine_in(y, weights, positions, base)
+        _same_device(y, weights, positions, base)
     out = y.new_empty((weights.shape[0], y.shape[1]))
     _combine_call(y, weights, positions, base, out)
     return out
@@ -954,11 +990,18 @@ def lora_add(base, x, a, b, ids, scale=None, groups=None, out=None):
     (none outside [0, L)); ``out`` may be base (in place).  ``groups`` =
     group_rows(ids, L) saves listing the rows again in every projection."""
     T, K = x.shape
-    L, r = a.shape[0], a.shape[1]
+    L, r, N = a.shape[0], a.shape[1], b.shape[1]
     if out is None:
-        out = x.new_empty((T, b.shape[1]))
+        out = x.new_empty((T, N))
+    bf = torch.bfloat16
+    if groups is None and _plain(x.get_device(), (x, bf, (T, K)), (a, bf, (L, r, K)),
+                                 (b, bf, (L, N, r)), (ids, torch.int32, (T,)), (base, bf, (T, N)),
+                                 (out, bf, (T, N)), (scale, torch.float32, (L,))):
+        strides = N, K, N
+    else:
+        strides = _lora_in(base, x, a, b, ids, scale, groups, out)
     need = load_library().fp8blk_lora_add_workspace_bytes(T, K, r, L, groups is not None)
-    fp8blk_lora_add(base, x, a, b, ids, scale, groups, out, _work(need, x))
+    _lora_call(base, x, a, b, ids, scale, groups, out, _work(need, x), strides)
     return out
 
 
