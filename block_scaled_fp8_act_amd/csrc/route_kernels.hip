@@ -750,13 +750,13 @@ hipError_t launch_route_backward(const void *logits, bool bf16, int64_t T, int32
 // count as group G: they are listed last and have position -1.  All sums are
 // integers, so the order never varies.
 //
-// Up to 8192 rows one workgroup does all of it.  Beyond, the workgroups' counts
-// come first (group_count_kernel), then their sums over workgroups, a wave per
-// group (group_scan_kernel), then the places: three launches, each of them
-// bound by latency at these sizes (1M rows move 17 MB).
+// Up to 2048 rows one workgroup does all of it.  Beyond, the workgroups' counts
+// come first (group_count_kernel), past 16 workgroups their sums over workgroups,
+// a wave per group (group_scan_kernel), then the places: two or three launches,
+// each of them bound by latency at these sizes (1M rows move 17 MB).
 constexpr int kGroupThreads = 1024;
 constexpr int kGroupWaves = kGroupThreads / 64;
-constexpr int64_t kGroupOneBlock = 8192;
+constexpr int64_t kGroupOneBlock = 2048;
 
 __device__ __forceinline__ int group_key(int id, int G) { return (unsigned)id < (unsigned)G ? id : G; }
 
@@ -819,21 +819,51 @@ __global__ __launch_bounds__(kScanThreads) void group_scan_kernel(int32_t *__res
   if (lane == 0) total[g] = before;
 }
 
-template <int STEPS>
+// Several workgroups: `part` holds their counts by group, summed over workgroups
+// by group_scan_kernel (SCANNED), or, up to kDirectBlocks of them, added up here.
+constexpr int kDirectBlocks = 16;
+
+template <int STEPS, bool SCANNED>
 __global__ __launch_bounds__(kGroupThreads) void group_place_kernel(
     const int32_t *__restrict__ ids, int64_t R, int G, const int32_t *__restrict__ part,
     const int32_t *__restrict__ total, int32_t *__restrict__ order,
     int32_t *__restrict__ positions, int32_t *__restrict__ offsets) {
-  extern __shared__ int hist[];          // [waves][G + 1]
-  __shared__ int wave_total[kGroupWaves];
+  extern __shared__ int sort_lds[];
+  __shared__ int wave_total[2][kGroupWaves];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int G1 = G + 1;
-  const int64_t lo = ((int64_t)blockIdx.x * kGroupWaves + wave) * (STEPS * 64);
+  int *hist = sort_lds;                         // [waves][G + 1]
+  int *shift = sort_lds + kGroupWaves * G1;          // [G + 1]: place in order less place in the workgroup
+  uint32_t *sorted = reinterpret_cast<uint32_t *>(shift + G1);   // [rows]: key, row
+  const bool one = gridDim.x == 1;
+  const int64_t base = (int64_t)blockIdx.x * (kGroupThreads * STEPS);
+  const int64_t lo = base + wave * (STEPS * 64);
   int key[STEPS], place[STEPS];
 #pragma unroll
   for (int s = 0; s < STEPS; ++s) {
     const int64_t i = lo + s * 64 + lane;
     key[s] = i < R ? group_key(ids[i], G) : -1;
+  }
+  // groups 2 tid and 2 tid + 1: rows in all workgroups, and in earlier ones
+  int all[2] = {0, 0}, before[2] = {0, 0};
+  if (!one) {
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      const int g = 2 * tid + q;
+      if (g >= G1) continue;
+      const int32_t *row = part + (int64_t)g * gridDim.x;
+      if constexpr (SCANNED) {
+        all[q] = total[g];
+        before[q] = row[blockIdx.x];
+      } else {
+#pragma unroll
+        for (int b = 0; b < kDirectBlocks; ++b) {
+          const int c = b < (int)gridDim.x ? row[b] : 0;
+          all[q] += c;
+          before[q] += b < (int)blockIdx.x ? c : 0;
+        }
+      }
+    }
   }
   for (int i = tid; i < kGroupWaves * G1; i += kGroupThreads) hist[i] = 0;
   __syncthreads();
@@ -850,37 +880,40 @@ __global__ __launch_bounds__(kGroupThreads) void group_place_kernel(
       same &= set ? m : ~m;
     }
     const int leader = in ? __builtin_ctzll(same) : lane;
-    int base = 0;
-    if (in && lane == leader) base = atomicAdd(&mine[key[s]], (int)__popcll(same));
-    place[s] = __shfl(base, leader) + (int)__popcll(same & lower);
+    int at = 0;
+    if (in && lane == leader) at = atomicAdd(&mine[key[s]], (int)__popcll(same));
+    place[s] = __shfl(at, leader) + (int)__popcll(same & lower);
   }
   __syncthreads();
-  // groups 2 tid and 2 tid + 1: rows of earlier groups, then the waves' first
-  // places
-  int all[2] = {0, 0};
+  // the groups' first places: in the workgroup's rows (here) and in all rows
+  int here[2] = {0, 0};
 #pragma unroll
   for (int q = 0; q < 2; ++q) {
     const int g = 2 * tid + q;
     if (g >= G1) continue;
-    if (gridDim.x > 1) {
-      all[q] = total[g];
-    } else {
 #pragma unroll
-      for (int w = 0; w < kGroupWaves; ++w) all[q] += hist[w * G1 + g];
-    }
+    for (int w = 0; w < kGroupWaves; ++w) here[q] += hist[w * G1 + g];
+    if (one) all[q] = here[q];
   }
-  const int pair = all[0] + all[1];
-  const int scan = wave_scan(pair, lane);
-  if (lane == 63) wave_total[wave] = scan;
+  const int scan = wave_scan(all[0] + all[1], lane);
+  const int scan_here = one ? scan : wave_scan(here[0] + here[1], lane);
+  if (lane == 63) {
+    wave_total[0][wave] = scan;
+    wave_total[1][wave] = scan_here;
+  }
   __syncthreads();
-  int first = scan - pair;
-  for (int w = 0; w < wave; ++w) first += wave_total[w];
+  int first = scan - all[0] - all[1], first_here = scan_here - here[0] - here[1];
+  for (int w = 0; w < wave; ++w) {
+    first += wave_total[0][w];
+    first_here += wave_total[1][w];
+  }
 #pragma unroll
   for (int q = 0; q < 2; ++q) {
     const int g = 2 * tid + q;
     if (g >= G1) continue;
     if (blockIdx.x == 0) offsets[g] = first;
-    int at = first + (gridDim.x > 1 ? part[(int64_t)g * gridDim.x + blockIdx.x] : 0);
+    shift[g] = first + before[q] - first_here;
+    int at = first_here;
 #pragma unroll
     for (int w = 0; w < kGroupWaves; ++w) {
       const int c = hist[w * G1 + g];
@@ -888,6 +921,7 @@ __global__ __launch_bounds__(kGroupThreads) void group_place_kernel(
       at += c;
     }
     first += all[q];
+    first_here += here[q];
   }
   __syncthreads();
 #pragma unroll
@@ -895,21 +929,30 @@ __global__ __launch_bounds__(kGroupThreads) void group_place_kernel(
     if (key[s] < 0) continue;
     const int64_t i = lo + s * 64 + lane;
     const int at = mine[key[s]] + place[s];
-    order[at] = (int)i;
-    positions[i] = key[s] < G ? at : -1;
+    positions[i] = key[s] < G ? at + shift[key[s]] : -1;
+    if (one) order[at] = (int)i;
+    else sorted[at] = ((uint32_t)key[s] << 16) | (uint32_t)(i - base);
+  }
+  if (one) return;
+  // the workgroup's rows in order, so that a group's run is written as a run
+  __syncthreads();
+  const int rows = (int)(base + kGroupThreads * STEPS < R ? kGroupThreads * STEPS : R - base);
+  for (int i = tid; i < rows; i += kGroupThreads) {
+    const uint32_t v = sorted[i];
+    order[i + shift[v >> 16]] = (int)(base + (v & 0xffff));
   }
 }
 
 namespace {
 
-// Steps of 64 rows a wave: the fewest that one workgroup needs; 4 beyond
-// (256 workgroups at 1M rows, one per compute unit), 16 past that.
+// Steps of 64 rows a wave.  Up to 2048 rows one workgroup does all; up to 16
+// workgroups of 1024 rows their counts are a launch of their own and each adds
+// them up (8192 rows: 11 us in one workgroup, bound by its ballots, 8 so);
+// beyond, three launches: 4 steps (256 workgroups at 1M rows, one per compute
+// unit), 16 past that.
 int group_steps(int64_t R) {
-  if (R <= kGroupOneBlock) {
-    int s = 1;
-    while (s * kGroupThreads < R) s *= 2;
-    return s;
-  }
+  if (R <= kGroupOneBlock) return R <= kGroupThreads ? 1 : 2;
+  if (R <= (int64_t)kDirectBlocks * kGroupThreads) return 1;
   return R <= (int64_t)256 * 4 * kGroupThreads ? 4 : 16;
 }
 
@@ -936,21 +979,21 @@ hipError_t launch_group_rows(const int32_t *ids, int64_t R, int32_t G, int32_t *
     group_count_kernel<<<blocks, kGroupThreads, sizeof(int) * (G + 1), stream>>>(
         ids, R, G, (int64_t)steps * kGroupThreads, part);
     if (hipError_t e = hipGetLastError()) return e;
-    constexpr int per = kScanThreads / 64;
-    group_scan_kernel<<<(G + per) / per, kScanThreads, 0, stream>>>(part, blocks, G + 1, total);
-    if (hipError_t e = hipGetLastError()) return e;
+    if (steps >= 4) {
+      constexpr int per = kScanThreads / 64;
+      group_scan_kernel<<<(G + per) / per, kScanThreads, 0, stream>>>(part, blocks, G + 1, total);
+      if (hipError_t e = hipGetLastError()) return e;
+    }
   }
-  const size_t lds = sizeof(int) * kGroupWaves * (G + 1);
-#define FP8BLK_PLACE(S)                                                                       \
-  group_place_kernel<S><<<blocks, kGroupThreads, lds, stream>>>(ids, R, G, part, total, order, \
-                                                                positions, offsets)
-  switch (steps) {
-    case 1: FP8BLK_PLACE(1); break;
-    case 2: FP8BLK_PLACE(2); break;
-    case 4: FP8BLK_PLACE(4); break;
-    case 8: FP8BLK_PLACE(8); break;
-    default: FP8BLK_PLACE(16); break;
-  }
+  const size_t lds = sizeof(int) * ((size_t)(kGroupWaves + 1) * (G + 1) +
+                                    (blocks > 1 ? (size_t)steps * kGroupThreads : 0));
+#define FP8BLK_PLACE(S, SCANNED)                                                        \
+  group_place_kernel<S, SCANNED><<<blocks, kGroupThreads, lds, stream>>>(               \
+      ids, R, G, part, total, order, positions, offsets)
+  if (steps == 1) FP8BLK_PLACE(1, false);
+  else if (steps == 2) FP8BLK_PLACE(2, false);
+  else if (steps == 4) FP8BLK_PLACE(4, true);
+  else FP8BLK_PLACE(16, true);
 #undef FP8BLK_PLACE
   return hipGetLastError();
 }
