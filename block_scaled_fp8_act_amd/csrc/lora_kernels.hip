@@ -528,11 +528,13 @@ __global__ __launch_bounds__(kLoraThreads) void lora_join_kernel(LoraArgs p) {
 // lane's F fragments are F consecutive columns: base and out move as 32 F
 // contiguous bytes of a row per 16 lanes.  h stays in registers for all ct
 // runs; B's run goes through LDS (it is contiguous in memory, but a fragment
-// takes a row per lane), loaded one run ahead in registers, with an odd number
-// of 16-byte chunks between rows so that 16 rows' chunks spread over the banks.
+// takes a row per lane), with an odd number of 16-byte chunks between rows so
+// that 16 rows' chunks spread over the banks.  B and base are loaded one run
+// ahead in registers (base in the run it is used in: 117 against 109 us below).
 // F = 8 up to rank 32, where base and out are all that counts, and 4 above,
 // where its fewer registers let more workgroups overlap (8192 rows, N = 18432,
 // r = 32: 117 us with 8, 127 with 4; 4099 rows, N = 4096, r = 128: 29 and 27).
+// Now 109 us (5.5 TB/s of base and out) and 23 us (2.9 TB/s).
 template <int NS, int F>
 __global__ __launch_bounds__(kLoraThreads) void lora_expand_wide_kernel(LoraArgs p, int ct) {
   extern __shared__ __align__(16) uint8_t lds[];   // B's run: [fragment][16] rows
@@ -577,16 +579,24 @@ __global__ __launch_bounds__(kLoraThreads) void lora_expand_wide_kernel(LoraArgs
       br[j] = off[j] < left ? *reinterpret_cast<const v4u *>(bg + (int64_t)run * COLS * p.r + off[j])
                             : v4u{0, 0, 0, 0};
   };
+  piece next[4];   // base of the run to come
+  auto load_base = [&](int run) {
+    const int64_t c = (int64_t)run * COLS + i16 * F;
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      next[q] = p.base && row[q] >= 0 && c + F <= p.N
+                    ? __builtin_nontemporal_load(reinterpret_cast<const piece *>(
+                          p.base + (int64_t)row[q] * p.ldb + c))
+                    : piece(0);
+  };
   if (worn) load_b(run0);
+  load_base(run0);
   for (int run = run0; run < run1; ++run) {
     const int64_t c0 = (int64_t)run * COLS + i16 * F;
     piece bs[4];
 #pragma unroll
-    for (int q = 0; q < 4; ++q)
-      bs[q] = p.base && row[q] >= 0 && c0 + F <= p.N
-                  ? __builtin_nontemporal_load(reinterpret_cast<const piece *>(
-                        p.base + (int64_t)row[q] * p.ldb + c0))
-                  : piece(0);
+    for (int q = 0; q < 4; ++q) bs[q] = next[q];
+    if (run + 1 < run1) load_base(run + 1);
     v4f acc[F];
 #pragma unroll
     for (int f = 0; f < F; ++f) acc[f] = v4f{0, 0, 0, 0};
@@ -751,8 +761,8 @@ hipError_t launch_lora_add(const void *base, int64_t ldb, const void *x, int64_t
 #define FP8BLK_EXPAND(NS, F)                                                              \
   do {                                                                                   \
     const int64_t runs = (N + 16 * F - 1) / (16 * F);                                    \
-    /* several runs of columns a workgroup where that leaves enough of them */           \
-    int64_t ct = tiles * runs / 1024;                                                    \
+    /* several runs of columns a workgroup where that leaves five per compute unit */    \
+    int64_t ct = tiles * runs / 1280;                                                    \
     ct = ct < 1 ? 1 : ct > 4 ? 4 : ct;                                                   \
     const size_t lds = (size_t)16 * F * ((r / 8) | 1) * 16;                              \
     lora_expand_wide_kernel<NS, F><<<(unsigned)(tiles * ((runs + ct - 1) / ct)),         \
