@@ -2,15 +2,22 @@
 //   out[t] = base[t] + scale[g] * (x[t] A[g]^T) B[g]^T,   g = the row's adapter,
 // with x [T, K], A [L, r, K], B [L, N, r], base and out [T, N] in bf16.
 //
-// Two launches: lora_shrink_kernel forms h = x A^T (fp32, in the workspace,
-// K split over workgroups where there are few rows) and lora_expand_kernel
-// adds the parts of h, multiplies by scale and B^T and adds the base in its
-// epilogue.  Rows of one adapter are taken 16 at a time, the width of a
-// matrix instruction, so every adapter in the batch is read once per 16 of
-// its rows and rows of different adapters never share a product.
+// The shrink kernels form h = x A^T in fp32 parts (K split over workgroups so
+// that they fill the chip), the expand kernels multiply it by B^T and add the
+// base in their epilogue.  Rows of one adapter are taken in tiles, so every
+// adapter in the batch is read from HBM once and rows of different adapters
+// never share a product.  Up to 64 rows the tiles are 16 rows and two launches
+// do all; beyond, the rows are listed by adapter (group_rows, unless the caller
+// did) in tiles of 64, and a small launch between the two adds h's parts up and
+// lays them out for the matrix instruction.
 //
-// Bound: HBM traffic (x once, base and out once, the adapters in use once);
-// at ranks up to 256 the products are far below the matrix cores' rate.
+// Bound: HBM traffic (x once, base and out once, the adapters in use once); at
+// ranks up to 256 the products are far below the matrix cores' rate.  Measured,
+// bf16 from HBM, all launches: 16 rows of 16 adapters, 4096 x 4096, r = 16: 9 us
+// (latency; 4.6 MB); 515 rows of 32, 7168 -> 1536, r = 64: 22 us; 8192 rows of
+// 8, 7168 -> 18432, r = 32: 149 us (723 MB, 4.9 TB/s); 4099 rows of 5, 14336 ->
+// 4096, r = 128: 74 us (208 MB, 2.8 TB/s: A's and x's way from L2 through the
+// compute units, 0.25 GB of it, takes longer than x's from HBM).
 #include "fp8blk_device.h"
 #include "fp8blk_launch.h"
 
@@ -373,20 +380,19 @@ __global__ __launch_bounds__(kLoraThreads) void lora_expand_kernel(LoraArgs p) {
 }
 
 // ---------------------------------------------------------------------------
-// Large batches: tiles of 64 rows.
+// Larger batches: tiles of 64 rows.
 //
-// A and B come from L2 once per 64 rows instead of 16 and x, base and out stay
-// the only HBM traffic of weight.  h is kept as the second product takes it:
-// per row and 8 ranks, the 8 upper halves and then the 8 rests in bf16.
-
-
+// A and B come from L2 once per 64 or 128 rows, and x, base and out stay the
+// only HBM traffic of weight.
+//
 // A lane of a matrix instruction holds 16 bytes of one row, and neighbouring
 // lanes hold different rows: loaded that way every lane's 16 bytes are a
 // request of their own (measured: 60 us at 8192 x 7168, r = 32, and no
 // faster with more loads in flight).  So both operands pass through LDS: 64
 // of K a stage, loaded with eight neighbouring lanes on a row's 128 bytes, two
 // stages ahead in registers.  WR x WN waves take MR row fragments and NR rank
-// fragments each.  h goes out in fp32 parts, one per K range.
+// fragments each.  h goes out in fp32 parts, one per K range.  Now 25 us there
+// (4.7 TB/s of x), and 36 us at 4099 x 14336, r = 128 (3.2 TB/s).
 template <int WR, int WN, int MR, int NR>
 __global__ __launch_bounds__(WR * WN * 64) void lora_shrink_wide_kernel(LoraArgs p) {
   constexpr int ROWS = WR * MR * 16, THREADS = WR * WN * 64;
@@ -644,8 +650,10 @@ __global__ __launch_bounds__(kLoraThreads) void lora_expand_wide_kernel(LoraArgs
 namespace {
 // Rows of a shrink tile of a larger batch.  From kBigBatch rows on 128, with
 // eight waves: A is read from L2 once per 128 rows, which is what bounds the
-// kernel there (4099 rows, K = 14336, r = 128: 45 -> 36 us).
-constexpr int64_t kBigBatch = 2048;
+// kernel there (4099 rows, K = 14336, r = 128: 45 -> 36 us; 4096 rows, K = 4096,
+// r = 64: 14.5 -> 12.0).  With fewer rows the larger tiles leave compute units
+// idle (2048 rows, K = 14336, r = 128: 20.6 us in tiles of 64, 25.3 in 128).
+constexpr int64_t kBigBatch = 4096;
 int shrink_rows(int64_t T) { return T >= kBigBatch ? 128 : kWideRows; }
 
 // Tiles a batch can have at most: full ones, and one more per adapter (and

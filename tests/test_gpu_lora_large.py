@@ -1,4 +1,4 @@
-"""Adapters beside large batches (the 128-row tiles, every rank's kernels) and
+"""Adapters beside large batches (64- and 128-row tiles, every rank's kernels) and
 in matrices whose offsets pass 32 bits.  Tolerance as in test_gpu_lora."""
 import numpy as np
 import pytest
@@ -12,7 +12,7 @@ pytestmark = pytest.mark.gpu
 
 
 @pytest.mark.parametrize("r", [8, 16, 24, 32, 40, 64, 72, 128, 136, 256])
-@pytest.mark.parametrize("T,L", [(2048, 3), (2100, 40)])
+@pytest.mark.parametrize("T,L", [(1100, 3), (4096, 3), (4200, 40)])
 def test_lora_large_batch(T, L, r):
     say("lora large", T, L, r)
     K, N = 384, 206
@@ -23,7 +23,7 @@ def test_lora_large_batch(T, L, r):
     check(got, base, x, a, b, ids, scale)
 
 
-@pytest.mark.parametrize("T", [3, 300, 2300])
+@pytest.mark.parametrize("T", [3, 300, 4300])
 def test_lora_rows_past_2_31_elements(T):
     """x, base and out are columns of matrices of T x ld with T * ld > 2^31."""
     K, N, r, L = 128, 70, 16, 2
