@@ -117,6 +117,7 @@ def lora(lib, base=A, ldb=64, x=B, ldx=128, a=C, b=D, ids=E_, scale=NULL, order=
     (dict(L=0), SHAPE), (dict(L=1025), SHAPE), (dict(ldx=127), SHAPE), (dict(ldb=63), SHAPE),
     (dict(ldo=63), SHAPE), (dict(out=A, ldo=65), SHAPE), (dict(nbytes=8), SHAPE),
     (dict(T=100000, ldx=1 << 30), SHAPE),
+    (dict(T=1 << 26, N=1 << 14, ldb=1 << 14, ldo=1 << 14, nbytes=1 << 60), SHAPE),  # over one grid
     (dict(x=MIS), ALIGN), (dict(a=MIS), ALIGN), (dict(b=MIS), ALIGN), (dict(base=MIS), ALIGN),
     (dict(out=MIS), ALIGN), (dict(work=MIS), ALIGN), (dict(ids=ODD), ALIGN), (dict(scale=ODD), ALIGN),
     (dict(order=ODD, offsets=H), ALIGN),

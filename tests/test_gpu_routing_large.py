@@ -7,6 +7,7 @@ import torch
 
 import block_scaled_fp8_act_amd as fb
 from gpu_helpers import dev, say
+from test_gpu_route import check, make
 
 pytestmark = pytest.mark.gpu
 
@@ -78,6 +79,16 @@ def test_route_equal_logits(E, k):
         r = fb.moe_route(torch.full((T, E), 0.25, device=dev()), k)
         assert torch.equal(r.ids.cpu(), torch.arange(k, dtype=torch.int32).expand(T, k))
         assert bool((r.weights - 1.0 / k).abs().max() <= 64 * 2.0 ** -24 / k)
+
+
+@pytest.mark.parametrize("E,k", [(24, 20), (40, 32), (100, 17), (131, 32), (256, 24), (253, 31)])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_route_many_choices(E, k, dtype):
+    """More than 16 choices among up to 256 experts, two slots a lane."""
+    t, mask = make(E + k, 90, E, dtype, masked=0.2)
+    check(t, k, mask, renorm=E % 2 == 0)
+    t, _ = make(E, 90, E, dtype, ties=True)
+    check(t, k)
 
 
 @pytest.mark.parametrize("T", [40, 700])
