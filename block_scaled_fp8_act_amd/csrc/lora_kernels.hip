@@ -228,7 +228,7 @@ __global__ __launch_bounds__(kLoraThreads) void lora_shrink_kernel(LoraArgs p) {
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       const int r = lane & 15;
-      const int at = r * 128 + (((h * 4 + (lane >> 4)) ^ swz_f(r)) << 4);
+      const int at = r * 128 + ((((lane >> 4) * 2 + h) ^ swz_f(r)) << 4);
       const v8bf xv = *reinterpret_cast<const v8bf *>(&lds[wave][at]);
       const v8bf av = *reinterpret_cast<const v8bf *>(&lds[wave][16 * 128 + at]);
       acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(av, xv, acc, 0, 0, 0);
@@ -454,7 +454,7 @@ __global__ __launch_bounds__(WR * WN * 64) void lora_shrink_wide_kernel(LoraArgs
     if (idle) return;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      const int chunk = h * 4 + (lane >> 4);
+      const int chunk = (lane >> 4) * 2 + h;
       v8bf xv[MR], av[NR];
 #pragma unroll
       for (int q = 0; q < MR; ++q) {
