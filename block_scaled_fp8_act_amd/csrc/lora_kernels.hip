@@ -16,8 +16,9 @@
 // bf16 from HBM, all launches: 16 rows of 16 adapters, 4096 x 4096, r = 16: 9 us
 // (latency; 4.6 MB); 515 rows of 32, 7168 -> 1536, r = 64: 22 us; 8192 rows of
 // 8, 7168 -> 18432, r = 32: 149 us (723 MB, 4.9 TB/s); 4099 rows of 5, 14336 ->
-// 4096, r = 128: 74 us (208 MB, 2.8 TB/s: A's and x's way from L2 through the
-// compute units, 0.25 GB of it, takes longer than x's from HBM).
+// 4096, r = 128: 74 us (208 MB, 2.8 TB/s: the shrink kernel's passes through LDS
+// and its products, which grow with the rank, take longer there than x's way
+// from HBM).
 #include "fp8blk_device.h"
 #include "fp8blk_launch.h"
 
@@ -392,7 +393,9 @@ __global__ __launch_bounds__(kLoraThreads) void lora_expand_kernel(LoraArgs p) {
 // of K a stage, loaded with eight neighbouring lanes on a row's 128 bytes, two
 // stages ahead in registers.  WR x WN waves take MR row fragments and NR rank
 // fragments each.  h goes out in fp32 parts, one per K range.  Now 25 us there
-// (4.7 TB/s of x), and 36 us at 4099 x 14336, r = 128 (3.2 TB/s).
+// (4.7 TB/s of x), and 36 us at 4099 x 14336, r = 128 (3.2 TB/s), where the time
+// grows with the rank and not with what is in flight: four stages ahead, more
+// workgroups, or a K range per XCD measured no faster.
 template <int WR, int WN, int MR, int NR>
 __global__ __launch_bounds__(WR * WN * 64) void lora_shrink_wide_kernel(LoraArgs p) {
   constexpr int ROWS = WR * MR * 16, THREADS = WR * WN * 64;
