@@ -41,6 +41,12 @@ constexpr int kLoraWaves = kLoraThreads / 64;
 constexpr int kDirectRows = 64;
 constexpr int kWideRows = 64;
 constexpr int kMaxSplit = 8;
+// h in the second product: the parts of a value's split, the ranks of an
+// instruction, and the bytes of 16 rows of both.
+constexpr int kParts = 3;
+constexpr int kStepRanks = 32;
+constexpr int kStepBytes = kParts * 64 * 16;
+__host__ __device__ constexpr int rank_steps(int r) { return (r + kStepRanks - 1) / kStepRanks; }
 
 struct LoraArgs {
   const uint16_t *x, *a, *b, *base;
@@ -247,17 +253,22 @@ __global__ __launch_bounds__(kLoraThreads) void lora_shrink_kernel(LoraArgs p) {
     *reinterpret_cast<v4f *>(p.h + ((int64_t)s * p.T + t.row) * p.r + rank) = acc;
 }
 
-// v as upper half and rest (an infinite or NaN value has no rest).
-__device__ __forceinline__ void split_bf16(float v, uint16_t *hi, uint16_t *lo) {
-  const uint32_t u = __float_as_uint(v) & 0xffff0000u;
-  *hi = (uint16_t)(u >> 16);
-  *lo = bf_bits(__builtin_isfinite(v) ? v - __uint_as_float(u) : 0.0f);
+// v as the sum of three bf16 values, its 24 bits eight at a time: each is cut, not
+// rounded, so each rest is exact and has at most 16, then 8 bits.  (An infinite
+// or NaN value has no rest.)
+__device__ __forceinline__ void split_bf16(float v, uint32_t *part) {
+  float rest = v;
+#pragma unroll
+  for (int i = 0; i < kParts; ++i) {
+    const uint32_t u = __float_as_uint(rest) & 0xffff0000u;
+    part[i] = u >> 16;
+    rest = __builtin_isfinite(v) ? rest - __uint_as_float(u) : 0.0f;
+  }
 }
 
-// scale times the sum of h's parts at hp (8 ranks), split: the upper halves,
-// then the rests.
+// scale times the sum of h's parts at hp (8 ranks), split.
 __device__ __forceinline__ void join_parts(const LoraArgs &p, const float *hp, float scale,
-                                           v4u *hi, v4u *lo) {
+                                           v4u (&out)[kParts]) {
   const int64_t step = p.T * p.r;
   v4f h[2] = {v4f{0, 0, 0, 0}, v4f{0, 0, 0, 0}};
   for (int s0 = 0; s0 < p.S; s0 += 8) {   // 8 parts' loads in flight
@@ -277,21 +288,20 @@ __device__ __forceinline__ void join_parts(const LoraArgs &p, const float *hp, f
   }
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
-    uint16_t a, b, c, d;
-    split_bf16(h[j >> 1][2 * j & 3] * scale, &a, &b);
-    split_bf16(h[j >> 1][(2 * j & 3) + 1] * scale, &c, &d);
-    (*hi)[j] = a | ((uint32_t)c << 16);
-    (*lo)[j] = b | ((uint32_t)d << 16);
+    uint32_t a[kParts], b[kParts];
+    split_bf16(h[j >> 1][2 * j & 3] * scale, a);
+    split_bf16(h[j >> 1][(2 * j & 3) + 1] * scale, b);
+#pragma unroll
+    for (int i = 0; i < kParts; ++i) out[i][j] = a[i] | (b[i] << 16);
   }
 }
 
 // out = base + (scale * sum of h's parts) B^T for a tile and 128 columns, 32 a
-// wave.  h enters the product as the sum of two bf16 values, its upper half
-// and the rest, which keeps 16 significant bits of it (2^-17, far below the
-// output's rounding): the instruction's 32 values of K hold 16 ranks' upper
-// halves and rests, against B's ranks twice.  B's 128 rows are contiguous in
-// memory and pass through LDS for the reason above, with an odd number of
-// 16-byte chunks between rows so that 16 rows' chunks spread over the banks.
+// wave.  h enters the product as the sum of three bf16 values, which holds every
+// bit of its fp32 value: three instructions of 32 ranks on one fragment of B.
+// B's 128 rows are contiguous in memory and pass through LDS for the reason
+// above, with an odd number of 16-byte chunks between rows so that 16 rows'
+// chunks spread over the banks.
 constexpr int kSmallCols = 128;
 
 __global__ __launch_bounds__(kLoraThreads) void lora_expand_kernel(LoraArgs p) {
@@ -302,9 +312,9 @@ __global__ __launch_bounds__(kLoraThreads) void lora_expand_kernel(LoraArgs p) {
   if (!find_tile_direct(p, blockIdx.x / runs, &t)) return;
   const int64_t n0 = (int64_t)(blockIdx.x % runs) * kSmallCols;
   const int i16 = lane & 15, g16 = lane >> 4;
-  const int chunks = p.r / 8, steps = (p.r + 15) / 16;
+  const int chunks = p.r / 8, steps = rank_steps(p.r);
   const int pitch = (chunks | 1) * 16;
-  uint8_t *lb = lds + steps * 1024;
+  uint8_t *lb = lds + steps * kStepBytes;
   const bool worn = t.g < p.L;
   // base of rows g16 * 4 + q, columns c0 and c0 + 1
   const int64_t c0 = n0 + wave * 32 + i16 * 2;
@@ -338,15 +348,14 @@ __global__ __launch_bounds__(kLoraThreads) void lora_expand_kernel(LoraArgs p) {
 #pragma unroll
     for (int j = 0; j < kHeld; ++j) fetch(min(tid + j * kLoraThreads, total - 1), &held[j], &at[j]);
     const float scale = p.scale ? p.scale[t.g] : 1.0f;
-    for (int c = tid; c < 32 * steps; c += kLoraThreads) {
+    for (int c = tid; c < 64 * steps; c += kLoraThreads) {
       const int slot = c & 15, ch = c >> 4;
       const int r = __shfl(t.row, slot);            // (lane & 15 == slot)
-      v4u hi = v4u{0, 0, 0, 0}, lo = hi;
-      if (r >= 0 && ch < chunks)
-        join_parts(p, p.h + (int64_t)r * p.r + ch * 8, scale, &hi, &lo);
-      v4u *f = reinterpret_cast<v4u *>(lds + (ch >> 1) * 1024) + (ch & 1) * 32 + slot;
-      f[0] = hi;
-      f[16] = lo;
+      v4u h[kParts] = {};
+      if (r >= 0 && ch < chunks) join_parts(p, p.h + (int64_t)r * p.r + ch * 8, scale, h);
+      v4u *f = reinterpret_cast<v4u *>(lds + (ch >> 2) * kStepBytes) + (ch & 3) * 16 + slot;
+#pragma unroll
+      for (int i = 0; i < kParts; ++i) f[i * 64] = h[i];
     }
 #pragma unroll
     for (int j = 0; j < kHeld; ++j) *reinterpret_cast<v4u *>(&lb[at[j]]) = held[j];
@@ -361,13 +370,15 @@ __global__ __launch_bounds__(kLoraThreads) void lora_expand_kernel(LoraArgs p) {
 #pragma unroll 2
     for (int st = 0; st < steps; ++st) {
       // past the rank h is zero, and B's last chunk stands in
-      const int chunk = min(st * 2 + (g16 >> 1), chunks - 1);
-      const v8bf hv = *reinterpret_cast<const v8bf *>(lds + st * 1024 + lane * 16);
+      const int chunk = min(st * 4 + g16, chunks - 1);
+      const v8bf *hv = reinterpret_cast<const v8bf *>(lds + st * kStepBytes) + lane;
 #pragma unroll
       for (int f = 0; f < 2; ++f) {
         const v8bf bv = *reinterpret_cast<const v8bf *>(
             &lb[(f * 64 + wave * 16 + i16) * pitch + chunk * 16]);
-        acc[f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(hv, bv, acc[f], 0, 0, 0);
+#pragma unroll
+        for (int i = 0; i < kParts; ++i)
+          acc[f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(hv[i * 64], bv, acc[f], 0, 0, 0);
       }
     }
   }
@@ -502,15 +513,15 @@ __global__ __launch_bounds__(WR * WN * 64) void lora_shrink_wide_kernel(LoraArgs
 
 // A tile's rows and adapter for the expand kernel, and its h: the parts added,
 // scaled, split, in the order in which the matrix instruction takes them (per
-// 16 rows and 16 ranks 64 lanes' 16 bytes), so that the many workgroups of the
-// expand kernel find all of it by the tile's number alone.  A workgroup takes
-// 4 runs of 8 ranks of a tile.
+// 16 rows, 32 ranks and part of the split 64 lanes' 16 bytes), so that the many
+// workgroups of the expand kernel find all of it by the tile's number alone.  A
+// workgroup takes 4 runs of 8 ranks of a tile.
 constexpr int kJoinChunks = kLoraThreads / kWideRows;
+static_assert(kJoinChunks * 8 == kStepRanks, "a workgroup per tile and step");
 
 __global__ __launch_bounds__(kLoraThreads) void lora_join_kernel(LoraArgs p) {
-  const int chunks = p.r / 8, steps = (p.r + 15) / 16;
-  const int blocks = (2 * steps + kJoinChunks - 1) / kJoinChunks;
-  const int tile = blockIdx.x / blocks, part = blockIdx.x % blocks;
+  const int chunks = p.r / 8, steps = rank_steps(p.r);
+  const int tile = blockIdx.x / steps, part = blockIdx.x % steps;
   ListedTile t;
   const bool found = find_listed<kWideRows>(p, tile, &t);
   if (part == 0 && threadIdx.x == 0) p.tile_adapter[tile] = found ? t.g : -1;
@@ -523,13 +534,13 @@ __global__ __launch_bounds__(kLoraThreads) void lora_join_kernel(LoraArgs p) {
   if (t.g >= p.L || row < 0) return;
   const float scale = p.scale ? p.scale[t.g] : 1.0f;
   const int ch = part * kJoinChunks + threadIdx.x % kJoinChunks;
-  if (ch >= 2 * steps) return;
-  v4u hi = v4u{0, 0, 0, 0}, lo = hi;   // (past a rank that is not a multiple of 16)
-  if (ch < chunks) join_parts(p, p.h + (int64_t)row * p.r + ch * 8, scale, &hi, &lo);
+  v4u h[kParts] = {};   // (zeros past a rank that is not a multiple of 32)
+  if (ch < chunks) join_parts(p, p.h + (int64_t)row * p.r + ch * 8, scale, h);
   v4u *o = reinterpret_cast<v4u *>(p.hs) +
-           (((int64_t)tile * 4 + (slot >> 4)) * steps + (ch >> 1)) * 64 + (ch & 1) * 32 + (slot & 15);
-  o[0] = hi;
-  o[16] = lo;
+           (((int64_t)tile * 4 + (slot >> 4)) * steps + part) * (kParts * 64) + (ch & 3) * 16 +
+           (slot & 15);
+#pragma unroll
+  for (int i = 0; i < kParts; ++i) o[i * 64] = h[i];
 }
 
 // out for a tile's 64 rows and ct runs of 16 F columns, 16 rows a wave.  Rows
@@ -543,12 +554,13 @@ __global__ __launch_bounds__(kLoraThreads) void lora_join_kernel(LoraArgs p) {
 // F = 8 up to rank 32, where base and out are all that counts, and 4 above,
 // where its fewer registers let more workgroups overlap (8192 rows, N = 18432,
 // r = 32: 117 us with 8, 127 with 4; 4099 rows, N = 4096, r = 128: 29 and 27).
-// Now 109 us (5.5 TB/s of base and out) and 23 us (2.9 TB/s).
-template <int NS, int F>
+// Now 110 us (5.5 TB/s of base and out) and 25 us (2.7 TB/s).
+template <int NS, int F>   // up to NS steps of 32 ranks (NS = 0: up to 16 ranks)
 __global__ __launch_bounds__(kLoraThreads) void lora_expand_wide_kernel(LoraArgs p, int ct) {
   extern __shared__ __align__(16) uint8_t lds[];   // B's run: [fragment][16] rows
   constexpr int COLS = 16 * F;
-  constexpr int NB = F * NS / 8;   // 16-byte chunks a thread loads of a run
+  constexpr int NH = NS ? NS : 1;
+  constexpr int NB = NS ? F * NS / 4 : F / 8;   // 16-byte chunks a thread loads of a run
   typedef unsigned piece __attribute__((ext_vector_type(F / 2), aligned(2)));   // F columns
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int runs = (int)((p.N + COLS - 1) / COLS);
@@ -562,12 +574,16 @@ __global__ __launch_bounds__(kLoraThreads) void lora_expand_wide_kernel(LoraArgs
   const int4 row4 = reinterpret_cast<const int4 *>(p.tile_rows)[(int64_t)tile * 16 + wave * 4 + g16];
   const int row[4] = {row4.x, row4.y, row4.z, row4.w};
   const int chunks = p.r / 8;                 // 16-byte chunks of a row of B
-  const int steps = (p.r + 15) / 16;
+  const int steps = rank_steps(p.r);
   const int pitch = (chunks | 1) * 16;
-  v4u hv[NS], br[NB];
-  const v4u *hr = reinterpret_cast<const v4u *>(p.hs) + ((int64_t)tile * 4 + wave) * steps * 64 + lane;
+  v4u hv[NH][kParts], br[NB];
+  const v4u *hr = reinterpret_cast<const v4u *>(p.hs) +
+                  ((int64_t)tile * 4 + wave) * steps * (kParts * 64) + lane;
 #pragma unroll
-  for (int st = 0; st < NS; ++st) hv[st] = st < steps ? hr[st * 64] : v4u{0, 0, 0, 0};
+  for (int st = 0; st < NH; ++st)
+#pragma unroll
+    for (int i = 0; i < kParts; ++i)
+      hv[st][i] = st < steps ? hr[(st * kParts + i) * 64] : v4u{0, 0, 0, 0};
   if (g < 0) return;
   const bool worn = g < p.L;
   // chunk c of a run is row (column of out) n = c / chunks of it, and n = F i + f
@@ -616,15 +632,19 @@ __global__ __launch_bounds__(kLoraThreads) void lora_expand_wide_kernel(LoraArgs
       lds_barrier();
       load_b(min(run + 1, run1 - 1));
 #pragma unroll
-      for (int st = 0; st < NS; ++st) {
+      for (int st = 0; st < NH; ++st) {
         // past the rank h is zero, and B's last chunk stands in
-        const int chunk = min(st * 2 + (g16 >> 1), chunks - 1);
+        const int chunk = min(st * 4 + g16, chunks - 1);
+        v8bf bv[F];
 #pragma unroll
-        for (int f = 0; f < F; ++f) {
-          const v8bf bv = *reinterpret_cast<const v8bf *>(&lds[(f * 16 + i16) * pitch + chunk * 16]);
-          acc[f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8bf, hv[st]), bv,
-                                                           acc[f], 0, 0, 0);
-        }
+        for (int f = 0; f < F; ++f)
+          bv[f] = *reinterpret_cast<const v8bf *>(&lds[(f * 16 + i16) * pitch + chunk * 16]);
+#pragma unroll
+        for (int i = 0; i < kParts; ++i)
+#pragma unroll
+          for (int f = 0; f < F; ++f)
+            acc[f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8bf, hv[st][i]),
+                                                             bv[f], acc[f], 0, 0, 0);
       }
     }
 #pragma unroll
@@ -681,8 +701,8 @@ int split_of(int64_t T, int64_t K, int32_t r, int L) {
 
 size_t align256(size_t n) { return (n + 255) / 256 * 256; }
 
-// h of the tiles, split: 64 lanes' 16 bytes per 16 rows and 16 ranks.
-size_t split_bytes(int64_t tiles, int32_t r) { return (size_t)tiles * 4 * ((r + 15) / 16) * 1024; }
+// h of the tiles, split: 64 lanes' 16 bytes per 16 rows, 32 ranks and part.
+size_t split_bytes(int64_t tiles, int32_t r) { return (size_t)tiles * 4 * rank_steps(r) * kStepBytes; }
 
 }  // namespace
 
@@ -728,10 +748,10 @@ hipError_t launch_lora_add(const void *base, int64_t ldb, const void *x, int64_t
   w += align256(sizeof(float) * (size_t)p.S * T * r);
   if (T <= kDirectRows) {
     const int64_t tiles = max_tiles(T, L, kTileRows);
-    const int steps = (r + 15) / 16;
-    lora_shrink_kernel<<<(unsigned)(tiles * steps * p.S), kLoraThreads, 0, stream>>>(p);
+    const int pieces = (r + 15) / 16;
+    lora_shrink_kernel<<<(unsigned)(tiles * pieces * p.S), kLoraThreads, 0, stream>>>(p);
     if (hipError_t e = hipGetLastError()) return e;
-    const size_t lds = (size_t)steps * 1024 + (size_t)kSmallCols * ((r / 8) | 1) * 16;
+    const size_t lds = (size_t)rank_steps(r) * kStepBytes + (size_t)kSmallCols * ((r / 8) | 1) * 16;
     lora_expand_kernel<<<(unsigned)(tiles * ((N + kSmallCols - 1) / kSmallCols)), kLoraThreads,
                          lds, stream>>>(p);
     return hipGetLastError();
@@ -766,8 +786,7 @@ hipError_t launch_lora_add(const void *base, int64_t ldb, const void *x, int64_t
   else FP8BLK_SHRINK(2, 8);
 #undef FP8BLK_SHRINK
   if (hipError_t e = hipGetLastError()) return e;
-  const int join_blocks = (2 * ((r + 15) / 16) + kJoinChunks - 1) / kJoinChunks;
-  lora_join_kernel<<<(unsigned)(tiles * join_blocks), kLoraThreads, 0, stream>>>(p);
+  lora_join_kernel<<<(unsigned)(tiles * rank_steps(r)), kLoraThreads, 0, stream>>>(p);
   if (hipError_t e = hipGetLastError()) return e;
 #define FP8BLK_EXPAND(NS, F)                                                              \
   do {                                                                                   \
@@ -780,11 +799,11 @@ hipError_t launch_lora_add(const void *base, int64_t ldb, const void *x, int64_t
                                      kLoraThreads, lds, stream>>>(p, (int)ct);           \
     return hipGetLastError();                                                            \
   } while (0)
-  if (r <= 16) FP8BLK_EXPAND(1, 8);
-  if (r <= 32) FP8BLK_EXPAND(2, 8);
-  if (r <= 64) FP8BLK_EXPAND(4, 4);
-  if (r <= 128) FP8BLK_EXPAND(8, 4);
-  FP8BLK_EXPAND(16, 4);
+  if (r <= 16) FP8BLK_EXPAND(0, 8);
+  if (r <= 32) FP8BLK_EXPAND(1, 8);
+  if (r <= 64) FP8BLK_EXPAND(2, 4);
+  if (r <= 128) FP8BLK_EXPAND(4, 4);
+  FP8BLK_EXPAND(8, 4);
 #undef FP8BLK_EXPAND
 }
 

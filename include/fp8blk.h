@@ -497,8 +497,8 @@ FP8BLK_API fp8blk_status fp8blk_moe_combine_backward(
 /* Low-rank adapters of many requests at once, beside a shared projection:
  * out[t] = bf16( base[t] + scale[g] * (x[t] A[g]^T) B[g]^T ), g = ids[t];
  * rows with ids[t] outside [0, L) have no adapter: out[t] = base[t].
- * Products accumulate in fp32; x A^T enters the second product with 16
- * significant bits.
+ * Products accumulate in fp32; x A^T enters the second product with every bit
+ * of its fp32 value.
  *   base_bf16 [T,N], row stride base_stride elements, in, or NULL (zero)
  *   x_bf16 [T,K], row stride x_stride, in
  *   a_bf16 [L,r,K], b_bf16 [L,N,r], scale [L] fp32 (or NULL: 1) in.  Adapters
