@@ -47,6 +47,11 @@ constexpr int kParts = 3;
 constexpr int kStepRanks = 32;
 constexpr int kStepBytes = kParts * 64 * 16;
 __host__ __device__ constexpr int rank_steps(int r) { return (r + kStepRanks - 1) / kStepRanks; }
+// Bytes between B's rows in LDS: whole steps, of which the chunks past the rank
+// hold zeros (h is zero there, and another rank's infinity must not meet it),
+// and an odd number of 16-byte chunks, so that 16 rows' chunks spread over the
+// banks.
+__host__ __device__ constexpr int rank_pitch(int r) { return rank_steps(r) * kStepRanks * 2 + 16; }
 
 struct LoraArgs {
   const uint16_t *x, *a, *b, *base;
@@ -254,16 +259,24 @@ __global__ __launch_bounds__(kLoraThreads) void lora_shrink_kernel(LoraArgs p) {
 }
 
 // v as the sum of three bf16 values, its 24 bits eight at a time: each is cut, not
-// rounded, so each rest is exact and has at most 16, then 8 bits.  (An infinite
-// or NaN value has no rest.)
+// rounded, so each rest is exact, has at most 16, then 8 bits, and v's sign.  A
+// part that would be zero takes half of the one before (exact too), so that
+// every part of a v other than zero times an infinite entry of B is the
+// infinity that v times it is, and no 0 times infinity makes a NaN.  An
+// infinite or NaN v is in every part.
+__device__ __forceinline__ float cut_bf16(float v) {
+  return __uint_as_float(__float_as_uint(v) & 0xffff0000u);
+}
 __device__ __forceinline__ void split_bf16(float v, uint32_t *part) {
-  float rest = v;
-#pragma unroll
-  for (int i = 0; i < kParts; ++i) {
-    const uint32_t u = __float_as_uint(rest) & 0xffff0000u;
-    part[i] = u >> 16;
-    rest = __builtin_isfinite(v) ? rest - __uint_as_float(u) : 0.0f;
-  }
+  static_assert(kParts == 3, "the parts below");
+  float a = cut_bf16(v);
+  float b = cut_bf16(v - a);
+  float c = v - a - b;
+  if (v == a || !__builtin_isfinite(v)) a = b = v * 0.5f;
+  if (c == 0.0f || !__builtin_isfinite(v)) b = c = b * 0.5f;
+  part[0] = __float_as_uint(a) >> 16;
+  part[1] = __float_as_uint(b) >> 16;
+  part[2] = __float_as_uint(c) >> 16;
 }
 
 // scale times the sum of h's parts at hp (8 ranks), split.
@@ -296,12 +309,20 @@ __device__ __forceinline__ void join_parts(const LoraArgs &p, const float *hp, f
   }
 }
 
+// Zeros in the chunks past the rank of B's ROWS rows in LDS.
+template <int ROWS>
+__device__ __forceinline__ void clear_past_rank(uint8_t *lb, int r, int tid) {
+  const int chunks = r / 8, pad = rank_steps(r) * (kStepRanks / 8) - chunks;   // 0..3
+  for (int c = tid / ROWS; c < pad; c += kLoraThreads / ROWS)
+    *reinterpret_cast<v4u *>(&lb[tid % ROWS * rank_pitch(r) + (chunks + c) * 16]) =
+        v4u{0, 0, 0, 0};
+}
+
 // out = base + (scale * sum of h's parts) B^T for a tile and 128 columns, 32 a
 // wave.  h enters the product as the sum of three bf16 values, which holds every
 // bit of its fp32 value: three instructions of 32 ranks on one fragment of B.
 // B's 128 rows are contiguous in memory and pass through LDS for the reason
-// above, with an odd number of 16-byte chunks between rows so that 16 rows'
-// chunks spread over the banks.
+// above.
 constexpr int kSmallCols = 128;
 
 __global__ __launch_bounds__(kLoraThreads) void lora_expand_kernel(LoraArgs p) {
@@ -313,7 +334,7 @@ __global__ __launch_bounds__(kLoraThreads) void lora_expand_kernel(LoraArgs p) {
   const int64_t n0 = (int64_t)(blockIdx.x % runs) * kSmallCols;
   const int i16 = lane & 15, g16 = lane >> 4;
   const int chunks = p.r / 8, steps = rank_steps(p.r);
-  const int pitch = (chunks | 1) * 16;
+  const int pitch = rank_pitch(p.r);
   uint8_t *lb = lds + steps * kStepBytes;
   const bool worn = t.g < p.L;
   // base of rows g16 * 4 + q, columns c0 and c0 + 1
@@ -347,6 +368,7 @@ __global__ __launch_bounds__(kLoraThreads) void lora_expand_kernel(LoraArgs p) {
     const int total = kSmallCols * chunks;
 #pragma unroll
     for (int j = 0; j < kHeld; ++j) fetch(min(tid + j * kLoraThreads, total - 1), &held[j], &at[j]);
+    clear_past_rank<kSmallCols>(lb, p.r, tid);
     const float scale = p.scale ? p.scale[t.g] : 1.0f;
     for (int c = tid; c < 64 * steps; c += kLoraThreads) {
       const int slot = c & 15, ch = c >> 4;
@@ -369,8 +391,7 @@ __global__ __launch_bounds__(kLoraThreads) void lora_expand_kernel(LoraArgs p) {
     lds_barrier();
 #pragma unroll 2
     for (int st = 0; st < steps; ++st) {
-      // past the rank h is zero, and B's last chunk stands in
-      const int chunk = min(st * 4 + g16, chunks - 1);
+      const int chunk = st * 4 + g16;
       const v8bf *hv = reinterpret_cast<const v8bf *>(lds + st * kStepBytes) + lane;
 #pragma unroll
       for (int f = 0; f < 2; ++f) {
@@ -548,8 +569,7 @@ __global__ __launch_bounds__(kLoraThreads) void lora_join_kernel(LoraArgs p) {
 // lane's F fragments are F consecutive columns: base and out move as 32 F
 // contiguous bytes of a row per 16 lanes.  h stays in registers for all ct
 // runs; B's run goes through LDS (it is contiguous in memory, but a fragment
-// takes a row per lane), with an odd number of 16-byte chunks between rows so
-// that 16 rows' chunks spread over the banks.  B and base are loaded one run
+// takes a row per lane).  B and base are loaded one run
 // ahead in registers (base in the run it is used in: 117 against 109 us below).
 // F = 8 up to rank 32, where base and out are all that counts, and 4 above,
 // where its fewer registers let more workgroups overlap (8192 rows, N = 18432,
@@ -575,7 +595,7 @@ __global__ __launch_bounds__(kLoraThreads) void lora_expand_wide_kernel(LoraArgs
   const int row[4] = {row4.x, row4.y, row4.z, row4.w};
   const int chunks = p.r / 8;                 // 16-byte chunks of a row of B
   const int steps = rank_steps(p.r);
-  const int pitch = (chunks | 1) * 16;
+  const int pitch = rank_pitch(p.r);
   v4u hv[NH][kParts], br[NB];
   const v4u *hr = reinterpret_cast<const v4u *>(p.hs) +
                   ((int64_t)tile * 4 + wave) * steps * (kParts * 64) + lane;
@@ -614,7 +634,10 @@ __global__ __launch_bounds__(kLoraThreads) void lora_expand_wide_kernel(LoraArgs
                           p.base + (int64_t)row[q] * p.ldb + c))
                     : piece(0);
   };
-  if (worn) load_b(run0);
+  if (worn) {
+    load_b(run0);
+    clear_past_rank<COLS>(lds, p.r, tid);
+  }
   load_base(run0);
   for (int run = run0; run < run1; ++run) {
     const int64_t c0 = (int64_t)run * COLS + i16 * F;
@@ -633,8 +656,8 @@ __global__ __launch_bounds__(kLoraThreads) void lora_expand_wide_kernel(LoraArgs
       load_b(min(run + 1, run1 - 1));
 #pragma unroll
       for (int st = 0; st < NH; ++st) {
-        // past the rank h is zero, and B's last chunk stands in
-        const int chunk = min(st * 4 + g16, chunks - 1);
+        if (st >= steps) break;
+        const int chunk = st * 4 + g16;
         v8bf bv[F];
 #pragma unroll
         for (int f = 0; f < F; ++f)
@@ -751,7 +774,7 @@ hipError_t launch_lora_add(const void *base, int64_t ldb, const void *x, int64_t
     const int pieces = (r + 15) / 16;
     lora_shrink_kernel<<<(unsigned)(tiles * pieces * p.S), kLoraThreads, 0, stream>>>(p);
     if (hipError_t e = hipGetLastError()) return e;
-    const size_t lds = (size_t)rank_steps(r) * kStepBytes + (size_t)kSmallCols * ((r / 8) | 1) * 16;
+    const size_t lds = (size_t)rank_steps(r) * kStepBytes + (size_t)kSmallCols * rank_pitch(r);
     lora_expand_kernel<<<(unsigned)(tiles * ((N + kSmallCols - 1) / kSmallCols)), kLoraThreads,
                          lds, stream>>>(p);
     return hipGetLastError();
@@ -794,7 +817,7 @@ hipError_t launch_lora_add(const void *base, int64_t ldb, const void *x, int64_t
     /* several runs of columns a workgroup where that leaves five per compute unit */    \
     int64_t ct = tiles * runs / 1280;                                                    \
     ct = ct < 1 ? 1 : ct > 4 ? 4 : ct;                                                   \
-    const size_t lds = (size_t)16 * F * ((r / 8) | 1) * 16;                              \
+    const size_t lds = (size_t)16 * F * rank_pitch(r);                                   \
     lora_expand_wide_kernel<NS, F><<<(unsigned)(tiles * ((runs + ct - 1) / ct)),         \
                                      kLoraThreads, lds, stream>>>(p, (int)ct);           \
     return hipGetLastError();                                                            \
