@@ -1056,14 +1056,18 @@ __device__ __forceinline__ void store8(uint16_t *row, int64_t c, int64_t N, cons
 
 constexpr int kCombineThreads = 256;
 constexpr int kCombineCols = 512;   // columns of a wave
+// Workgroups of one launch: a grid of 2^32 threads or more is not refused but
+// wraps, so larger batches take several launches.
+constexpr int64_t kCombineBlocks = int64_t(1) << 23;
 
 __global__ __launch_bounds__(kCombineThreads) void combine_kernel(
     const uint16_t *__restrict__ y, int64_t R, const float *__restrict__ weights,
     const int32_t *__restrict__ positions, const uint16_t *base, int64_t T, int k, int64_t N,
-    uint16_t *out) {   // out may be base: each lane reads its columns first
+    uint16_t *out,   // may be base: each lane reads its columns first
+    int64_t block0) {
   const int lane = threadIdx.x & 63;
   const int64_t chunks = (N + kCombineCols - 1) / kCombineCols;
-  const int64_t unit = (int64_t)blockIdx.x * (kCombineThreads / 64) +
+  const int64_t unit = (block0 + blockIdx.x) * (kCombineThreads / 64) +
                        __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int64_t t = unit / chunks;
   if (t >= T) return;
@@ -1088,11 +1092,15 @@ hipError_t launch_combine(const void *y, int64_t R, const float *weights, const 
                           const void *base, int64_t T, int32_t k, int64_t N, void *out,
                           hipStream_t stream) {
   const int64_t units = T * ((N + kCombineCols - 1) / kCombineCols);
-  const int64_t per = kCombineThreads / 64;
-  combine_kernel<<<(unsigned)((units + per - 1) / per), kCombineThreads, 0, stream>>>(
-      static_cast<const uint16_t *>(y), R, weights, positions, static_cast<const uint16_t *>(base),
-      T, k, N, static_cast<uint16_t *>(out));
-  return hipGetLastError();
+  const int64_t per = kCombineThreads / 64, blocks = (units + per - 1) / per;
+  for (int64_t b = 0; b < blocks; b += kCombineBlocks) {
+    const int64_t n = blocks - b < kCombineBlocks ? blocks - b : kCombineBlocks;
+    combine_kernel<<<(unsigned)n, kCombineThreads, 0, stream>>>(
+        static_cast<const uint16_t *>(y), R, weights, positions,
+        static_cast<const uint16_t *>(base), T, k, N, static_cast<uint16_t *>(out), b);
+    if (hipError_t e = hipGetLastError()) return e;
+  }
+  return hipSuccess;
 }
 
 // Combine, backward: dy[pos] = bf16(w * d), dw = <d, y[pos]> (fp32, a fixed
@@ -1106,11 +1114,11 @@ __global__ __launch_bounds__(kCombineThreads) void combine_backward_kernel(
     const uint16_t *__restrict__ d_out, const uint16_t *__restrict__ y, int64_t R,
     const float *__restrict__ weights, const int32_t *__restrict__ positions,
     const int32_t *__restrict__ n_used, int64_t T, int k, int64_t N, uint16_t *__restrict__ dy,
-    float *__restrict__ dw) {
+    float *__restrict__ dw, int64_t t0) {
   constexpr int J = 8;
   __shared__ float sums[kCombineThreads / 64][J];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int64_t t = blockIdx.x;
+  const int64_t t = t0 + blockIdx.x;
   if (t < T) {
     for (int j0 = 0; j0 < k; j0 += J) {
       float acc[J];
@@ -1149,6 +1157,7 @@ __global__ __launch_bounds__(kCombineThreads) void combine_backward_kernel(
       __syncthreads();
     }
   }
+  if (t0) return;   // the first launch zeroes the rows past the used ones
   const int64_t used = max(*n_used, 0);
   const float zero[8] = {0, 0, 0, 0, 0, 0, 0, 0};
   for (int64_t p = used + blockIdx.x; p < R; p += gridDim.x)
@@ -1160,10 +1169,14 @@ hipError_t launch_combine_backward(const void *d_out, const void *y, int64_t R,
                                    const int32_t *n_used, int64_t T, int32_t k, int64_t N,
                                    void *dy, float *dw, hipStream_t stream) {
   const int64_t blocks = T > 0 ? T : (R < 1024 ? R : 1024);
-  combine_backward_kernel<<<(unsigned)blocks, kCombineThreads, 0, stream>>>(
-      static_cast<const uint16_t *>(d_out), static_cast<const uint16_t *>(y), R, weights,
-      positions, n_used, T, k, N, static_cast<uint16_t *>(dy), dw);
-  return hipGetLastError();
+  for (int64_t t = 0; t < blocks; t += kCombineBlocks) {
+    const int64_t n = blocks - t < kCombineBlocks ? blocks - t : kCombineBlocks;
+    combine_backward_kernel<<<(unsigned)n, kCombineThreads, 0, stream>>>(
+        static_cast<const uint16_t *>(d_out), static_cast<const uint16_t *>(y), R, weights,
+        positions, n_used, T, k, N, static_cast<uint16_t *>(dy), dw, t);
+    if (hipError_t e = hipGetLastError()) return e;
+  }
+  return hipSuccess;
 }
 
 }  // namespace fp8blk
