@@ -82,11 +82,17 @@ __device__ __forceinline__ int row_larger(float v) {
 }
 
 // e^(v - peak) for v <= peak: the difference first, so that logits of any size
-// (a row of the type's lowest value among them) leave it small, then one product
-// and the hardware exponential: 2 |v - peak| 2^-24 of the term and 1 ulp.
-// v = -inf gives 0.
+// (a row of the type's lowest value among them) leave it small.  The hardware's
+// 2^y takes the rounded y = d log2 e; what e^d has beyond it, d - y ln 2, is tiny and
+// added to first order.  That leaves 3 units of 2^-24 and the constant's 0.05 |d|,
+// not |d| for y's rounding.  Where 2^y is 0 the correction can be of any size, an
+// infinity or (v = -inf) NaN: the bounds make a number of it.  NaN stays NaN.
 __device__ __forceinline__ float exp_from(float v, float peak) {
-  return __builtin_amdgcn_exp2f((v - peak) * 0x1.715476p+0f);   // log2 e
+  const float d = v - peak;
+  const float y = d * 0x1.715476p+0f;                                    // log2 e
+  const float e = __builtin_amdgcn_exp2f(y);
+  const float rest = __builtin_amdgcn_fmed3f(fmaf(y, -0x1.62e43p-1f, d), -1.0f, 1.0f);   // ln 2
+  return fmaf(e, rest, e);
 }
 
 // Element c of lane `sub` of a row: VEC consecutive experts per load.
@@ -185,9 +191,10 @@ __device__ __forceinline__ void store_row(T *row, int E, int sub, const float *v
 // fixed order, so results do not vary between runs; counts are integer LDS
 // atomics.  The workgroup's sums go to `part` and route_finish_kernel adds them,
 // except when one workgroup does all rows.
-// Measured: 131072 x 256 fp32, k = 8, with the loss: 47 us (2.9 TB/s of logits;
-// the vector ALU bounds it: 78 us with the rounds alone), finish 6 us; 4096 x 32:
-// 4.9 and 3.7 us; 16 x 256, one workgroup: 3.6 us.
+// Measured: 131072 x 256 fp32, k = 8, with the loss: 49-50 us (2.7 TB/s of logits;
+// the vector ALU bounds it: 78 us with the rounds alone, 47 with exponentials of
+// one uncorrected product), finish 6 us; 4096 x 32: 4.9 and 3.8 us; 16 x 256, one
+// workgroup: 3.6 us.
 constexpr int kRouteMaxThreads = 1024;
 constexpr int kRouteMaxWaves = kRouteMaxThreads / 64;
 constexpr int kRouteMaxBlocks = 256;
