@@ -510,7 +510,7 @@ static_assert(kRouteMaxBlocks <= kFinishThreads, "one entry of live rows a threa
 // The counts carry no gradient.  g enters as c_e minus the mean count: p sums
 // to one, so the constant cancels exactly in dl and not in the rounding.
 // The k values on S reach their lanes through LDS, each wave its own rows.
-// Bound by HBM: 131072 x 256 fp32 54 us (5.1 TB/s of logits in and gradients
+// Bound by HBM: 131072 x 256 fp32 57 us (4.7 TB/s of logits in and gradients
 // out); 4096 x 32: 4 us.
 struct RouteBackArgs {
   const void *logits;
@@ -616,7 +616,8 @@ __global__ __launch_bounds__(kBackThreads) void route_backward_kernel(RouteBackA
 #pragma unroll
     for (int c = 0; c < V; ++c) {
       const int e = expert_of<LPR, VEC>(c, sub);
-      d[c] = v[c] * inv * (g[c] - inner) + (e < a.E ? mine[e] : 0.0f);
+      // (not a product with 0: g and inner can be infinite or NaN)
+      d[c] = live ? v[c] * inv * (g[c] - inner) + (e < a.E ? mine[e] : 0.0f) : 0.0f;
     }
     __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
     __builtin_amdgcn_wave_barrier();
