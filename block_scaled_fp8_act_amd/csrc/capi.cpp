@@ -529,7 +529,7 @@ fp8blk_status fp8blk_lora_add(const void *base_bf16, int64_t base_stride, const 
       too_big(T, x_stride) || too_big(T, out_stride) || too_big(int64_t(L) * r, K) ||
       too_big(int64_t(L) * r, N) ||
       (base_bf16 && (base_stride < N || too_big(T, base_stride))) ||
-      (base_bf16 == out_bf16 && base_stride != out_stride) ||
+      (base_bf16 && base_bf16 == out_bf16 && base_stride != out_stride) ||
       // tiles times the runs of 64 columns (or K ranges, or rank pieces) of a launch
       (T / 16 + L + 64) > kMaxRows / (N / 64 + 256))
     return FP8BLK_ERR_SHAPE;
