@@ -1015,9 +1015,20 @@ def moe_experts(x, routing, gate_up_q, gate_up_s, down_q, down_s, base=None):
     """The routed experts of a mixture-of-experts layer: x's rows listed by
     expert and quantized, the gate/up product, SwiGLU, the down product, and
     the weighted sum back to the tokens, on top of ``base`` (the shared
-    expert's output).  Scale formats as the weights'."""
-    k = routing.ids.shape[1]
-    groups = group_rows(routing.ids, gate_up_q.shape[0])
+    expert's output).  Scale formats as the weights'; the routing is that of x's
+    rows over the weights' experts."""
+    (T, k), E = routing.ids.shape, gate_up_q.shape[0]
+    if x.dim() != 2 or x.shape[0] != T:
+        raise ValueError(f"x has shape {tuple(x.shape)}, the routing is of {T} rows")
+    if down_q.shape[0] != E or (routing.counts is not None and routing.counts.numel() != E):
+        raise ValueError("the routing and the weights have different numbers of experts")
+    if gate_up_q.shape[2] != x.shape[1]:
+        raise ValueError("x and gate_up_q disagree on K")
+    if gate_up_q.shape[1] != 2 * down_q.shape[2]:
+        raise ValueError("gate_up_q's rows are not twice down_q's columns")
+    if base is not None:
+        _shape_eq(base, (T, down_q.shape[1]), "base")
+    groups = group_rows(routing.ids, E)
     fmt = "ue8m0" if _is_e8m0(gate_up_s) else "float"
     # rows past the last used one belong to no expert; no product reads them
     x_q, x_s = act_quant_group(x.index_select(0, groups.order // k), fmt)
