@@ -530,8 +530,7 @@ fp8blk_status fp8blk_lora_add(const void *base_bf16, int64_t base_stride, const 
       too_big(int64_t(L) * r, N) ||
       (base_bf16 && (base_stride < N || too_big(T, base_stride))) ||
       (base_bf16 && base_bf16 == out_bf16 && base_stride != out_stride) ||
-      // tiles times the runs of 64 columns (or K ranges, or rank pieces) of a launch
-      (T / 16 + L + 64) > kMaxRows / (N / 64 + 256))
+      !fp8blk::lora_fits(T, K, N, r, L))
     return FP8BLK_ERR_SHAPE;
   if (work && !workspace) return FP8BLK_ERR_NULL;
   if (work && workspace_bytes < fp8blk::lora_workspace_bytes(T, K, r, L, order != nullptr))

@@ -90,6 +90,7 @@ hipError_t launch_combine_backward(const void *d_out, const void *y, int64_t R,
                                    void *dy, float *dw, hipStream_t stream);
 
 // Low-rank adapters (lora_kernels.hip).
+bool lora_fits(int64_t T, int64_t K, int64_t N, int32_t r, int32_t L);
 size_t lora_workspace_bytes(int64_t T, int64_t K, int32_t r, int32_t L, bool listed);
 hipError_t launch_lora_add(const void *base, int64_t ldb, const void *x, int64_t ldx,
                            const void *a, const void *b, const int32_t *ids, const float *scale,

@@ -727,7 +727,41 @@ size_t align256(size_t n) { return (n + 255) / 256 * 256; }
 // h of the tiles, split: 64 lanes' 16 bytes per 16 rows, 32 ranks and part.
 size_t split_bytes(int64_t tiles, int32_t r) { return (size_t)tiles * 4 * rank_steps(r) * kStepBytes; }
 
+// Columns of a run of the larger batches' expand kernel: 16 times its F.
+int run_cols(int32_t r) { return r <= 32 ? 128 : 64; }
+
+// Workgroups of a batch's launches and the columns' runs of one of the last.
+struct LoraGrid {
+  int64_t shrink, join, expand, ct;
+};
+LoraGrid lora_grid(int64_t T, int64_t K, int64_t N, int32_t r, int L) {
+  LoraGrid g{};
+  if (T <= kDirectRows) {
+    const int64_t tiles = max_tiles(T, L, kTileRows);
+    g.shrink = tiles * ((r + 15) / 16) * split_of(T, K, r, L);
+    g.expand = tiles * ((N + kSmallCols - 1) / kSmallCols);
+    return g;
+  }
+  const int64_t tiles = max_tiles(T, L, kWideRows);
+  const int64_t runs = (N + run_cols(r) - 1) / run_cols(r);
+  g.shrink = max_tiles(T, L, shrink_rows(T)) * split_of(T, K, r, L);
+  g.join = tiles * rank_steps(r);
+  // several runs of columns a workgroup where that leaves five per compute unit
+  g.ct = tiles * runs / 1280;
+  g.ct = g.ct < 1 ? 1 : g.ct > 4 ? 4 : g.ct;
+  g.expand = tiles * ((runs + g.ct - 1) / g.ct);
+  return g;
+}
+
 }  // namespace
+
+// Whether every launch stays below 2^32 threads (a larger grid wraps).
+bool lora_fits(int64_t T, int64_t K, int64_t N, int32_t r, int32_t L) {
+  if (T == 0) return true;
+  const LoraGrid g = lora_grid(T, K, N, r, L);
+  constexpr int64_t most = ((int64_t(1) << 32) - 1) / (2 * kLoraThreads);   // (shrink: 512)
+  return g.shrink <= most && g.join <= 2 * most && g.expand <= 2 * most;
+}
 
 size_t lora_workspace_bytes(int64_t T, int64_t K, int32_t r, int32_t L, bool listed) {
   size_t n = align256(sizeof(float) * (size_t)split_of(T, K, r, L) * T * r);
@@ -769,14 +803,12 @@ hipError_t launch_lora_add(const void *base, int64_t ldb, const void *x, int64_t
   char *w = static_cast<char *>(work);
   p.h = reinterpret_cast<float *>(w);
   w += align256(sizeof(float) * (size_t)p.S * T * r);
+  const LoraGrid grid = lora_grid(T, K, N, r, L);
   if (T <= kDirectRows) {
-    const int64_t tiles = max_tiles(T, L, kTileRows);
-    const int pieces = (r + 15) / 16;
-    lora_shrink_kernel<<<(unsigned)(tiles * pieces * p.S), kLoraThreads, 0, stream>>>(p);
+    lora_shrink_kernel<<<(unsigned)grid.shrink, kLoraThreads, 0, stream>>>(p);
     if (hipError_t e = hipGetLastError()) return e;
     const size_t lds = (size_t)rank_steps(r) * kStepBytes + (size_t)kSmallCols * rank_pitch(r);
-    lora_expand_kernel<<<(unsigned)(tiles * ((N + kSmallCols - 1) / kSmallCols)), kLoraThreads,
-                         lds, stream>>>(p);
+    lora_expand_kernel<<<(unsigned)grid.expand, kLoraThreads, lds, stream>>>(p);
     return hipGetLastError();
   }
   const int64_t tiles = max_tiles(T, L, kWideRows);
@@ -797,7 +829,7 @@ hipError_t launch_lora_add(const void *base, int64_t ldb, const void *x, int64_t
     p.order = ord;
     p.offsets = off;
   }
-  const unsigned gs = (unsigned)(max_tiles(T, L, shrink_rows(T)) * p.S);
+  const unsigned gs = (unsigned)grid.shrink;
 #define FP8BLK_SHRINK(W, NR)                                                                 \
   (shrink_rows(T) == kWideRows                                                               \
        ? (lora_shrink_wide_kernel<4 / W, W, W, NR><<<gs, 256, 0, stream>>>(p), hipSuccess)   \
@@ -809,25 +841,19 @@ hipError_t launch_lora_add(const void *base, int64_t ldb, const void *x, int64_t
   else FP8BLK_SHRINK(2, 8);
 #undef FP8BLK_SHRINK
   if (hipError_t e = hipGetLastError()) return e;
-  lora_join_kernel<<<(unsigned)(tiles * rank_steps(r)), kLoraThreads, 0, stream>>>(p);
+  lora_join_kernel<<<(unsigned)grid.join, kLoraThreads, 0, stream>>>(p);
   if (hipError_t e = hipGetLastError()) return e;
 #define FP8BLK_EXPAND(NS, F)                                                              \
-  do {                                                                                   \
-    const int64_t runs = (N + 16 * F - 1) / (16 * F);                                    \
-    /* several runs of columns a workgroup where that leaves five per compute unit */    \
-    int64_t ct = tiles * runs / 1280;                                                    \
-    ct = ct < 1 ? 1 : ct > 4 ? 4 : ct;                                                   \
-    const size_t lds = (size_t)16 * F * rank_pitch(r);                                   \
-    lora_expand_wide_kernel<NS, F><<<(unsigned)(tiles * ((runs + ct - 1) / ct)),         \
-                                     kLoraThreads, lds, stream>>>(p, (int)ct);           \
-    return hipGetLastError();                                                            \
-  } while (0)
+  (lora_expand_wide_kernel<NS, F><<<(unsigned)grid.expand, kLoraThreads, lds, stream>>>(   \
+      p, (int)grid.ct))
+  const size_t lds = (size_t)run_cols(r) * rank_pitch(r);
   if (r <= 16) FP8BLK_EXPAND(0, 8);
-  if (r <= 32) FP8BLK_EXPAND(1, 8);
-  if (r <= 64) FP8BLK_EXPAND(2, 4);
-  if (r <= 128) FP8BLK_EXPAND(4, 4);
-  FP8BLK_EXPAND(8, 4);
+  else if (r <= 32) FP8BLK_EXPAND(1, 8);
+  else if (r <= 64) FP8BLK_EXPAND(2, 4);
+  else if (r <= 128) FP8BLK_EXPAND(4, 4);
+  else FP8BLK_EXPAND(8, 4);
 #undef FP8BLK_EXPAND
+  return hipGetLastError();
 }
 
 }  // namespace fp8blk

@@ -510,7 +510,10 @@ FP8BLK_API fp8blk_status fp8blk_moe_combine_backward(
  *   out_bf16 [T,N], row stride out_stride, out; may be base_bf16 (with the
  *       same stride), and rows without adapter are then left alone.
  * K a positive multiple of 128, r a multiple of 8 up to FP8BLK_MAX_RANK,
- * 1 <= L <= FP8BLK_MAX_GROUPS; strides at least the rows' widths. */
+ * 1 <= L <= FP8BLK_MAX_GROUPS; strides at least the rows' widths.  A batch whose
+ * launches would need 2^32 threads is refused (FP8BLK_ERR_SHAPE): with tiles =
+ * min(T, T / 64 + L + 1), or T / 16 instead of T / 64 for T <= 64, sizes pass
+ * while tiles * (N + 256) < 2^31 and tiles * (r + 32) < 2^29. */
 FP8BLK_API size_t fp8blk_lora_add_workspace_bytes(int64_t T, int64_t K, int32_t r, int32_t L,
                                                   int listed);
 FP8BLK_API fp8blk_status fp8blk_lora_add(const void *base_bf16, int64_t base_stride,
