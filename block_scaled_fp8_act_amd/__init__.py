@@ -707,6 +707,12 @@ def _bytes(t):
     return t.numel() * t.element_size() if t is not None else 0
 
 
+def _need_work(t):
+    """A caller's workspace: contiguous, so that its size is what it covers."""
+    if t is not None:
+        _need(t, "workspace", (t.dtype,))
+
+
 # Each operator's call of the library, its arguments checked: the low-level entry
 # points check every buffer, the wrappers what the caller gave them.
 
@@ -742,6 +748,7 @@ def fp8blk_moe_route(logits, mask, renormalize, loss_coef, ids, weights, counts,
             _need(t, name, dtype)
             if t.numel() != 1:
                 raise ValueError(f"{name} holds one value")
+    _need_work(workspace)
     _same_device(logits, mask, ids, weights, counts, rows, loss, workspace)
     _route_call(logits, mask, k, bool(renormalize), loss_coef, ids, weights, counts, rows, loss,
                 workspace)
@@ -802,6 +809,7 @@ def fp8blk_group_rows(ids, order, positions, offsets, workspace=None):
     R = ids.numel()
     if order.numel() != R or positions.numel() != R:
         raise ValueError("order and positions have an entry per row")
+    _need_work(workspace)
     _same_device(ids, order, positions, offsets, workspace)
     _group_call(ids, offsets.numel() - 1, order, positions, offsets, workspace)
 
@@ -902,6 +910,7 @@ def fp8blk_lora_add(base, x, a, b, ids, scale, groups, out, workspace):
     x, may be column slices of wider matrices.  ``workspace`` holds
     fp8blk_lora_add_workspace_bytes(T, K, r, L, listed) bytes."""
     strides = _lora_in(base, x, a, b, ids, scale, groups, out)
+    _need_work(workspace)
     _same_device(x, workspace)
     _lora_call(base, x, a, b, ids, scale, groups, out, workspace, strides)
 
