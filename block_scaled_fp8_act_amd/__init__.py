@@ -773,6 +773,8 @@ def _route_back_in(logits, routing, d_weights, d_loss):
         if routing.rows is None:
             raise ValueError("d_loss needs a routing that computed the loss")
         _need(routing.rows, "routing.rows", _I32)
+        if routing.rows.numel() != 1:
+            raise ValueError("routing.rows holds one value")
 
 
 def _route_back_call(logits, routing, d_weights, d_loss, d_logits):

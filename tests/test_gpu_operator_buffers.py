@@ -33,3 +33,15 @@ def test_workspaces_that_are_not_contiguous():
     fb.fp8blk_group_rows(i32(T), i32(T), i32(T), i32(E + 1), work)
     fb.fp8blk_lora_add(None, bf(70, 128), bf(2, 8, 128), bf(2, 16, 8), i32(70), None, None, bf(70, 16), work)
     torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("rows", [0, 2])
+def test_routing_rows_is_one_value(rows):
+    x = torch.randn(4, 8, device=dev())
+    r = fb.moe_route(x, 2, loss_coef=0.1)
+    r = r._replace(rows=torch.zeros(8, dtype=torch.int32, device=dev())[8 - rows:])
+    one = torch.ones(1, device=dev())
+    with pytest.raises(ValueError, match="rows"):
+        fb.moe_route_backward(x, r, d_loss=one)
+    with pytest.raises(ValueError, match="rows"):
+        fb.fp8blk_moe_route_backward(x, r, None, one, torch.empty_like(x))
