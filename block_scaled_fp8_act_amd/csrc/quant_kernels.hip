@@ -553,27 +553,30 @@ hipError_t launch_act_quant_static(const void *x, int64_t M, int64_t K, const fl
   return hipGetLastError();
 }
 
+// A workgroup per row.  A grid of 2^32 threads or more is not refused but wraps, so
+// more rows than 2^23 take several launches.
 hipError_t launch_rowwise_quant(const void *x, int64_t R, int64_t K, void *q, float *s,
                                 hipStream_t stream) {
   const int64_t chunks = (K / 8 + kRowThreads - 1) / kRowThreads;  // 16-byte loads per thread
-  const auto *xp = static_cast<const uint16_t *>(x);
-  auto *qp = static_cast<uint8_t *>(q);
-  if (chunks <= 2)
-    hipLaunchKernelGGL(rowwise_quant_kernel<2>, dim3((unsigned)R), dim3(kRowThreads), 0, stream,
-                       xp, K, qp, s);
-  else if (chunks <= 4)
-    hipLaunchKernelGGL(rowwise_quant_kernel<4>, dim3((unsigned)R), dim3(kRowThreads), 0, stream,
-                       xp, K, qp, s);
-  else if (chunks <= 8)
-    hipLaunchKernelGGL(rowwise_quant_kernel<8>, dim3((unsigned)R), dim3(kRowThreads), 0, stream,
-                       xp, K, qp, s);
-  else if (chunks <= 16)
-    hipLaunchKernelGGL(rowwise_quant_kernel<16>, dim3((unsigned)R), dim3(kRowThreads), 0, stream,
-                       xp, K, qp, s);
-  else
-    hipLaunchKernelGGL(rowwise_quant_kernel<0>, dim3((unsigned)R), dim3(kRowThreads), 0, stream,
-                       xp, K, qp, s);
-  return hipGetLastError();
+  constexpr int64_t most = int64_t(1) << 23;
+  for (int64_t r = 0; r < R; r += most) {
+    const dim3 rows((unsigned)(R - r < most ? R - r : most)), threads(kRowThreads);
+    const auto *xp = static_cast<const uint16_t *>(x) + r * K;
+    auto *qp = static_cast<uint8_t *>(q) + r * K;
+    float *sp = s + r;
+    if (chunks <= 2)
+      hipLaunchKernelGGL(rowwise_quant_kernel<2>, rows, threads, 0, stream, xp, K, qp, sp);
+    else if (chunks <= 4)
+      hipLaunchKernelGGL(rowwise_quant_kernel<4>, rows, threads, 0, stream, xp, K, qp, sp);
+    else if (chunks <= 8)
+      hipLaunchKernelGGL(rowwise_quant_kernel<8>, rows, threads, 0, stream, xp, K, qp, sp);
+    else if (chunks <= 16)
+      hipLaunchKernelGGL(rowwise_quant_kernel<16>, rows, threads, 0, stream, xp, K, qp, sp);
+    else
+      hipLaunchKernelGGL(rowwise_quant_kernel<0>, rows, threads, 0, stream, xp, K, qp, sp);
+    if (hipError_t e = hipGetLastError()) return e;
+  }
+  return hipSuccess;
 }
 
 hipError_t launch_weight_quant(const void *w, int64_t N, int64_t K, void *q, float *s,
