@@ -988,7 +988,8 @@ def moe_combine(y, weights, positions, base=None):
 
 def moe_combine_backward(d_out, y, weights, positions, offsets):
     """(d_y, d_weights) of moe_combine; the last entry of offsets is the number
-    of y's rows in use (rows past it get 0)."""
+    of y's rows in use (rows past it get 0).  positions names each row in use
+    once, as group_rows gives them: one that no slot names is left unwritten."""
     _combine_back_in(d_out, y, weights, positions, offsets)
     _same_device(d_out, y, weights, positions, offsets)
     d_y, d_weights = torch.empty_like(y), torch.empty_like(weights)

@@ -13,12 +13,17 @@
 //
 // Bound: HBM traffic (x once, base and out once, the adapters in use once); at
 // ranks up to 256 the products are far below the matrix cores' rate.  Measured,
-// bf16 from HBM, all launches: 16 rows of 16 adapters, 4096 x 4096, r = 16: 9 us
-// (latency; 4.6 MB); 515 rows of 32, 7168 -> 1536, r = 64: 22 us; 8192 rows of
-// 8, 7168 -> 18432, r = 32: 149 us (723 MB, 4.9 TB/s); 4099 rows of 5, 14336 ->
-// 4096, r = 128: 74 us (208 MB, 2.8 TB/s: the shrink kernel's passes through LDS
+// bf16 from HBM, all launches: 16 rows of 16 adapters, 4096 x 4096, r = 16: 10 us
+// (latency; 4.6 MB); 515 rows of 32, 7168 -> 1536, r = 64: 23 us; 8192 rows of
+// 8, 7168 -> 18432, r = 32: 152 us (723 MB, 4.8 TB/s); 4099 rows of 5, 14336 ->
+// 4096, r = 128: 75 us (208 MB, 2.8 TB/s: the shrink kernel's passes through LDS
 // and its products, which grow with the rank, take longer there than x's way
 // from HBM).
+//
+// Grids and K ranges are sized for a tile of every adapter of the pool, used or
+// not: the host does not know which are.  A pool far larger than the batch's use
+// of it so leaves compute units without work in the shrink kernel (one adapter in
+// use of 256, 515 rows: 9 workgroups).
 #include "fp8blk_device.h"
 #include "fp8blk_launch.h"
 
@@ -425,9 +430,11 @@ __global__ __launch_bounds__(kLoraThreads) void lora_expand_kernel(LoraArgs p) {
 // of K a stage, loaded with eight neighbouring lanes on a row's 128 bytes, two
 // stages ahead in registers.  WR x WN waves take MR row fragments and NR rank
 // fragments each.  h goes out in fp32 parts, one per K range.  Now 25 us there
-// (4.7 TB/s of x), and 36 us at 4099 x 14336, r = 128 (3.2 TB/s), where the time
+// (4.7 TB/s of x), and 35 us at 4099 x 14336, r = 128 (3.3 TB/s), where the time
 // grows with the rank and not with what is in flight: four stages ahead, more
-// workgroups, or a K range per XCD measured no faster.
+// workgroups, or a K range per XCD measured no faster.  No unit is full there (LDS
+// 32 %, matrix cores 25 % of the busy cycles, no bank conflicts): a workgroup's
+// writes, barrier, reads and products follow one another.
 template <int WR, int WN, int MR, int NR>
 __global__ __launch_bounds__(WR * WN * 64) void lora_shrink_wide_kernel(LoraArgs p) {
   constexpr int ROWS = WR * MR * 16, THREADS = WR * WN * 64;
@@ -569,12 +576,13 @@ __global__ __launch_bounds__(kLoraThreads) void lora_join_kernel(LoraArgs p) {
 // lane's F fragments are F consecutive columns: base and out move as 32 F
 // contiguous bytes of a row per 16 lanes.  h stays in registers for all ct
 // runs; B's run goes through LDS (it is contiguous in memory, but a fragment
-// takes a row per lane).  B and base are loaded one run
-// ahead in registers (base in the run it is used in: 117 against 109 us below).
+// takes a row per lane).  B and base are loaded one run ahead in registers (base
+// in the run it is used in: 117 against 109 us below).
 // F = 8 up to rank 32, where base and out are all that counts, and 4 above,
 // where its fewer registers let more workgroups overlap (8192 rows, N = 18432,
 // r = 32: 117 us with 8, 127 with 4; 4099 rows, N = 4096, r = 128: 29 and 27).
-// Now 110 us (5.5 TB/s of base and out) and 25 us (2.7 TB/s).
+// Now 110 us (5.5 TB/s of base and out) and 24 us (2.8 TB/s; vector ALU 46 %, matrix
+// cores 29 %, LDS 24 % of the busy cycles).
 template <int NS, int F>   // up to NS steps of 32 ranks (NS = 0: up to 16 ranks)
 __global__ __launch_bounds__(kLoraThreads) void lora_expand_wide_kernel(LoraArgs p, int ct) {
   extern __shared__ __align__(16) uint8_t lds[];   // B's run: [fragment][16] rows
@@ -698,7 +706,11 @@ namespace {
 // eight waves: A is read from L2 once per 128 rows, which is what bounds the
 // kernel there (4099 rows, K = 14336, r = 128: 45 -> 36 us; 4096 rows, K = 4096,
 // r = 64: 14.5 -> 12.0).  With fewer rows the larger tiles leave compute units
-// idle (2048 rows, K = 14336, r = 128: 20.6 us in tiles of 64, 25.3 in 128).
+// idle (2048 rows, K = 14336, r = 128: 20.6 us in tiles of 64, 25.3 in 128).  With
+// many adapters of few rows each they cost more than they save (K = 4096, r = 16:
+// 4096 rows of 512 adapters 30.3 us against 22.4 in 64, of 64 adapters 11.6 against
+// 9.4, 8192 rows of 200 19.2 against 17.8), but the pool's size, all that is known
+// here, does not tell how many are in use.
 constexpr int64_t kBigBatch = 4096;
 int shrink_rows(int64_t T) { return T >= kBigBatch ? 128 : kWideRows; }
 

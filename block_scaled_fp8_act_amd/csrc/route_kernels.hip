@@ -191,10 +191,12 @@ __device__ __forceinline__ void store_row(T *row, int E, int sub, const float *v
 // fixed order, so results do not vary between runs; counts are integer LDS
 // atomics.  The workgroup's sums go to `part` and route_finish_kernel adds them,
 // except when one workgroup does all rows.
-// Measured: 131072 x 256 fp32, k = 8, with the loss: 49-50 us (2.7 TB/s of logits;
-// the vector ALU bounds it: 78 us with the rounds alone, 47 with exponentials of
-// one uncorrected product), finish 6 us; 4096 x 32: 4.9 and 3.8 us; 16 x 256, one
-// workgroup: 3.6 us.
+// Measured: 131072 x 256 fp32, k = 8, with the loss: 49-51 us (2.7 TB/s of logits;
+// the vector ALU bounds it: 600 instructions for four rows keep it active 79 % of
+// the compute units' busy cycles; 78 us with the rounds alone, 47 with exponentials
+// of one uncorrected product), finish 6 us; 4096 x 32: 4.8 and 4 us; 16 x 256, one
+// workgroup: 3.6 us.  The more experts a row chooses, the more often it has over 16
+// candidates, and one such row takes its wave through both ways.
 constexpr int kRouteMaxThreads = 1024;
 constexpr int kRouteMaxWaves = kRouteMaxThreads / 64;
 constexpr int kRouteMaxBlocks = 256;
@@ -510,7 +512,7 @@ static_assert(kRouteMaxBlocks <= kFinishThreads, "one entry of live rows a threa
 // The counts carry no gradient.  g enters as c_e minus the mean count: p sums
 // to one, so the constant cancels exactly in dl and not in the rounding.
 // The k values on S reach their lanes through LDS, each wave its own rows.
-// Bound by HBM: 131072 x 256 fp32 57 us (4.7 TB/s of logits in and gradients
+// Bound by HBM: 131072 x 256 fp32 57-59 us (4.6 TB/s of logits in and gradients
 // out); 4096 x 32: 4 us.
 struct RouteBackArgs {
   const void *logits;
@@ -770,7 +772,8 @@ hipError_t launch_route_backward(const void *logits, bool bf16, int64_t T, int32
 // come first (group_count_kernel), past 16 workgroups their sums over workgroups,
 // a wave per group (group_scan_kernel), then the places: two or three launches,
 // each of them bound by latency at these sizes.  Measured: 128 rows of 256 groups
-// 3.5 us; 8192 of 9 4.4 + 5.1 us; 1M of 256 4.3 + 4.1 + 9.8 us (17 MB).
+// 3.7 us; 8192 of 9 4.0 + 4.4 us; 1M of 256 4.0 + 2.8 + 10.4 us (17 MB; the places:
+// ballots, scans and writes one after another in one workgroup per compute unit).
 constexpr int kGroupThreads = 1024;
 constexpr int kGroupWaves = kGroupThreads / 64;
 constexpr int64_t kGroupOneBlock = 2048;
@@ -964,9 +967,10 @@ namespace {
 
 // Steps of 64 rows a wave.  Up to 2048 rows one workgroup does all; up to 16
 // workgroups of 1024 rows their counts are a launch of their own and each adds
-// them up (8192 rows: 11 us in one workgroup, bound by its ballots, 8 so);
-// beyond, three launches: 4 steps (256 workgroups at 1M rows, one per compute
-// unit), 16 past that.
+// them up.  Both sides, a call among others in a graph, one workgroup and so:
+// 3000 rows 6.0 and 6.3 us of 9 groups, 8.0 and 7.4 of 256; 8192 rows 9.4 and 7.0,
+// 13.2 and 8.6; 15000 rows 14.8 and 7.1, 21.4 and 8.5.  Beyond, three launches: 4
+// steps (256 workgroups at 1M rows, one per compute unit), 16 past that.
 int group_steps(int64_t R) {
   if (R <= kGroupOneBlock) return R <= kGroupThreads ? 1 : 2;
   if (R <= (int64_t)kDirectBlocks * kGroupThreads) return 1;
@@ -1115,9 +1119,11 @@ hipError_t launch_combine(const void *y, int64_t R, const float *weights, const 
 // order), one workgroup per token; each column of d is read once per 8 slots
 // and stays in registers while the slots' rows stream past.  Rows of dy past
 // the last used one (n_used, in device memory) are zeroed.  Dropped slots get
-// dw = 0.  d_y is stored through the caches: non-temporal stores beside the
-// non-temporal loads measured slower (203 against 191 us at 4096 tokens of 8
-// rows, N = 7168: 1.0 GB, 5.2 TB/s).
+// dw = 0.  A row below n_used that no slot names is not written, and one that two
+// slots name gets either's gradient.  d_y is stored through the caches:
+// non-temporal stores beside the non-temporal loads measured slower (203 against
+// 191 us at 4096 tokens of 8 rows, N = 7168: 1.0 GB, 5.2 TB/s; 212 us in the
+// kernel trace).
 __global__ __launch_bounds__(kCombineThreads) void combine_backward_kernel(
     const uint16_t *__restrict__ d_out, const uint16_t *__restrict__ y, int64_t R,
     const float *__restrict__ weights, const int32_t *__restrict__ positions,

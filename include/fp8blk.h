@@ -484,7 +484,7 @@ FP8BLK_API fp8blk_status fp8blk_moe_combine(const void *y_bf16, int64_t R, const
 /* Gradients of fp8blk_moe_combine (that of base is d_out itself).
  *   rows_used [1] int32 in (device memory): the rows of y in use come first,
  *       e.g. offsets[G] of fp8blk_group_rows; positions names each of them
- *       once
+ *       once (the gradient of one that no slot names is not written)
  *   d_y_bf16 [R,N] out: bf16(weights[t,j] * d_out[t]) at positions[t,j]; rows
  *       from rows_used on get 0
  *   d_weights [T,k] fp32 out: <d_out[t], y[positions[t,j]]>, 0 for slots
