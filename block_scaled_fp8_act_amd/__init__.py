@@ -83,6 +83,8 @@ __all__ = [
     "fp8blk_lora_add", "moe_route", "moe_route_backward", "group_rows", "moe_combine",
     "moe_combine_backward", "lora_add", "lora_linear", "moe_experts",
     "MAX_GROUPS", "MAX_TOPK", "MAX_RANK",
+    "ACTS", "fp8blk_gated_linear", "fp8blk_gated_linear_backward", "gated_linear",
+    "gated_linear_backward",
 ]
 
 BLOCK = 128
@@ -150,6 +152,9 @@ def load_library() -> ctypes.CDLL:
         "fp8blk_moe_combine_backward": [vp, vp, i64, vp, vp, vp, i64, i32, i64, vp, vp, vp],
         "fp8blk_lora_add": [vp, i64, vp, i64, vp, vp, vp, vp, vp, vp, i64, i64, i64, i32, i32,
                             vp, i64, vp, sz, vp],
+        "fp8blk_gated_linear": [vp, i64, vp, ci, ci, i64, i64, i64, vp, vp, vp, sz, vp],
+        "fp8blk_gated_linear_backward": [vp, vp, i64, vp, vp, ci, ci, i64, i64, i64, vp, vp, vp,
+                                         sz, vp],
     }
     for name, args in sigs.items():
         fn = getattr(lib, name)
@@ -160,7 +165,10 @@ def load_library() -> ctypes.CDLL:
         getattr(lib, name).restype = ctypes.c_size_t
     for name, args in {"fp8blk_moe_route_workspace_bytes": [i64, i32],
                        "fp8blk_group_rows_workspace_bytes": [i64, i32],
-                       "fp8blk_lora_add_workspace_bytes": [i64, i64, i32, i32, ci]}.items():
+                       "fp8blk_lora_add_workspace_bytes": [i64, i64, i32, i32, ci],
+                       "fp8blk_gated_linear_workspace_bytes": [i64, i64, i64, i64],
+                       "fp8blk_gated_linear_backward_workspace_bytes": [i64, i64, i64, i64, ci,
+                                                                        ci]}.items():
         getattr(lib, name).argtypes = args
         getattr(lib, name).restype = sz
     lib.fp8blk_status_string.argtypes = [ctypes.c_int]
@@ -654,10 +662,10 @@ _BF16 = (torch.bfloat16,)
 _MASK = (torch.bool, torch.uint8)
 
 
-def _rows_2d(t, name):
-    """A bf16 matrix whose rows are contiguous and a fixed stride apart; the stride."""
-    if not isinstance(t, torch.Tensor) or t.dtype != torch.bfloat16:
-        raise TypeError(f"{name} must be a bfloat16 torch.Tensor")
+def _rows_2d(t, name, dtypes=(torch.bfloat16,)):
+    """A matrix whose rows are contiguous and a fixed stride apart; the stride."""
+    if not isinstance(t, torch.Tensor) or t.dtype not in dtypes:
+        raise TypeError(f"{name} must be a torch.Tensor of a type in {dtypes}")
     if not t.is_cuda:
         raise ValueError(f"{name} must be a device (cuda/hip) tensor")
     if t.dim() != 2:
@@ -1048,3 +1056,101 @@ def moe_experts(x, routing, gate_up_q, gate_up_s, down_q, down_s, base=None):
     h_q, h_s = swiglu_act_quant(h, fmt)
     y = grouped_block_gemm(h_q, h_s, down_q, down_s, groups.offsets)
     return moe_combine(y, routing.weights, groups.positions, base)
+
+
+# --------------------------------------------------------------------------
+# gated projections in 16 bits
+
+_HALF = {torch.bfloat16: 1, torch.float16: 2}      # FP8BLK_BF16, FP8BLK_F16
+_HALF_TYPES = tuple(_HALF)
+ACTS = {"silu": 0, "gelu": 1, "gelu_tanh": 2}      # FP8BLK_SILU, ...
+
+
+def _act(act):
+    if act not in ACTS:
+        raise ValueError(f"act must be one of {tuple(ACTS)}, got {act!r}")
+    return ACTS[act]
+
+
+def _gated_in(x, w, *more):
+    """Row stride of x, sizes (M, I, K); ``more`` are (tensor, name, columns in
+    units of I) of x's rows."""
+    ldx = _rows_2d(x, "x", _HALF_TYPES)
+    _need(w, "w", (x.dtype,), 2)
+    M, K = x.shape
+    if w.shape[1] != K:
+        raise ValueError("x and w disagree on K")
+    if K == 0:
+        raise ValueError("K must be positive")
+    if w.shape[0] % 2:
+        raise ValueError("w must hold 2I rows, the gates' first")
+    I = w.shape[0] // 2
+    for t, name, wide in more:
+        if t is not None:
+            _need(t, name, (x.dtype,), 2)
+            _shape_eq(t, (M, wide * I), name)
+    _same_device(x, w, *(t for t, _, _ in more))
+    return ldx, M, I, K
+
+
+def _gated_call(x, ldx, w, act, M, I, K, h, factors, workspace):
+    _check(load_library().fp8blk_gated_linear(
+        x.data_ptr(), ldx, w.data_ptr(), _HALF[x.dtype], act, M, I, K, h.data_ptr(), _at(factors),
+        _at(workspace), _bytes(workspace), _stream()), "fp8blk_gated_linear")
+
+
+def fp8blk_gated_linear(x, w, act, h, factors, workspace=None):
+    """The gated projections into h [M,I]; ``factors`` [M,2I] (for the backward
+    pass) may be None, x may be a column slice of a wider matrix.  ``workspace``
+    holds fp8blk_gated_linear_workspace_bytes(M, I, K, x's row stride) bytes."""
+    ldx, M, I, K = _gated_in(x, w, (h, "h", 1), (factors, "factors", 2))
+    _need_work(workspace)
+    _same_device(x, workspace)
+    _gated_call(x, ldx, w, _act(act), M, I, K, h, factors, workspace)
+
+
+def _gated_back_call(d_h, x, ldx, w, factors, act, M, I, K, d_x, d_w, workspace):
+    _check(load_library().fp8blk_gated_linear_backward(
+        d_h.data_ptr(), x.data_ptr(), ldx, w.data_ptr(), _at(factors), _HALF[x.dtype], act, M, I, K,
+        _at(d_x), _at(d_w), _at(workspace), _bytes(workspace), _stream()),
+        "fp8blk_gated_linear_backward")
+
+
+def fp8blk_gated_linear_backward(d_h, x, w, factors, act, d_x, d_w, workspace=None):
+    """Gradients into d_x [M,K] and d_w [2I,K], either may be None; ``factors``
+    None: the projections are computed again.  ``workspace`` holds
+    fp8blk_gated_linear_backward_workspace_bytes(M, I, K, x's row stride,
+    d_x wanted, d_w wanted) bytes."""
+    ldx, M, I, K = _gated_in(x, w, (d_h, "d_h", 1), (factors, "factors", 2))
+    for t, like, name in ((d_x, x, "d_x"), (d_w, w, "d_w")):
+        if t is not None:
+            _need(t, name, (x.dtype,), 2)
+            _shape_eq(t, like.shape, name)
+    _need_work(workspace)
+    _same_device(x, d_x, d_w, workspace)
+    _gated_back_call(d_h, x, ldx, w, factors, _act(act), M, I, K, d_x, d_w, workspace)
+
+
+def gated_linear(x, w, act="silu", save=False):
+    """h = act(x Wg^T) * (x Wu^T), w [2I,K] with the gate rows first, in x's type
+    (bf16 or fp16).  With ``save`` also the factors that
+    gated_linear_backward takes (otherwise it computes the projections again)."""
+    ldx, M, I, K = _gated_in(x, w)
+    act = _act(act)
+    h = x.new_empty((M, I))
+    factors = x.new_empty((M, 2 * I)) if save else None
+    need = load_library().fp8blk_gated_linear_workspace_bytes(M, I, K, ldx)
+    _gated_call(x, ldx, w, act, M, I, K, h, factors, _work(need, x))
+    return (h, factors) if save else h
+
+
+def gated_linear_backward(d_h, x, w, factors=None, act="silu", need_x=True, need_w=True):
+    """(d_x, d_w) of gated_linear; None in the place of one that is not needed."""
+    ldx, M, I, K = _gated_in(x, w, (d_h, "d_h", 1), (factors, "factors", 2))
+    act = _act(act)
+    d_x = x.new_empty((M, K)) if need_x else None
+    d_w = torch.empty_like(w) if need_w else None
+    need = load_library().fp8blk_gated_linear_backward_workspace_bytes(M, I, K, ldx, bool(need_x),
+                                                                       bool(need_w))
+    _gated_back_call(d_h, x, ldx, w, factors, act, M, I, K, d_x, d_w, _work(need, x))
+    return d_x, d_w

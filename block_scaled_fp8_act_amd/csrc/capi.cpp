@@ -546,4 +546,66 @@ fp8blk_status fp8blk_lora_add(const void *base_bf16, int64_t base_stride, const 
                                           static_cast<hipStream_t>(stream)));
 }
 
+// ---- gated projections -----------------------------------------------------
+
+namespace {
+constexpr int64_t kMaxWidth = int64_t(1) << 22;   // 256 rows stay below 2^32 bytes
+bool bad_gated(int type, int act, int64_t M, int64_t I, int64_t K, int64_t x_stride) {
+  return (type != FP8BLK_BF16 && type != FP8BLK_F16) || act < FP8BLK_SILU ||
+         act > FP8BLK_GELU_TANH || bad_rows(M) || I < 0 || 2 * I > kMaxWidth || K < 1 ||
+         K > kMaxWidth || x_stride < K || x_stride > kMaxWidth || !fp8blk::gated_fits(M, I, K);
+}
+}  // namespace
+
+size_t fp8blk_gated_linear_workspace_bytes(int64_t M, int64_t I, int64_t K, int64_t x_stride) {
+  if (bad_gated(FP8BLK_BF16, FP8BLK_SILU, M, I, K, x_stride) || M == 0 || I == 0) return 0;
+  return fp8blk::gated_workspace_bytes(M, I, K, x_stride);
+}
+
+fp8blk_status fp8blk_gated_linear(const void *x, int64_t x_stride, const void *w, int type, int act,
+                                  int64_t M, int64_t I, int64_t K, void *h, void *factors,
+                                  void *workspace, size_t workspace_bytes, void *stream) {
+  const bool work = M > 0 && I > 0;
+  if (work && (!x || !w || !h)) return FP8BLK_ERR_NULL;
+  if (bad_gated(type, act, M, I, K, x_stride)) return FP8BLK_ERR_SHAPE;
+  const size_t need = work ? fp8blk::gated_workspace_bytes(M, I, K, x_stride) : 0;
+  if (need > 0 && !workspace) return FP8BLK_ERR_NULL;
+  if (workspace_bytes < need) return FP8BLK_ERR_SHAPE;
+  if (work && (any_misaligned({x, w, h, factors}, 16) || (need > 0 && misaligned(workspace))))
+    return FP8BLK_ERR_ALIGN;
+  if (fp8blk_status d = check_device()) return d;
+  if (!work) return FP8BLK_OK;
+  const fp8blk::GatedCall c{x, w, x_stride, M, I, K, type == FP8BLK_BF16, act};
+  return launched(
+      fp8blk::launch_gated(c, h, factors, workspace, static_cast<hipStream_t>(stream)));
+}
+
+size_t fp8blk_gated_linear_backward_workspace_bytes(int64_t M, int64_t I, int64_t K,
+                                                    int64_t x_stride, int want_d_x, int want_d_w) {
+  if (bad_gated(FP8BLK_BF16, FP8BLK_SILU, M, I, K, x_stride) || M == 0 || I == 0) return 0;
+  return fp8blk::gated_backward_workspace_bytes(M, I, K, x_stride, want_d_x != 0, want_d_w != 0);
+}
+
+fp8blk_status fp8blk_gated_linear_backward(const void *d_h, const void *x, int64_t x_stride,
+                                           const void *w, const void *factors, int type, int act,
+                                           int64_t M, int64_t I, int64_t K, void *d_x, void *d_w,
+                                           void *workspace, size_t workspace_bytes, void *stream) {
+  const bool work = M > 0 && I > 0 && (d_x || d_w);
+  if (work && (!d_h || !x || !w)) return FP8BLK_ERR_NULL;
+  if (bad_gated(type, act, M, I, K, x_stride)) return FP8BLK_ERR_SHAPE;
+  const size_t need = work ? fp8blk::gated_backward_workspace_bytes(M, I, K, x_stride,
+                                                                    d_x != nullptr, d_w != nullptr)
+                           : 0;
+  if (need > 0 && !workspace) return FP8BLK_ERR_NULL;
+  if (workspace_bytes < need) return FP8BLK_ERR_SHAPE;
+  if (any_misaligned({d_x, d_w}, 16) ||
+      (work && (any_misaligned({d_h, x, w, factors}, 16) || (need > 0 && misaligned(workspace)))))
+    return FP8BLK_ERR_ALIGN;
+  if (fp8blk_status d = check_device()) return d;
+  if (!d_x && !d_w) return FP8BLK_OK;
+  const fp8blk::GatedCall c{x, w, x_stride, M, I, K, type == FP8BLK_BF16, act};
+  return launched(fp8blk::launch_gated_backward(c, d_h, factors, d_x, d_w, workspace,
+                                                static_cast<hipStream_t>(stream)));
+}
+
 }  // extern "C"

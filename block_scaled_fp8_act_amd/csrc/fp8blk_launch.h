@@ -2,6 +2,7 @@
 #pragma once
 
 #include <hip/hip_runtime.h>
+#include <stddef.h>
 #include <stdint.h>
 
 namespace fp8blk {
@@ -97,5 +98,22 @@ hipError_t launch_lora_add(const void *base, int64_t ldb, const void *x, int64_t
                            const int32_t *order, const int32_t *offsets, int64_t T, int64_t K,
                            int64_t N, int32_t r, int32_t L, void *out, int64_t ldo, void *work,
                            hipStream_t stream);
+
+// Gated projections and their gradients (gated_kernels.hip).
+enum GatedAct { kSilu = 0, kGelu = 1, kGeluTanh = 2 };
+struct GatedCall {
+  const void *x, *w;      // [M, K] with row stride ldx; [2I, K]
+  int64_t ldx, M, I, K;
+  bool bf16;              // else fp16
+  int act;
+};
+bool gated_fits(int64_t M, int64_t I, int64_t K);
+size_t gated_workspace_bytes(int64_t M, int64_t I, int64_t K, int64_t ldx);
+hipError_t launch_gated(const GatedCall &c, void *h, void *factors, void *work,
+                        hipStream_t stream);
+size_t gated_backward_workspace_bytes(int64_t M, int64_t I, int64_t K, int64_t ldx, bool dx,
+                                      bool dw);
+hipError_t launch_gated_backward(const GatedCall &c, const void *dh, const void *factors, void *dx,
+                                 void *dw, void *work, hipStream_t stream);
 
 }  // namespace fp8blk

@@ -1,0 +1,242 @@
+// Tiled products of 16-bit floats for gfx950, shared by the gated projections
+// (gated_kernels.hip) and the 4-bit weights' batches (w4_kernels.hip):
+//   D[m, n] = sum_k A[m, k] B[n, k],   fp32 sums.
+//
+// An operand lies in memory with the summed index contiguous (kRows: a row of
+// the operand per row of memory) or with it going down (kCols: a row of the
+// operand is a column of memory), so that a layer's forward product, the
+// gradient of its input and that of its weights all read their operands where
+// they are.  Both kinds pass through LDS by direct-to-LDS loads, 64 of K a
+// stage, two stages:
+//   kRows  [rows][64 of K], 128 bytes a row, 16-byte chunk c of row r kept at
+//          c ^ swz_f(r); a fragment is two ds_read_b128 a lane.
+//   kCols  [64 of K][rows], 32-byte pairs p of K row k kept at p ^ col_f(k); a
+//          fragment is four ds_read_b64_tr_b16 a lane, which transpose 4 x 16
+//          values among 16 lanes.
+// A lane (r = lane & 15, q = lane >> 4) of a matrix instruction holds 8 values of
+// K of the operand's row r.  A stage is two instructions deep, and since both
+// operands agree, instruction h takes K = 16 q + 8 h + 0..7.
+#pragma once
+
+#include "fp8blk_device.h"
+
+namespace fp8blk {
+
+typedef unsigned v4u __attribute__((ext_vector_type(4)));
+typedef unsigned v2u __attribute__((ext_vector_type(2)));
+typedef short v4s __attribute__((ext_vector_type(4)));
+typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
+typedef _Float16 v8h __attribute__((ext_vector_type(8)));
+
+namespace t16 {
+
+// 16 and 8 bytes at any even address (gfx950's global loads and stores take those).
+typedef unsigned v4u_any __attribute__((ext_vector_type(4), aligned(2)));
+typedef unsigned v2u_any __attribute__((ext_vector_type(2), aligned(2)));
+
+// The 16-bit types: fp32 -> bits (round to nearest even), bits -> fp32, product.
+struct Bf16 {
+  static __device__ __forceinline__ uint32_t bits(float f) {
+    return __builtin_bit_cast(uint16_t, (__bf16)f);
+  }
+  static __device__ __forceinline__ float value(uint32_t b) { return __uint_as_float(b << 16); }
+  static __device__ __forceinline__ v4f mfma(v4u a, v4u b, v4f c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8bf, a),
+                                                   __builtin_bit_cast(v8bf, b), c, 0, 0, 0);
+  }
+};
+struct F16 {
+  static __device__ __forceinline__ uint32_t bits(float f) {
+    return __builtin_bit_cast(uint16_t, (_Float16)f);
+  }
+  static __device__ __forceinline__ float value(uint32_t b) {
+    return (float)__builtin_bit_cast(_Float16, (uint16_t)b);
+  }
+  static __device__ __forceinline__ v4f mfma(v4u a, v4u b, v4f c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(v8h, a),
+                                                  __builtin_bit_cast(v8h, b), c, 0, 0, 0);
+  }
+};
+template <typename T>
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+  return T::bits(lo) | (T::bits(hi) << 16);
+}
+
+typedef __attribute__((address_space(3))) void lds_void;
+typedef __attribute__((address_space(3))) v4s lds_v4s;
+
+constexpr int kK = 64;              // of K a stage
+constexpr uint32_t kOut = 0xfffffff0u;   // an offset past every resource: reads zeros
+
+// Loads through a buffer resource read zeros past its byte count.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc(const void *base, int64_t bytes) {
+  const uint32_t n = bytes <= 0 ? 0u : (uint32_t)min(bytes, (int64_t)kOut);
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(base), (short)0, (int)n, 0x00020000);
+}
+__device__ __forceinline__ void dma16(__amdgpu_buffer_rsrc_t r, uint32_t off, void *lds) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void *)lds, 16, (int)off, 0, 0, 0);
+}
+
+// As in the fp8 tiles: 16 lanes on one chunk of 16 consecutive rows meet no bank twice.
+__device__ __forceinline__ int swz_f(int row) { return ((row & 3) << 1) | ((row >> 2) & 1); }
+// 32 lanes of a transposing read take 32 bytes of K rows k, k + 1, k + 2, k + 3 and
+// of those 16 further: eight different pairs of the 256 bytes that the banks span.
+__device__ __forceinline__ int col_f(int k) { return (k & 3) | (((k >> 4) & 1) << 2); }
+
+// A workgroup's tile: WM x WN waves of FM x 4 fragments of 16 x 16.
+template <int WM, int WN, int FM>
+struct Shape {
+  static constexpr int kWaves = WM * WN, kThreads = kWaves * 64;
+  static constexpr int TM = WM * FM * 16, TN = WN * 64;
+  static constexpr int kFM = FM, kWM = WM, kWN = WN;
+  static constexpr int kDmaA = TM / 8 / kWaves, kDmaB = TN / 8 / kWaves;   // 1 KB loads a wave
+  static_assert(kDmaA * 8 * kWaves == TM && kDmaB * 8 * kWaves == TN, "tile and loads");
+  struct Smem {
+    uint8_t a[2][TM * kK * 2];
+    uint8_t b[2][TN * kK * 2];
+  };
+};
+// 256 x 256 on 8 waves (a wave 128 x 64), and 128 x 128 on 4 (64 x 64) for grids
+// that the large tile would leave mostly idle.
+using Large = Shape<2, 4, 8>;
+using Small = Shape<2, 2, 4>;
+
+// An operand in memory: `rows` of it along the output, `k` along the sum, both
+// counted from p; `ld` elements from one row of memory to the next.  Rows of
+// memory are 16-byte aligned and whole 16-byte chunks (ld and the contiguous
+// extent are multiples of 8).
+struct Operand {
+  const uint16_t *p;
+  int64_t ld;
+  int64_t rows, k;
+};
+
+// The loads of one operand of ROWS rows, kDma of 1 KB a wave, into a stage.
+enum Kind { kRows, kCols };
+template <Kind KIND, int ROWS, int kDma>
+struct Loader {
+  uint32_t off[kDma];
+  uint32_t chunk[kDma];   // kRows: the lane's chunk of the stage's K
+  int wave;
+  Operand o;
+
+  __device__ __forceinline__ void init(const Operand &op, int wave_, int lane) {
+    o = op;
+    wave = wave_;
+#pragma unroll
+    for (int i = 0; i < kDma; ++i) {
+      if constexpr (KIND == kRows) {
+        const int row = 8 * (kDma * wave + i) + (lane >> 3);
+        chunk[i] = (lane & 7) ^ swz_f(row);
+        off[i] = row < o.rows ? (uint32_t)(row * o.ld * 2) + chunk[i] * 16 : kOut;
+      } else {
+        constexpr int kChunks = ROWS / 8;     // 16-byte chunks of a K row
+        const int at = (kDma * wave + i) * 64 + lane;
+        const int k = at / kChunks, c = (at % kChunks) ^ (col_f(at / kChunks) << 1);
+        chunk[i] = k;
+        off[i] = c * 8 < o.rows ? (uint32_t)(k * o.ld * 2) + c * 16 : kOut;
+      }
+    }
+  }
+  // K values past the last one read as zeros, and so do rows past the last.
+  __device__ __forceinline__ void issue(int step, uint8_t *stage) const {
+    const int64_t k0 = (int64_t)step * kK;
+    const int64_t left = o.k - k0;     // > 0
+    if constexpr (KIND == kRows) {
+      const __amdgpu_buffer_rsrc_t r = rsrc(o.p + k0, ((o.rows - 1) * o.ld + left) * 2);
+      const uint32_t chunks = (uint32_t)min(left, (int64_t)kK) >> 3;
+#pragma unroll
+      for (int i = 0; i < kDma; ++i)
+        dma16(r, chunk[i] < chunks ? off[i] : kOut, stage + (kDma * wave + i) * 1024);
+    } else {
+      const __amdgpu_buffer_rsrc_t r =
+          rsrc(o.p + k0 * o.ld, ((min(left, (int64_t)kK) - 1) * o.ld + o.rows) * 2);
+#pragma unroll
+      for (int i = 0; i < kDma; ++i) dma16(r, off[i], stage + (kDma * wave + i) * 1024);
+    }
+  }
+};
+
+struct Frag {
+  v4u h[2];
+};
+
+// The fragment of 16 rows from `row0` of a stage of ROWS rows.
+template <Kind KIND, int ROWS>
+__device__ __forceinline__ Frag read_frag(const uint8_t *stage, int row0, int lane) {
+  Frag f;
+  const int r = lane & 15, q = lane >> 4;
+  if constexpr (KIND == kRows) {
+    const int row = row0 + r, s = swz_f(row);
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+      f.h[h] = *reinterpret_cast<const v4u *>(stage + row * 128 + (((2 * q + h) ^ s) << 4));
+  } else {
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const int k = 16 * q + 8 * h + 4 * j + (r >> 2);
+        const uint8_t *at = stage + k * (ROWS * 2) + (((row0 >> 4) ^ col_f(k)) << 5) + (r & 3) * 8;
+        const v4s v = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s *)at);
+        const v2u u = __builtin_bit_cast(v2u, v);
+        f.h[h][2 * j] = u[0];
+        f.h[h][2 * j + 1] = u[1];
+      }
+  }
+  return f;
+}
+
+// The wave's sums acc[mi][ni][r] = D[16 mi + (lane & 15)][16 ni + 4 (lane >> 4) + r]
+// of its FM x 4 fragments, over `steps` stages from `step0`.  LoadB has
+// issue(step, stage) as Loader does; with REGB it goes through registers: fetch(step)
+// before a step's products, put(stage) after them.
+template <typename T, typename S, Kind KA, Kind KB, typename LoadA, typename LoadB>
+__device__ __forceinline__ void multiply(const LoadA &la, const LoadB &lb, int step0, int steps,
+                                         typename S::Smem &sm, v4f (&acc)[S::kFM][4]) {
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int arow = wave / S::kWN * (S::kFM * 16), brow = wave % S::kWN * 64;
+  constexpr int FM = S::kFM;
+#pragma unroll
+  for (int mi = 0; mi < FM; ++mi)
+#pragma unroll
+    for (int ni = 0; ni < 4; ++ni) acc[mi][ni] = v4f{0, 0, 0, 0};
+  auto issue = [&](int s) {
+    la.issue(step0 + s, sm.a[s & 1]);
+    lb.issue(step0 + s, sm.b[s & 1]);
+  };
+  issue(0);
+  for (int s = 0; s < steps; ++s) {
+    __builtin_amdgcn_s_waitcnt(0);
+    __syncthreads();
+    if (s + 1 < steps) issue(s + 1);
+    const uint8_t *a = sm.a[s & 1], *b = sm.b[s & 1];
+    Frag bf[4];
+#pragma unroll
+    for (int ni = 0; ni < 4; ++ni) bf[ni] = read_frag<KB, S::TN>(b, brow + ni * 16, lane);
+#pragma unroll
+    for (int mi = 0; mi < FM; ++mi) {
+      const Frag af = read_frag<KA, S::TM>(a, arow + mi * 16, lane);
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int ni = 0; ni < 4; ++ni) acc[mi][ni] = T::mfma(bf[ni].h[h], af.h[h], acc[mi][ni]);
+    }
+  }
+}
+
+// Tile (tm, tn) of workgroup `bid` of tiles_m x tiles_n: workgroups go round-robin
+// over the 8 XCDs, so each XCD gets a consecutive run of tiles, in groups of 8
+// tile rows whose neighbours share operands in its L2.
+__device__ __forceinline__ void tile_of(int bid, int tiles_m, int tiles_n, int &tm, int &tn) {
+  const int total = tiles_m * tiles_n, per = total >> 3, more = total & 7, x = bid & 7;
+  const int at = x * per + min(x, more) + (bid >> 3);
+  const int group = at / (8 * tiles_n), first = group * 8, in = at - group * 8 * tiles_n;
+  const int height = min(tiles_m - first, 8);
+  tm = first + in % height;
+  tn = in / height;
+}
+
+}  // namespace t16
+}  // namespace fp8blk

@@ -407,6 +407,7 @@ FP8BLK_API fp8blk_status fp8_grouped_block_gemm_ue8m0(const void *x_q, const uin
 
 #define FP8BLK_F32 0
 #define FP8BLK_BF16 1
+#define FP8BLK_F16 2            /* gated projections and 4-bit weights */
 #define FP8BLK_MAX_GROUPS 1024  /* experts, groups or adapters of one call */
 #define FP8BLK_MAX_TOPK 32
 #define FP8BLK_MAX_RANK 256
@@ -524,6 +525,54 @@ FP8BLK_API fp8blk_status fp8blk_lora_add(const void *base_bf16, int64_t base_str
                                          int64_t K, int64_t N, int32_t r, int32_t L,
                                          void *out_bf16, int64_t out_stride, void *workspace,
                                          size_t workspace_bytes, void *stream);
+
+/* ------------------------------------------------------------------------
+ * The gated projections of a feed-forward block in 16 bits, with their
+ * gradients: g = x Wg^T, u = x Wu^T, h = act(g) * u.
+ *
+ * Conventions as in the section before: rows of any width start at any even
+ * address, base pointers are 16-byte aligned, workspaces likewise, nothing
+ * synchronises, and the same inputs give the same bits.
+ *   type: FP8BLK_BF16 or FP8BLK_F16, of every matrix of the call
+ *   act: FP8BLK_SILU (g / (1 + e^-g)), FP8BLK_GELU (g times the normal
+ *       distribution's function) or FP8BLK_GELU_TANH (its form by tanh,
+ *       g (1 + tanh(sqrt(2 / pi) (g + 0.044715 g^3))) / 2)
+ *   x [M,K], row stride x_stride elements
+ *   w [2I,K]: the I gate rows first, then the I up rows (the order of
+ *       fp8_swiglu_act_quant's columns)
+ * Sums are kept in fp32; g, u and act(g) enter what follows unrounded.
+ * 1 <= K <= 2^22, 0 <= I <= 2^21, K <= x_stride <= 2^22, M < 2^31, and fewer
+ * than 2^23 tiles of 256 x 256 in any of the products (FP8BLK_ERR_SHAPE). */
+
+#define FP8BLK_SILU 0
+#define FP8BLK_GELU 1
+#define FP8BLK_GELU_TANH 2
+
+/*   h [M,I] out
+ *   factors [M,2I] out, or NULL (not wanted): what the gradient of h is
+ *       multiplied by, u act'(g) in columns [0, I) and act(g) in [I, 2I), each
+ *       rounded once; kept for the backward pass. */
+FP8BLK_API size_t fp8blk_gated_linear_workspace_bytes(int64_t M, int64_t I, int64_t K,
+                                                      int64_t x_stride);
+FP8BLK_API fp8blk_status fp8blk_gated_linear(const void *x, int64_t x_stride, const void *w,
+                                             int type, int act, int64_t M, int64_t I, int64_t K,
+                                             void *h, void *factors, void *workspace,
+                                             size_t workspace_bytes, void *stream);
+
+/* Gradients of fp8blk_gated_linear: dgu = (d_h u act'(g), d_h act(g)) rounded
+ * once to type, d_x = dgu W, d_w = dgu^T x.
+ *   d_h [M,I] in
+ *   factors [M,2I] in, as the forward call wrote it, or NULL: g and u are then
+ *       computed again (act is read only in this case)
+ *   d_x [M,K], d_w [2I,K] out, either may be NULL (not wanted)
+ * With M = 0 d_w, and with I = 0 d_x, is cleared. */
+FP8BLK_API size_t fp8blk_gated_linear_backward_workspace_bytes(int64_t M, int64_t I, int64_t K,
+                                                               int64_t x_stride, int want_d_x,
+                                                               int want_d_w);
+FP8BLK_API fp8blk_status fp8blk_gated_linear_backward(
+    const void *d_h, const void *x, int64_t x_stride, const void *w, const void *factors, int type,
+    int act, int64_t M, int64_t I, int64_t K, void *d_x, void *d_w, void *workspace,
+    size_t workspace_bytes, void *stream);
 
 /* Human-readable name of a status code (static storage, never NULL). */
 FP8BLK_API const char *fp8blk_status_string(int status);
