@@ -85,6 +85,8 @@ __all__ = [
     "MAX_GROUPS", "MAX_TOPK", "MAX_RANK",
     "ACTS", "fp8blk_gated_linear", "fp8blk_gated_linear_backward", "gated_linear",
     "gated_linear_backward",
+    "W4_GROUPS", "W4Weight", "fp8blk_w4_quant", "fp8blk_w4_dequant", "fp8blk_w4_linear",
+    "fp8blk_w4_gated_linear", "w4_quant", "w4_dequant", "w4_linear", "w4_gated_linear",
 ]
 
 BLOCK = 128
@@ -155,6 +157,10 @@ def load_library() -> ctypes.CDLL:
         "fp8blk_gated_linear": [vp, i64, vp, ci, ci, i64, i64, i64, vp, vp, vp, sz, vp],
         "fp8blk_gated_linear_backward": [vp, vp, i64, vp, vp, ci, ci, i64, i64, i64, vp, vp, vp,
                                          sz, vp],
+        "fp8blk_w4_quant": [vp, ci, i64, i64, ci, vp, vp, vp, vp],
+        "fp8blk_w4_dequant": [vp, vp, vp, ci, i64, i64, ci, vp, vp],
+        "fp8blk_w4_linear": [vp, i64, vp, vp, vp, ci, ci, i64, i64, i64, vp, vp, sz, vp],
+        "fp8blk_w4_gated_linear": [vp, i64, vp, vp, vp, ci, ci, ci, i64, i64, i64, vp, vp, sz, vp],
     }
     for name, args in sigs.items():
         fn = getattr(lib, name)
@@ -168,7 +174,9 @@ def load_library() -> ctypes.CDLL:
                        "fp8blk_lora_add_workspace_bytes": [i64, i64, i32, i32, ci],
                        "fp8blk_gated_linear_workspace_bytes": [i64, i64, i64, i64],
                        "fp8blk_gated_linear_backward_workspace_bytes": [i64, i64, i64, i64, ci,
-                                                                        ci]}.items():
+                                                                        ci],
+                       "fp8blk_w4_linear_workspace_bytes": [i64, i64, i64, i64],
+                       "fp8blk_w4_gated_linear_workspace_bytes": [i64, i64, i64, i64]}.items():
         getattr(lib, name).argtypes = args
         getattr(lib, name).restype = sz
     lib.fp8blk_status_string.argtypes = [ctypes.c_int]
@@ -1154,3 +1162,150 @@ def gated_linear_backward(d_h, x, w, factors=None, act="silu", need_x=True, need
                                                                        bool(need_w))
     _gated_back_call(d_h, x, ldx, w, factors, act, M, I, K, d_x, d_w, _work(need, x))
     return d_x, d_w
+
+
+# --------------------------------------------------------------------------
+# 4-bit weights
+
+W4_GROUPS = (32, 64, 128)
+
+
+class W4Weight(NamedTuple):
+    """Weights W[n,k] = (q - z) * s in 4 bits, as w4_linear takes them."""
+    codes: torch.Tensor          # [N, K/2] uint8: two codes q, the even k in the low half
+    scale: torch.Tensor          # [N, K/group] in the weights' type: s
+    zeros: torch.Tensor | None   # [N, K/group] uint8: z (None: 8)
+
+
+def _w4_in(codes, scale, zeros):
+    """Sizes (N, K, group)."""
+    _need(codes, "codes", (torch.uint8,), 2)
+    _need(scale, "scale", _HALF_TYPES, 2)
+    N, K = codes.shape[0], 2 * codes.shape[1]
+    groups = scale.shape[1]
+    if scale.shape[0] != N or groups < 1 or K % groups or K // groups not in W4_GROUPS:
+        raise ValueError(f"scale has shape {tuple(scale.shape)}, which is no scale per group of "
+                         f"{W4_GROUPS} for codes of shape {tuple(codes.shape)}")
+    if zeros is not None:
+        _need(zeros, "zeros", (torch.uint8,), 2)
+        _shape_eq(zeros, scale.shape, "zeros")
+    return N, K, K // groups
+
+
+def _w4_product_in(x, codes, scale, zeros):
+    """Row stride of x, sizes (M, N, K, group)."""
+    N, K, group = _w4_in(codes, scale, zeros)
+    ldx = _rows_2d(x, "x", (scale.dtype,))
+    if x.shape[1] != K:
+        raise ValueError("x and codes disagree on K")
+    _same_device(x, codes, scale, zeros)
+    return ldx, x.shape[0], N, K, group
+
+
+def fp8blk_w4_quant(w, codes, scale, zeros):
+    """Weights w [N,K] to 4 bits into codes, scale and (None: no zero points)
+    zeros; the group is K over scale's columns."""
+    _need(w, "w", (scale.dtype,), 2)
+    N, K, group = _w4_in(codes, scale, zeros)
+    _shape_eq(w, (N, K), "w")
+    _same_device(w, codes, scale, zeros)
+    _check(load_library().fp8blk_w4_quant(w.data_ptr(), _HALF[w.dtype], N, K, group, codes.data_ptr(),
+                                          scale.data_ptr(), _at(zeros), _stream()), "fp8blk_w4_quant")
+
+
+def fp8blk_w4_dequant(codes, scale, zeros, w):
+    """The weights that codes stand for into w [N,K] (scale's type)."""
+    N, K, group = _w4_in(codes, scale, zeros)
+    _need(w, "w", (scale.dtype,), 2)
+    _shape_eq(w, (N, K), "w")
+    _same_device(w, codes, scale, zeros)
+    _check(load_library().fp8blk_w4_dequant(codes.data_ptr(), scale.data_ptr(), _at(zeros),
+                                            _HALF[w.dtype], N, K, group, w.data_ptr(), _stream()),
+           "fp8blk_w4_dequant")
+
+
+def _w4_call(x, sizes, codes, scale, zeros, y, workspace):
+    ldx, M, N, K, group = sizes
+    _check(load_library().fp8blk_w4_linear(
+        x.data_ptr(), ldx, codes.data_ptr(), scale.data_ptr(), _at(zeros), _HALF[x.dtype], group, M,
+        N, K, y.data_ptr(), _at(workspace), _bytes(workspace), _stream()), "fp8blk_w4_linear")
+
+
+def fp8blk_w4_linear(x, codes, scale, zeros, y, workspace=None):
+    """y [M,N] = x W^T with 4-bit weights; zeros may be None, x a column slice of
+    a wider matrix.  ``workspace`` holds fp8blk_w4_linear_workspace_bytes(M, N, K,
+    x's row stride) bytes."""
+    sizes = _w4_product_in(x, codes, scale, zeros)
+    _need(y, "y", (x.dtype,), 2)
+    _shape_eq(y, sizes[1:3], "y")
+    _need_work(workspace)
+    _same_device(x, y, workspace)
+    _w4_call(x, sizes, codes, scale, zeros, y, workspace)
+
+
+def _w4_half(N):
+    if N % 2:
+        raise ValueError("codes must hold 2I rows, the gates' first")
+    return N // 2
+
+
+def _w4_gated_call(x, sizes, codes, scale, zeros, act, h, workspace):
+    ldx, M, N, K, group = sizes
+    _check(load_library().fp8blk_w4_gated_linear(
+        x.data_ptr(), ldx, codes.data_ptr(), scale.data_ptr(), _at(zeros), _HALF[x.dtype], group, act,
+        M, N // 2, K, h.data_ptr(), _at(workspace), _bytes(workspace), _stream()),
+        "fp8blk_w4_gated_linear")
+
+
+def fp8blk_w4_gated_linear(x, codes, scale, zeros, act, h, workspace=None):
+    """h [M,I] = act(x Wg^T) * (x Wu^T) with 4-bit weights [2I,K].  ``workspace``
+    holds fp8blk_w4_gated_linear_workspace_bytes(M, I, K, x's row stride) bytes."""
+    sizes = _w4_product_in(x, codes, scale, zeros)
+    _need(h, "h", (x.dtype,), 2)
+    _shape_eq(h, (sizes[1], _w4_half(sizes[2])), "h")
+    _need_work(workspace)
+    _same_device(x, h, workspace)
+    _w4_gated_call(x, sizes, codes, scale, zeros, _act(act), h, workspace)
+
+
+def w4_quant(w, group=128, zeros=False):
+    """Weights [N,K] (bf16 or fp16) to 4 bits with a scale, and with ``zeros`` a
+    zero point, per ``group`` of K: W4Weight(codes, scale, zeros)."""
+    _need(w, "w", _HALF_TYPES, 2)
+    _same_device(w)
+    N, K = w.shape
+    if group not in W4_GROUPS:
+        raise ValueError(f"group must be one of {W4_GROUPS}, got {group}")
+    if K == 0 or K % group:
+        raise ValueError(f"K must be a positive multiple of the group, got {K}")
+    q = W4Weight(w.new_empty((N, K // 2), dtype=torch.uint8), w.new_empty((N, K // group)),
+                 w.new_empty((N, K // group), dtype=torch.uint8) if zeros else None)
+    fp8blk_w4_quant(w, *q)
+    return q
+
+
+def w4_dequant(codes, scale, zeros=None):
+    """The weights [N,K] that 4-bit codes stand for, in the scales' type."""
+    N, K, _ = _w4_in(codes, scale, zeros)
+    w = scale.new_empty((N, K))
+    fp8blk_w4_dequant(codes, scale, zeros, w)
+    return w
+
+
+def w4_linear(x, codes, scale, zeros=None):
+    """y = x W^T with 4-bit weights (w4_linear(x, *w4_quant(w))), from one row,
+    where it reads a quarter of a 16-bit weight's bytes, to many."""
+    sizes = ldx, M, N, K, _ = _w4_product_in(x, codes, scale, zeros)
+    y = x.new_empty((M, N))
+    need = load_library().fp8blk_w4_linear_workspace_bytes(M, N, K, ldx)
+    _w4_call(x, sizes, codes, scale, zeros, y, _work(need, x))
+    return y
+
+
+def w4_gated_linear(x, codes, scale, zeros=None, act="silu"):
+    """gated_linear with 4-bit weights [2I,K], the gate rows first: h [M,I]."""
+    sizes = ldx, M, N, K, _ = _w4_product_in(x, codes, scale, zeros)
+    h = x.new_empty((M, _w4_half(N)))
+    need = load_library().fp8blk_w4_gated_linear_workspace_bytes(M, N // 2, K, ldx)
+    _w4_gated_call(x, sizes, codes, scale, zeros, _act(act), h, _work(need, x))
+    return h

@@ -21,7 +21,7 @@ CSRC = os.path.join(PKG, "csrc")
 LIBDIR = os.path.join(PKG, "lib")
 LIB = os.path.join(LIBDIR, "libfp8blk.so")
 SOURCES = ["quant_kernels.hip", "gemm_kernels.hip", "route_kernels.hip", "lora_kernels.hip",
-           "gated_kernels.hip", "capi.cpp"]
+           "gated_kernels.hip", "w4_kernels.hip", "capi.cpp"]
 CEIL_LIB = os.path.join(LIBDIR, "libfp8ceil.so")
 CEIL_SOURCES = ["ceiling_kernels.hip"]
 ARCH = "gfx950"

@@ -608,4 +608,94 @@ fp8blk_status fp8blk_gated_linear_backward(const void *d_h, const void *x, int64
                                                 static_cast<hipStream_t>(stream)));
 }
 
+// ---- 4-bit weights ---------------------------------------------------------
+
+namespace {
+bool bad_w4(int type, int group, int64_t rows, int64_t K) {
+  return (type != FP8BLK_BF16 && type != FP8BLK_F16) ||
+         (group != 32 && group != 64 && group != 128) || bad_rows(rows) || K < group ||
+         K > kMaxWidth || K % group != 0;
+}
+bool bad_w4_product(int type, int group, int64_t M, int64_t rows, int64_t K, int64_t x_stride) {
+  return bad_w4(type, group, rows, K) || bad_rows(M) || x_stride < K || x_stride > kMaxWidth ||
+         !fp8blk::w4_fits(M, rows);
+}
+// Arguments of the two products; `need` is the workspace they take.
+fp8blk_status check_w4(const fp8blk::W4Call &c, int type, const void *out, const void *workspace,
+                       size_t workspace_bytes, size_t need) {
+  const bool work = c.M > 0 && c.rows > 0;
+  if (work && (!c.x || !c.codes || !c.scale || !out)) return FP8BLK_ERR_NULL;
+  if (bad_w4_product(type, c.group, c.M, c.rows, c.K, c.ldx)) return FP8BLK_ERR_SHAPE;
+  if (need > 0 && !workspace) return FP8BLK_ERR_NULL;
+  if (workspace_bytes < need) return FP8BLK_ERR_SHAPE;
+  if (work && (any_misaligned({c.x, c.codes, c.scale, c.zeros, out}, 16) ||
+               (need > 0 && misaligned(workspace))))
+    return FP8BLK_ERR_ALIGN;
+  return check_device();
+}
+}  // namespace
+
+fp8blk_status fp8blk_w4_quant(const void *w, int type, int64_t N, int64_t K, int group, void *codes,
+                              void *scale, void *zeros, void *stream) {
+  if (N > 0 && (!w || !codes || !scale)) return FP8BLK_ERR_NULL;
+  if (bad_w4(type, group, N, K)) return FP8BLK_ERR_SHAPE;
+  if (N > 0 && any_misaligned({w, codes, scale, zeros}, 16)) return FP8BLK_ERR_ALIGN;
+  if (fp8blk_status d = check_device()) return d;
+  if (N == 0) return FP8BLK_OK;
+  return launched(fp8blk::launch_w4_quant(w, type == FP8BLK_BF16, N, K, group, codes, scale, zeros,
+                                          static_cast<hipStream_t>(stream)));
+}
+
+fp8blk_status fp8blk_w4_dequant(const void *codes, const void *scale, const void *zeros, int type,
+                                int64_t N, int64_t K, int group, void *w, void *stream) {
+  if (N > 0 && (!w || !codes || !scale)) return FP8BLK_ERR_NULL;
+  if (bad_w4(type, group, N, K)) return FP8BLK_ERR_SHAPE;
+  if (N > 0 && any_misaligned({w, codes, scale, zeros}, 16)) return FP8BLK_ERR_ALIGN;
+  if (fp8blk_status d = check_device()) return d;
+  if (N == 0) return FP8BLK_OK;
+  const fp8blk::W4Call c{nullptr, K, 0, codes, scale, zeros, N, K, group, type == FP8BLK_BF16};
+  return launched(fp8blk::launch_w4_dequant(c, w, static_cast<hipStream_t>(stream)));
+}
+
+size_t fp8blk_w4_linear_workspace_bytes(int64_t M, int64_t N, int64_t K, int64_t x_stride) {
+  if (M == 0 || N == 0 || bad_w4_product(FP8BLK_BF16, 32, M, N, K, x_stride)) return 0;
+  return fp8blk::w4_linear_workspace_bytes(M, N, K, x_stride);
+}
+
+fp8blk_status fp8blk_w4_linear(const void *x, int64_t x_stride, const void *codes,
+                               const void *scale, const void *zeros, int type, int group, int64_t M,
+                               int64_t N, int64_t K, void *y, void *workspace,
+                               size_t workspace_bytes, void *stream) {
+  const fp8blk::W4Call c{x, x_stride, M, codes, scale, zeros, N, K, group, type == FP8BLK_BF16};
+  if (fp8blk_status e = check_w4(c, type, y, workspace, workspace_bytes,
+                                 fp8blk_w4_linear_workspace_bytes(M, N, K, x_stride)))
+    return e;
+  if (M == 0 || N == 0) return FP8BLK_OK;
+  return launched(
+      fp8blk::launch_w4_linear(c, y, workspace, static_cast<hipStream_t>(stream)));
+}
+
+size_t fp8blk_w4_gated_linear_workspace_bytes(int64_t M, int64_t I, int64_t K, int64_t x_stride) {
+  if (M == 0 || I <= 0 || I > kMaxRows / 2 ||
+      bad_w4_product(FP8BLK_BF16, 32, M, 2 * I, K, x_stride))
+    return 0;
+  return fp8blk::w4_gated_workspace_bytes(M, I, K, x_stride);
+}
+
+fp8blk_status fp8blk_w4_gated_linear(const void *x, int64_t x_stride, const void *codes,
+                                     const void *scale, const void *zeros, int type, int group,
+                                     int act, int64_t M, int64_t I, int64_t K, void *h,
+                                     void *workspace, size_t workspace_bytes, void *stream) {
+  // (a negative or too large I stays one through the doubling)
+  const int64_t rows = I < 0 ? -1 : I > kMaxRows / 2 ? kMaxRows + 1 : 2 * I;
+  const fp8blk::W4Call c{x, x_stride, M, codes, scale, zeros, rows, K, group, type == FP8BLK_BF16};
+  if (act < FP8BLK_SILU || act > FP8BLK_GELU_TANH) return FP8BLK_ERR_SHAPE;
+  if (fp8blk_status e = check_w4(c, type, h, workspace, workspace_bytes,
+                                 fp8blk_w4_gated_linear_workspace_bytes(M, I, K, x_stride)))
+    return e;
+  if (M == 0 || I == 0) return FP8BLK_OK;
+  return launched(
+      fp8blk::launch_w4_gated(c, act, h, workspace, static_cast<hipStream_t>(stream)));
+}
+
 }  // extern "C"

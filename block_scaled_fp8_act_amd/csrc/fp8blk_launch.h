@@ -116,4 +116,22 @@ size_t gated_backward_workspace_bytes(int64_t M, int64_t I, int64_t K, int64_t l
 hipError_t launch_gated_backward(const GatedCall &c, const void *dh, const void *factors, void *dx,
                                  void *dw, void *work, hipStream_t stream);
 
+// 4-bit weights (w4_kernels.hip).
+struct W4Call {
+  const void *x;                        // [M, K], row stride ldx
+  int64_t ldx, M;
+  const void *codes, *scale, *zeros;    // [rows, K / 2], [rows, K / group] twice
+  int64_t rows, K;                      // rows: N, or 2I
+  int group;
+  bool bf16;                            // else fp16
+};
+bool w4_fits(int64_t M, int64_t rows);
+hipError_t launch_w4_quant(const void *w, bool bf16, int64_t rows, int64_t K, int group,
+                           void *codes, void *scale, void *zeros, hipStream_t stream);
+hipError_t launch_w4_dequant(const W4Call &c, void *w, hipStream_t stream);
+size_t w4_linear_workspace_bytes(int64_t M, int64_t N, int64_t K, int64_t ldx);
+hipError_t launch_w4_linear(const W4Call &c, void *y, void *work, hipStream_t stream);
+size_t w4_gated_workspace_bytes(int64_t M, int64_t I, int64_t K, int64_t ldx);
+hipError_t launch_w4_gated(const W4Call &c, int act, void *h, void *work, hipStream_t stream);
+
 }  // namespace fp8blk

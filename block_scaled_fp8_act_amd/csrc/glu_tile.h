@@ -1,0 +1,165 @@
+// The gated projections of one tile, for 16-bit weights (gated_kernels.hip) and
+// 4-bit ones (w4_kernels.hip): a wave's columns are half gates and half the ups
+// beside them, so g and u of an output meet in one lane's registers and the
+// activation and the product are the epilogue.
+#pragma once
+
+#include "gated_act.h"
+#include "tile16.h"
+
+namespace fp8blk {
+namespace t16 {
+
+struct GluArgs {
+  const uint16_t *x;
+  int64_t ldx, M, I, K;
+  int tiles_m, tiles_n;
+  int steps, ranges;              // of K
+  float *parts;                   // [ranges][M][2I], ranges > 1
+  int act;
+  uint16_t *h, *factors;          // forward: factors may be NULL
+  const uint16_t *dh;             // gradient: dgu = d_h times the factors
+  uint16_t *dgu;
+  int64_t ld_dgu;                 // >= 2I; the rows end in zeros
+};
+
+// Row of W (counted in its half's rows from the tile's first output) and half of
+// row `row` of the tile: FN / 2 fragments of gates, then of ups, for each wave.
+template <typename S>
+struct PairRow {
+  int half, c;
+  __device__ __forceinline__ explicit PairRow(int row) {
+    constexpr int kHalf = S::kFN * 8;
+    const int in = row % (2 * kHalf);
+    half = in / kHalf;
+    c = row / (2 * kHalf) * kHalf + in % kHalf;
+  }
+};
+
+// Four outputs of row m at column n from their g and u.
+template <typename T, int ACT, bool GRAD>
+__device__ __forceinline__ void glu_store4(const GluArgs &p, int64_t m, int64_t n, v4f g, v4f u) {
+  const int64_t left = p.I - n;
+  float a[4], f[4];
+  if constexpr (GRAD) {
+    float d[4];
+    load4<T>(p.dh + m * p.I + n, d, left);
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      f[r] = d[r] * (u[r] * act_slope<ACT>(g[r]));
+      a[r] = d[r] * act_value<ACT>(g[r]);
+    }
+    uint16_t *row = p.dgu + m * p.ld_dgu;
+    store4<T>(row + n, f, left);
+    store4<T>(row + p.I + n, a, left);
+    if (left <= 4)
+      for (int64_t c = 2 * p.I; c < p.ld_dgu; ++c) row[c] = 0;
+  } else {
+    float h[4];
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      a[r] = act_value<ACT>(g[r]);
+      h[r] = a[r] * u[r];
+    }
+    store4<T>(p.h + m * p.I + n, h, left);
+    if (p.factors) {
+#pragma unroll
+      for (int r = 0; r < 4; ++r) f[r] = u[r] * act_slope<ACT>(g[r]);
+      uint16_t *row = p.factors + m * 2 * p.I;
+      store4<T>(row + n, f, left);
+      store4<T>(row + p.I + n, a, left);
+    }
+  }
+}
+
+template <typename T, typename S, int ACT, bool GRAD>
+__device__ __forceinline__ void glu_store(const GluArgs &p, const v4f (&acc)[S::kFM][S::kFN],
+                                          int64_t m0, int64_t n0, int lane) {
+#pragma unroll
+  for (int mi = 0; mi < S::kFM; ++mi) {
+    const int64_t m = m0 + mi * 16 + (lane & 15);
+    if (m >= p.M) continue;
+#pragma unroll
+    for (int ni = 0; ni < S::kFN / 2; ++ni) {
+      const int64_t n = n0 + ni * 16 + 4 * (lane >> 4);
+      if (n < p.I) glu_store4<T, ACT, GRAD>(p, m, n, acc[mi][ni], acc[mi][ni + S::kFN / 2]);
+    }
+  }
+}
+
+// W::Pair<T, S> loads the tile's rows of the weights: init(w, p, n0, wave, lane).
+template <typename T, typename S, bool GRAD, typename W>
+__global__ __launch_bounds__(S::kThreads) void glu_kernel(GluArgs p, W w) {
+  __shared__ typename S::Smem sm;
+  const int tiles = p.tiles_m * p.tiles_n, range = blockIdx.x / tiles;
+  int tm, tn;
+  tile_of(blockIdx.x - range * tiles, p.tiles_m, p.tiles_n, tm, tn);
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  int64_t m = (int64_t)tm * S::TM, n = (int64_t)tn * (S::TN / 2);
+  Loader<kRows, S::TM, S::kWaves> la;
+  la.init(Operand{p.x + m * p.ldx, p.ldx, min(p.M - m, (int64_t)S::TM), p.K}, wave, lane);
+  typename W::template Pair<T, S> lb;
+  lb.init(w, p, n, wave, lane);
+  const int s0 = (int)((int64_t)p.steps * range / p.ranges);
+  const int s1 = (int)((int64_t)p.steps * (range + 1) / p.ranges);
+  v4f acc[S::kFM][S::kFN];
+  multiply<T, S, kRows, kRows>(la, lb, s0, s1 - s0, sm, acc);
+  m += wave / S::kWN * (S::kFM * 16);
+  n += wave % S::kWN * (S::kFN * 8);
+  if (p.ranges > 1) {
+#pragma unroll
+    for (int mi = 0; mi < S::kFM; ++mi)
+#pragma unroll
+      for (int ni = 0; ni < S::kFN; ++ni) {
+        const int64_t row = m + mi * 16 + (lane & 15);
+        const int64_t col = n + ni % (S::kFN / 2) * 16 + 4 * (lane >> 4);
+        if (row < p.M && col < p.I)
+          store4(p.parts + ((int64_t)range * p.M + row) * 2 * p.I +
+                     (ni >= S::kFN / 2 ? p.I : 0) + col, acc[mi][ni], p.I - col);
+      }
+    return;
+  }
+  if (p.act == kSilu) glu_store<T, S, kSilu, GRAD>(p, acc, m, n, lane);
+  else if (p.act == kGelu) glu_store<T, S, kGelu, GRAD>(p, acc, m, n, lane);
+  else glu_store<T, S, kGeluTanh, GRAD>(p, acc, m, n, lane);
+}
+
+// The outputs of parts, four a thread.
+template <typename T, bool GRAD>
+__global__ __launch_bounds__(256) void glu_join_kernel(GluArgs p) {
+  const int64_t quads = (p.I + 3) / 4, step = p.M * 2 * p.I;
+  for (int64_t at = first_item(); at < p.M * quads; at += all_threads()) {
+    const int64_t m = at / quads, n = (at - m * quads) * 4;
+    const float *q = p.parts + m * 2 * p.I + n;
+    const v4f g = join4(q, p.ranges, step, p.I - n), u = join4(q + p.I, p.ranges, step, p.I - n);
+    if (p.act == kSilu) glu_store4<T, kSilu, GRAD>(p, m, n, g, u);
+    else if (p.act == kGelu) glu_store4<T, kGelu, GRAD>(p, m, n, g, u);
+    else glu_store4<T, kGeluTanh, GRAD>(p, m, n, g, u);
+  }
+}
+
+// Launches for a plan; p's sizes, pointers and act are set.
+template <typename T, bool GRAD, typename W>
+hipError_t launch_glu(GluArgs p, const W &w, hipStream_t stream) {
+  const Plan plan = plan_of(p.M, 2 * p.I, p.K);
+  p.steps = (int)tiles(p.K, kK);
+  p.ranges = plan.ranges;
+  p.tiles_m = (int)tiles(p.M, plan.large ? Large::TM : Small::TM);
+  p.tiles_n = (int)tiles(p.I, (plan.large ? Large::TN : Small::TN) / 2);
+  const dim3 grid((unsigned)p.tiles_m * p.tiles_n * p.ranges);
+  if (plan.large) glu_kernel<T, Large, GRAD, W><<<grid, Large::kThreads, 0, stream>>>(p, w);
+  else glu_kernel<T, Small, GRAD, W><<<grid, Small::kThreads, 0, stream>>>(p, w);
+  if (p.ranges > 1) {
+    if (hipError_t e = hipGetLastError()) return e;
+    glu_join_kernel<T, GRAD><<<groups(p.M * tiles(p.I, 4)), 256, 0, stream>>>(p);
+  }
+  return hipGetLastError();
+}
+inline size_t glu_part_bytes(int64_t M, int64_t I, int64_t K) {
+  const int r = plan_of(M, 2 * I, K).ranges;
+  return r == 1 ? 0 : (size_t)r * M * 2 * I * sizeof(float);
+}
+
+}  // namespace t16
+}  // namespace fp8blk

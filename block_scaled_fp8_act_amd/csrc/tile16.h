@@ -30,6 +30,10 @@ typedef _Float16 v8h __attribute__((ext_vector_type(8)));
 
 namespace t16 {
 
+constexpr int kCUs = 256;
+inline int64_t up(int64_t a, int64_t b) { return (a + b - 1) / b * b; }
+inline int64_t tiles(int64_t n, int64_t t) { return (n + t - 1) / t; }
+
 // 16 and 8 bytes at any even address (gfx950's global loads and stores take those).
 typedef unsigned v4u_any __attribute__((ext_vector_type(4), aligned(2)));
 typedef unsigned v2u_any __attribute__((ext_vector_type(2), aligned(2)));
@@ -83,14 +87,12 @@ __device__ __forceinline__ int swz_f(int row) { return ((row & 3) << 1) | ((row 
 // of those 16 further: eight different pairs of the 256 bytes that the banks span.
 __device__ __forceinline__ int col_f(int k) { return (k & 3) | (((k >> 4) & 1) << 2); }
 
-// A workgroup's tile: WM x WN waves of FM x 4 fragments of 16 x 16.
-template <int WM, int WN, int FM>
+// A workgroup's tile: WM x WN waves of FM x FN fragments of 16 x 16.
+template <int WM, int WN, int FM, int FN>
 struct Shape {
   static constexpr int kWaves = WM * WN, kThreads = kWaves * 64;
-  static constexpr int TM = WM * FM * 16, TN = WN * 64;
-  static constexpr int kFM = FM, kWM = WM, kWN = WN;
-  static constexpr int kDmaA = TM / 8 / kWaves, kDmaB = TN / 8 / kWaves;   // 1 KB loads a wave
-  static_assert(kDmaA * 8 * kWaves == TM && kDmaB * 8 * kWaves == TN, "tile and loads");
+  static constexpr int TM = WM * FM * 16, TN = WN * FN * 16;
+  static constexpr int kFM = FM, kFN = FN, kWM = WM, kWN = WN;
   struct Smem {
     uint8_t a[2][TM * kK * 2];
     uint8_t b[2][TN * kK * 2];
@@ -98,8 +100,8 @@ struct Shape {
 };
 // 256 x 256 on 8 waves (a wave 128 x 64), and 128 x 128 on 4 (64 x 64) for grids
 // that the large tile would leave mostly idle.
-using Large = Shape<2, 4, 8>;
-using Small = Shape<2, 2, 4>;
+using Large = Shape<2, 4, 8, 4>;
+using Small = Shape<2, 2, 4, 4>;
 
 // An operand in memory: `rows` of it along the output, `k` along the sum, both
 // counted from p; `ld` elements from one row of memory to the next.  Rows of
@@ -111,15 +113,22 @@ struct Operand {
   int64_t rows, k;
 };
 
-// The loads of one operand of ROWS rows, kDma of 1 KB a wave, into a stage.
+// The loads of one operand of ROWS rows into a stage, 1 KB each, shared among the
+// waves.
 enum Kind { kRows, kCols };
-template <Kind KIND, int ROWS, int kDma>
+template <Kind KIND, int ROWS, int WAVES>
 struct Loader {
+  static constexpr bool kRegs = false;
+  static constexpr int kLoads = ROWS / 8, kDma = (kLoads + WAVES - 1) / WAVES;
   uint32_t off[kDma];
   uint32_t chunk[kDma];   // kRows: the lane's chunk of the stage's K
   int wave;
   Operand o;
 
+  // Whether load i of this wave exists (where the loads do not divide evenly).
+  __device__ __forceinline__ bool has(int i) const {
+    return kLoads % WAVES == 0 || kDma * wave + i < kLoads;
+  }
   __device__ __forceinline__ void init(const Operand &op, int wave_, int lane) {
     o = op;
     wave = wave_;
@@ -147,12 +156,14 @@ struct Loader {
       const uint32_t chunks = (uint32_t)min(left, (int64_t)kK) >> 3;
 #pragma unroll
       for (int i = 0; i < kDma; ++i)
-        dma16(r, chunk[i] < chunks ? off[i] : kOut, stage + (kDma * wave + i) * 1024);
+        if (has(i))
+          dma16(r, chunk[i] < chunks ? off[i] : kOut, stage + (kDma * wave + i) * 1024);
     } else {
       const __amdgpu_buffer_rsrc_t r =
           rsrc(o.p + k0 * o.ld, ((min(left, (int64_t)kK) - 1) * o.ld + o.rows) * 2);
 #pragma unroll
-      for (int i = 0; i < kDma; ++i) dma16(r, off[i], stage + (kDma * wave + i) * 1024);
+      for (int i = 0; i < kDma; ++i)
+        if (has(i)) dma16(r, off[i], stage + (kDma * wave + i) * 1024);
     }
   }
 };
@@ -188,40 +199,48 @@ __device__ __forceinline__ Frag read_frag(const uint8_t *stage, int row0, int la
 }
 
 // The wave's sums acc[mi][ni][r] = D[16 mi + (lane & 15)][16 ni + 4 (lane >> 4) + r]
-// of its FM x 4 fragments, over `steps` stages from `step0`.  LoadB has
-// issue(step, stage) as Loader does; with REGB it goes through registers: fetch(step)
-// before a step's products, put(stage) after them.
+// of its FM x FN fragments, over `steps` stages from `step0`.  LoadB is a Loader, or
+// (kRegs) brings B through registers: fetch(step) before a step's products, put(stage)
+// among them.
 template <typename T, typename S, Kind KA, Kind KB, typename LoadA, typename LoadB>
-__device__ __forceinline__ void multiply(const LoadA &la, const LoadB &lb, int step0, int steps,
-                                         typename S::Smem &sm, v4f (&acc)[S::kFM][4]) {
+__device__ __forceinline__ void multiply(const LoadA &la, LoadB &lb, int step0, int steps,
+                                         typename S::Smem &sm, v4f (&acc)[S::kFM][S::kFN]) {
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int arow = wave / S::kWN * (S::kFM * 16), brow = wave % S::kWN * 64;
-  constexpr int FM = S::kFM;
+  constexpr int FM = S::kFM, FN = S::kFN;
+  const int arow = wave / S::kWN * (FM * 16), brow = wave % S::kWN * (FN * 16);
 #pragma unroll
   for (int mi = 0; mi < FM; ++mi)
 #pragma unroll
-    for (int ni = 0; ni < 4; ++ni) acc[mi][ni] = v4f{0, 0, 0, 0};
+    for (int ni = 0; ni < FN; ++ni) acc[mi][ni] = v4f{0, 0, 0, 0};
   auto issue = [&](int s) {
+    if constexpr (LoadB::kRegs) lb.fetch(step0 + s);
     la.issue(step0 + s, sm.a[s & 1]);
-    lb.issue(step0 + s, sm.b[s & 1]);
+    if constexpr (!LoadB::kRegs) lb.issue(step0 + s, sm.b[s & 1]);
   };
-  issue(0);
+  if (steps > 0) {
+    issue(0);
+    if constexpr (LoadB::kRegs) lb.put(sm.b[0]);
+  }
   for (int s = 0; s < steps; ++s) {
     __builtin_amdgcn_s_waitcnt(0);
     __syncthreads();
-    if (s + 1 < steps) issue(s + 1);
+    const bool more = s + 1 < steps;
+    if (more) issue(s + 1);
     const uint8_t *a = sm.a[s & 1], *b = sm.b[s & 1];
-    Frag bf[4];
+    Frag bf[FN];
 #pragma unroll
-    for (int ni = 0; ni < 4; ++ni) bf[ni] = read_frag<KB, S::TN>(b, brow + ni * 16, lane);
+    for (int ni = 0; ni < FN; ++ni) bf[ni] = read_frag<KB, S::TN>(b, brow + ni * 16, lane);
 #pragma unroll
     for (int mi = 0; mi < FM; ++mi) {
       const Frag af = read_frag<KA, S::TM>(a, arow + mi * 16, lane);
 #pragma unroll
       for (int h = 0; h < 2; ++h)
 #pragma unroll
-        for (int ni = 0; ni < 4; ++ni) acc[mi][ni] = T::mfma(bf[ni].h[h], af.h[h], acc[mi][ni]);
+        for (int ni = 0; ni < FN; ++ni) acc[mi][ni] = T::mfma(bf[ni].h[h], af.h[h], acc[mi][ni]);
+      // (the other stage's last reads ended before this step's barrier)
+      if constexpr (LoadB::kRegs)
+        if (mi == FM / 2 && more) lb.put(sm.b[(s + 1) & 1]);
     }
   }
 }
@@ -236,6 +255,170 @@ __device__ __forceinline__ void tile_of(int bid, int tiles_m, int tiles_n, int &
   const int height = min(tiles_m - first, 8);
   tm = first + in % height;
   tn = in / height;
+}
+
+// ---------------------------------------------------------------------------
+// Stores and loads of four neighbouring columns, of which `left` > 0 exist.
+
+template <typename T>
+__device__ __forceinline__ void store4(uint16_t *p, const float (&v)[4], int64_t left) {
+  if (left >= 4) {
+    const v2u u = {pack2<T>(v[0], v[1]), pack2<T>(v[2], v[3])};
+    *reinterpret_cast<v2u_any *>(p) = u;
+  } else {
+#pragma unroll
+    for (int r = 0; r < 3; ++r)
+      if (r < left) p[r] = (uint16_t)T::bits(v[r]);
+  }
+}
+template <typename T>
+__device__ __forceinline__ void load4(const uint16_t *p, float (&v)[4], int64_t left) {
+  if (left >= 4) {
+    const v2u u = *reinterpret_cast<const v2u_any *>(p);
+    v[0] = T::value(u[0] & 0xffff);
+    v[1] = T::value(u[0] >> 16);
+    v[2] = T::value(u[1] & 0xffff);
+    v[3] = T::value(u[1] >> 16);
+  } else {
+#pragma unroll
+    for (int r = 0; r < 4; ++r) v[r] = r < left ? T::value(p[r]) : 0.0f;
+  }
+}
+// The same of fp32 sums, at any 4-byte address.
+typedef float v4f_any __attribute__((ext_vector_type(4), aligned(4)));
+__device__ __forceinline__ void store4(float *p, v4f v, int64_t left) {
+  if (left >= 4) {
+    *reinterpret_cast<v4f_any *>(p) = v;
+  } else {
+#pragma unroll
+    for (int r = 0; r < 3; ++r)
+      if (r < left) p[r] = v[r];
+  }
+}
+__device__ __forceinline__ v4f load4(const float *p, int64_t left) {
+  if (left >= 4) return *reinterpret_cast<const v4f_any *>(p);
+  v4f v = {0, 0, 0, 0};
+#pragma unroll
+  for (int r = 0; r < 3; ++r)
+    if (r < left) v[r] = p[r];
+  return v;
+}
+// The sum of four columns' `ranges` parts, `step` apart, in order.
+__device__ __forceinline__ v4f join4(const float *p, int ranges, int64_t step, int64_t left) {
+  v4f v = load4(p, left);
+  for (int s = 1; s < ranges; ++s) v += load4(p + s * step, left);
+  return v;
+}
+
+// Element-wise kernels: as many workgroups as the work has, up to a grid that HIP
+// runs whole, whose threads then take several items each.
+constexpr int64_t kMostGroups = 1 << 20;
+inline dim3 groups(int64_t items) {
+  return dim3((unsigned)(tiles(items, 256) < kMostGroups ? tiles(items, 256) : kMostGroups));
+}
+__device__ __forceinline__ int64_t first_item() { return (int64_t)blockIdx.x * 256 + threadIdx.x; }
+__device__ __forceinline__ int64_t all_threads() { return (int64_t)gridDim.x * 256; }
+
+// Workspace parts start at multiples of 256 bytes.
+struct Space {
+  uint8_t *base;
+  size_t used;
+  uint8_t *take(size_t n) {
+    uint8_t *at = base + used;
+    used += (n + 255) / 256 * 256;
+    return at;
+  }
+};
+
+template <typename S>
+int64_t grid_of(int64_t rows, int64_t cols) {
+  return tiles(rows, S::TM) * tiles(cols, S::TN);
+}
+
+// How a product of rows x cols outputs over k is tiled.
+struct Plan {
+  bool large;
+  int ranges;     // of K, a workgroup each
+};
+inline Plan plan_of(int64_t rows, int64_t cols, int64_t k) {
+  // 256 x 256 tiles where they fill most of the chip
+  if (grid_of<Large>(rows, cols) >= 192) return {true, 1};
+  // ranges of K: enough workgroups for two a compute unit, at least 8 stages each
+  const int64_t grid = grid_of<Small>(rows, cols), steps = tiles(k, kK);
+  int64_t r = 2 * kCUs / grid;
+  r = r < steps / 8 ? r : steps / 8;
+  return {false, (int)(r > 1 ? r : 1)};
+}
+
+// A product's outputs, or its parts.
+struct Out {
+  int64_t rows, cols;
+  uint16_t *out;          // [rows, cols]
+  float *parts;           // [ranges][rows][cols], ranges > 1
+  int steps, ranges;
+  int tiles_m, tiles_n;
+
+  __device__ __forceinline__ int first_step(int range) const {
+    return (int)((int64_t)steps * range / ranges);
+  }
+};
+
+template <typename T, typename S>
+__device__ __forceinline__ void store_tile(const Out &p, const v4f (&acc)[S::kFM][S::kFN],
+                                           int64_t m0, int64_t n0, int range) {
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int r16 = lane & 15, q = lane >> 4;
+  m0 += wave / S::kWN * (S::kFM * 16);
+  n0 += wave % S::kWN * (S::kFN * 16);
+#pragma unroll
+  for (int mi = 0; mi < S::kFM; ++mi) {
+    const int64_t m = m0 + mi * 16 + r16;
+    if (m >= p.rows) continue;
+#pragma unroll
+    for (int ni = 0; ni < S::kFN; ++ni) {
+      const int64_t n = n0 + ni * 16 + 4 * q;
+      const int64_t left = p.cols - n;
+      if (left <= 0) continue;
+      if (p.ranges == 1) {
+        const float v[4] = {acc[mi][ni][0], acc[mi][ni][1], acc[mi][ni][2], acc[mi][ni][3]};
+        store4<T>(p.out + m * p.cols + n, v, left);
+      } else {
+        store4(p.parts + ((int64_t)range * p.rows + m) * p.cols + n, acc[mi][ni], left);
+      }
+    }
+  }
+}
+
+template <typename T>
+__global__ __launch_bounds__(256) void join_kernel(Out p) {
+  const int64_t n = p.rows * p.cols;
+  for (int64_t i = first_item() * 4; i < n; i += all_threads() * 4) {
+    const v4f s = join4(p.parts + i, p.ranges, n, n - i);
+    const float v[4] = {s[0], s[1], s[2], s[3]};
+    store4<T>(p.out + i, v, n - i);
+  }
+}
+
+// Rows brought to a 16-byte pitch (whole chunks, zeros past a row's end).
+__device__ __forceinline__ void align_rows(const uint16_t *in, int64_t ld, int64_t rows,
+                                           int64_t cols, uint16_t *out, int64_t ldo) {
+  const int64_t chunks = ldo / 8;
+  for (int64_t at = first_item(); at < rows * chunks; at += all_threads()) {
+    const int64_t r = at / chunks, c = (at - r * chunks) * 8;
+    const uint16_t *p = in + r * ld + c;
+    v4u v;
+    if (c + 8 <= cols) {
+      v = *reinterpret_cast<const v4u_any *>(p);
+    } else {
+      uint32_t e[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) e[j] = c + j < cols ? p[j] : 0;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) v[j] = e[2 * j] | (e[2 * j + 1] << 16);
+    }
+    *reinterpret_cast<v4u *>(out + r * ldo + c) = v;
+  }
 }
 
 }  // namespace t16

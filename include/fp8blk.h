@@ -574,6 +574,52 @@ FP8BLK_API fp8blk_status fp8blk_gated_linear_backward(
     int act, int64_t M, int64_t I, int64_t K, void *d_x, void *d_w, void *workspace,
     size_t workspace_bytes, void *stream);
 
+/* ------------------------------------------------------------------------
+ * 4-bit weights with a scale, and if wanted a zero point, per group of K:
+ *   W[n,k] = (q[n,k] - z[n,k/group]) * s[n,k/group]
+ * Conventions, type and act as in the section before.
+ *   codes [N,K/2] bytes: q in 0..15, two to a byte, the even k in the low half
+ *   scale [N,K/group] of type
+ *   zeros [N,K/group] bytes in 0..15, or NULL: every z is 8
+ *   group: 32, 64 or 128; K a multiple of it, K <= 2^22
+ * N < 2^31 rows (2I of them for the gated form), M < 2^31, K <= x_stride <=
+ * 2^22, and fewer than 2^23 tiles of 256 x 256 in a product
+ * (FP8BLK_ERR_SHAPE). */
+
+/* Weights [N,K] of type to 4 bits; per group
+ *   with zero points: lo = min(0, least weight), hi = max(0, largest),
+ *     s = type(fl32(fl32(hi - lo) / 15)), z = clamp(rint(-lo / s), 0, 15)
+ *   zeros NULL: s = type(fl32(max |w| / 7)), z = 8
+ *   q = clamp(rint(w / s) + z, 0, 15)
+ * rint to the nearest whole number, ties to even; s = 0 gives q = z (0 with zero
+ * points).  hi - lo has to be finite in fp32. */
+FP8BLK_API fp8blk_status fp8blk_w4_quant(const void *w, int type, int64_t N, int64_t K, int group,
+                                         void *codes, void *scale, void *zeros, void *stream);
+
+/* The weights that codes stand for, rounded once to type: w [N,K] out. */
+FP8BLK_API fp8blk_status fp8blk_w4_dequant(const void *codes, const void *scale, const void *zeros,
+                                           int type, int64_t N, int64_t K, int group, void *w,
+                                           void *stream);
+
+/* y = x W^T: x [M,K] of type with row stride x_stride, y [M,N] out, fp32 sums.
+ * The weights are decoded on the way: W as fp8blk_w4_dequant gives it. */
+FP8BLK_API size_t fp8blk_w4_linear_workspace_bytes(int64_t M, int64_t N, int64_t K,
+                                                   int64_t x_stride);
+FP8BLK_API fp8blk_status fp8blk_w4_linear(const void *x, int64_t x_stride, const void *codes,
+                                          const void *scale, const void *zeros, int type, int group,
+                                          int64_t M, int64_t N, int64_t K, void *y, void *workspace,
+                                          size_t workspace_bytes, void *stream);
+
+/* fp8blk_gated_linear's forward pass with 4-bit weights [2I,K], the gate rows
+ * first: h [M,I] out. */
+FP8BLK_API size_t fp8blk_w4_gated_linear_workspace_bytes(int64_t M, int64_t I, int64_t K,
+                                                         int64_t x_stride);
+FP8BLK_API fp8blk_status fp8blk_w4_gated_linear(const void *x, int64_t x_stride, const void *codes,
+                                                const void *scale, const void *zeros, int type,
+                                                int group, int act, int64_t M, int64_t I, int64_t K,
+                                                void *h, void *workspace, size_t workspace_bytes,
+                                                void *stream);
+
 /* Human-readable name of a status code (static storage, never NULL). */
 FP8BLK_API const char *fp8blk_status_string(int status);
 
