@@ -83,7 +83,7 @@ __all__ = [
     "fp8blk_lora_add", "moe_route", "moe_route_backward", "group_rows", "moe_combine",
     "moe_combine_backward", "lora_add", "lora_linear", "moe_experts",
     "MAX_GROUPS", "MAX_TOPK", "MAX_RANK",
-    "ACTS", "fp8blk_gated_linear", "fp8blk_gated_linear_backward", "gated_linear",
+    "ACTS", "factor_row", "fp8blk_gated_linear", "fp8blk_gated_linear_backward", "gated_linear",
     "gated_linear_backward",
     "W4_GROUPS", "W4Weight", "fp8blk_w4_quant", "fp8blk_w4_dequant", "fp8blk_w4_linear",
     "fp8blk_w4_gated_linear", "w4_quant", "w4_dequant", "w4_linear", "w4_gated_linear",
@@ -1080,9 +1080,13 @@ def _act(act):
     return ACTS[act]
 
 
-def _gated_in(x, w, *more):
-    """Row stride of x, sizes (M, I, K); ``more`` are (tensor, name, columns in
-    units of I) of x's rows."""
+def factor_row(I):
+    """Bytes of a row of factors that gated_linear saves for I outputs."""
+    return -(-I // 4) * 24
+
+
+def _gated_in(x, w, *more, factors=None):
+    """Row stride of x, sizes (M, I, K); ``more`` are (tensor, name) of [M,I]."""
     ldx = _rows_2d(x, "x", _HALF_TYPES)
     _need(w, "w", (x.dtype,), 2)
     M, K = x.shape
@@ -1093,11 +1097,13 @@ def _gated_in(x, w, *more):
     if w.shape[0] % 2:
         raise ValueError("w must hold 2I rows, the gates' first")
     I = w.shape[0] // 2
-    for t, name, wide in more:
-        if t is not None:
-            _need(t, name, (x.dtype,), 2)
-            _shape_eq(t, (M, wide * I), name)
-    _same_device(x, w, *(t for t, _, _ in more))
+    for t, name in more:
+        _need(t, name, (x.dtype,), 2)
+        _shape_eq(t, (M, I), name)
+    if factors is not None:
+        _need(factors, "factors", (torch.uint8,), 2)
+        _shape_eq(factors, (M, factor_row(I)), "factors")
+    _same_device(x, w, factors, *(t for t, _ in more))
     return ldx, M, I, K
 
 
@@ -1108,10 +1114,10 @@ def _gated_call(x, ldx, w, act, M, I, K, h, factors, workspace):
 
 
 def fp8blk_gated_linear(x, w, act, h, factors, workspace=None):
-    """The gated projections into h [M,I]; ``factors`` [M,2I] (for the backward
-    pass) may be None, x may be a column slice of a wider matrix.  ``workspace``
+    """The gated projections into h [M,I]; ``factors`` uint8 [M,factor_row(I)]
+    (for the backward pass) may be None, x may be a column slice of a wider matrix.  ``workspace``
     holds fp8blk_gated_linear_workspace_bytes(M, I, K, x's row stride) bytes."""
-    ldx, M, I, K = _gated_in(x, w, (h, "h", 1), (factors, "factors", 2))
+    ldx, M, I, K = _gated_in(x, w, (h, "h"), factors=factors)
     _need_work(workspace)
     _same_device(x, workspace)
     _gated_call(x, ldx, w, _act(act), M, I, K, h, factors, workspace)
@@ -1129,7 +1135,7 @@ def fp8blk_gated_linear_backward(d_h, x, w, factors, act, d_x, d_w, workspace=No
     None: the projections are computed again.  ``workspace`` holds
     fp8blk_gated_linear_backward_workspace_bytes(M, I, K, x's row stride,
     d_x wanted, d_w wanted) bytes."""
-    ldx, M, I, K = _gated_in(x, w, (d_h, "d_h", 1), (factors, "factors", 2))
+    ldx, M, I, K = _gated_in(x, w, (d_h, "d_h"), factors=factors)
     for t, like, name in ((d_x, x, "d_x"), (d_w, w, "d_w")):
         if t is not None:
             _need(t, name, (x.dtype,), 2)
@@ -1141,12 +1147,12 @@ def fp8blk_gated_linear_backward(d_h, x, w, factors, act, d_x, d_w, workspace=No
 
 def gated_linear(x, w, act="silu", save=False):
     """h = act(x Wg^T) * (x Wu^T), w [2I,K] with the gate rows first, in x's type
-    (bf16 or fp16).  With ``save`` also the factors that
-    gated_linear_backward takes (otherwise it computes the projections again)."""
+    (bf16 or fp16).  With ``save`` also the factors that gated_linear_backward
+    takes (bytes, 6 an output; without them it computes the projections again)."""
     ldx, M, I, K = _gated_in(x, w)
     act = _act(act)
     h = x.new_empty((M, I))
-    factors = x.new_empty((M, 2 * I)) if save else None
+    factors = x.new_empty((M, factor_row(I)), dtype=torch.uint8) if save else None
     need = load_library().fp8blk_gated_linear_workspace_bytes(M, I, K, ldx)
     _gated_call(x, ldx, w, act, M, I, K, h, factors, _work(need, x))
     return (h, factors) if save else h
@@ -1154,7 +1160,7 @@ def gated_linear(x, w, act="silu", save=False):
 
 def gated_linear_backward(d_h, x, w, factors=None, act="silu", need_x=True, need_w=True):
     """(d_x, d_w) of gated_linear; None in the place of one that is not needed."""
-    ldx, M, I, K = _gated_in(x, w, (d_h, "d_h", 1), (factors, "factors", 2))
+    ldx, M, I, K = _gated_in(x, w, (d_h, "d_h"), factors=factors)
     act = _act(act)
     d_x = x.new_empty((M, K)) if need_x else None
     d_w = torch.empty_like(w) if need_w else None

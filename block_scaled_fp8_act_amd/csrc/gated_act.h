@@ -23,6 +23,11 @@ __device__ __forceinline__ float act_value(float g) {
   return g * logistic(1.59576912160573071f * c * __builtin_fmaf(0.044715f * c, c, 1.0f));
 }
 
+__device__ __forceinline__ float act_any(int act, float g) {
+  return act == kSilu ? act_value<kSilu>(g)
+                      : act == kGelu ? act_value<kGelu>(g) : act_value<kGeluTanh>(g);
+}
+
 template <int ACT>
 __device__ __forceinline__ float act_slope(float g) {
   if constexpr (ACT == kSilu) {
@@ -39,6 +44,11 @@ __device__ __forceinline__ float act_slope(float g) {
   const float z = 1.59576912160573071f * c * __builtin_fmaf(0.044715f * c, c, 1.0f);
   const float dz = 1.59576912160573071f * __builtin_fmaf(0.134145f * c, c, 1.0f);
   return logistic(z) * __builtin_fmaf(c * dz, logistic(-z), 1.0f);
+}
+
+__device__ __forceinline__ float slope_any(int act, float g) {
+  return act == kSilu ? act_slope<kSilu>(g)
+                      : act == kGelu ? act_slope<kGelu>(g) : act_slope<kGeluTanh>(g);
 }
 
 }  // namespace fp8blk

@@ -26,6 +26,14 @@ __global__ __launch_bounds__(256) void align_rows_kernel(const uint16_t *in, int
 struct Dense {
   const uint16_t *w;
   int64_t ld;
+  template <typename S>
+  using Smem = typename S::Smem;
+  template <typename T, typename S, typename LA, typename LB>
+  static __device__ __forceinline__ void multiply(const LA &la, const LB &lb, int step0, int steps,
+                                                  typename S::Smem &sm,
+                                                  v4f (&acc)[S::kFM][S::kFN]) {
+    t16::multiply<T, S, kRows, kRows>(la, lb, step0, steps, sm, acc);
+  }
   template <typename T, typename S>
   struct Pair : Loader<kRows, S::TN, S::kWaves> {
     __device__ __forceinline__ void init(const Dense &d, const GluArgs &p, int64_t n0, int wave_,
@@ -47,34 +55,147 @@ struct Dense {
   };
 };
 
-// dgu from the saved factors, 8 outputs a thread.
+// ---------------------------------------------------------------------------
+// A few rows of x (single decoding sequences): W streams past once, a wave per few
+// outputs, 8 values a lane and row, 512 of K at a time; a lane's products are summed
+// by the two-element dot product and the lanes' sums joined at the end.  Rows of any
+// width: 16 bytes at any even address, the last few of K one by one.  Bound: HBM
+// traffic of W.
 template <typename T>
-__global__ __launch_bounds__(256) void factors_kernel(const uint16_t *dh, const uint16_t *factors,
+struct Dot;
+template <>
+struct Dot<Bf16> {
+  typedef __bf16 V __attribute__((ext_vector_type(2)));
+  static __device__ __forceinline__ float two(uint32_t a, uint32_t b, float c) {
+    return __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(V, a), __builtin_bit_cast(V, b), c,
+                                           false);
+  }
+};
+template <>
+struct Dot<F16> {
+  typedef _Float16 V __attribute__((ext_vector_type(2)));
+  static __device__ __forceinline__ float two(uint32_t a, uint32_t b, float c) {
+    return __builtin_amdgcn_fdot2(__builtin_bit_cast(V, a), __builtin_bit_cast(V, b), c, false);
+  }
+};
+
+__device__ __forceinline__ v4u load8(const uint16_t *p, int64_t left) {
+  if (left >= 8) return *reinterpret_cast<const v4u_any *>(p);
+  v4u v = {0, 0, 0, 0};
+#pragma unroll
+  for (int j = 0; j < 7; ++j)
+    if (j < left) v[j / 2] |= (uint32_t)p[j] << (16 * (j & 1));
+  return v;
+}
+
+struct FewArgs {
+  const uint16_t *x, *w;
+  int64_t ldx, K, I;
+  int M, act;
+  uint16_t *h;
+  uint8_t *factors;
+};
+
+// R outputs a wave, MT rows of x (M of them there), the K range shared by KS waves.
+template <typename T, int R, int MT, int KS>
+__global__ __launch_bounds__(256) void few_kernel(FewArgs p) {
+  constexpr int kRows = 2 * R, kOuts = 4 / KS * R;
+  __shared__ float red[4][kRows * MT];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int64_t n0 = (int64_t)blockIdx.x * kOuts;
+  const uint16_t *w[kRows], *x[MT];
+#pragma unroll
+  for (int i = 0; i < kRows; ++i)
+    w[i] = p.w + (min(n0 + wave / KS * R + i % R, p.I - 1) + (i >= R ? p.I : 0)) * p.K + lane * 8;
+#pragma unroll
+  for (int m = 0; m < MT; ++m) x[m] = p.x + min(m, p.M - 1) * p.ldx + lane * 8;
+  float acc[kRows * MT];
+#pragma unroll
+  for (int i = 0; i < kRows * MT; ++i) acc[i] = 0.0f;
+  auto add = [&](const v4u (&wv)[kRows], const v4u (&xv)[MT]) {
+#pragma unroll
+    for (int i = 0; i < kRows; ++i)
+#pragma unroll
+      for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          acc[i * MT + m] = Dot<T>::two(wv[i][e], xv[m][e], acc[i * MT + m]);
+  };
+  const int64_t whole = p.K / 512 * 512;
+  v4u wv[kRows], xv[MT];
+#pragma unroll 2
+  for (int64_t k = (int64_t)(wave % KS) * 512; k < whole; k += KS * 512) {
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) wv[i] = *reinterpret_cast<const v4u_any *>(w[i] + k);
+#pragma unroll
+    for (int m = 0; m < MT; ++m) xv[m] = *reinterpret_cast<const v4u_any *>(x[m] + k);
+    add(wv, xv);
+  }
+  if (whole < p.K && wave % KS == KS - 1) {
+    const int64_t left = p.K - whole - lane * 8;
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) wv[i] = load8(w[i] + whole, left);
+#pragma unroll
+    for (int m = 0; m < MT; ++m) xv[m] = load8(x[m] + whole, left);
+    add(wv, xv);
+  }
+  wave_sums<kRows * MT>(acc, red[wave], lane);
+  __syncthreads();
+  // a thread an output
+  if ((int)threadIdx.x >= kOuts * MT) return;
+  const int m = threadIdx.x % MT, o = threadIdx.x / MT, r = o % R, w0 = o / R * KS;
+  const int64_t n = n0 + o;
+  if (m >= p.M || n >= p.I) return;
+  float g = 0.0f, u = 0.0f;
+#pragma unroll
+  for (int i = 0; i < KS; ++i) {
+    g += red[w0 + i][r * MT + m];
+    u += red[w0 + i][(R + r) * MT + m];
+  }
+  const float a = act_any(p.act, g);
+  p.h[m * p.I + n] = (uint16_t)T::bits(a * u);
+  if (p.factors) {
+    uint8_t *f = p.factors + m * factor_row(p.I) + n * 3;
+    store_24_one(f, u * slope_any(p.act, g));
+    store_24_one(f + factor_half(p.I), a);
+  }
+}
+
+template <typename T, int MT>
+hipError_t few(const FewArgs &p, hipStream_t stream) {
+  // whole K a wave where the rows alone give the chip enough waves
+  constexpr int R = MT == 4 ? 2 : 4;
+  if (p.I / R >= 2048 || p.K < 1024)
+    few_kernel<T, R, MT, 1><<<dim3((unsigned)tiles(p.I, 4 * R)), 256, 0, stream>>>(p);
+  else
+    few_kernel<T, R, MT, 4><<<dim3((unsigned)tiles(p.I, R)), 256, 0, stream>>>(p);
+  return hipGetLastError();
+}
+
+// dgu from the saved factors, 4 outputs a thread.
+template <typename T>
+__global__ __launch_bounds__(256) void factors_kernel(const uint16_t *dh, const uint8_t *factors,
                                                       int64_t M, int64_t I, uint16_t *dgu,
                                                       int64_t ld_dgu) {
-  const int64_t chunks = (I + 7) / 8;
-  for (int64_t at = first_item(); at < M * chunks; at += all_threads()) {
-    const int64_t m = at / chunks, n = (at - m * chunks) * 8;
+  const int64_t quads = (I + 3) / 4;
+  for (int64_t at = first_item(); at < M * quads; at += all_threads()) {
+    const int64_t m = at / quads, n = (at - m * quads) * 4, left = I - n;
+    float d[4], f[4], a[4];
+    load4<T>(dh + m * I + n, d, left);
+    const uint8_t *p = factors + m * factor_row(I) + n * 3;
+    load_24(p, f);
+    load_24(p + factor_half(I), a);
 #pragma unroll
-    for (int half = 0; half < 2; ++half) {
-      const uint16_t *f = factors + (m * 2 + half) * I + n;
-      uint16_t *out = dgu + m * ld_dgu + half * I + n;
-      if (n + 8 <= I) {
-        const v4u dv = *reinterpret_cast<const v4u_any *>(dh + m * I + n);
-        const v4u fv = *reinterpret_cast<const v4u_any *>(f);
-        v4u o;
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          o[j] = pack2<T>(T::value(dv[j] & 0xffff) * T::value(fv[j] & 0xffff),
-                          T::value(dv[j] >> 16) * T::value(fv[j] >> 16));
-        *reinterpret_cast<v4u_any *>(out) = o;
-      } else {
-        for (int j = 0; n + j < I; ++j)
-          out[j] = (uint16_t)T::bits(T::value(dh[m * I + n + j]) * T::value(f[j]));
-      }
+    for (int r = 0; r < 4; ++r) {
+      f[r] *= d[r];
+      a[r] *= d[r];
     }
-    if (n + 8 >= I)
-      for (int64_t c = 2 * I; c < ld_dgu; ++c) dgu[m * ld_dgu + c] = 0;
+    uint16_t *row = dgu + m * ld_dgu;
+    store4<T>(row + n, f, left);
+    store4<T>(row + I + n, a, left);
+    if (left <= 4)
+      for (int64_t c = 2 * I; c < ld_dgu; ++c) row[c] = 0;
   }
 }
 
@@ -188,14 +309,22 @@ GluArgs glu_args(const GatedCall &c, const Inputs &in, const Space &s) {
   return p;
 }
 
+constexpr int64_t kFewRows = 4;
+
 template <typename T>
 hipError_t forward(const GatedCall &c, void *h, void *factors, void *work, hipStream_t stream) {
+  if (c.M <= kFewRows) {
+    const FewArgs p{static_cast<const uint16_t *>(c.x), static_cast<const uint16_t *>(c.w), c.ldx,
+                    c.K, c.I, (int)c.M, c.act, static_cast<uint16_t *>(h),
+                    static_cast<uint8_t *>(factors)};
+    return c.M == 1 ? few<T, 1>(p, stream) : c.M == 2 ? few<T, 2>(p, stream) : few<T, 4>(p, stream);
+  }
   Space s{static_cast<uint8_t *>(work), 0};
   Inputs in;
   if (hipError_t e = lay_inputs(c, in, s, stream)) return e;
   GluArgs p = glu_args(c, in, s);
   p.h = static_cast<uint16_t *>(h);
-  p.factors = static_cast<uint16_t *>(factors);
+  p.factors = static_cast<uint8_t *>(factors);
   return launch_glu<T, false>(p, Dense{in.w, in.ldw}, stream);
 }
 
@@ -210,9 +339,8 @@ hipError_t backward(const GatedCall &c, const void *dh, const void *factors, voi
   // the parts of one product after the other
   float *parts = reinterpret_cast<float *>(s.base + s.used);
   if (factors) {
-    factors_kernel<T><<<groups(c.M * tiles(c.I, 8)), 256, 0, stream>>>(
-        static_cast<const uint16_t *>(dh), static_cast<const uint16_t *>(factors), c.M, c.I, dgu,
-        ld);
+    factors_kernel<T><<<groups(c.M * tiles(c.I, 4)), 256, 0, stream>>>(
+        static_cast<const uint16_t *>(dh), static_cast<const uint8_t *>(factors), c.M, c.I, dgu, ld);
     if (hipError_t e = hipGetLastError()) return e;
   } else {
     GluArgs p = glu_args(c, in, s);
@@ -245,6 +373,7 @@ bool gated_fits(int64_t M, int64_t I, int64_t K) {
 }
 
 size_t gated_workspace_bytes(int64_t M, int64_t I, int64_t K, int64_t ldx) {
+  if (M <= kFewRows) return 0;
   Space s{nullptr, 0};
   inputs_space(M, I, K, ldx, s);
   return s.used + glu_part_bytes(M, I, up(K, 8));

@@ -10,6 +10,10 @@
 namespace fp8blk {
 namespace t16 {
 
+// A row of saved factors: both halves, four outputs' in 12 bytes.
+__host__ __device__ inline int64_t factor_half(int64_t I) { return (I + 3) / 4 * 12; }
+__host__ __device__ inline int64_t factor_row(int64_t I) { return 2 * factor_half(I); }
+
 struct GluArgs {
   const uint16_t *x;
   int64_t ldx, M, I, K;
@@ -17,7 +21,8 @@ struct GluArgs {
   int steps, ranges;              // of K
   float *parts;                   // [ranges][M][2I], ranges > 1
   int act;
-  uint16_t *h, *factors;          // forward: factors may be NULL
+  uint16_t *h;                    // forward
+  uint8_t *factors;               // rows of factor_row(I) bytes, or NULL
   const uint16_t *dh;             // gradient: dgu = d_h times the factors
   uint16_t *dgu;
   int64_t ld_dgu;                 // >= 2I; the rows end in zeros
@@ -65,9 +70,9 @@ __device__ __forceinline__ void glu_store4(const GluArgs &p, int64_t m, int64_t 
     if (p.factors) {
 #pragma unroll
       for (int r = 0; r < 4; ++r) f[r] = u[r] * act_slope<ACT>(g[r]);
-      uint16_t *row = p.factors + m * 2 * p.I;
-      store4<T>(row + n, f, left);
-      store4<T>(row + p.I + n, a, left);
+      uint8_t *row = p.factors + m * factor_row(p.I) + n * 3;
+      store_24(row, f);      // (past the last output: of zero sums)
+      store_24(row + factor_half(p.I), a);
     }
   }
 }
@@ -87,10 +92,11 @@ __device__ __forceinline__ void glu_store(const GluArgs &p, const v4f (&acc)[S::
   }
 }
 
-// W::Pair<T, S> loads the tile's rows of the weights: init(w, p, n0, wave, lane).
+// W::Pair<T, S> loads the tile's rows of the weights (init(w, p, n0, wave, lane)),
+// W::multiply<T, S> forms the tile's sums with it, in W::Smem<S>.
 template <typename T, typename S, bool GRAD, typename W>
 __global__ __launch_bounds__(S::kThreads) void glu_kernel(GluArgs p, W w) {
-  __shared__ typename S::Smem sm;
+  __shared__ typename W::template Smem<S> sm;
   const int tiles = p.tiles_m * p.tiles_n, range = blockIdx.x / tiles;
   int tm, tn;
   tile_of(blockIdx.x - range * tiles, p.tiles_m, p.tiles_n, tm, tn);
@@ -104,7 +110,7 @@ __global__ __launch_bounds__(S::kThreads) void glu_kernel(GluArgs p, W w) {
   const int s0 = (int)((int64_t)p.steps * range / p.ranges);
   const int s1 = (int)((int64_t)p.steps * (range + 1) / p.ranges);
   v4f acc[S::kFM][S::kFN];
-  multiply<T, S, kRows, kRows>(la, lb, s0, s1 - s0, sm, acc);
+  W::template multiply<T, S>(la, lb, s0, s1 - s0, sm, acc);
   m += wave / S::kWN * (S::kFM * 16);
   n += wave % S::kWN * (S::kFN * 8);
   if (p.ranges > 1) {

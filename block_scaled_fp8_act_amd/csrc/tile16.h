@@ -15,7 +15,8 @@
 //          values among 16 lanes.
 // A lane (r = lane & 15, q = lane >> 4) of a matrix instruction holds 8 values of
 // K of the operand's row r.  A stage is two instructions deep, and since both
-// operands agree, instruction h takes K = 16 q + 8 h + 0..7.
+// operands agree, instruction h takes K = 16 q + 8 h + 0..7 (or, where an
+// instruction has to stay within 32 neighbouring K, 32 h + 8 q + 0..7).
 #pragma once
 
 #include "fp8blk_device.h"
@@ -118,7 +119,6 @@ struct Operand {
 enum Kind { kRows, kCols };
 template <Kind KIND, int ROWS, int WAVES>
 struct Loader {
-  static constexpr bool kRegs = false;
   static constexpr int kLoads = ROWS / 8, kDma = (kLoads + WAVES - 1) / WAVES;
   uint32_t off[kDma];
   uint32_t chunk[kDma];   // kRows: the lane's chunk of the stage's K
@@ -173,7 +173,7 @@ struct Frag {
 };
 
 // The fragment of 16 rows from `row0` of a stage of ROWS rows.
-template <Kind KIND, int ROWS>
+template <Kind KIND, int ROWS, bool HALVES = false>
 __device__ __forceinline__ Frag read_frag(const uint8_t *stage, int row0, int lane) {
   Frag f;
   const int r = lane & 15, q = lane >> 4;
@@ -181,8 +181,10 @@ __device__ __forceinline__ Frag read_frag(const uint8_t *stage, int row0, int la
     const int row = row0 + r, s = swz_f(row);
 #pragma unroll
     for (int h = 0; h < 2; ++h)
-      f.h[h] = *reinterpret_cast<const v4u *>(stage + row * 128 + (((2 * q + h) ^ s) << 4));
+      f.h[h] = *reinterpret_cast<const v4u *>(
+          stage + row * 128 + (((HALVES ? 4 * h + q : 2 * q + h) ^ s) << 4));
   } else {
+    static_assert(!HALVES, "K rows are placed for the other order");
 #pragma unroll
     for (int h = 0; h < 2; ++h)
 #pragma unroll
@@ -199,11 +201,9 @@ __device__ __forceinline__ Frag read_frag(const uint8_t *stage, int row0, int la
 }
 
 // The wave's sums acc[mi][ni][r] = D[16 mi + (lane & 15)][16 ni + 4 (lane >> 4) + r]
-// of its FM x FN fragments, over `steps` stages from `step0`.  LoadB is a Loader, or
-// (kRegs) brings B through registers: fetch(step) before a step's products, put(stage)
-// among them.
+// of its FM x FN fragments, over `steps` stages from `step0`.
 template <typename T, typename S, Kind KA, Kind KB, typename LoadA, typename LoadB>
-__device__ __forceinline__ void multiply(const LoadA &la, LoadB &lb, int step0, int steps,
+__device__ __forceinline__ void multiply(const LoadA &la, const LoadB &lb, int step0, int steps,
                                          typename S::Smem &sm, v4f (&acc)[S::kFM][S::kFN]) {
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -214,19 +214,14 @@ __device__ __forceinline__ void multiply(const LoadA &la, LoadB &lb, int step0, 
 #pragma unroll
     for (int ni = 0; ni < FN; ++ni) acc[mi][ni] = v4f{0, 0, 0, 0};
   auto issue = [&](int s) {
-    if constexpr (LoadB::kRegs) lb.fetch(step0 + s);
     la.issue(step0 + s, sm.a[s & 1]);
-    if constexpr (!LoadB::kRegs) lb.issue(step0 + s, sm.b[s & 1]);
+    lb.issue(step0 + s, sm.b[s & 1]);
   };
-  if (steps > 0) {
-    issue(0);
-    if constexpr (LoadB::kRegs) lb.put(sm.b[0]);
-  }
+  if (steps > 0) issue(0);
   for (int s = 0; s < steps; ++s) {
     __builtin_amdgcn_s_waitcnt(0);
     __syncthreads();
-    const bool more = s + 1 < steps;
-    if (more) issue(s + 1);
+    if (s + 1 < steps) issue(s + 1);
     const uint8_t *a = sm.a[s & 1], *b = sm.b[s & 1];
     Frag bf[FN];
 #pragma unroll
@@ -238,9 +233,6 @@ __device__ __forceinline__ void multiply(const LoadA &la, LoadB &lb, int step0, 
       for (int h = 0; h < 2; ++h)
 #pragma unroll
         for (int ni = 0; ni < FN; ++ni) acc[mi][ni] = T::mfma(bf[ni].h[h], af.h[h], acc[mi][ni]);
-      // (the other stage's last reads ended before this step's barrier)
-      if constexpr (LoadB::kRegs)
-        if (mi == FM / 2 && more) lb.put(sm.b[(s + 1) & 1]);
     }
   }
 }
@@ -303,6 +295,32 @@ __device__ __forceinline__ v4f load4(const float *p, int64_t left) {
     if (r < left) v[r] = p[r];
   return v;
 }
+// Four fp32 values in 24 bits each (the top ones, to nearest even), 12 bytes.
+typedef unsigned v3u __attribute__((ext_vector_type(3), aligned(4)));
+__device__ __forceinline__ void store_24(uint8_t *p, const float (&v)[4]) {
+  uint32_t b[4];
+#pragma unroll
+  for (int r = 0; r < 4; ++r) {
+    const uint32_t u = __float_as_uint(v[r]);
+    b[r] = (u + 0x7fu + ((u >> 8) & 1u)) >> 8;
+  }
+  *reinterpret_cast<v3u *>(p) =
+      v3u{b[0] | (b[1] << 24), (b[1] >> 8) | (b[2] << 16), (b[2] >> 16) | (b[3] << 8)};
+}
+__device__ __forceinline__ void store_24_one(uint8_t *p, float v) {
+  const uint32_t u = __float_as_uint(v), b = u + 0x7fu + ((u >> 8) & 1u);
+  p[0] = (uint8_t)(b >> 8);
+  p[1] = (uint8_t)(b >> 16);
+  p[2] = (uint8_t)(b >> 24);
+}
+__device__ __forceinline__ void load_24(const uint8_t *p, float (&v)[4]) {
+  const v3u d = *reinterpret_cast<const v3u *>(p);
+  v[0] = __uint_as_float(d[0] << 8);
+  v[1] = __uint_as_float(((d[0] >> 24) << 8) | (d[1] << 16));
+  v[2] = __uint_as_float(((d[1] >> 16) << 8) | (d[2] << 24));
+  v[3] = __uint_as_float(d[2] & 0xffffff00u);
+}
+
 // The sum of four columns' `ranges` parts, `step` apart, in order.
 __device__ __forceinline__ v4f join4(const float *p, int ranges, int64_t step, int64_t left) {
   v4f v = load4(p, left);
@@ -398,6 +416,26 @@ __global__ __launch_bounds__(256) void join_kernel(Out p) {
     const float v[4] = {s[0], s[1], s[2], s[3]};
     store4<T>(p.out + i, v, n - i);
   }
+}
+
+// The sums over a wave of N values (a power of two up to 64) of each lane, to out[N]:
+// halves of the values are traded between halves of the lanes until a lane has one.
+template <int N>
+__device__ __forceinline__ void wave_sums(float (&v)[N], float *out, int lane) {
+  static_assert(N <= 64 && (N & (N - 1)) == 0, "a power of two");
+  int d = 32;
+#pragma unroll
+  for (int n = N / 2; n >= 1; n /= 2, d /= 2) {
+    const bool upper = lane & d;
+#pragma unroll
+    for (int i = 0; i < n; ++i) {
+      const float keep = upper ? v[i + n] : v[i], send = upper ? v[i] : v[i + n];
+      v[i] = keep + __shfl_xor(send, d);
+    }
+  }
+  const int same = 2 * d;      // lanes that hold parts of one value
+  for (; d >= 1; d /= 2) v[0] += __shfl_xor(v[0], d);
+  if (lane % same == 0) out[lane / same] = v[0];
 }
 
 // Rows brought to a 16-byte pitch (whole chunks, zeros past a row's end).

@@ -10,14 +10,11 @@ using namespace t16;
 
 namespace {
 
-struct W4 {
+struct Weights {
   const uint8_t *codes;      // [rows, K / 2]
   const uint16_t *scale;     // [rows, K >> shift]
   const uint8_t *zeros;      // [rows, K >> shift] or NULL (8)
   int shift;                 // log2 of the group
-
-  template <typename T, typename S>
-  struct Pair;
 };
 
 // ---------------------------------------------------------------------------
@@ -90,46 +87,55 @@ __global__ __launch_bounds__(256) void w4_quant_kernel(const uint16_t *w, int64_
   }
 }
 
-// Eight codes of a dword as fp32 weights, (q - z) s = q s - z s: both products have
-// at most 4 + 11 bits, so each is exact and the sum rounds at most once (never in
-// bf16's or fp16's range of scales: it has 5 + 11 bits).
-__device__ __forceinline__ void decode8(uint32_t c, float s, float zs, float (&w)[8]) {
+// Eight codes of a dword less their zero point, as fp32: whole numbers from -15
+// to 15.
+__device__ __forceinline__ void decode8(uint32_t c, float z, float (&w)[8]) {
   const uint32_t even = c & 0x0f0f0f0fu, odd = (c >> 4) & 0x0f0f0f0fu;
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
-    w[2 * j] = __builtin_fmaf((float)((even >> (8 * j)) & 0xffu), s, zs);
-    w[2 * j + 1] = __builtin_fmaf((float)((odd >> (8 * j)) & 0xffu), s, zs);
+    w[2 * j] = (float)((even >> (8 * j)) & 0xffu) - z;
+    w[2 * j + 1] = (float)((odd >> (8 * j)) & 0xffu) - z;
   }
-}
-template <typename T>
-__device__ __forceinline__ v4u decode16(uint32_t c, float s, float zs) {
-  float w[8];
-  decode8(c, s, zs, w);
-  return v4u{pack2<T>(w[0], w[1]), pack2<T>(w[2], w[3]), pack2<T>(w[4], w[5]),
-             pack2<T>(w[6], w[7])};
 }
 
 template <typename T>
-__global__ __launch_bounds__(256) void w4_dequant_kernel(W4 p, int64_t chunks, uint16_t *w) {
+__global__ __launch_bounds__(256) void w4_dequant_kernel(Weights p, int64_t chunks, uint16_t *w) {
   for (int64_t at = first_item(); at < chunks; at += all_threads()) {
     const int64_t g = at * 8 >> p.shift;
-    const float s = T::value(p.scale[g]), z = p.zeros ? (float)p.zeros[g] : 8.0f;
+    const float s = T::value(p.scale[g]);
+    float v[8];     // (the products are exact in fp32: at most 5 + 11 bits)
+    decode8(reinterpret_cast<const uint32_t *>(p.codes)[at], p.zeros ? (float)p.zeros[g] : 8.0f, v);
     *reinterpret_cast<v4u *>(w + at * 8) =
-        decode16<T>(reinterpret_cast<const uint32_t *>(p.codes)[at], s, -z * s);
+        v4u{pack2<T>(v[0] * s, v[1] * s), pack2<T>(v[2] * s, v[3] * s),
+            pack2<T>(v[4] * s, v[5] * s), pack2<T>(v[6] * s, v[7] * s)};
   }
 }
 
 // ---------------------------------------------------------------------------
 // Batches: the tiled product, the codes decoded on their way into LDS, once a
-// workgroup.  A weight enters the product rounded to the activations' type, as
-// fp8blk_w4_dequant gives it: at most half a step, an error of the size of the
-// inputs' own rounding, for a product whose matrix instructions run as with 16-bit
-// weights.
-//
+// workgroup, as whole numbers (q - z), which bf16 and fp16 hold exactly.  The
+// matrix instructions form a group's sum (or 64 of a longer one's), and one fp32
+// multiply-add an output puts it on the accumulator with its scale.  Weights
+// rounded to 16 bits instead, with the scale, would take no such multiply-adds and
+// carry an error as large as the result's own rounding into it.
+
+// Eight codes less their zero point as 16-bit floats, in the order of k.
+template <typename T>
+__device__ __forceinline__ v4u whole16(uint32_t c, float z) {
+  float w[8];
+  decode8(c, z, w);
+  return v4u{pack2<T>(w[0], w[1]), pack2<T>(w[2], w[3]), pack2<T>(w[4], w[5]),
+             pack2<T>(w[6], w[7])};
+}
+
+template <typename S>
+struct W4Smem : S::Smem {
+  float scale[2][2][S::TN];      // by stage and half of its K
+};
+
 // A thread decodes half a stage of one row of W (32 codes, 16 bytes).
 template <typename T, typename S>
 struct W4Loader {
-  static constexpr bool kRegs = true;
   static_assert(S::kThreads == 2 * S::TN, "two threads a row");
   const uint8_t *codes;
   const uint16_t *scale;
@@ -137,10 +143,10 @@ struct W4Loader {
   int row, half, shift;
   int64_t K;
   v4u c;
-  float s, zs;
+  float s, z;
 
   // This thread's row of the tile is row `n` of the weights.
-  __device__ __forceinline__ void at(const W4 &w, int64_t k, int64_t n) {
+  __device__ __forceinline__ void at(const Weights &w, int64_t k, int64_t n) {
     K = k;
     shift = w.shift;
     row = threadIdx.x >> 1;
@@ -152,34 +158,109 @@ struct W4Loader {
   __device__ __forceinline__ void fetch(int step) {
     const int64_t k = (int64_t)step * kK + half * 32;
     const bool in = k < K;       // (K is a multiple of 32)
-    const int64_t at = in ? (int64_t)step * 32 : 0, g = in ? k >> shift : 0;
-    c = *reinterpret_cast<const v4u *>(codes + (in ? at : -half * 16));
+    const int64_t at = in ? (int64_t)step * 32 : -half * 16, g = in ? k >> shift : 0;
+    c = *reinterpret_cast<const v4u *>(codes + at);
     s = in ? T::value(scale[g]) : 0.0f;
-    zs = -(zeros ? (float)zeros[g] : 8.0f) * s;
+    z = zeros ? (float)zeros[g] : 8.0f;
   }
-  __device__ __forceinline__ void put(uint8_t *stage) const {
+  __device__ __forceinline__ void put(W4Smem<S> &sm, int stage) const {
 #pragma unroll
     for (int j = 0; j < 4; ++j)
-      *reinterpret_cast<v4u *>(stage + row * 128 + (((half * 4 + j) ^ swz_f(row)) << 4)) =
-          decode16<T>(c[j], s, zs);
+      *reinterpret_cast<v4u *>(sm.b[stage] + row * 128 + (((half * 4 + j) ^ swz_f(row)) << 4)) =
+          whole16<T>(c[j], z);
+    sm.scale[stage][half][row] = s;
   }
 };
 
-}  // namespace
+// G32: groups of 32, two a stage; else a stage lies within a group.
+template <bool G32>
+struct W4 : Weights {
+  template <typename S>
+  using Smem = W4Smem<S>;
+  template <typename T, typename S>
+  struct Pair : W4Loader<T, S> {
+    __device__ __forceinline__ void init(const W4 &w, const GluArgs &p, int64_t n0, int, int) {
+      const PairRow<S> r(threadIdx.x >> 1);
+      this->at(w, p.K, r.half * p.I + min(n0 + r.c, p.I - 1));
+    }
+  };
 
-template <typename T, typename S>
-struct W4::Pair : W4Loader<T, S> {
-  __device__ __forceinline__ void init(const W4 &w, const GluArgs &p, int64_t n0, int, int) {
-    const PairRow<S> r(threadIdx.x >> 1);
-    this->at(w, p.K, r.half * p.I + min(n0 + r.c, p.I - 1));
+  // As t16::multiply, with the groups' scales.  The multiply-adds of a row of
+  // fragments follow the next row's matrix instructions, whose results they do
+  // not wait for.
+  template <typename T, typename S, typename LA, typename LB>
+  static __device__ __forceinline__ void multiply(const LA &la, LB &lb, int step0, int steps,
+                                                  W4Smem<S> &sm, v4f (&acc)[S::kFM][S::kFN]) {
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    constexpr int FM = S::kFM, FN = S::kFN, kParts = G32 ? 2 : 1;
+    const int arow = wave / S::kWN * (FM * 16), brow = wave % S::kWN * (FN * 16);
+#pragma unroll
+    for (int mi = 0; mi < FM; ++mi)
+#pragma unroll
+      for (int ni = 0; ni < FN; ++ni) acc[mi][ni] = v4f{0, 0, 0, 0};
+    if (steps > 0) {
+      lb.fetch(step0);
+      la.issue(step0, sm.a[0]);
+      lb.put(sm, 0);
+    }
+    for (int s = 0; s < steps; ++s) {
+      const int st = s & 1;
+      __builtin_amdgcn_s_waitcnt(0);
+      __syncthreads();
+      // (past the last step it is brought again, and not read: a branch around the
+      // put below would let the multiply-adds sink past it and spill)
+      const int next = step0 + min(s + 1, steps - 1);
+      lb.fetch(next);
+      la.issue(next, sm.a[st ^ 1]);
+      __builtin_amdgcn_sched_barrier(0);
+      Frag bf[FN];
+      v4f scale[FN][kParts];
+#pragma unroll
+      for (int ni = 0; ni < FN; ++ni) {
+        bf[ni] = read_frag<kRows, S::TN, true>(sm.b[st], brow + ni * 16, lane);
+#pragma unroll
+        for (int h = 0; h < kParts; ++h)
+          scale[ni][h] =
+              *reinterpret_cast<const v4f *>(&sm.scale[st][h][brow + ni * 16 + 4 * (lane >> 4)]);
+      }
+      // unit u: a row of fragments over a stage, or over half of one
+      v4f part[2][FN];
+      Frag af;
+#pragma unroll
+      for (int u = 0; u <= FM * kParts; ++u) {
+        const int mi = u / kParts, h = u % kParts;
+        if (mi < FM) {
+          if (h == 0) af = read_frag<kRows, S::TM, true>(sm.a[st], arow + mi * 16, lane);
+#pragma unroll
+          for (int ni = 0; ni < FN; ++ni)
+            part[u & 1][ni] = T::mfma(bf[ni].h[h], af.h[h], v4f{0, 0, 0, 0});
+          if constexpr (!G32) {
+#pragma unroll
+            for (int ni = 0; ni < FN; ++ni)
+              part[u & 1][ni] = T::mfma(bf[ni].h[1], af.h[1], part[u & 1][ni]);
+          }
+        }
+        if (u > 0) {
+          const int m = (u - 1) / kParts;
+          __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+          for (int ni = 0; ni < FN; ++ni)
+            acc[m][ni] = __builtin_elementwise_fma(part[(u - 1) & 1][ni],
+                                                   scale[ni][(u - 1) % kParts], acc[m][ni]);
+        }
+        // (the other stage's last reads ended before this step's barrier)
+        if (u == FM * kParts / 2) lb.put(sm, st ^ 1);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    }
+    __builtin_amdgcn_s_waitcnt(0);    // LDS is left with no load into it in flight
   }
 };
 
-namespace {
-
-template <typename T, typename S>
-__global__ __launch_bounds__(S::kThreads) void w4_product_kernel(Operand a, W4 w, Out p) {
-  __shared__ typename S::Smem sm;
+template <typename T, typename S, bool G32>
+__global__ __launch_bounds__(S::kThreads) void w4_product_kernel(Operand a, W4<G32> w, Out p) {
+  __shared__ W4Smem<S> sm;
   const int tiles = p.tiles_m * p.tiles_n, range = blockIdx.x / tiles;
   int tm, tn;
   tile_of(blockIdx.x - range * tiles, p.tiles_m, p.tiles_n, tm, tn);
@@ -194,8 +275,154 @@ __global__ __launch_bounds__(S::kThreads) void w4_product_kernel(Operand a, W4 w
   lb.at(w, a.k, min(n0 + (int64_t)(threadIdx.x >> 1), p.cols - 1));
   const int s0 = p.first_step(range);
   v4f acc[S::kFM][S::kFN];
-  multiply<T, S, kRows, kRows>(la, lb, s0, p.first_step(range + 1) - s0, sm, acc);
+  W4<G32>::template multiply<T, S>(la, lb, s0, p.first_step(range + 1) - s0, sm, acc);
   store_tile<T, S>(p, acc, m0, n0, range);
+}
+
+// ---------------------------------------------------------------------------
+// A few rows of x (single decoding sequences): the weights stream past once, a
+// wave per few rows of W, 32 codes a lane and row.  Bound: HBM traffic of the
+// codes.
+//
+// Codes become 16-bit floats 16 + q by placing them in the mantissa of 16, two at a
+// time; the dot product's instruction takes them by pairs (k, k + 4) against x in
+// the same order, and what the 16 and the zero point add is taken off the 32 codes'
+// sum, (16 + z) times the sum of their x.  The bias is of the codes' own size, so
+// nothing is lost to it in fp32 (128 + q would cost three bits more).
+template <typename T>
+struct Pairs;
+template <>
+struct Pairs<Bf16> {
+  typedef __bf16 V __attribute__((ext_vector_type(2)));
+  static constexpr uint32_t kOne = 0x3f803f80u;
+  static __device__ __forceinline__ float dot(uint32_t a, uint32_t b, float c) {
+    return __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(V, a), __builtin_bit_cast(V, b), c,
+                                           false);
+  }
+  template <int J>   // codes J and J + 4 of a dword
+  static __device__ __forceinline__ uint32_t codes(uint32_t c) {
+    const uint32_t v = J == 0 ? c << 3 : c >> (4 * J - 3);
+    return (v & 0x00780078u) | 0x41804180u;
+  }
+};
+template <>
+struct Pairs<F16> {
+  typedef _Float16 V __attribute__((ext_vector_type(2)));
+  static constexpr uint32_t kOne = 0x3c003c00u;
+  static __device__ __forceinline__ float dot(uint32_t a, uint32_t b, float c) {
+    return __builtin_amdgcn_fdot2(__builtin_bit_cast(V, a), __builtin_bit_cast(V, b), c, false);
+  }
+  template <int J>
+  static __device__ __forceinline__ uint32_t codes(uint32_t c) {
+    const uint32_t v = J == 0 ? c << 6 : J == 1 ? c << 2 : J == 2 ? c >> 2 : c >> 6;
+    return (v & 0x03c003c0u) | 0x4c004c00u;
+  }
+};
+
+// x's 8 values at k as pairs (k, k + 4).
+__device__ __forceinline__ v4u pair_order(v4u x) {
+  return v4u{__builtin_amdgcn_perm(x[2], x[0], 0x05040100u),
+             __builtin_amdgcn_perm(x[2], x[0], 0x07060302u),
+             __builtin_amdgcn_perm(x[3], x[1], 0x05040100u),
+             __builtin_amdgcn_perm(x[3], x[1], 0x07060302u)};
+}
+
+struct W4Few {
+  Weights w;
+  const uint16_t *x;
+  int64_t ldx, K, I;      // I: outputs (rows of W, or half of them)
+  int M, act;
+  uint16_t *out;          // [M, I]
+};
+
+// R outputs a wave, MT rows of x (M of them there), the K range shared by KS waves.
+template <typename T, bool PAIR, int R, int MT, int KS>
+__global__ __launch_bounds__(256) void w4_few_kernel(W4Few p) {
+  using P = Pairs<T>;
+  constexpr int kHalves = PAIR ? 2 : 1, kRows = R * kHalves, kOuts = 4 / KS * R;
+  __shared__ float red[4][kRows * MT];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int64_t n0 = (int64_t)blockIdx.x * kOuts;
+  const uint8_t *codes[kRows];
+  int64_t at[kRows];        // first scale of the row
+#pragma unroll
+  for (int i = 0; i < kRows; ++i) {
+    const int64_t n = min(n0 + wave / KS * R + i % R, p.I - 1) + (i >= R ? p.I : 0);
+    codes[i] = p.w.codes + n * (p.K / 2) + lane * 16;
+    at[i] = n * (p.K >> p.w.shift);
+  }
+  float acc[kRows * MT];
+#pragma unroll
+  for (int i = 0; i < kRows * MT; ++i) acc[i] = 0.0f;
+  for (int64_t k0 = (int64_t)(wave % KS) * 2048; k0 < p.K; k0 += KS * 2048) {
+    const int64_t k = k0 + lane * 32;
+    const bool in = k < p.K;          // (K is a multiple of 32)
+    v4u c[kRows];
+    float s[kRows], z[kRows];
+    const int64_t g = in ? k >> p.w.shift : 0;
+#pragma unroll
+    for (int i = 0; i < kRows; ++i)
+      c[i] = *reinterpret_cast<const v4u *>(codes[i] + (in ? k0 / 2 : -(int64_t)lane * 16));
+    v4u xv[MT][4];
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+      const uint16_t *x = p.x + min(m, p.M - 1) * p.ldx + (in ? k : 0);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) xv[m][j] = *reinterpret_cast<const v4u_any *>(x + 8 * j);
+    }
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) {
+      s[i] = T::value(p.w.scale[at[i] + g]);
+      z[i] = p.w.zeros ? (float)p.w.zeros[at[i] + g] : 8.0f;
+    }
+    float sum[MT];
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+      sum[m] = 0.0f;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        xv[m][j] = in ? pair_order(xv[m][j]) : v4u{0, 0, 0, 0};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) sum[m] = P::dot(xv[m][j][i], P::kOne, sum[m]);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) {
+      float part[MT];
+#pragma unroll
+      for (int m = 0; m < MT; ++m) part[m] = -(16.0f + z[i]) * sum[m];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const uint32_t q[4] = {P::template codes<0>(c[i][j]), P::template codes<1>(c[i][j]),
+                               P::template codes<2>(c[i][j]), P::template codes<3>(c[i][j])};
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) part[m] = P::dot(q[e], xv[m][j][e], part[m]);
+      }
+#pragma unroll
+      for (int m = 0; m < MT; ++m)
+        acc[i * MT + m] = __builtin_fmaf(part[m], s[i], acc[i * MT + m]);
+    }
+  }
+  wave_sums<kRows * MT>(acc, red[wave], lane);
+  __syncthreads();
+  // a thread an output
+  if ((int)threadIdx.x >= kOuts * MT) return;
+  const int m = threadIdx.x % MT, o = threadIdx.x / MT, r = o % R, w0 = o / R * KS;
+  const int64_t n = n0 + o;
+  if (m >= p.M || n >= p.I) return;
+  float v[kHalves];
+#pragma unroll
+  for (int h = 0; h < kHalves; ++h) {
+    v[h] = 0.0f;
+#pragma unroll
+    for (int i = 0; i < KS; ++i) v[h] += red[w0 + i][(h * R + r) * MT + m];
+  }
+  float y = v[0];
+  if constexpr (PAIR) y = act_any(p.act, v[0]) * v[1];
+  p.out[m * p.I + n] = (uint16_t)T::bits(y);
 }
 
 __global__ __launch_bounds__(256) void align_x_kernel(const uint16_t *in, int64_t ld, int64_t rows,
@@ -206,7 +433,7 @@ __global__ __launch_bounds__(256) void align_x_kernel(const uint16_t *in, int64_
 // ---------------------------------------------------------------------------
 // Host side.
 
-W4 weights(const W4Call &c) {
+Weights weights(const W4Call &c) {
   return {static_cast<const uint8_t *>(c.codes), static_cast<const uint16_t *>(c.scale),
           static_cast<const uint8_t *>(c.zeros), c.group == 32 ? 5 : c.group == 64 ? 6 : 7};
 }
@@ -225,8 +452,29 @@ hipError_t lay_x(const W4Call &c, Operand &a, Space &s, hipStream_t stream) {
   return hipGetLastError();
 }
 
-template <typename T>
+constexpr int64_t kFewRows = 4;
+
+template <typename T, bool PAIR, int MT>
+hipError_t few(const W4Few &p, hipStream_t stream) {
+  // whole K a wave where the rows alone give the chip enough waves
+  constexpr int R = PAIR ? 2 : 4;
+  if (p.I / R >= 2048 || p.K <= 2048)
+    w4_few_kernel<T, PAIR, R, MT, 1><<<dim3((unsigned)tiles(p.I, 4 * R)), 256, 0, stream>>>(p);
+  else
+    w4_few_kernel<T, PAIR, R, MT, 4><<<dim3((unsigned)tiles(p.I, R)), 256, 0, stream>>>(p);
+  return hipGetLastError();
+}
+template <typename T, bool PAIR>
+hipError_t few(const W4Call &c, int act, void *out, hipStream_t stream) {
+  const W4Few p{weights(c), static_cast<const uint16_t *>(c.x), c.ldx, c.K,
+                PAIR ? c.rows / 2 : c.rows, (int)c.M, act, static_cast<uint16_t *>(out)};
+  return c.M == 1 ? few<T, PAIR, 1>(p, stream) : c.M == 2 ? few<T, PAIR, 2>(p, stream)
+                                                          : few<T, PAIR, 4>(p, stream);
+}
+
+template <typename T, bool G32>
 hipError_t linear(const W4Call &c, void *y, void *work, hipStream_t stream) {
+  if (c.M <= kFewRows) return few<T, false>(c, 0, y, stream);
   Space s{static_cast<uint8_t *>(work), 0};
   Operand a;
   if (hipError_t e = lay_x(c, a, s, stream)) return e;
@@ -237,8 +485,9 @@ hipError_t linear(const W4Call &c, void *y, void *work, hipStream_t stream) {
   p.tiles_m = (int)tiles(p.rows, plan.large ? Large::TM : Small::TM);
   p.tiles_n = (int)tiles(p.cols, plan.large ? Large::TN : Small::TN);
   const dim3 grid((unsigned)p.tiles_m * p.tiles_n * p.ranges);
-  if (plan.large) w4_product_kernel<T, Large><<<grid, Large::kThreads, 0, stream>>>(a, weights(c), p);
-  else w4_product_kernel<T, Small><<<grid, Small::kThreads, 0, stream>>>(a, weights(c), p);
+  const W4<G32> w{weights(c)};
+  if (plan.large) w4_product_kernel<T, Large, G32><<<grid, Large::kThreads, 0, stream>>>(a, w, p);
+  else w4_product_kernel<T, Small, G32><<<grid, Small::kThreads, 0, stream>>>(a, w, p);
   if (p.ranges > 1) {
     if (hipError_t e = hipGetLastError()) return e;
     join_kernel<T><<<groups(tiles(p.rows * p.cols, 4)), 256, 0, stream>>>(p);
@@ -246,8 +495,9 @@ hipError_t linear(const W4Call &c, void *y, void *work, hipStream_t stream) {
   return hipGetLastError();
 }
 
-template <typename T>
+template <typename T, bool G32>
 hipError_t gated(const W4Call &c, int act, void *h, void *work, hipStream_t stream) {
+  if (c.M <= kFewRows) return few<T, true>(c, act, h, stream);
   Space s{static_cast<uint8_t *>(work), 0};
   Operand a;
   if (hipError_t e = lay_x(c, a, s, stream)) return e;
@@ -260,7 +510,7 @@ hipError_t gated(const W4Call &c, int act, void *h, void *work, hipStream_t stre
   p.act = act;
   p.h = static_cast<uint16_t *>(h);
   p.parts = reinterpret_cast<float *>(s.base + s.used);
-  return launch_glu<T, false>(p, weights(c), stream);
+  return launch_glu<T, false>(p, W4<G32>{weights(c)}, stream);
 }
 
 template <typename T>
@@ -294,10 +544,11 @@ hipError_t launch_w4_dequant(const W4Call &c, void *w, hipStream_t stream) {
 }
 
 bool w4_fits(int64_t M, int64_t rows) {
-  return grid_of<Large>(M, rows) < (int64_t(1) << 32) / Large::kThreads;
+  return rows < (int64_t(1) << 28) && grid_of<Large>(M, rows) < (int64_t(1) << 32) / Large::kThreads;
 }
 
 size_t w4_linear_workspace_bytes(int64_t M, int64_t N, int64_t K, int64_t ldx) {
+  if (M <= kFewRows) return 0;
   Space s{nullptr, 0};
   x_space(M, K, ldx, s);
   const int r = plan_of(M, N, K).ranges;
@@ -305,17 +556,24 @@ size_t w4_linear_workspace_bytes(int64_t M, int64_t N, int64_t K, int64_t ldx) {
 }
 
 size_t w4_gated_workspace_bytes(int64_t M, int64_t I, int64_t K, int64_t ldx) {
+  if (M <= kFewRows) return 0;
   Space s{nullptr, 0};
   x_space(M, K, ldx, s);
   return s.used + glu_part_bytes(M, I, K);
 }
 
 hipError_t launch_w4_linear(const W4Call &c, void *y, void *work, hipStream_t stream) {
-  return c.bf16 ? linear<Bf16>(c, y, work, stream) : linear<F16>(c, y, work, stream);
+  if (c.group == 32)
+    return c.bf16 ? linear<Bf16, true>(c, y, work, stream) : linear<F16, true>(c, y, work, stream);
+  return c.bf16 ? linear<Bf16, false>(c, y, work, stream) : linear<F16, false>(c, y, work, stream);
 }
 
 hipError_t launch_w4_gated(const W4Call &c, int act, void *h, void *work, hipStream_t stream) {
-  return c.bf16 ? gated<Bf16>(c, act, h, work, stream) : gated<F16>(c, act, h, work, stream);
+  if (c.group == 32)
+    return c.bf16 ? gated<Bf16, true>(c, act, h, work, stream)
+                  : gated<F16, true>(c, act, h, work, stream);
+  return c.bf16 ? gated<Bf16, false>(c, act, h, work, stream)
+                : gated<F16, false>(c, act, h, work, stream);
 }
 
 }  // namespace fp8blk

@@ -549,9 +549,11 @@ FP8BLK_API fp8blk_status fp8blk_lora_add(const void *base_bf16, int64_t base_str
 #define FP8BLK_GELU_TANH 2
 
 /*   h [M,I] out
- *   factors [M,2I] out, or NULL (not wanted): what the gradient of h is
- *       multiplied by, u act'(g) in columns [0, I) and act(g) in [I, 2I), each
- *       rounded once; kept for the backward pass. */
+ *   factors out, or NULL (not wanted): M rows of FP8BLK_FACTOR_ROW(I) bytes that
+ *       fp8blk_gated_linear_backward takes: what the gradient of h is multiplied
+ *       by, u act'(g) and act(g), in 24 bits each (of 16 the gradients would
+ *       carry their rounding on top of dgu's). */
+#define FP8BLK_FACTOR_ROW(I) (((I) + 3) / 4 * 24)
 FP8BLK_API size_t fp8blk_gated_linear_workspace_bytes(int64_t M, int64_t I, int64_t K,
                                                       int64_t x_stride);
 FP8BLK_API fp8blk_status fp8blk_gated_linear(const void *x, int64_t x_stride, const void *w,
@@ -562,7 +564,7 @@ FP8BLK_API fp8blk_status fp8blk_gated_linear(const void *x, int64_t x_stride, co
 /* Gradients of fp8blk_gated_linear: dgu = (d_h u act'(g), d_h act(g)) rounded
  * once to type, d_x = dgu W, d_w = dgu^T x.
  *   d_h [M,I] in
- *   factors [M,2I] in, as the forward call wrote it, or NULL: g and u are then
+ *   factors in, as the forward call wrote it, or NULL: g and u are then
  *       computed again (act is read only in this case)
  *   d_x [M,K], d_w [2I,K] out, either may be NULL (not wanted)
  * With M = 0 d_w, and with I = 0 d_x, is cleared. */
@@ -582,7 +584,7 @@ FP8BLK_API fp8blk_status fp8blk_gated_linear_backward(
  *   scale [N,K/group] of type
  *   zeros [N,K/group] bytes in 0..15, or NULL: every z is 8
  *   group: 32, 64 or 128; K a multiple of it, K <= 2^22
- * N < 2^31 rows (2I of them for the gated form), M < 2^31, K <= x_stride <=
+ * Products: N < 2^28 rows (2I of them for the gated form), M < 2^31, K <= x_stride <=
  * 2^22, and fewer than 2^23 tiles of 256 x 256 in a product
  * (FP8BLK_ERR_SHAPE). */
 
@@ -602,7 +604,8 @@ FP8BLK_API fp8blk_status fp8blk_w4_dequant(const void *codes, const void *scale,
                                            void *stream);
 
 /* y = x W^T: x [M,K] of type with row stride x_stride, y [M,N] out, fp32 sums.
- * The weights are decoded on the way: W as fp8blk_w4_dequant gives it. */
+ * The codes enter the products as whole numbers and a group's sum is multiplied
+ * by its scale in fp32, so no weight is rounded. */
 FP8BLK_API size_t fp8blk_w4_linear_workspace_bytes(int64_t M, int64_t N, int64_t K,
                                                    int64_t x_stride);
 FP8BLK_API fp8blk_status fp8blk_w4_linear(const void *x, int64_t x_stride, const void *codes,

@@ -8,8 +8,8 @@ Test infrastructure: see the package docstring for who may import this.
 Each result comes with the largest error that the library's roundings allow:
 fp32 sums of n terms in any order, at most 2^-23 of their magnitudes an
 addition; the activation within 2^-20; one rounding to the 16-bit type (half a
-step, `half`) of h, of the factors where they are saved, of dgu, and of the
-gradients.
+step, `half`) of h, of dgu, and of the gradients; 24 bits of the factors where
+they are saved.
 """
 from __future__ import annotations
 
@@ -19,7 +19,7 @@ import numpy as np
 
 HALF = {"bfloat16": 2.0 ** -8, "float16": 2.0 ** -11}
 TINY = {"bfloat16": 2.0 ** -133, "float16": 2.0 ** -25}    # half the smallest step
-ADD, EVAL = 2.0 ** -23, 2.0 ** -20
+ADD, EVAL, KEPT = 2.0 ** -23, 2.0 ** -20, 2.0 ** -16
 SLOPE = 1.13        # |act'| <= 1.129 and |act''| <= 1 for all three
 
 _erf = np.vectorize(math.erf, otypes=[np.float64])
@@ -72,7 +72,7 @@ def backward(d_h, x, w, name, dtype, saved):
     half, tiny = HALF[dtype], TINY[dtype]
     f, e = factors(x, w, name)
     if saved:
-        e = e + half * (np.abs(f) + e) + tiny
+        e = e + KEPT * (np.abs(f) + e)
     d = np.concatenate([d_h, d_h], 1)
     dgu = d * f
     t = np.abs(d) * e

@@ -55,9 +55,10 @@ def values(codes, s, z, group):
     return (q - off) * np.repeat(s, group, 1)
 
 
-def product(x, w, half):
-    """x W^T and the errors allowed before its own rounding: a weight's rounding to
-    the 16-bit type (half a step), fp32 sums in any order."""
-    y = x @ w.T
-    mag = np.abs(x) @ np.abs(w).T
-    return y, mag * (half + (x.shape[1] + 2) * ADD)
+def product(x, codes, s, z, group):
+    """x W^T and the error allowed before its own rounding: fp32 sums in any order,
+    of products with the codes less any bias up to 16 within a group, each group's
+    then multiplied by its scale."""
+    y = x @ values(codes, s, z, group).T
+    big = np.abs(x) @ np.repeat(np.abs(s), group, 1).T * 31.0
+    return y, big * (group + s.shape[1] + 4) * ADD

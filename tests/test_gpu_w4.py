@@ -1,6 +1,6 @@
 """4-bit weights: codes, scales and zero points equal to the oracle's, and the
-products within its tolerance (a weight's rounding to the 16-bit type, fp32 sums,
-one rounding of the result; the gated form's own beside them)."""
+products within its tolerance (fp32 sums of products with the codes, one rounding
+of the result; the gated form's own beside them).  No weight is rounded."""
 import numpy as np
 import pytest
 import torch
@@ -89,13 +89,19 @@ def near(got, want, tol, dtype, what):
                            float(np.max(np.abs(got - want) / tol)))
 
 
-def check(x, t, values, act, dtype, on_dev=None):
+def product(x, t):
+    """The oracle's x W^T of 4-bit weights t, and its tolerance."""
+    codes, s, z = n64(t[0]).astype(np.uint8), n64(t[1]), n64(t[2])
+    return ow.product(n64(x), codes, s, z, 2 * codes.shape[1] // s.shape[1])
+
+
+def check(x, t, act, dtype, on_dev=None):
     xd = x.to(dev()) if on_dev is None else on_dev
+    y, tol = product(x, t)
     t = on(t)
-    y, tol = ow.product(n64(x), values, og.HALF[dtype])
     near(fb.w4_linear(xd, *t), y, tol, dtype, "linear")
-    if values.shape[0] % 2 == 0:
-        i = values.shape[0] // 2
+    if y.shape[1] % 2 == 0:
+        i = y.shape[1] // 2
         a, _ = og.act(y[:, :i], act)
         eg, eu = og.SLOPE * tol[:, :i], tol[:, i:]
         h = a * y[:, i:]
@@ -116,19 +122,19 @@ def test_w4_products(M, N, K, zeros, dtype):
         if K % group == 0:
             act = list(fb.ACTS)[(M + N) % 3]
             say("w4", M, N, K, group, zeros, dtype, act)
-            _, t, values = make(M + N + K, N, K, group, zeros, dtype)
-            check(rnd(M, M, K).to(DTYPES[dtype]), t, values, act, dtype)
+            _, t, _ = make(M + N + K, N, K, group, zeros, dtype)
+            check(rnd(M, M, K).to(DTYPES[dtype]), t, act, dtype)
 
 
 @pytest.mark.parametrize("M", [1, 3, 20, 140])
 @pytest.mark.parametrize("pad", [8, 3, 1])
 def test_w4_rows_of_a_wider_matrix(M, pad):
     N, K = 70, 160
-    _, t, values = make(M, N, K, 32, True, "float16")
+    _, t, _ = make(M, N, K, 32, True, "float16")
     x = rnd(M + 1, M, K).half()
     wide = torch.full((M, K + 8 + pad), float("nan"), dtype=torch.float16, device=dev())
     wide[:, 8:8 + K] = x.to(dev())
-    check(x, t, values, "gelu", "float16", on_dev=wide[:, 8:8 + K])
+    check(x, t, "gelu", "float16", on_dev=wide[:, 8:8 + K])
 
 
 @pytest.mark.parametrize("M", [1, 4, 12, 64, 200])
@@ -143,17 +149,17 @@ def test_w4_outlier_under_a_zero_weight(M):
     q[:, 70] = z[:, 1]
     q[:, 200] = z[:, 3]
     t = (torch.from_numpy(ow.pack(q)), t[1], t[2])
-    values = ow.values(t[0].numpy(), n64(t[1]), z, 64)
     x = rnd(M, M, K)
     x[:, 70] = 4096.0
     x[:, 200] = -4096.0
     x = x.bfloat16()
     got = n64(fb.w4_linear(x.to(dev()), *on(t)))
-    want, _ = ow.product(n64(x), values, 0.0)
+    want, _ = product(x, t)
     # fp32 sums: the outlier's product with codes up to 31 (q and a bias) may pass
     # through them, a few additions' rounding (2^-24 each) of it stays behind
     left = 64 * 2.0 ** -24 * 31 * 4096 * np.abs(n64(t[1])).max()
-    tol = (np.abs(n64(x)) @ np.abs(values).T) * (2.0 ** -8 + 300 * 2.0 ** -23) + left
+    values = ow.values(t[0].numpy(), n64(t[1]), z, 64)
+    tol = (np.abs(n64(x)) @ np.abs(values).T) * 300 * 2.0 ** -23 + left
     assert np.all(np.abs(got - want) <= tol + 2.0 ** -8 * (np.abs(want) + tol))
 
 
@@ -163,7 +169,8 @@ def test_w4_large_tiles(M, N, K):
     w = (torch.randn(N, K, device=dev(), generator=g) * K ** -0.5).bfloat16()
     x = torch.randn(M, K, device=dev(), generator=g).bfloat16()
     t = fb.w4_quant(w, 64, True)
-    v = fb.w4_dequant(*t).double()
+    q = torch.stack([t.codes & 15, t.codes >> 4], 2).flatten(1).double()
+    v = (q - t.zeros.double().repeat_interleave(64, 1)) * t.scale.double().repeat_interleave(64, 1)
     y = x.double() @ v.t()
     # the result's rounding (half a step, 2^-8 in any norm), and fp32 sums
     for got, want in ((fb.w4_linear(x, *t), y),
@@ -245,13 +252,13 @@ def test_w4_feed_forward_block(M, dtype):
     """A decoding step's whole block in 4 bits: gated projections, then the down
     projection; and the 16-bit block on the dequantized weights beside it."""
     K, I = 256, 384
-    _, up, vu = make(1, 2 * I, K, 64, False, dtype)
-    _, down, vd = make(2, K, I, 128, True, dtype)
+    _, up, _ = make(1, 2 * I, K, 64, False, dtype)
+    _, down, _ = make(2, K, I, 128, True, dtype)
     x = rnd(M, M, K).to(DTYPES[dtype])
+    check(x, up, "silu", dtype)
     xd, up, down = x.to(dev()), on(up), on(down)
     h = fb.w4_gated_linear(xd, *up)
-    check(x, tuple(None if t is None else t.cpu() for t in up), vu, "silu", dtype)
-    y, tol = ow.product(n64(h), vd, og.HALF[dtype])
+    y, tol = product(h, down)
     near(fb.w4_linear(h, *down), y, tol, dtype, "down")
     h16 = fb.gated_linear(xd, fb.w4_dequant(*up))
     want, tol = og.forward(n64(x), n64(fb.w4_dequant(*up)), "silu", dtype)
