@@ -30,8 +30,7 @@ struct Dense {
   using Smem = typename S::Smem;
   template <typename T, typename S, typename LA, typename LB>
   static __device__ __forceinline__ void multiply(const LA &la, const LB &lb, int step0, int steps,
-                                                  typename S::Smem &sm,
-                                                  v4f (&acc)[S::kFM][S::kFN]) {
+                                                  typename S::Smem &sm, typename S::Acc &acc) {
     t16::multiply<T, S, kRows, kRows>(la, lb, step0, steps, sm, acc);
   }
   template <typename T, typename S>
@@ -39,17 +38,17 @@ struct Dense {
     __device__ __forceinline__ void init(const Dense &d, const GluArgs &p, int64_t n0, int wave_,
                                          int lane) {
       using L = Loader<kRows, S::TN, S::kWaves>;
-      static_assert(S::kFN * 8 == L::kDma * 8, "a wave loads its half's rows, gates or ups");
-      this->wave = wave_;
+      static_assert(S::kWaveN / 2 == L::kDma * 8, "a wave loads its half's rows, gates or ups");
       const int half = PairRow<S>(8 * L::kDma * wave_).half;
       const int64_t left = p.I - n0;
-      this->o = Operand{d.w + (half * p.I + n0) * d.ld, d.ld, min(left, (int64_t)S::TN / 2), p.K};
+      this->place(Operand{d.w + (half * p.I + n0) * d.ld, d.ld, min(left, (int64_t)S::TN / 2), p.K},
+                  wave_);
 #pragma unroll
       for (int i = 0; i < L::kDma; ++i) {
         const int row = 8 * (L::kDma * wave_ + i) + (lane >> 3);
         const int c = PairRow<S>(row).c;
         this->chunk[i] = (lane & 7) ^ swz_f(row);
-        this->off[i] = c < left ? (uint32_t)(c * d.ld * 2) + this->chunk[i] * 16 : kOut;
+        this->off[i] = c < left ? c * (uint32_t)d.ld * 2 + this->chunk[i] * 16 : kOut;
       }
     }
   };
@@ -221,7 +220,7 @@ __global__ __launch_bounds__(S::kThreads) void product_kernel(Operand a, Operand
   la.init(a, wave, lane);
   lb.init(b, wave, lane);
   const int s0 = p.first_step(range);
-  v4f acc[S::kFM][S::kFN];
+  typename S::Acc acc;
   multiply<T, S, KA, KB>(la, lb, s0, p.first_step(range + 1) - s0, sm, acc);
   store_tile<T, S>(p, acc, m0, n0, range);
 }
@@ -325,7 +324,7 @@ hipError_t forward(const GatedCall &c, void *h, void *factors, void *work, hipSt
   GluArgs p = glu_args(c, in, s);
   p.h = static_cast<uint16_t *>(h);
   p.factors = static_cast<uint8_t *>(factors);
-  return launch_glu<T, false>(p, Dense{in.w, in.ldw}, stream);
+  return launch_glu<T, false, Large, Small>(p, Dense{in.w, in.ldw}, stream);
 }
 
 template <typename T>
@@ -347,7 +346,7 @@ hipError_t backward(const GatedCall &c, const void *dh, const void *factors, voi
     p.dh = static_cast<const uint16_t *>(dh);
     p.dgu = dgu;
     p.ld_dgu = ld;
-    if (hipError_t e = launch_glu<T, true>(p, Dense{in.w, in.ldw}, stream)) return e;
+    if (hipError_t e = launch_glu<T, true, Large, Small>(p, Dense{in.w, in.ldw}, stream)) return e;
   }
   if (dx) {
     const Out o{c.M, c.K, static_cast<uint16_t *>(dx), parts};

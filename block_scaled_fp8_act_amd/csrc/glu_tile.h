@@ -29,12 +29,12 @@ struct GluArgs {
 };
 
 // Row of W (counted in its half's rows from the tile's first output) and half of
-// row `row` of the tile: FN / 2 fragments of gates, then of ups, for each wave.
+// row `row` of the tile: of each wave's rows, first the gates', then the ups'.
 template <typename S>
 struct PairRow {
   int half, c;
   __device__ __forceinline__ explicit PairRow(int row) {
-    constexpr int kHalf = S::kFN * 8;
+    constexpr int kHalf = S::kWaveN / 2;
     const int in = row % (2 * kHalf);
     half = in / kHalf;
     c = row / (2 * kHalf) * kHalf + in % kHalf;
@@ -78,16 +78,16 @@ __device__ __forceinline__ void glu_store4(const GluArgs &p, int64_t m, int64_t 
 }
 
 template <typename T, typename S, int ACT, bool GRAD>
-__device__ __forceinline__ void glu_store(const GluArgs &p, const v4f (&acc)[S::kFM][S::kFN],
-                                          int64_t m0, int64_t n0, int lane) {
+__device__ __forceinline__ void glu_store(const GluArgs &p, const typename S::Acc &acc, int64_t m0,
+                                          int64_t n0, int lane) {
 #pragma unroll
-  for (int mi = 0; mi < S::kFM; ++mi) {
-    const int64_t m = m0 + mi * 16 + (lane & 15);
+  for (int i = 0; i < S::kRowsHeld; ++i) {
+    const int64_t m = m0 + S::row(i, lane);
     if (m >= p.M) continue;
 #pragma unroll
-    for (int ni = 0; ni < S::kFN / 2; ++ni) {
-      const int64_t n = n0 + ni * 16 + 4 * (lane >> 4);
-      if (n < p.I) glu_store4<T, ACT, GRAD>(p, m, n, acc[mi][ni], acc[mi][ni + S::kFN / 2]);
+    for (int j = 0; j < S::kQuads / 2; ++j) {
+      const int64_t n = n0 + S::col(j, lane);
+      if (n < p.I) glu_store4<T, ACT, GRAD>(p, m, n, acc[i][j], acc[i][j + S::kQuads / 2]);
     }
   }
 }
@@ -109,20 +109,20 @@ __global__ __launch_bounds__(S::kThreads) void glu_kernel(GluArgs p, W w) {
   lb.init(w, p, n, wave, lane);
   const int s0 = (int)((int64_t)p.steps * range / p.ranges);
   const int s1 = (int)((int64_t)p.steps * (range + 1) / p.ranges);
-  v4f acc[S::kFM][S::kFN];
+  typename S::Acc acc;
   W::template multiply<T, S>(la, lb, s0, s1 - s0, sm, acc);
-  m += wave / S::kWN * (S::kFM * 16);
-  n += wave % S::kWN * (S::kFN * 8);
+  m += wave / S::kWN * S::kWaveM;
+  n += wave % S::kWN * (S::kWaveN / 2);
   if (p.ranges > 1) {
+    constexpr int kHalf = S::kQuads / 2;
 #pragma unroll
-    for (int mi = 0; mi < S::kFM; ++mi)
+    for (int i = 0; i < S::kRowsHeld; ++i)
 #pragma unroll
-      for (int ni = 0; ni < S::kFN; ++ni) {
-        const int64_t row = m + mi * 16 + (lane & 15);
-        const int64_t col = n + ni % (S::kFN / 2) * 16 + 4 * (lane >> 4);
+      for (int j = 0; j < S::kQuads; ++j) {
+        const int64_t row = m + S::row(i, lane), col = n + S::col(j % kHalf, lane);
         if (row < p.M && col < p.I)
-          store4(p.parts + ((int64_t)range * p.M + row) * 2 * p.I +
-                     (ni >= S::kFN / 2 ? p.I : 0) + col, acc[mi][ni], p.I - col);
+          store4(p.parts + ((int64_t)range * p.M + row) * 2 * p.I + (j >= kHalf ? p.I : 0) + col,
+                 acc[i][j], p.I - col);
       }
     return;
   }
@@ -146,16 +146,18 @@ __global__ __launch_bounds__(256) void glu_join_kernel(GluArgs p) {
 }
 
 // Launches for a plan; p's sizes, pointers and act are set.
-template <typename T, bool GRAD, typename W>
+template <typename T, bool GRAD, typename L, typename S, typename W>
 hipError_t launch_glu(GluArgs p, const W &w, hipStream_t stream) {
+  static_assert(L::TM == Large::TM && L::TN == Large::TN && S::TM == Small::TM &&
+                S::TN == Small::TN, "the plan's tiles");
   const Plan plan = plan_of(p.M, 2 * p.I, p.K);
   p.steps = (int)tiles(p.K, kK);
   p.ranges = plan.ranges;
-  p.tiles_m = (int)tiles(p.M, plan.large ? Large::TM : Small::TM);
-  p.tiles_n = (int)tiles(p.I, (plan.large ? Large::TN : Small::TN) / 2);
+  p.tiles_m = (int)tiles(p.M, plan.large ? L::TM : S::TM);
+  p.tiles_n = (int)tiles(p.I, (plan.large ? L::TN : S::TN) / 2);
   const dim3 grid((unsigned)p.tiles_m * p.tiles_n * p.ranges);
-  if (plan.large) glu_kernel<T, Large, GRAD, W><<<grid, Large::kThreads, 0, stream>>>(p, w);
-  else glu_kernel<T, Small, GRAD, W><<<grid, Small::kThreads, 0, stream>>>(p, w);
+  if (plan.large) glu_kernel<T, L, GRAD, W><<<grid, L::kThreads, 0, stream>>>(p, w);
+  else glu_kernel<T, S, GRAD, W><<<grid, S::kThreads, 0, stream>>>(p, w);
   if (p.ranges > 1) {
     if (hipError_t e = hipGetLastError()) return e;
     glu_join_kernel<T, GRAD><<<groups(p.M * tiles(p.I, 4)), 256, 0, stream>>>(p);

@@ -13,11 +13,12 @@
 //   kCols  [64 of K][rows], 32-byte pairs p of K row k kept at p ^ col_f(k); a
 //          fragment is four ds_read_b64_tr_b16 a lane, which transpose 4 x 16
 //          values among 16 lanes.
-// A lane (r = lane & 15, q = lane >> 4) of a matrix instruction holds 8 values of
-// K of the operand's row r.  A stage is two instructions deep, and since both
-// operands agree, instruction h takes K = 16 q + 8 h + 0..7 (or, where an
-// instruction has to stay within 32 neighbouring K, 32 h + 8 q + 0..7).
+// Lane l of a matrix instruction on F x F outputs (16 x 16 x 32 or 32 x 32 x 16)
+// holds 8 values of K of the operand's row l % F, from K = 8 (l / F) of the
+// instruction's.
 #pragma once
+
+#include <type_traits>
 
 #include "fp8blk_device.h"
 
@@ -28,6 +29,7 @@ typedef unsigned v2u __attribute__((ext_vector_type(2)));
 typedef short v4s __attribute__((ext_vector_type(4)));
 typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
 typedef _Float16 v8h __attribute__((ext_vector_type(8)));
+typedef float v16f __attribute__((ext_vector_type(16)));
 
 namespace t16 {
 
@@ -49,6 +51,10 @@ struct Bf16 {
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8bf, a),
                                                    __builtin_bit_cast(v8bf, b), c, 0, 0, 0);
   }
+  static __device__ __forceinline__ v16f mfma(v4u a, v4u b, v16f c) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(v8bf, a),
+                                                   __builtin_bit_cast(v8bf, b), c, 0, 0, 0);
+  }
 };
 struct F16 {
   static __device__ __forceinline__ uint32_t bits(float f) {
@@ -59,6 +65,10 @@ struct F16 {
   }
   static __device__ __forceinline__ v4f mfma(v4u a, v4u b, v4f c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(v8h, a),
+                                                  __builtin_bit_cast(v8h, b), c, 0, 0, 0);
+  }
+  static __device__ __forceinline__ v16f mfma(v4u a, v4u b, v16f c) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(v8h, a),
                                                   __builtin_bit_cast(v8h, b), c, 0, 0, 0);
   }
 };
@@ -73,27 +83,63 @@ typedef __attribute__((address_space(3))) v4s lds_v4s;
 constexpr int kK = 64;              // of K a stage
 constexpr uint32_t kOut = 0xfffffff0u;   // an offset past every resource: reads zeros
 
-// Loads through a buffer resource read zeros past its byte count.
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc(const void *base, int64_t bytes) {
-  const uint32_t n = bytes <= 0 ? 0u : (uint32_t)min(bytes, (int64_t)kOut);
-  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(base), (short)0, (int)n, 0x00020000);
+__device__ __forceinline__ uint32_t uniform(uint32_t v) {
+  return __builtin_amdgcn_readfirstlane(v);
 }
-__device__ __forceinline__ void dma16(__amdgpu_buffer_rsrc_t r, uint32_t off, void *lds) {
-  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void *)lds, 16, (int)off, 0, 0, 0);
+__device__ __forceinline__ uint64_t uniform(uint64_t v) {
+  return uniform((uint32_t)v) | ((uint64_t)uniform((uint32_t)(v >> 32)) << 32);
 }
 
-// As in the fp8 tiles: 16 lanes on one chunk of 16 consecutive rows meet no bank twice.
-__device__ __forceinline__ int swz_f(int row) { return ((row & 3) << 1) | ((row >> 2) & 1); }
-// 32 lanes of a transposing read take 32 bytes of K rows k, k + 1, k + 2, k + 3 and
-// of those 16 further: eight different pairs of the 256 bytes that the banks span.
-__device__ __forceinline__ int col_f(int k) { return (k & 3) | (((k >> 4) & 1) << 2); }
+// A buffer resource of `bytes` bytes from `base` (both uniform); loads past them
+// read zeros.
+__device__ __forceinline__ v4u rsrc(uint64_t base, uint32_t bytes) {
+  return v4u{(uint32_t)base, (uint32_t)(base >> 32) & 0xffffu, bytes, 0x00020000u};
+}
+// 16 bytes a lane from r at byte `off` to LDS at `lds` + 16 lane.  In assembly,
+// because the compiler takes every later transposing read of LDS for one of what the
+// load writes and waits for it there; the one wait that is needed stands before the
+// barrier that opens the stage.  (It has no output register.)  The first of a stage's
+// loads keeps the five wait states that a resource register written by a vector
+// instruction (readfirstlane) needs before a load reads it.
+template <bool FIRST>
+__device__ __forceinline__ void dma16(v4u r, uint32_t off, const void *lds) {
+  const uint32_t to = (uint32_t)(uintptr_t)(const lds_void *)lds;
+  if constexpr (FIRST)
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
+                 :
+                 : "s"(to), "v"(off), "s"(r)
+                 : "memory", "m0");
+  else
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
+                 :
+                 : "s"(to), "v"(off), "s"(r)
+                 : "memory", "m0");
+}
 
-// A workgroup's tile: WM x WN waves of FM x FN fragments of 16 x 16.
-template <int WM, int WN, int FM, int FN>
+// Fragment reads of both sizes run at the LDS's full rate so: 247-251 bytes a clock
+// and compute unit measured, half that with row & 7, or with the fp8 tiles' order,
+// whose lanes take other chunks.
+__device__ __forceinline__ int swz_f(int row) { return (row >> 1) & 7; }
+// 32 lanes of a transposing read take 32 bytes of each of K rows k .. k + 3, and with
+// F = 16 of those 8 further, with F = 32 the 32 bytes beside them: either way eight
+// different pairs of the 256 bytes that the banks span.
+__device__ __forceinline__ int col_f(int k) { return ((k & 3) << 1) | ((k >> 3) & 1); }
+
+// A workgroup's tile: WM x WN waves of FM x FN fragments of F x F (16 or 32).  A
+// lane holds its outputs by fours: kRows rows F * i + lane % F, in each kQuads runs
+// of four columns from col(j).
+template <int F, int WM, int WN, int FM, int FN>
 struct Shape {
+  static constexpr int kF = F, kFM = FM, kFN = FN, kWM = WM, kWN = WN;
   static constexpr int kWaves = WM * WN, kThreads = kWaves * 64;
-  static constexpr int TM = WM * FM * 16, TN = WN * FN * 16;
-  static constexpr int kFM = FM, kFN = FN, kWM = WM, kWN = WN;
+  static constexpr int kWaveM = FM * F, kWaveN = FN * F;
+  static constexpr int TM = WM * kWaveM, TN = WN * kWaveN;
+  static constexpr int kRowsHeld = FM, kQuads = FN * F * F / 256;
+  using Acc = v4f[kRowsHeld][kQuads];
+  static __device__ __forceinline__ int row(int i, int lane) { return i * F + lane % F; }
+  static __device__ __forceinline__ int col(int j, int lane) {
+    return F == 16 ? 16 * j + 4 * (lane >> 4) : 32 * (j / 4) + 8 * (j % 4) + 4 * (lane >> 5);
+  }
   struct Smem {
     uint8_t a[2][TM * kK * 2];
     uint8_t b[2][TN * kK * 2];
@@ -101,21 +147,22 @@ struct Shape {
 };
 // 256 x 256 on 8 waves (a wave 128 x 64), and 128 x 128 on 4 (64 x 64) for grids
 // that the large tile would leave mostly idle.
-using Large = Shape<2, 4, 8, 4>;
-using Small = Shape<2, 2, 4, 4>;
+using Large = Shape<16, 2, 4, 8, 4>;
+using Small = Shape<16, 2, 2, 4, 4>;
 
 // An operand in memory: `rows` of it along the output, `k` along the sum, both
 // counted from p; `ld` elements from one row of memory to the next.  Rows of
 // memory are 16-byte aligned and whole 16-byte chunks (ld and the contiguous
-// extent are multiples of 8).
+// extent are multiples of 8, and at most 2^22).
 struct Operand {
   const uint16_t *p;
   int64_t ld;
   int64_t rows, k;
 };
 
-// The loads of one operand of ROWS rows into a stage, 1 KB each, shared among the
-// waves.
+// The loads of one operand's ROWS rows into a stage, 1 KB each, shared among the
+// waves.  K values past the last one read as zeros, and so do rows past the last.
+// Offsets and byte counts of a stage stay below 2^32: 256 rows of 2^22 elements.
 enum Kind { kRows, kCols };
 template <Kind KIND, int ROWS, int WAVES>
 struct Loader {
@@ -123,76 +170,95 @@ struct Loader {
   uint32_t off[kDma];
   uint32_t chunk[kDma];   // kRows: the lane's chunk of the stage's K
   int wave;
-  Operand o;
+  // uniform
+  uint64_t base;
+  uint32_t step_bytes;    // from one stage to the next
+  uint32_t bytes;         // kRows: of the first stage's resource; kCols: of a row of memory
+  uint32_t row_bytes;     // kCols: valid bytes of a row
+  int k;                  // left at the first stage
 
   // Whether load i of this wave exists (where the loads do not divide evenly).
   __device__ __forceinline__ bool has(int i) const {
     return kLoads % WAVES == 0 || kDma * wave + i < kLoads;
   }
-  __device__ __forceinline__ void init(const Operand &op, int wave_, int lane) {
-    o = op;
+  __device__ __forceinline__ void place(const Operand &o, int wave_) {
     wave = wave_;
+    base = uniform((uint64_t)(uintptr_t)o.p);
+    k = (int)uniform((uint32_t)o.k);
+    const uint32_t ld = uniform((uint32_t)o.ld) * 2, rows = uniform((uint32_t)o.rows);
+    step_bytes = KIND == kRows ? kK * 2 : ld * kK;
+    bytes = KIND == kRows ? (rows - 1) * ld + k * 2 : ld;
+    row_bytes = rows * 2;
+  }
+  __device__ __forceinline__ void init(const Operand &o, int wave_, int lane) {
+    place(o, wave_);
 #pragma unroll
     for (int i = 0; i < kDma; ++i) {
       if constexpr (KIND == kRows) {
         const int row = 8 * (kDma * wave + i) + (lane >> 3);
         chunk[i] = (lane & 7) ^ swz_f(row);
-        off[i] = row < o.rows ? (uint32_t)(row * o.ld * 2) + chunk[i] * 16 : kOut;
+        off[i] = row < o.rows ? row * (uint32_t)o.ld * 2 + chunk[i] * 16 : kOut;
       } else {
         constexpr int kChunks = ROWS / 8;     // 16-byte chunks of a K row
         const int at = (kDma * wave + i) * 64 + lane;
-        const int k = at / kChunks, c = (at % kChunks) ^ (col_f(at / kChunks) << 1);
-        chunk[i] = k;
-        off[i] = c * 8 < o.rows ? (uint32_t)(k * o.ld * 2) + c * 16 : kOut;
+        const int kr = at / kChunks, c = (at % kChunks) ^ (col_f(at / kChunks) << 1);
+        off[i] = c * 8 < o.rows ? kr * (uint32_t)o.ld * 2 + c * 16 : kOut;
       }
     }
   }
-  // K values past the last one read as zeros, and so do rows past the last.
-  __device__ __forceinline__ void issue(int step, uint8_t *stage) const {
-    const int64_t k0 = (int64_t)step * kK;
-    const int64_t left = o.k - k0;     // > 0
+  template <typename F>
+  __device__ __forceinline__ void each(F f) const {
+    if (has(0)) f(std::true_type{}, 0);
+#pragma unroll
+    for (int i = 1; i < kDma; ++i)
+      if (has(i)) f(std::false_type{}, i);
+  }
+  __device__ __forceinline__ void issue(int step, const uint8_t *stage) const {
+    const uint64_t from = base + (uint64_t)(uint32_t)step * step_bytes;
+    const int left = k - step * kK;     // > 0
     if constexpr (KIND == kRows) {
-      const __amdgpu_buffer_rsrc_t r = rsrc(o.p + k0, ((o.rows - 1) * o.ld + left) * 2);
-      const uint32_t chunks = (uint32_t)min(left, (int64_t)kK) >> 3;
-#pragma unroll
-      for (int i = 0; i < kDma; ++i)
-        if (has(i))
-          dma16(r, chunk[i] < chunks ? off[i] : kOut, stage + (kDma * wave + i) * 1024);
+      const v4u r = rsrc(from, bytes - step * (kK * 2));
+      const uint32_t chunks = min(left, kK) >> 3;
+      each([&](auto first, int i) {
+        dma16<first.value>(r, chunk[i] < chunks ? off[i] : kOut, stage + (kDma * wave + i) * 1024);
+      });
     } else {
-      const __amdgpu_buffer_rsrc_t r =
-          rsrc(o.p + k0 * o.ld, ((min(left, (int64_t)kK) - 1) * o.ld + o.rows) * 2);
-#pragma unroll
-      for (int i = 0; i < kDma; ++i)
-        if (has(i)) dma16(r, off[i], stage + (kDma * wave + i) * 1024);
+      const v4u r = rsrc(from, (min(left, kK) - 1) * bytes + row_bytes);
+      each([&](auto first, int i) {
+        dma16<first.value>(r, off[i], stage + (kDma * wave + i) * 1024);
+      });
     }
   }
 };
 
+// A fragment of F rows over a stage: F / 8 instructions' operands.
+template <int F>
 struct Frag {
-  v4u h[2];
+  static constexpr int kSteps = F / 8;
+  v4u h[kSteps];
 };
 
-// The fragment of 16 rows from `row0` of a stage of ROWS rows.
-template <Kind KIND, int ROWS, bool HALVES = false>
-__device__ __forceinline__ Frag read_frag(const uint8_t *stage, int row0, int lane) {
-  Frag f;
-  const int r = lane & 15, q = lane >> 4;
+// The fragment of the F rows from `row0` of a stage of ROWS rows.
+template <Kind KIND, int ROWS, int F>
+__device__ __forceinline__ Frag<F> read_frag(const uint8_t *stage, int row0, int lane) {
+  Frag<F> f;
+  constexpr int kSteps = Frag<F>::kSteps;
+  const int q = lane / F;               // of the 512 / F values of an instruction's K
   if constexpr (KIND == kRows) {
-    const int row = row0 + r, s = swz_f(row);
+    const int row = row0 + lane % F, s = swz_f(row);
 #pragma unroll
-    for (int h = 0; h < 2; ++h)
-      f.h[h] = *reinterpret_cast<const v4u *>(
-          stage + row * 128 + (((HALVES ? 4 * h + q : 2 * q + h) ^ s) << 4));
+    for (int h = 0; h < kSteps; ++h)
+      f.h[h] = *reinterpret_cast<const v4u *>(stage + row * 128 + (((64 / F * h + q) ^ s) << 4));
   } else {
-    static_assert(!HALVES, "K rows are placed for the other order");
+    const int r = lane & 15, row16 = (row0 + lane % F) >> 4;
 #pragma unroll
-    for (int h = 0; h < 2; ++h)
+    for (int h = 0; h < kSteps; ++h)
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
-        const int k = 16 * q + 8 * h + 4 * j + (r >> 2);
-        const uint8_t *at = stage + k * (ROWS * 2) + (((row0 >> 4) ^ col_f(k)) << 5) + (r & 3) * 8;
-        const v4s v = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s *)at);
-        const v2u u = __builtin_bit_cast(v2u, v);
+        const int k = 512 / F * h + 8 * q + 4 * j + (r >> 2);
+        const uint8_t *at = stage + k * (ROWS * 2) + ((row16 ^ col_f(k)) << 5) + (r & 3) * 8;
+        const v2u u = __builtin_bit_cast(
+            v2u, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s *)at));
         f.h[h][2 * j] = u[0];
         f.h[h][2 * j + 1] = u[1];
       }
@@ -200,41 +266,83 @@ __device__ __forceinline__ Frag read_frag(const uint8_t *stage, int row0, int la
   return f;
 }
 
-// The wave's sums acc[mi][ni][r] = D[16 mi + (lane & 15)][16 ni + 4 (lane >> 4) + r]
-// of its FM x FN fragments, over `steps` stages from `step0`.
+// The wave's sums over `steps` >= 1 stages from `step0`, as Shape places them.
+//
+// Step s reads stage s & 1.  Its barrier sits before the last row of fragments'
+// matrix instructions: every wave has then read the stage, and the next one has
+// landed in the other.  That stage's first fragments are read under the last row's
+// instructions, and the loads of the stage after it go out into the one just read, a
+// whole step ahead, so the matrix cores do not wait at a step's start.  Past the last
+// step the loads bring the last stage again, which nobody uses: a branch inside the
+// unrolled instructions would cost more.
 template <typename T, typename S, Kind KA, Kind KB, typename LoadA, typename LoadB>
 __device__ __forceinline__ void multiply(const LoadA &la, const LoadB &lb, int step0, int steps,
-                                         typename S::Smem &sm, v4f (&acc)[S::kFM][S::kFN]) {
+                                         typename S::Smem &sm, typename S::Acc &out) {
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  constexpr int FM = S::kFM, FN = S::kFN;
-  const int arow = wave / S::kWN * (FM * 16), brow = wave % S::kWN * (FN * 16);
+  constexpr int F = S::kF, FM = S::kFM, FN = S::kFN, kSteps = F / 8;
+  const int arow = wave / S::kWN * S::kWaveM, brow = wave % S::kWN * S::kWaveN;
+  typename std::conditional<F == 16, v4f, v16f>::type acc[FM][FN];
 #pragma unroll
   for (int mi = 0; mi < FM; ++mi)
 #pragma unroll
-    for (int ni = 0; ni < FN; ++ni) acc[mi][ni] = v4f{0, 0, 0, 0};
-  auto issue = [&](int s) {
-    la.issue(step0 + s, sm.a[s & 1]);
-    lb.issue(step0 + s, sm.b[s & 1]);
-  };
-  if (steps > 0) issue(0);
-  for (int s = 0; s < steps; ++s) {
-    __builtin_amdgcn_s_waitcnt(0);
-    __syncthreads();
-    if (s + 1 < steps) issue(s + 1);
-    const uint8_t *a = sm.a[s & 1], *b = sm.b[s & 1];
-    Frag bf[FN];
+    for (int ni = 0; ni < FN; ++ni)
 #pragma unroll
-    for (int ni = 0; ni < FN; ++ni) bf[ni] = read_frag<KB, S::TN>(b, brow + ni * 16, lane);
+      for (int e = 0; e < F * F / 64; ++e) acc[mi][ni][e] = 0.0f;
+  auto issue = [&](int s) {
+    const int at = step0 + min(s, steps - 1);
+    la.issue(at, sm.a[s & 1]);
+    lb.issue(at, sm.b[s & 1]);
+  };
+  auto read_a = [&](int st, int mi) {
+    return read_frag<KA, S::TM, F>(sm.a[st], arow + mi * F, lane);
+  };
+  auto read_b = [&](int st, int ni) {
+    return read_frag<KB, S::TN, F>(sm.b[st], brow + ni * F, lane);
+  };
+  issue(0);
+  issue(1);
+  __builtin_amdgcn_s_waitcnt(0);
+  __syncthreads();
+  Frag<F> bf[FN], af = read_a(0, 0);
+#pragma unroll
+  for (int ni = 0; ni < FN; ++ni) bf[ni] = read_b(0, ni);
+  for (int s = 0; s < steps; ++s) {
+    const int st = s & 1;
 #pragma unroll
     for (int mi = 0; mi < FM; ++mi) {
-      const Frag af = read_frag<KA, S::TM>(a, arow + mi * 16, lane);
+      Frag<F> an;
+      if (mi < FM - 1) {
+        an = read_a(st, mi + 1);
+      } else {
+        __builtin_amdgcn_s_waitcnt(0);
+        __syncthreads();
+        issue(s + 2);
+        an = read_a(st ^ 1, 0);
+      }
+      __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-      for (int h = 0; h < 2; ++h)
+      for (int h = 0; h < kSteps; ++h)
 #pragma unroll
-        for (int ni = 0; ni < FN; ++ni) acc[mi][ni] = T::mfma(bf[ni].h[h], af.h[h], acc[mi][ni]);
+        for (int ni = 0; ni < FN; ++ni) {
+          acc[mi][ni] = T::mfma(bf[ni].h[h], af.h[h], acc[mi][ni]);
+          if (mi == FM - 1 && h == kSteps - 1) {
+            __builtin_amdgcn_sched_barrier(0);
+            bf[ni] = read_b(st ^ 1, ni);
+            __builtin_amdgcn_sched_barrier(0);
+          }
+        }
+      af = an;
     }
   }
+  __builtin_amdgcn_s_waitcnt(0);    // LDS is left with no load into it in flight
+#pragma unroll
+  for (int i = 0; i < FM; ++i)
+#pragma unroll
+    for (int j = 0; j < S::kQuads; ++j)
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+        out[i][j][r] = acc[i][j / (S::kQuads / FN)][j % (S::kQuads / FN) * 4 + r];
 }
 
 // Tile (tm, tn) of workgroup `bid` of tiles_m x tiles_n: workgroups go round-robin
@@ -382,27 +490,26 @@ struct Out {
 };
 
 template <typename T, typename S>
-__device__ __forceinline__ void store_tile(const Out &p, const v4f (&acc)[S::kFM][S::kFN],
-                                           int64_t m0, int64_t n0, int range) {
+__device__ __forceinline__ void store_tile(const Out &p, const typename S::Acc &acc, int64_t m0,
+                                           int64_t n0, int range) {
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int r16 = lane & 15, q = lane >> 4;
-  m0 += wave / S::kWN * (S::kFM * 16);
-  n0 += wave % S::kWN * (S::kFN * 16);
+  m0 += wave / S::kWN * S::kWaveM;
+  n0 += wave % S::kWN * S::kWaveN;
 #pragma unroll
-  for (int mi = 0; mi < S::kFM; ++mi) {
-    const int64_t m = m0 + mi * 16 + r16;
+  for (int i = 0; i < S::kRowsHeld; ++i) {
+    const int64_t m = m0 + S::row(i, lane);
     if (m >= p.rows) continue;
 #pragma unroll
-    for (int ni = 0; ni < S::kFN; ++ni) {
-      const int64_t n = n0 + ni * 16 + 4 * q;
+    for (int j = 0; j < S::kQuads; ++j) {
+      const int64_t n = n0 + S::col(j, lane);
       const int64_t left = p.cols - n;
       if (left <= 0) continue;
       if (p.ranges == 1) {
-        const float v[4] = {acc[mi][ni][0], acc[mi][ni][1], acc[mi][ni][2], acc[mi][ni][3]};
+        const float v[4] = {acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3]};
         store4<T>(p.out + m * p.cols + n, v, left);
       } else {
-        store4(p.parts + ((int64_t)range * p.rows + m) * p.cols + n, acc[mi][ni], left);
+        store4(p.parts + ((int64_t)range * p.rows + m) * p.cols + n, acc[i][j], left);
       }
     }
   }

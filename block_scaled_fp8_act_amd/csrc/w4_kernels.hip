@@ -10,6 +10,9 @@ using namespace t16;
 
 namespace {
 
+
+
+
 struct Weights {
   const uint8_t *codes;      // [rows, K / 2]
   const uint16_t *scale;     // [rows, K >> shift]
@@ -133,7 +136,8 @@ struct W4Smem : S::Smem {
   float scale[2][2][S::TN];      // by stage and half of its K
 };
 
-// A thread decodes half a stage of one row of W (32 codes, 16 bytes).
+// A thread decodes half a stage of one row of W (32 codes, 16 bytes); neighbouring
+// lanes take neighbouring rows, whose chunks fall into different banks.
 template <typename T, typename S>
 struct W4Loader {
   static_assert(S::kThreads == 2 * S::TN, "two threads a row");
@@ -145,12 +149,15 @@ struct W4Loader {
   v4u c;
   float s, z;
 
+  static __device__ __forceinline__ int tile_row() {
+    return (threadIdx.x >> 6) * 32 + (threadIdx.x & 31);
+  }
   // This thread's row of the tile is row `n` of the weights.
   __device__ __forceinline__ void at(const Weights &w, int64_t k, int64_t n) {
     K = k;
     shift = w.shift;
-    row = threadIdx.x >> 1;
-    half = threadIdx.x & 1;
+    row = tile_row();
+    half = (threadIdx.x >> 5) & 1;
     codes = w.codes + n * (K / 2) + half * 16;
     scale = w.scale + n * (K >> shift);
     zeros = w.zeros ? w.zeros + n * (K >> shift) : nullptr;
@@ -180,7 +187,7 @@ struct W4 : Weights {
   template <typename T, typename S>
   struct Pair : W4Loader<T, S> {
     __device__ __forceinline__ void init(const W4 &w, const GluArgs &p, int64_t n0, int, int) {
-      const PairRow<S> r(threadIdx.x >> 1);
+      const PairRow<S> r(W4Loader<T, S>::tile_row());
       this->at(w, p.K, r.half * p.I + min(n0 + r.c, p.I - 1));
     }
   };
@@ -190,11 +197,12 @@ struct W4 : Weights {
   // not wait for.
   template <typename T, typename S, typename LA, typename LB>
   static __device__ __forceinline__ void multiply(const LA &la, LB &lb, int step0, int steps,
-                                                  W4Smem<S> &sm, v4f (&acc)[S::kFM][S::kFN]) {
+                                                  W4Smem<S> &sm, typename S::Acc &acc) {
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     constexpr int FM = S::kFM, FN = S::kFN, kParts = G32 ? 2 : 1;
-    const int arow = wave / S::kWN * (FM * 16), brow = wave % S::kWN * (FN * 16);
+    static_assert(S::kF == 16, "a quad is a fragment's");
+    const int arow = wave / S::kWN * S::kWaveM, brow = wave % S::kWN * S::kWaveN;
 #pragma unroll
     for (int mi = 0; mi < FM; ++mi)
 #pragma unroll
@@ -214,11 +222,11 @@ struct W4 : Weights {
       lb.fetch(next);
       la.issue(next, sm.a[st ^ 1]);
       __builtin_amdgcn_sched_barrier(0);
-      Frag bf[FN];
+      Frag<16> bf[FN];
       v4f scale[FN][kParts];
 #pragma unroll
       for (int ni = 0; ni < FN; ++ni) {
-        bf[ni] = read_frag<kRows, S::TN, true>(sm.b[st], brow + ni * 16, lane);
+        bf[ni] = read_frag<kRows, S::TN, 16>(sm.b[st], brow + ni * 16, lane);
 #pragma unroll
         for (int h = 0; h < kParts; ++h)
           scale[ni][h] =
@@ -226,12 +234,12 @@ struct W4 : Weights {
       }
       // unit u: a row of fragments over a stage, or over half of one
       v4f part[2][FN];
-      Frag af;
+      Frag<16> af;
 #pragma unroll
       for (int u = 0; u <= FM * kParts; ++u) {
         const int mi = u / kParts, h = u % kParts;
         if (mi < FM) {
-          if (h == 0) af = read_frag<kRows, S::TM, true>(sm.a[st], arow + mi * 16, lane);
+          if (h == 0) af = read_frag<kRows, S::TM, 16>(sm.a[st], arow + mi * 16, lane);
 #pragma unroll
           for (int ni = 0; ni < FN; ++ni)
             part[u & 1][ni] = T::mfma(bf[ni].h[h], af.h[h], v4f{0, 0, 0, 0});
@@ -272,9 +280,9 @@ __global__ __launch_bounds__(S::kThreads) void w4_product_kernel(Operand a, W4<G
   Loader<kRows, S::TM, S::kWaves> la;
   W4Loader<T, S> lb;
   la.init(a, wave, lane);
-  lb.at(w, a.k, min(n0 + (int64_t)(threadIdx.x >> 1), p.cols - 1));
+  lb.at(w, a.k, min(n0 + (int64_t)W4Loader<T, S>::tile_row(), p.cols - 1));
   const int s0 = p.first_step(range);
-  v4f acc[S::kFM][S::kFN];
+  typename S::Acc acc;
   W4<G32>::template multiply<T, S>(la, lb, s0, p.first_step(range + 1) - s0, sm, acc);
   store_tile<T, S>(p, acc, m0, n0, range);
 }
@@ -510,7 +518,7 @@ hipError_t gated(const W4Call &c, int act, void *h, void *work, hipStream_t stre
   p.act = act;
   p.h = static_cast<uint16_t *>(h);
   p.parts = reinterpret_cast<float *>(s.base + s.used);
-  return launch_glu<T, false>(p, W4<G32>{weights(c)}, stream);
+  return launch_glu<T, false, Large, Small>(p, W4<G32>{weights(c)}, stream);
 }
 
 template <typename T>
