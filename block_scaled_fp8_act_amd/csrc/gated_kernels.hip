@@ -242,23 +242,16 @@ hipError_t align(const uint16_t *in, int64_t ld, int64_t rows, int64_t cols, uin
 template <typename T, Kind KA, Kind KB>
 hipError_t product(const Operand &a, const Operand &b, Out p, hipStream_t stream) {
   const Plan plan = plan_of(p.rows, p.cols, a.k);
-  p.steps = (int)tiles(a.k, kK);
-  p.ranges = plan.ranges;
-  p.tiles_m = (int)tiles(p.rows, plan.large ? Large::TM : Small::TM);
-  p.tiles_n = (int)tiles(p.cols, plan.large ? Large::TN : Small::TN);
-  const dim3 grid((unsigned)p.tiles_m * p.tiles_n * p.ranges);
-  if (plan.large) product_kernel<T, Large, KA, KB><<<grid, Large::kThreads, 0, stream>>>(a, b, p);
-  else product_kernel<T, Small, KA, KB><<<grid, Small::kThreads, 0, stream>>>(a, b, p);
+  with_shape(plan.shape, [&](auto shape) {
+    using S = decltype(shape);
+    const dim3 grid = p.tile<S>(plan, a.k);
+    product_kernel<T, S, KA, KB><<<grid, S::kThreads, 0, stream>>>(a, b, p);
+  });
   if (p.ranges > 1) {
     if (hipError_t e = hipGetLastError()) return e;
     join_kernel<T><<<groups(tiles(p.rows * p.cols, 4)), 256, 0, stream>>>(p);
   }
   return hipGetLastError();
-}
-
-size_t part_bytes(int64_t rows, int64_t cols, int64_t k) {
-  const int r = plan_of(rows, cols, k).ranges;
-  return r == 1 ? 0 : (size_t)r * rows * cols * sizeof(float);
 }
 
 hipError_t zero(void *out, int64_t n, hipStream_t stream) {
@@ -324,7 +317,7 @@ hipError_t forward(const GatedCall &c, void *h, void *factors, void *work, hipSt
   GluArgs p = glu_args(c, in, s);
   p.h = static_cast<uint16_t *>(h);
   p.factors = static_cast<uint8_t *>(factors);
-  return launch_glu<T, false, Large, Small>(p, Dense{in.w, in.ldw}, stream);
+  return launch_glu<T, false>(p, Dense{in.w, in.ldw}, stream);
 }
 
 template <typename T>
@@ -346,7 +339,7 @@ hipError_t backward(const GatedCall &c, const void *dh, const void *factors, voi
     p.dh = static_cast<const uint16_t *>(dh);
     p.dgu = dgu;
     p.ld_dgu = ld;
-    if (hipError_t e = launch_glu<T, true, Large, Small>(p, Dense{in.w, in.ldw}, stream)) return e;
+    if (hipError_t e = launch_glu<T, true>(p, Dense{in.w, in.ldw}, stream)) return e;
   }
   if (dx) {
     const Out o{c.M, c.K, static_cast<uint16_t *>(dx), parts};
@@ -366,16 +359,14 @@ hipError_t backward(const GatedCall &c, const void *dh, const void *factors, voi
 }  // namespace
 
 bool gated_fits(int64_t M, int64_t I, int64_t K) {
-  const int64_t most = (int64_t(1) << 32) / Large::kThreads;   // workgroups of a grid
-  return grid_of<Large>(M, 2 * I) < most && grid_of<Large>(M, K) < most &&
-         grid_of<Large>(2 * I, K) < most;
+  return grid_fits(M, 2 * I) && grid_fits(M, K) && grid_fits(2 * I, K);
 }
 
 size_t gated_workspace_bytes(int64_t M, int64_t I, int64_t K, int64_t ldx) {
   if (M <= kFewRows) return 0;
   Space s{nullptr, 0};
   inputs_space(M, I, K, ldx, s);
-  return s.used + glu_part_bytes(M, I, up(K, 8));
+  return s.used + part_bytes(M, 2 * I, up(K, 8));
 }
 
 hipError_t launch_gated(const GatedCall &c, void *h, void *factors, void *work,
@@ -390,7 +381,7 @@ size_t gated_backward_workspace_bytes(int64_t M, int64_t I, int64_t K, int64_t l
   Space s{nullptr, 0};
   inputs_space(M, I, K, ldx, s);
   s.take((size_t)M * up(2 * I, 8) * 2);
-  return s.used + std::max({glu_part_bytes(M, I, up(K, 8)),
+  return s.used + std::max({part_bytes(M, 2 * I, up(K, 8)),
                             dx ? part_bytes(M, K, up(2 * I, 8)) : 0,
                             dw ? part_bytes(2 * I, K, M) : 0});
 }

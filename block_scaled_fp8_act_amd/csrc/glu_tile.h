@@ -145,28 +145,24 @@ __global__ __launch_bounds__(256) void glu_join_kernel(GluArgs p) {
   }
 }
 
-// Launches for a plan; p's sizes, pointers and act are set.
-template <typename T, bool GRAD, typename L, typename S, typename W>
+// Launches by plan; p's sizes, pointers and act are set.
+template <typename T, bool GRAD, typename W>
 hipError_t launch_glu(GluArgs p, const W &w, hipStream_t stream) {
-  static_assert(L::TM == Large::TM && L::TN == Large::TN && S::TM == Small::TM &&
-                S::TN == Small::TN, "the plan's tiles");
   const Plan plan = plan_of(p.M, 2 * p.I, p.K);
-  p.steps = (int)tiles(p.K, kK);
-  p.ranges = plan.ranges;
-  p.tiles_m = (int)tiles(p.M, plan.large ? L::TM : S::TM);
-  p.tiles_n = (int)tiles(p.I, (plan.large ? L::TN : S::TN) / 2);
-  const dim3 grid((unsigned)p.tiles_m * p.tiles_n * p.ranges);
-  if (plan.large) glu_kernel<T, L, GRAD, W><<<grid, L::kThreads, 0, stream>>>(p, w);
-  else glu_kernel<T, S, GRAD, W><<<grid, S::kThreads, 0, stream>>>(p, w);
+  with_shape(plan.shape, [&](auto shape) {
+    using S = decltype(shape);
+    p.steps = (int)tiles(p.K, kK);
+    p.ranges = plan.ranges;
+    p.tiles_m = (int)tiles(p.M, S::TM);
+    p.tiles_n = (int)tiles(p.I, S::TN / 2);
+    glu_kernel<T, S, GRAD, W>
+        <<<dim3((unsigned)p.tiles_m * p.tiles_n * p.ranges), S::kThreads, 0, stream>>>(p, w);
+  });
   if (p.ranges > 1) {
     if (hipError_t e = hipGetLastError()) return e;
     glu_join_kernel<T, GRAD><<<groups(p.M * tiles(p.I, 4)), 256, 0, stream>>>(p);
   }
   return hipGetLastError();
-}
-inline size_t glu_part_bytes(int64_t M, int64_t I, int64_t K) {
-  const int r = plan_of(M, 2 * I, K).ranges;
-  return r == 1 ? 0 : (size_t)r * M * 2 * I * sizeof(float);
 }
 
 }  // namespace t16

@@ -35,7 +35,7 @@ namespace t16 {
 
 constexpr int kCUs = 256;
 inline int64_t up(int64_t a, int64_t b) { return (a + b - 1) / b * b; }
-inline int64_t tiles(int64_t n, int64_t t) { return (n + t - 1) / t; }
+constexpr int64_t tiles(int64_t n, int64_t t) { return (n + t - 1) / t; }
 
 // 16 and 8 bytes at any even address (gfx950's global loads and stores take those).
 typedef unsigned v4u_any __attribute__((ext_vector_type(4), aligned(2)));
@@ -122,8 +122,12 @@ __device__ __forceinline__ void dma16(v4u r, uint32_t off, const void *lds) {
 __device__ __forceinline__ int swz_f(int row) { return (row >> 1) & 7; }
 // 32 lanes of a transposing read take 32 bytes of each of K rows k .. k + 3, and with
 // F = 16 of those 8 further, with F = 32 the 32 bytes beside them: either way eight
-// different pairs of the 256 bytes that the banks span.
-__device__ __forceinline__ int col_f(int k) { return ((k & 3) << 1) | ((k >> 3) & 1); }
+// different pairs of the 256 bytes that the banks span (of all there are, in
+// operands of fewer than 128 rows).
+template <int ROWS>
+__device__ __forceinline__ int col_f(int k) {
+  return (((k & 3) << 1) | ((k >> 3) & 1)) & (ROWS / 16 - 1);
+}
 
 // A workgroup's tile: WM x WN waves of FM x FN fragments of F x F (16 or 32).  A
 // lane holds its outputs by fours: kRows rows F * i + lane % F, in each kQuads runs
@@ -145,10 +149,12 @@ struct Shape {
     uint8_t b[2][TN * kK * 2];
   };
 };
-// 256 x 256 on 8 waves (a wave 128 x 64), and 128 x 128 on 4 (64 x 64) for grids
-// that the large tile would leave mostly idle.
+// 256 x 256 on 8 waves (a wave 128 x 64); 128 x 128, 64 x 128 and 32 x 128 on 4 for
+// grids that the larger tiles would leave mostly idle, and for few rows.
 using Large = Shape<16, 2, 4, 8, 4>;
 using Small = Shape<16, 2, 2, 4, 4>;
+using Low = Shape<16, 2, 2, 2, 4>;
+using Flat = Shape<16, 2, 2, 1, 4>;
 
 // An operand in memory: `rows` of it along the output, `k` along the sum, both
 // counted from p; `ld` elements from one row of memory to the next.  Rows of
@@ -201,7 +207,7 @@ struct Loader {
       } else {
         constexpr int kChunks = ROWS / 8;     // 16-byte chunks of a K row
         const int at = (kDma * wave + i) * 64 + lane;
-        const int kr = at / kChunks, c = (at % kChunks) ^ (col_f(at / kChunks) << 1);
+        const int kr = at / kChunks, c = (at % kChunks) ^ (col_f<ROWS>(at / kChunks) << 1);
         off[i] = c * 8 < o.rows ? kr * (uint32_t)o.ld * 2 + c * 16 : kOut;
       }
     }
@@ -256,7 +262,7 @@ __device__ __forceinline__ Frag<F> read_frag(const uint8_t *stage, int row0, int
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
         const int k = 512 / F * h + 8 * q + 4 * j + (r >> 2);
-        const uint8_t *at = stage + k * (ROWS * 2) + ((row16 ^ col_f(k)) << 5) + (r & 3) * 8;
+        const uint8_t *at = stage + k * (ROWS * 2) + ((row16 ^ col_f<ROWS>(k)) << 5) + (r & 3) * 8;
         const v2u u = __builtin_bit_cast(
             v2u, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s *)at));
         f.h[h][2 * j] = u[0];
@@ -456,24 +462,69 @@ struct Space {
   }
 };
 
-template <typename S>
-int64_t grid_of(int64_t rows, int64_t cols) {
-  return tiles(rows, S::TM) * tiles(cols, S::TN);
+// Whether a product's launches stay below 2^32 threads, whatever its plan: the
+// smaller tiles (half the threads or less) are launched for grids of a few thousand,
+// and for few rows, where they are at most twice the large ones.
+inline bool grid_fits(int64_t rows, int64_t cols) {
+  return tiles(rows, Large::TM) * tiles(cols, Large::TN) <
+         (int64_t(1) << 32) / Large::kThreads;
 }
 
-// How a product of rows x cols outputs over k is tiled.
+// How a product of rows x cols outputs over k is tiled: the shape, and ranges of K
+// on workgroups of their own (fp32 parts, added in order by a second kernel) where
+// the tiles alone leave the chip idle.  The plan with the least time by a model
+// whose constants are measurements: a workgroup alone on its compute unit takes
+// `alone` us a stage, several take `shared` each (both follow the bytes that pass
+// into LDS, 50 to 58 GB/s a compute unit), `start` covers launch, first stage and
+// epilogue, and the parts travel twice at 5 TB/s.
+enum ShapeId { kLarge, kSmall, kLow, kFlat };
 struct Plan {
-  bool large;
-  int ranges;     // of K, a workgroup each
+  ShapeId shape;
+  int ranges;
 };
 inline Plan plan_of(int64_t rows, int64_t cols, int64_t k) {
-  // 256 x 256 tiles where they fill most of the chip
-  if (grid_of<Large>(rows, cols) >= 192) return {true, 1};
-  // ranges of K: enough workgroups for two a compute unit, at least 8 stages each
-  const int64_t grid = grid_of<Small>(rows, cols), steps = tiles(k, kK);
-  int64_t r = 2 * kCUs / grid;
-  r = r < steps / 8 ? r : steps / 8;
-  return {false, (int)(r > 1 ? r : 1)};
+  struct Cost {
+    int tm, tn;
+    double alone, shared, start;
+  };
+  static constexpr Cost kCosts[] = {{Large::TM, Large::TN, 1.25, 1.45, 9.0},
+                                    {Small::TM, Small::TN, 0.64, 0.55, 4.5},
+                                    {Low::TM, Low::TN, 0.50, 0.42, 4.5},
+                                    {Flat::TM, Flat::TN, 0.45, 0.36, 4.5}};
+  const int64_t steps = tiles(k, kK);
+  Plan best{kSmall, 1};
+  double least = 1e30;
+  for (int s = 0; s < 4; ++s) {
+    const Cost &c = kCosts[s];
+    // a flatter tile only reads the columns' operand more often
+    if ((s == kLow && rows > 2 * Low::TM) || (s == kFlat && rows > 2 * Flat::TM)) continue;
+    const int64_t grid = tiles(rows, c.tm) * tiles(cols, c.tn);
+    for (int r = 1; r <= 16 && (r == 1 || (steps / r >= 4 && grid * r <= 4 * kCUs)); ++r) {
+      const int64_t n = tiles(grid * r, kCUs);
+      const double per = n == 1 && (s != kLarge || grid * r <= kCUs / 2) ? c.alone : n * c.shared;
+      double t = c.start + per * tiles(steps, r);
+      if (r > 1) t += 4.0 + 8e-6 / 5 * r * (double)rows * (double)cols;
+      if (t < least) {
+        least = t;
+        best = {(ShapeId)s, r};
+      }
+    }
+  }
+  return best;
+}
+inline size_t part_bytes(int64_t rows, int64_t cols, int64_t k) {
+  const int r = plan_of(rows, cols, k).ranges;
+  return r == 1 ? 0 : (size_t)r * rows * cols * sizeof(float);
+}
+// f of the plan's shape (a value of its type).
+template <typename F>
+void with_shape(ShapeId s, F f) {
+  switch (s) {
+    case kLarge: f(Large{}); break;
+    case kSmall: f(Small{}); break;
+    case kLow: f(Low{}); break;
+    case kFlat: f(Flat{}); break;
+  }
 }
 
 // A product's outputs, or its parts.
@@ -484,6 +535,15 @@ struct Out {
   int steps, ranges;
   int tiles_m, tiles_n;
 
+  // Sets the plan's tiling over k; the grid.
+  template <typename S>
+  dim3 tile(const Plan &plan, int64_t k) {
+    steps = (int)tiles(k, kK);
+    ranges = plan.ranges;
+    tiles_m = (int)tiles(rows, S::TM);
+    tiles_n = (int)tiles(cols, S::TN);
+    return dim3((unsigned)tiles_m * tiles_n * ranges);
+  }
   __device__ __forceinline__ int first_step(int range) const {
     return (int)((int64_t)steps * range / ranges);
   }

@@ -488,14 +488,12 @@ hipError_t linear(const W4Call &c, void *y, void *work, hipStream_t stream) {
   if (hipError_t e = lay_x(c, a, s, stream)) return e;
   const Plan plan = plan_of(c.M, c.rows, c.K);
   Out p{c.M, c.rows, static_cast<uint16_t *>(y), reinterpret_cast<float *>(s.base + s.used)};
-  p.steps = (int)tiles(c.K, kK);
-  p.ranges = plan.ranges;
-  p.tiles_m = (int)tiles(p.rows, plan.large ? Large::TM : Small::TM);
-  p.tiles_n = (int)tiles(p.cols, plan.large ? Large::TN : Small::TN);
-  const dim3 grid((unsigned)p.tiles_m * p.tiles_n * p.ranges);
   const W4<G32> w{weights(c)};
-  if (plan.large) w4_product_kernel<T, Large, G32><<<grid, Large::kThreads, 0, stream>>>(a, w, p);
-  else w4_product_kernel<T, Small, G32><<<grid, Small::kThreads, 0, stream>>>(a, w, p);
+  with_shape(plan.shape, [&](auto shape) {
+    using S = decltype(shape);
+    const dim3 grid = p.tile<S>(plan, c.K);
+    w4_product_kernel<T, S, G32><<<grid, S::kThreads, 0, stream>>>(a, w, p);
+  });
   if (p.ranges > 1) {
     if (hipError_t e = hipGetLastError()) return e;
     join_kernel<T><<<groups(tiles(p.rows * p.cols, 4)), 256, 0, stream>>>(p);
@@ -518,7 +516,7 @@ hipError_t gated(const W4Call &c, int act, void *h, void *work, hipStream_t stre
   p.act = act;
   p.h = static_cast<uint16_t *>(h);
   p.parts = reinterpret_cast<float *>(s.base + s.used);
-  return launch_glu<T, false, Large, Small>(p, W4<G32>{weights(c)}, stream);
+  return launch_glu<T, false>(p, W4<G32>{weights(c)}, stream);
 }
 
 template <typename T>
@@ -552,22 +550,21 @@ hipError_t launch_w4_dequant(const W4Call &c, void *w, hipStream_t stream) {
 }
 
 bool w4_fits(int64_t M, int64_t rows) {
-  return rows < (int64_t(1) << 28) && grid_of<Large>(M, rows) < (int64_t(1) << 32) / Large::kThreads;
+  return rows < (int64_t(1) << 28) && grid_fits(M, rows);
 }
 
 size_t w4_linear_workspace_bytes(int64_t M, int64_t N, int64_t K, int64_t ldx) {
   if (M <= kFewRows) return 0;
   Space s{nullptr, 0};
   x_space(M, K, ldx, s);
-  const int r = plan_of(M, N, K).ranges;
-  return s.used + (r == 1 ? 0 : (size_t)r * M * N * sizeof(float));
+  return s.used + part_bytes(M, N, K);
 }
 
 size_t w4_gated_workspace_bytes(int64_t M, int64_t I, int64_t K, int64_t ldx) {
   if (M <= kFewRows) return 0;
   Space s{nullptr, 0};
   x_space(M, K, ldx, s);
-  return s.used + glu_part_bytes(M, I, K);
+  return s.used + part_bytes(M, 2 * I, K);
 }
 
 hipError_t launch_w4_linear(const W4Call &c, void *y, void *work, hipStream_t stream) {
