@@ -27,6 +27,8 @@ struct Dense {
   const uint16_t *w;
   int64_t ld;
   template <typename S>
+  using Place = S;
+  template <typename S>
   using Smem = typename S::Smem;
   template <typename T, typename S, typename LA, typename LB>
   static __device__ __forceinline__ void multiply(const LA &la, const LB &lb, int step0, int steps,
@@ -222,7 +224,7 @@ __global__ __launch_bounds__(S::kThreads) void product_kernel(Operand a, Operand
   const int s0 = p.first_step(range);
   typename S::Acc acc;
   multiply<T, S, KA, KB>(la, lb, s0, p.first_step(range + 1) - s0, sm, acc);
-  store_tile<T, S>(p, acc, m0, n0, range);
+  store_tile<T, S>(p, acc, m0, n0, range, reinterpret_cast<uint8_t *>(&sm));
 }
 
 __global__ __launch_bounds__(256) void zero_kernel(uint16_t *out, int64_t n) {

@@ -41,68 +41,94 @@ struct PairRow {
   }
 };
 
-// Four outputs of row m at column n from their g and u.
-template <typename T, int ACT, bool GRAD>
-__device__ __forceinline__ void glu_store4(const GluArgs &p, int64_t m, int64_t n, v4f g, v4f u) {
-  const int64_t left = p.I - n;
-  float a[4], f[4];
-  if constexpr (GRAD) {
-    float d[4];
-    load4<T>(p.dh + m * p.I + n, d, left);
+// What becomes of a g and its u: forward h (and the saved factors), or from the
+// gradient d of h those of g and u.
+template <int ACT>
+__device__ __forceinline__ void glu(v4f g, v4f u, float (&h)[4]) {
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      f[r] = d[r] * (u[r] * act_slope<ACT>(g[r]));
-      a[r] = d[r] * act_value<ACT>(g[r]);
-    }
-    uint16_t *row = p.dgu + m * p.ld_dgu;
-    store4<T>(row + n, f, left);
-    store4<T>(row + p.I + n, a, left);
-    if (left <= 4)
-      for (int64_t c = 2 * p.I; c < p.ld_dgu; ++c) row[c] = 0;
-  } else {
-    float h[4];
+  for (int r = 0; r < 4; ++r) h[r] = act_value<ACT>(g[r]) * u[r];
+}
+template <int ACT>
+__device__ __forceinline__ void glu_factors(v4f g, v4f u, float (&f)[4], float (&a)[4]) {
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      a[r] = act_value<ACT>(g[r]);
-      h[r] = a[r] * u[r];
-    }
-    store4<T>(p.h + m * p.I + n, h, left);
-    if (p.factors) {
-#pragma unroll
-      for (int r = 0; r < 4; ++r) f[r] = u[r] * act_slope<ACT>(g[r]);
-      uint8_t *row = p.factors + m * factor_row(p.I) + n * 3;
-      store_24(row, f);      // (past the last output: of zero sums)
-      store_24(row + factor_half(p.I), a);
-    }
+  for (int r = 0; r < 4; ++r) {
+    f[r] = u[r] * act_slope<ACT>(g[r]);
+    a[r] = act_value<ACT>(g[r]);
   }
 }
+__device__ __forceinline__ void save_factors(const GluArgs &p, int64_t m, int64_t n,
+                                             const float (&f)[4], const float (&a)[4]) {
+  uint8_t *row = p.factors + m * factor_row(p.I) + n * 3;
+  store_24(row, f);      // (past the last output: of zero sums)
+  store_24(row + factor_half(p.I), a);
+}
 
+// The tile's outputs from (m0, n0) on; the wave's begin row, col further.
 template <typename T, typename S, int ACT, bool GRAD>
 __device__ __forceinline__ void glu_store(const GluArgs &p, const typename S::Acc &acc, int64_t m0,
-                                          int64_t n0, int lane) {
+                                          int64_t n0, int row, int col, uint8_t *lds) {
+  constexpr int kHalf = S::kFN / 2, kCols = S::TN / 2;
+  static_assert(!(S::kAcross && GRAD), "factors and d_h are taken four columns at a time");
+  const int lane = threadIdx.x & 63;
+  __syncthreads();      // every wave is past its last stage
 #pragma unroll
-  for (int i = 0; i < S::kRowsHeld; ++i) {
-    const int64_t m = m0 + S::row(i, lane);
-    if (m >= p.M) continue;
+  for (int i = 0; i < S::kFM; ++i)
 #pragma unroll
-    for (int j = 0; j < S::kQuads / 2; ++j) {
-      const int64_t n = n0 + S::col(j, lane);
-      if (n < p.I) glu_store4<T, ACT, GRAD>(p, m, n, acc[i][j], acc[i][j + S::kQuads / 2]);
+    for (int j = 0; j < kHalf; ++j) {
+      const v4f g = acc[i][j], u = acc[i][j + kHalf];
+      const int64_t m = m0 + row + S::row(i, 0, lane), n = n0 + col + S::col(j, 0, lane);
+      const bool in = m < p.M && n < p.I;
+      if constexpr (GRAD) {
+        float d[4] = {0, 0, 0, 0}, f[4], a[4];
+        if (in) load4<T>(p.dh + m * p.I + n, d, p.I - n);
+        glu_factors<ACT>(g, u, f, a);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          f[r] *= d[r];
+          a[r] *= d[r];
+        }
+        stage4<T, S, kCols>(lds, row, col, i, j, f, lane);
+        stage4<T, S, kCols>(lds + S::TM * kCols * 2, row, col, i, j, a, lane);
+      } else {
+        float h[4];
+        glu<ACT>(g, u, h);
+        stage4<T, S, kCols>(lds, row, col, i, j, h, lane);
+        if constexpr (!S::kAcross) {
+          if (p.factors && in) {
+            float f[4], a[4];
+            glu_factors<ACT>(g, u, f, a);
+            save_factors(p, m, n, f, a);
+          }
+        }
+      }
     }
+  __syncthreads();
+  const int64_t rows = p.M - m0, cols = p.I - n0;
+  if constexpr (GRAD) {
+    uint16_t *out = p.dgu + m0 * p.ld_dgu + n0;
+    store_staged<S::kThreads, S::TM, kCols>(lds, out, p.ld_dgu, rows, cols);
+    store_staged<S::kThreads, S::TM, kCols>(lds + S::TM * kCols * 2, out + p.I, p.ld_dgu, rows,
+                                            cols);
+    if (cols <= kCols)      // the rows end in zeros
+      for (int r = threadIdx.x; r < S::TM && r < rows; r += S::kThreads)
+        for (int64_t c = 2 * p.I; c < p.ld_dgu; ++c) p.dgu[(m0 + r) * p.ld_dgu + c] = 0;
+  } else {
+    store_staged<S::kThreads, S::TM, kCols>(lds, p.h + m0 * p.I + n0, p.I, rows, cols);
   }
 }
 
 // W::Pair<T, S> loads the tile's rows of the weights (init(w, p, n0, wave, lane)),
-// W::multiply<T, S> forms the tile's sums with it, in W::Smem<S>.
-template <typename T, typename S, bool GRAD, typename W>
-__global__ __launch_bounds__(S::kThreads) void glu_kernel(GluArgs p, W w) {
+// W::multiply<T, S> forms the tile's sums with it, in W::Smem<S>, placed as W::Place<S>.
+template <typename T, typename Tile, bool GRAD, typename W>
+__global__ __launch_bounds__(Tile::kThreads) void glu_kernel(GluArgs p, W w) {
+  using S = typename W::template Place<Tile>;
   __shared__ typename W::template Smem<S> sm;
   const int tiles = p.tiles_m * p.tiles_n, range = blockIdx.x / tiles;
   int tm, tn;
   tile_of(blockIdx.x - range * tiles, p.tiles_m, p.tiles_n, tm, tn);
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  int64_t m = (int64_t)tm * S::TM, n = (int64_t)tn * (S::TN / 2);
+  const int64_t m = (int64_t)tm * S::TM, n = (int64_t)tn * (S::TN / 2);
   Loader<kRows, S::TM, S::kWaves> la;
   la.init(Operand{p.x + m * p.ldx, p.ldx, min(p.M - m, (int64_t)S::TM), p.K}, wave, lane);
   typename W::template Pair<T, S> lb;
@@ -111,27 +137,52 @@ __global__ __launch_bounds__(S::kThreads) void glu_kernel(GluArgs p, W w) {
   const int s1 = (int)((int64_t)p.steps * (range + 1) / p.ranges);
   typename S::Acc acc;
   W::template multiply<T, S>(la, lb, s0, s1 - s0, sm, acc);
-  m += wave / S::kWN * S::kWaveM;
-  n += wave % S::kWN * (S::kWaveN / 2);
+  const int row = wave_row<S>(), col = wave_col<S>() / 2;
   if (p.ranges > 1) {
-    constexpr int kHalf = S::kQuads / 2;
+    constexpr int kHalf = S::kFN / 2;
+    float *parts = p.parts + ((int64_t)range * p.M + m + row) * 2 * p.I + n + col;
 #pragma unroll
-    for (int i = 0; i < S::kRowsHeld; ++i)
+    for (int i = 0; i < S::kFM; ++i)
 #pragma unroll
-      for (int j = 0; j < S::kQuads; ++j) {
-        const int64_t row = m + S::row(i, lane), col = n + S::col(j % kHalf, lane);
-        if (row < p.M && col < p.I)
-          store4(p.parts + ((int64_t)range * p.M + row) * 2 * p.I + (j >= kHalf ? p.I : 0) + col,
-                 acc[i][j], p.I - col);
-      }
+      for (int j = 0; j < S::kFN; ++j)
+        store_part<S>(parts + i * 32 * p.I + (j >= kHalf ? p.I : 0) + j % kHalf * 16, 2 * p.I,
+                      p.M - m - row - i * 16, p.I - n - col - j % kHalf * 16, acc[i][j], lane);
     return;
   }
-  if (p.act == kSilu) glu_store<T, S, kSilu, GRAD>(p, acc, m, n, lane);
-  else if (p.act == kGelu) glu_store<T, S, kGelu, GRAD>(p, acc, m, n, lane);
-  else glu_store<T, S, kGeluTanh, GRAD>(p, acc, m, n, lane);
+  uint8_t *lds = reinterpret_cast<uint8_t *>(&sm);
+  if (p.act == kSilu) glu_store<T, S, kSilu, GRAD>(p, acc, m, n, row, col, lds);
+  else if (p.act == kGelu) glu_store<T, S, kGelu, GRAD>(p, acc, m, n, row, col, lds);
+  else glu_store<T, S, kGeluTanh, GRAD>(p, acc, m, n, row, col, lds);
 }
 
 // The outputs of parts, four a thread.
+template <typename T, int ACT, bool GRAD>
+__device__ __forceinline__ void glu_store4(const GluArgs &p, int64_t m, int64_t n, v4f g, v4f u) {
+  const int64_t left = p.I - n;
+  float a[4], f[4];
+  if constexpr (GRAD) {
+    float d[4];
+    load4<T>(p.dh + m * p.I + n, d, left);
+    glu_factors<ACT>(g, u, f, a);
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      f[r] *= d[r];
+      a[r] *= d[r];
+    }
+    uint16_t *row = p.dgu + m * p.ld_dgu;
+    store4<T>(row + n, f, left);
+    store4<T>(row + p.I + n, a, left);
+    if (left <= 4)
+      for (int64_t c = 2 * p.I; c < p.ld_dgu; ++c) row[c] = 0;
+  } else {
+    glu<ACT>(g, u, a);
+    store4<T>(p.h + m * p.I + n, a, left);
+    if (p.factors) {
+      glu_factors<ACT>(g, u, f, a);
+      save_factors(p, m, n, f, a);
+    }
+  }
+}
 template <typename T, bool GRAD>
 __global__ __launch_bounds__(256) void glu_join_kernel(GluArgs p) {
   const int64_t quads = (p.I + 3) / 4, step = p.M * 2 * p.I;

@@ -13,9 +13,9 @@
 //   kCols  [64 of K][rows], 32-byte pairs p of K row k kept at p ^ col_f(k); a
 //          fragment is four ds_read_b64_tr_b16 a lane, which transpose 4 x 16
 //          values among 16 lanes.
-// Lane l of a matrix instruction on F x F outputs (16 x 16 x 32 or 32 x 32 x 16)
-// holds 8 values of K of the operand's row l % F, from K = 8 (l / F) of the
-// instruction's.
+// Lane l of a matrix instruction (16 x 16 outputs, 32 of K) holds 8 values of K of
+// the operand's row l % 16, from K = 8 (l / 16) of the instruction's.  (On the 32 x 32
+// form the same tiles measured 10-15 % slower.)
 #pragma once
 
 #include <type_traits>
@@ -29,7 +29,6 @@ typedef unsigned v2u __attribute__((ext_vector_type(2)));
 typedef short v4s __attribute__((ext_vector_type(4)));
 typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
 typedef _Float16 v8h __attribute__((ext_vector_type(8)));
-typedef float v16f __attribute__((ext_vector_type(16)));
 
 namespace t16 {
 
@@ -51,10 +50,6 @@ struct Bf16 {
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8bf, a),
                                                    __builtin_bit_cast(v8bf, b), c, 0, 0, 0);
   }
-  static __device__ __forceinline__ v16f mfma(v4u a, v4u b, v16f c) {
-    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(v8bf, a),
-                                                   __builtin_bit_cast(v8bf, b), c, 0, 0, 0);
-  }
 };
 struct F16 {
   static __device__ __forceinline__ uint32_t bits(float f) {
@@ -65,10 +60,6 @@ struct F16 {
   }
   static __device__ __forceinline__ v4f mfma(v4u a, v4u b, v4f c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(v8h, a),
-                                                  __builtin_bit_cast(v8h, b), c, 0, 0, 0);
-  }
-  static __device__ __forceinline__ v16f mfma(v4u a, v4u b, v16f c) {
-    return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(v8h, a),
                                                   __builtin_bit_cast(v8h, b), c, 0, 0, 0);
   }
 };
@@ -120,41 +111,45 @@ __device__ __forceinline__ void dma16(v4u r, uint32_t off, const void *lds) {
 // and compute unit measured, half that with row & 7, or with the fp8 tiles' order,
 // whose lanes take other chunks.
 __device__ __forceinline__ int swz_f(int row) { return (row >> 1) & 7; }
-// 32 lanes of a transposing read take 32 bytes of each of K rows k .. k + 3, and with
-// F = 16 of those 8 further, with F = 32 the 32 bytes beside them: either way eight
-// different pairs of the 256 bytes that the banks span (of all there are, in
-// operands of fewer than 128 rows).
+// 32 lanes of a transposing read take 32 bytes of each of K rows k .. k + 3 and of
+// those 8 further: eight different pairs of the 256 bytes that the banks span (of all
+// there are, in operands of fewer than 128 rows).
 template <int ROWS>
 __device__ __forceinline__ int col_f(int k) {
   return (((k & 3) << 1) | ((k >> 3) & 1)) & (ROWS / 16 - 1);
 }
 
-// A workgroup's tile: WM x WN waves of FM x FN fragments of F x F (16 or 32).  A
-// lane holds its outputs by fours: kRows rows F * i + lane % F, in each kQuads runs
-// of four columns from col(j).
-template <int F, int WM, int WN, int FM, int FN>
+// A workgroup's tile: WM x WN waves of FM x FN fragments of 16 x 16.  A lane holds
+// four outputs of each fragment (i, j): of one row, neighbouring columns, or (ACROSS,
+// where the products with the operands exchanged are formed) of one column,
+// neighbouring rows; row(i, r, lane) and col(j, r, lane) are the r-th's place.
+template <int WM, int WN, int FM, int FN, bool ACROSS = false>
 struct Shape {
-  static constexpr int kF = F, kFM = FM, kFN = FN, kWM = WM, kWN = WN;
+  static constexpr int kFM = FM, kFN = FN, kWM = WM, kWN = WN;
+  static constexpr bool kAcross = ACROSS;
   static constexpr int kWaves = WM * WN, kThreads = kWaves * 64;
-  static constexpr int kWaveM = FM * F, kWaveN = FN * F;
+  static constexpr int kWaveM = FM * 16, kWaveN = FN * 16;
   static constexpr int TM = WM * kWaveM, TN = WN * kWaveN;
-  static constexpr int kRowsHeld = FM, kQuads = FN * F * F / 256;
-  using Acc = v4f[kRowsHeld][kQuads];
-  static __device__ __forceinline__ int row(int i, int lane) { return i * F + lane % F; }
-  static __device__ __forceinline__ int col(int j, int lane) {
-    return F == 16 ? 16 * j + 4 * (lane >> 4) : 32 * (j / 4) + 8 * (j % 4) + 4 * (lane >> 5);
+  using Across = Shape<WM, WN, FM, FN, true>;
+  using Acc = v4f[FM][FN];
+  static __device__ __forceinline__ int row(int i, int r, int lane) {
+    return 16 * i + (ACROSS ? 4 * (lane >> 4) + r : lane & 15);
+  }
+  static __device__ __forceinline__ int col(int j, int r, int lane) {
+    return 16 * j + (ACROSS ? lane & 15 : 4 * (lane >> 4) + r);
   }
   struct Smem {
     uint8_t a[2][TM * kK * 2];
     uint8_t b[2][TN * kK * 2];
   };
+  static_assert(sizeof(Smem) >= TM * TN * 2, "room for the outputs on their way out");
 };
 // 256 x 256 on 8 waves (a wave 128 x 64); 128 x 128, 64 x 128 and 32 x 128 on 4 for
 // grids that the larger tiles would leave mostly idle, and for few rows.
-using Large = Shape<16, 2, 4, 8, 4>;
-using Small = Shape<16, 2, 2, 4, 4>;
-using Low = Shape<16, 2, 2, 2, 4>;
-using Flat = Shape<16, 2, 2, 1, 4>;
+using Large = Shape<2, 4, 8, 4>;
+using Small = Shape<2, 2, 4, 4>;
+using Low = Shape<2, 2, 2, 4>;
+using Flat = Shape<2, 2, 1, 4>;
 
 // An operand in memory: `rows` of it along the output, `k` along the sum, both
 // counted from p; `ld` elements from one row of memory to the next.  Rows of
@@ -237,32 +232,29 @@ struct Loader {
   }
 };
 
-// A fragment of F rows over a stage: F / 8 instructions' operands.
-template <int F>
+// A fragment of 16 rows over a stage: two instructions' operands.
 struct Frag {
-  static constexpr int kSteps = F / 8;
-  v4u h[kSteps];
+  v4u h[2];
 };
 
-// The fragment of the F rows from `row0` of a stage of ROWS rows.
-template <Kind KIND, int ROWS, int F>
-__device__ __forceinline__ Frag<F> read_frag(const uint8_t *stage, int row0, int lane) {
-  Frag<F> f;
-  constexpr int kSteps = Frag<F>::kSteps;
-  const int q = lane / F;               // of the 512 / F values of an instruction's K
+// The fragment of the 16 rows from `row0` of a stage of ROWS rows.
+template <Kind KIND, int ROWS>
+__device__ __forceinline__ Frag read_frag(const uint8_t *stage, int row0, int lane) {
+  Frag f;
+  const int r = lane & 15, q = lane >> 4;
   if constexpr (KIND == kRows) {
-    const int row = row0 + lane % F, s = swz_f(row);
+    const int row = row0 + r, s = swz_f(row);
 #pragma unroll
-    for (int h = 0; h < kSteps; ++h)
-      f.h[h] = *reinterpret_cast<const v4u *>(stage + row * 128 + (((64 / F * h + q) ^ s) << 4));
+    for (int h = 0; h < 2; ++h)
+      f.h[h] = *reinterpret_cast<const v4u *>(stage + row * 128 + (((4 * h + q) ^ s) << 4));
   } else {
-    const int r = lane & 15, row16 = (row0 + lane % F) >> 4;
 #pragma unroll
-    for (int h = 0; h < kSteps; ++h)
+    for (int h = 0; h < 2; ++h)
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
-        const int k = 512 / F * h + 8 * q + 4 * j + (r >> 2);
-        const uint8_t *at = stage + k * (ROWS * 2) + ((row16 ^ col_f<ROWS>(k)) << 5) + (r & 3) * 8;
+        const int k = 32 * h + 8 * q + 4 * j + (r >> 2);
+        const uint8_t *at =
+            stage + k * (ROWS * 2) + (((row0 >> 4) ^ col_f<ROWS>(k)) << 5) + (r & 3) * 8;
         const v2u u = __builtin_bit_cast(
             v2u, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s *)at));
         f.h[h][2 * j] = u[0];
@@ -283,41 +275,38 @@ __device__ __forceinline__ Frag<F> read_frag(const uint8_t *stage, int row0, int
 // unrolled instructions would cost more.
 template <typename T, typename S, Kind KA, Kind KB, typename LoadA, typename LoadB>
 __device__ __forceinline__ void multiply(const LoadA &la, const LoadB &lb, int step0, int steps,
-                                         typename S::Smem &sm, typename S::Acc &out) {
+                                         typename S::Smem &sm, typename S::Acc &acc) {
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  constexpr int F = S::kF, FM = S::kFM, FN = S::kFN, kSteps = F / 8;
+  constexpr int FM = S::kFM, FN = S::kFN;
   const int arow = wave / S::kWN * S::kWaveM, brow = wave % S::kWN * S::kWaveN;
-  typename std::conditional<F == 16, v4f, v16f>::type acc[FM][FN];
 #pragma unroll
   for (int mi = 0; mi < FM; ++mi)
 #pragma unroll
-    for (int ni = 0; ni < FN; ++ni)
-#pragma unroll
-      for (int e = 0; e < F * F / 64; ++e) acc[mi][ni][e] = 0.0f;
+    for (int ni = 0; ni < FN; ++ni) acc[mi][ni] = v4f{0, 0, 0, 0};
   auto issue = [&](int s) {
     const int at = step0 + min(s, steps - 1);
     la.issue(at, sm.a[s & 1]);
     lb.issue(at, sm.b[s & 1]);
   };
   auto read_a = [&](int st, int mi) {
-    return read_frag<KA, S::TM, F>(sm.a[st], arow + mi * F, lane);
+    return read_frag<KA, S::TM>(sm.a[st], arow + mi * 16, lane);
   };
   auto read_b = [&](int st, int ni) {
-    return read_frag<KB, S::TN, F>(sm.b[st], brow + ni * F, lane);
+    return read_frag<KB, S::TN>(sm.b[st], brow + ni * 16, lane);
   };
   issue(0);
   issue(1);
   __builtin_amdgcn_s_waitcnt(0);
   __syncthreads();
-  Frag<F> bf[FN], af = read_a(0, 0);
+  Frag bf[FN], af = read_a(0, 0);
 #pragma unroll
   for (int ni = 0; ni < FN; ++ni) bf[ni] = read_b(0, ni);
   for (int s = 0; s < steps; ++s) {
     const int st = s & 1;
 #pragma unroll
     for (int mi = 0; mi < FM; ++mi) {
-      Frag<F> an;
+      Frag an;
       if (mi < FM - 1) {
         an = read_a(st, mi + 1);
       } else {
@@ -328,11 +317,11 @@ __device__ __forceinline__ void multiply(const LoadA &la, const LoadB &lb, int s
       }
       __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-      for (int h = 0; h < kSteps; ++h)
+      for (int h = 0; h < 2; ++h)
 #pragma unroll
         for (int ni = 0; ni < FN; ++ni) {
           acc[mi][ni] = T::mfma(bf[ni].h[h], af.h[h], acc[mi][ni]);
-          if (mi == FM - 1 && h == kSteps - 1) {
+          if (mi == FM - 1 && h == 1) {
             __builtin_amdgcn_sched_barrier(0);
             bf[ni] = read_b(st ^ 1, ni);
             __builtin_amdgcn_sched_barrier(0);
@@ -342,13 +331,6 @@ __device__ __forceinline__ void multiply(const LoadA &la, const LoadB &lb, int s
     }
   }
   __builtin_amdgcn_s_waitcnt(0);    // LDS is left with no load into it in flight
-#pragma unroll
-  for (int i = 0; i < FM; ++i)
-#pragma unroll
-    for (int j = 0; j < S::kQuads; ++j)
-#pragma unroll
-      for (int r = 0; r < 4; ++r)
-        out[i][j][r] = acc[i][j / (S::kQuads / FN)][j % (S::kQuads / FN) * 4 + r];
 }
 
 // Tile (tm, tn) of workgroup `bid` of tiles_m x tiles_n: workgroups go round-robin
@@ -549,30 +531,103 @@ struct Out {
   }
 };
 
-template <typename T, typename S>
-__device__ __forceinline__ void store_tile(const Out &p, const typename S::Acc &acc, int64_t m0,
-                                           int64_t n0, int range) {
-  const int lane = threadIdx.x & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  m0 += wave / S::kWN * S::kWaveM;
-  n0 += wave % S::kWN * S::kWaveN;
+// ---------------------------------------------------------------------------
+// A tile's outputs of COLS columns pass through the stages' LDS, so that they leave
+// in 16-byte pieces of whole rows: 16-byte chunk c of row r is kept at
+// c ^ (r % (COLS / 8)), which spreads the writes of 16 rows over the banks.
+
+template <int COLS>
+__device__ __forceinline__ uint8_t *staged(uint8_t *lds, int row, int col) {
+  return lds + row * (COLS * 2) + (((col >> 3) ^ (row & (COLS / 8 - 1))) << 4) + (col & 7) * 2;
+}
+// The four values of fragment (i, j) of the wave whose outputs begin at (row0, col0).
+template <typename T, typename S, int COLS>
+__device__ __forceinline__ void stage4(uint8_t *lds, int row0, int col0, int i, int j,
+                                       const float (&v)[4], int lane) {
+  if constexpr (S::kAcross) {
 #pragma unroll
-  for (int i = 0; i < S::kRowsHeld; ++i) {
-    const int64_t m = m0 + S::row(i, lane);
-    if (m >= p.rows) continue;
+    for (int r = 0; r < 4; ++r)
+      *reinterpret_cast<uint16_t *>(
+          staged<COLS>(lds, row0 + S::row(i, r, lane), col0 + S::col(j, r, lane))) =
+          (uint16_t)T::bits(v[r]);
+  } else {
+    *reinterpret_cast<v2u *>(
+        staged<COLS>(lds, row0 + S::row(i, 0, lane), col0 + S::col(j, 0, lane))) =
+        v2u{pack2<T>(v[0], v[1]), pack2<T>(v[2], v[3])};
+  }
+}
+// The staged tile's first `rows` x `cols` outputs to out, ld apart.
+template <int THREADS, int ROWS, int COLS>
+__device__ __forceinline__ void store_staged(uint8_t *lds, uint16_t *out, int64_t ld, int64_t rows,
+                                             int64_t cols) {
+  constexpr int kChunks = COLS / 8;
+#pragma unroll 4
+  for (int at = threadIdx.x; at < ROWS * kChunks; at += THREADS) {
+    const int row = at / kChunks, col = at % kChunks * 8;
+    if (row >= rows || col >= cols) continue;
+    const v4u v = *reinterpret_cast<const v4u *>(staged<COLS>(lds, row, col));
+    uint16_t *p = out + row * ld + col;
+    if (col + 8 <= cols) {
+      // read by another kernel, if at all: not kept beside the operands in L2
+      __builtin_nontemporal_store(v, reinterpret_cast<v4u_any *>(p));
+    } else {
 #pragma unroll
-    for (int j = 0; j < S::kQuads; ++j) {
-      const int64_t n = n0 + S::col(j, lane);
-      const int64_t left = p.cols - n;
-      if (left <= 0) continue;
-      if (p.ranges == 1) {
-        const float v[4] = {acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3]};
-        store4<T>(p.out + m * p.cols + n, v, left);
-      } else {
-        store4(p.parts + ((int64_t)range * p.rows + m) * p.cols + n, acc[i][j], left);
-      }
+      for (int e = 0; e < 7; ++e)
+        if (col + e < cols) p[e] = (uint16_t)(v[e / 2] >> (16 * (e & 1)));
     }
   }
+}
+// A fragment's fp32 sums as parts, at p in rows ld apart; rows and cols are what is
+// there from the fragment's first output on.
+template <typename S>
+__device__ __forceinline__ void store_part(float *p, int64_t ld, int64_t rows, int64_t cols, v4f v,
+                                           int lane) {
+  if constexpr (S::kAcross) {
+    const int c = S::col(0, 0, lane);
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+      if (S::row(0, r, lane) < rows && c < cols) p[S::row(0, r, lane) * ld + c] = v[r];
+  } else {
+    const int m = S::row(0, 0, lane), c = S::col(0, 0, lane);
+    if (m < rows && c < cols) store4(p + m * ld + c, v, cols - c);
+  }
+}
+
+// A wave's place among its workgroup's.
+template <typename S>
+__device__ __forceinline__ int wave_row() {
+  return __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) / S::kWN * S::kWaveM;
+}
+template <typename S>
+__device__ __forceinline__ int wave_col() {
+  return __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) % S::kWN * S::kWaveN;
+}
+
+template <typename T, typename S>
+__device__ __forceinline__ void store_tile(const Out &p, const typename S::Acc &acc, int64_t m0,
+                                           int64_t n0, int range, uint8_t *lds) {
+  const int lane = threadIdx.x & 63, row = wave_row<S>(), col = wave_col<S>();
+  if (p.ranges > 1) {
+    float *parts = p.parts + ((int64_t)range * p.rows + m0 + row) * p.cols + n0 + col;
+#pragma unroll
+    for (int i = 0; i < S::kFM; ++i)
+#pragma unroll
+      for (int j = 0; j < S::kFN; ++j)
+        store_part<S>(parts + i * 16 * p.cols + j * 16, p.cols, p.rows - m0 - row - i * 16,
+                      p.cols - n0 - col - j * 16, acc[i][j], lane);
+    return;
+  }
+  __syncthreads();      // every wave is past its last stage
+#pragma unroll
+  for (int i = 0; i < S::kFM; ++i)
+#pragma unroll
+    for (int j = 0; j < S::kFN; ++j) {
+      const float v[4] = {acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3]};
+      stage4<T, S, S::TN>(lds, row, col, i, j, v, lane);
+    }
+  __syncthreads();
+  store_staged<S::kThreads, S::TM, S::TN>(lds, p.out + m0 * p.cols + n0, p.cols, p.rows - m0,
+                                          p.cols - n0);
 }
 
 template <typename T>

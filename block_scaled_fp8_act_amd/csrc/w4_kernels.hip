@@ -146,7 +146,10 @@ struct W4Loader {
   const uint8_t *zeros;
   int row, half, shift;
   int64_t K;
-  v4u c;
+  v4u next;              // fetched
+  uint32_t next_s, next_z;
+  bool in, has_zeros;
+  v4u c;                 // taken
   float s, z;
 
   static __device__ __forceinline__ int tile_row() {
@@ -160,28 +163,38 @@ struct W4Loader {
     half = (threadIdx.x >> 5) & 1;
     codes = w.codes + n * (K / 2) + half * 16;
     scale = w.scale + n * (K >> shift);
-    zeros = w.zeros ? w.zeros + n * (K >> shift) : nullptr;
+    has_zeros = w.zeros != nullptr;
+    // (without zero points their loads bring bytes of the scales, not used)
+    zeros = (has_zeros ? w.zeros : reinterpret_cast<const uint8_t *>(w.scale)) + n * (K >> shift);
   }
+  // Loads without branches, which the unrolled loop around them would pay for.
   __device__ __forceinline__ void fetch(int step) {
     const int64_t k = (int64_t)step * kK + half * 32;
-    const bool in = k < K;       // (K is a multiple of 32)
+    in = k < K;       // (K is a multiple of 32; past it the scale is zero)
     const int64_t at = in ? (int64_t)step * 32 : -half * 16, g = in ? k >> shift : 0;
-    c = *reinterpret_cast<const v4u *>(codes + at);
-    s = in ? T::value(scale[g]) : 0.0f;
-    z = zeros ? (float)zeros[g] : 8.0f;
+    next = *reinterpret_cast<const v4u *>(codes + at);
+    next_s = scale[g];
+    next_z = zeros[g];
   }
-  __device__ __forceinline__ void put(W4Smem<S> &sm, int stage) const {
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-      *reinterpret_cast<v4u *>(sm.b[stage] + row * 128 + (((half * 4 + j) ^ swz_f(row)) << 4)) =
-          whole16<T>(c[j], z);
-    sm.scale[stage][half][row] = s;
+  __device__ __forceinline__ void take() {
+    c = next;
+    s = in ? T::value(next_s) : 0.0f;
+    z = has_zeros ? (float)next_z : 8.0f;
+  }
+  // Quarter j of the codes taken into a stage.
+  __device__ __forceinline__ void put(W4Smem<S> &sm, int stage, int j) const {
+    *reinterpret_cast<v4u *>(sm.b[stage] + row * 128 + (((half * 4 + j) ^ swz_f(row)) << 4)) =
+        whole16<T>(c[j], z);
+    if (j == 0) sm.scale[stage][half][row] = s;
   }
 };
 
 // G32: groups of 32, two a stage; else a stage lies within a group.
 template <bool G32>
 struct W4 : Weights {
+  // (a lane then holds outputs of one column of each fragment: one scale)
+  template <typename S>
+  using Place = typename S::Across;
   template <typename S>
   using Smem = W4Smem<S>;
   template <typename T, typename S>
@@ -192,82 +205,121 @@ struct W4 : Weights {
     }
   };
 
-  // As t16::multiply, with the groups' scales.  The multiply-adds of a row of
-  // fragments follow the next row's matrix instructions, whose results they do
-  // not wait for.
+  // As t16::multiply, with the groups' scales: the multiply-adds of a row of
+  // fragments follow the next row's matrix instructions, whose results they do not
+  // wait for.  The codes of the stage after next are fetched at a step's start and
+  // taken at its barrier, to be decoded into the stage just read among the next step's
+  // rows of fragments.
+  // Past the last step the last stage is brought again, and not read.
   template <typename T, typename S, typename LA, typename LB>
   static __device__ __forceinline__ void multiply(const LA &la, LB &lb, int step0, int steps,
                                                   W4Smem<S> &sm, typename S::Acc &acc) {
     const int lane = threadIdx.x & 63;
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    constexpr int FM = S::kFM, FN = S::kFN, kParts = G32 ? 2 : 1;
-    static_assert(S::kF == 16, "a quad is a fragment's");
-    const int arow = wave / S::kWN * S::kWaveM, brow = wave % S::kWN * S::kWaveN;
+    constexpr int FM = S::kFM, FN = S::kFN, kParts = G32 ? 2 : 1, kUnits = FM * kParts;
+    const int arow = wave_row<S>(), brow = wave_col<S>();
 #pragma unroll
     for (int mi = 0; mi < FM; ++mi)
 #pragma unroll
       for (int ni = 0; ni < FN; ++ni) acc[mi][ni] = v4f{0, 0, 0, 0};
-    if (steps > 0) {
-      lb.fetch(step0);
-      la.issue(step0, sm.a[0]);
-      lb.put(sm, 0);
+    auto at = [&](int s) { return step0 + min(s, steps - 1); };
+    auto read_a = [&](int st, int mi) {
+      return read_frag<kRows, S::TM>(sm.a[st], arow + mi * 16, lane);
+    };
+    auto read_b = [&](int st, int ni) {
+      return read_frag<kRows, S::TN>(sm.b[st], brow + ni * 16, lane);
+    };
+    auto read_scale = [&](int st, int ni, int h) {
+      return sm.scale[st][h][brow + ni * 16 + (lane & 15)];
+    };
+    la.issue(at(0), sm.a[0]);
+    la.issue(at(1), sm.a[1]);
+    lb.fetch(at(0));
+    lb.take();
+#pragma unroll
+    for (int j = 0; j < 4; ++j) lb.put(sm, 0, j);
+    lb.fetch(at(1));
+    lb.take();
+    __builtin_amdgcn_s_waitcnt(0);
+    __syncthreads();
+    Frag bf[FN], af = read_a(0, 0);
+    float scale[FN][kParts];
+#pragma unroll
+    for (int ni = 0; ni < FN; ++ni) {
+      bf[ni] = read_b(0, ni);
+#pragma unroll
+      for (int h = 0; h < kParts; ++h) scale[ni][h] = read_scale(0, ni, h);
     }
+    // unit u: a row of fragments over a stage, or over half of one
+    v4f part[2][FN];
     for (int s = 0; s < steps; ++s) {
       const int st = s & 1;
-      __builtin_amdgcn_s_waitcnt(0);
-      __syncthreads();
-      // (past the last step it is brought again, and not read: a branch around the
-      // put below would let the multiply-adds sink past it and spill)
-      const int next = step0 + min(s + 1, steps - 1);
-      lb.fetch(next);
-      la.issue(next, sm.a[st ^ 1]);
-      __builtin_amdgcn_sched_barrier(0);
-      Frag<16> bf[FN];
-      v4f scale[FN][kParts];
 #pragma unroll
-      for (int ni = 0; ni < FN; ++ni) {
-        bf[ni] = read_frag<kRows, S::TN, 16>(sm.b[st], brow + ni * 16, lane);
-#pragma unroll
-        for (int h = 0; h < kParts; ++h)
-          scale[ni][h] =
-              *reinterpret_cast<const v4f *>(&sm.scale[st][h][brow + ni * 16 + 4 * (lane >> 4)]);
-      }
-      // unit u: a row of fragments over a stage, or over half of one
-      v4f part[2][FN];
-      Frag<16> af;
-#pragma unroll
-      for (int u = 0; u <= FM * kParts; ++u) {
+      for (int u = 0; u < kUnits; ++u) {
         const int mi = u / kParts, h = u % kParts;
-        if (mi < FM) {
-          if (h == 0) af = read_frag<kRows, S::TM, 16>(sm.a[st], arow + mi * 16, lane);
+        const bool last = u == kUnits - 1;
+        // quarters of the next stage's codes, taken at the last barrier
+        auto put = [&]() {
+          constexpr int kEach = kUnits >= 4 ? 1 : 4 / kUnits;
 #pragma unroll
-          for (int ni = 0; ni < FN; ++ni)
-            part[u & 1][ni] = T::mfma(bf[ni].h[h], af.h[h], v4f{0, 0, 0, 0});
-          if constexpr (!G32) {
-#pragma unroll
-            for (int ni = 0; ni < FN; ++ni)
-              part[u & 1][ni] = T::mfma(bf[ni].h[1], af.h[1], part[u & 1][ni]);
+          for (int j = u * kEach; j < (u + 1) * kEach && j < 4; ++j) lb.put(sm, st ^ 1, j);
+        };
+        if (u == 0) lb.fetch(at(s + 2));
+        if (last) put();
+        Frag an;
+        if (h == kParts - 1) {
+          if (!last) {
+            an = read_a(st, mi + 1);
+          } else {
+            __builtin_amdgcn_s_waitcnt(0);
+            __syncthreads();
+            la.issue(at(s + 2), sm.a[st]);
+            lb.take();
+            an = read_a(st ^ 1, 0);
           }
         }
-        if (u > 0) {
-          const int m = (u - 1) / kParts;
-          __builtin_amdgcn_sched_barrier(0);
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int ni = 0; ni < FN; ++ni)
+          part[u & 1][ni] = T::mfma(af.h[h], bf[ni].h[h], v4f{0, 0, 0, 0});
+        if constexpr (!G32) {
 #pragma unroll
           for (int ni = 0; ni < FN; ++ni)
-            acc[m][ni] = __builtin_elementwise_fma(part[(u - 1) & 1][ni],
-                                                   scale[ni][(u - 1) % kParts], acc[m][ni]);
+            part[u & 1][ni] = T::mfma(af.h[1], bf[ni].h[1], part[u & 1][ni]);
         }
-        // (the other stage's last reads ended before this step's barrier)
-        if (u == FM * kParts / 2) lb.put(sm, st ^ 1);
         __builtin_amdgcn_sched_barrier(0);
+        // the unit before this one
+        if (u > 0) {
+          const int m = (u - 1) / kParts, p = (u - 1) % kParts;
+#pragma unroll
+          for (int ni = 0; ni < FN; ++ni)
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+              acc[m][ni][r] =
+                  __builtin_fmaf(part[(u - 1) & 1][ni][r], scale[ni][p], acc[m][ni][r]);
+        }
+        if (!last) put();
+        __builtin_amdgcn_sched_barrier(0);
+        if (h == kParts - 1) af = an;
       }
+#pragma unroll
+      for (int ni = 0; ni < FN; ++ni) {
+        bf[ni] = read_b(st ^ 1, ni);
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+          acc[FM - 1][ni][r] = __builtin_fmaf(part[(kUnits - 1) & 1][ni][r],
+                                              scale[ni][kParts - 1], acc[FM - 1][ni][r]);
+#pragma unroll
+        for (int h = 0; h < kParts; ++h) scale[ni][h] = read_scale(st ^ 1, ni, h);
+      }
+      __builtin_amdgcn_sched_barrier(0);
     }
     __builtin_amdgcn_s_waitcnt(0);    // LDS is left with no load into it in flight
   }
 };
 
-template <typename T, typename S, bool G32>
-__global__ __launch_bounds__(S::kThreads) void w4_product_kernel(Operand a, W4<G32> w, Out p) {
+template <typename T, typename Tile, bool G32>
+__global__ __launch_bounds__(Tile::kThreads) void w4_product_kernel(Operand a, W4<G32> w, Out p) {
+  using S = typename Tile::Across;
   __shared__ W4Smem<S> sm;
   const int tiles = p.tiles_m * p.tiles_n, range = blockIdx.x / tiles;
   int tm, tn;
@@ -284,7 +336,7 @@ __global__ __launch_bounds__(S::kThreads) void w4_product_kernel(Operand a, W4<G
   const int s0 = p.first_step(range);
   typename S::Acc acc;
   W4<G32>::template multiply<T, S>(la, lb, s0, p.first_step(range + 1) - s0, sm, acc);
-  store_tile<T, S>(p, acc, m0, n0, range);
+  store_tile<T, S>(p, acc, m0, n0, range, reinterpret_cast<uint8_t *>(&sm));
 }
 
 // ---------------------------------------------------------------------------
