@@ -42,6 +42,7 @@ typedef unsigned v2u_any __attribute__((ext_vector_type(2), aligned(2)));
 
 // The 16-bit types: fp32 -> bits (round to nearest even), bits -> fp32, product.
 struct Bf16 {
+  typedef __bf16 Pair __attribute__((ext_vector_type(2)));
   static __device__ __forceinline__ uint32_t bits(float f) {
     return __builtin_bit_cast(uint16_t, (__bf16)f);
   }
@@ -52,6 +53,7 @@ struct Bf16 {
   }
 };
 struct F16 {
+  typedef _Float16 Pair __attribute__((ext_vector_type(2)));
   static __device__ __forceinline__ uint32_t bits(float f) {
     return __builtin_bit_cast(uint16_t, (_Float16)f);
   }
@@ -65,7 +67,9 @@ struct F16 {
 };
 template <typename T>
 __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
-  return T::bits(lo) | (T::bits(hi) << 16);
+  typedef float v2f __attribute__((ext_vector_type(2)));
+  return __builtin_bit_cast(uint32_t,
+                            __builtin_convertvector(v2f{lo, hi}, typename T::Pair));
 }
 
 typedef __attribute__((address_space(3))) void lds_void;

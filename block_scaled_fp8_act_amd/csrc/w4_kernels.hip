@@ -122,13 +122,35 @@ __global__ __launch_bounds__(256) void w4_dequant_kernel(Weights p, int64_t chun
 // rounded to 16 bits instead, with the scale, would take no such multiply-adds and
 // carry an error as large as the result's own rounding into it.
 
-// Eight codes less their zero point as 16-bit floats, in the order of k.
+// Eight codes less their zero point as 16-bit floats, in the order of k: in bf16 the
+// upper halves of the fp32 values (exact), in fp16 by 1024 + q, whose low bits are q,
+// less 1024 + z.
 template <typename T>
-__device__ __forceinline__ v4u whole16(uint32_t c, float z) {
+__device__ __forceinline__ v4u whole16(uint32_t c, float z);
+template <>
+__device__ __forceinline__ v4u whole16<Bf16>(uint32_t c, float z) {
   float w[8];
   decode8(c, z, w);
-  return v4u{pack2<T>(w[0], w[1]), pack2<T>(w[2], w[3]), pack2<T>(w[4], w[5]),
-             pack2<T>(w[6], w[7])};
+  v4u out;
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    out[j] = __builtin_amdgcn_perm(__float_as_uint(w[2 * j + 1]), __float_as_uint(w[2 * j]),
+                                   0x07060302u);
+  return out;
+}
+template <>
+__device__ __forceinline__ v4u whole16<F16>(uint32_t c, float z) {
+  const _Float16 bias = (_Float16)(1024.0f + z);
+  uint32_t p[4];      // codes j and j + 4
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    p[j] = __builtin_bit_cast(
+        uint32_t, __builtin_bit_cast(F16::Pair, ((c >> (4 * j)) & 0x000f000fu) | 0x64006400u) -
+                      F16::Pair{bias, bias});
+  return v4u{__builtin_amdgcn_perm(p[1], p[0], 0x05040100u),
+             __builtin_amdgcn_perm(p[3], p[2], 0x05040100u),
+             __builtin_amdgcn_perm(p[1], p[0], 0x07060302u),
+             __builtin_amdgcn_perm(p[3], p[2], 0x07060302u)};
 }
 
 template <typename S>
@@ -286,7 +308,6 @@ struct W4 : Weights {
           for (int ni = 0; ni < FN; ++ni)
             part[u & 1][ni] = T::mfma(af.h[1], bf[ni].h[1], part[u & 1][ni]);
         }
-        __builtin_amdgcn_sched_barrier(0);
         // the unit before this one
         if (u > 0) {
           const int m = (u - 1) / kParts, p = (u - 1) % kParts;
@@ -298,6 +319,13 @@ struct W4 : Weights {
                   __builtin_fmaf(part[(u - 1) & 1][ni][r], scale[ni][p], acc[m][ni][r]);
         }
         if (!last) put();
+        // vector instructions in the shadow of each matrix instruction
+#pragma unroll
+        for (int i = 0; i < (G32 ? FN : 2 * FN); ++i) {
+          __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+          if (u < 4) __builtin_amdgcn_sched_group_barrier(0x002, 6, 0);
+          else __builtin_amdgcn_sched_group_barrier(0x002, 2, 0);
+        }
         __builtin_amdgcn_sched_barrier(0);
         if (h == kParts - 1) af = an;
       }
@@ -361,7 +389,8 @@ struct Pairs<Bf16> {
   }
   template <int J>   // codes J and J + 4 of a dword
   static __device__ __forceinline__ uint32_t codes(uint32_t c) {
-    const uint32_t v = J == 0 ? c << 3 : c >> (4 * J - 3);
+    uint32_t v = c << 3;
+    if constexpr (J > 0) v = c >> (4 * J - 3);
     return (v & 0x00780078u) | 0x41804180u;
   }
 };
