@@ -26,6 +26,7 @@ __global__ __launch_bounds__(256) void align_rows_kernel(const uint16_t *in, int
 struct Dense {
   const uint16_t *w;
   int64_t ld;
+  static constexpr bool kFourBits = false;
   template <typename S>
   using Place = S;
   template <typename S>

@@ -199,7 +199,7 @@ __global__ __launch_bounds__(256) void glu_join_kernel(GluArgs p) {
 // Launches by plan; p's sizes, pointers and act are set.
 template <typename T, bool GRAD, typename W>
 hipError_t launch_glu(GluArgs p, const W &w, hipStream_t stream) {
-  const Plan plan = plan_of(p.M, 2 * p.I, p.K);
+  const Plan plan = plan_of(p.M, 2 * p.I, p.K, W::kFourBits);
   with_shape(plan.shape, [&](auto shape) {
     using S = decltype(shape);
     p.steps = (int)tiles(p.K, kK);

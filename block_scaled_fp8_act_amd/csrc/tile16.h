@@ -460,28 +460,33 @@ inline bool grid_fits(int64_t rows, int64_t cols) {
 // on workgroups of their own (fp32 parts, added in order by a second kernel) where
 // the tiles alone leave the chip idle.  The plan with the least time by a model
 // whose constants are measurements: a workgroup alone on its compute unit takes
-// `alone` us a stage, several take `shared` each (both follow the bytes that pass
-// into LDS, 50 to 58 GB/s a compute unit), `start` covers launch, first stage and
-// epilogue, and the parts travel twice at 5 TB/s.
+// `alone` us a stage, several take `shared` each (with 16-bit operands both follow the
+// bytes that pass into LDS, 50 to 58 GB/s a compute unit; with 4-bit weights the
+// decoding), `start` covers launch, first stage and epilogue, and the parts travel
+// twice at 5 TB/s.
 enum ShapeId { kLarge, kSmall, kLow, kFlat };
 struct Plan {
   ShapeId shape;
   int ranges;
 };
-inline Plan plan_of(int64_t rows, int64_t cols, int64_t k) {
+inline Plan plan_of(int64_t rows, int64_t cols, int64_t k, bool w4 = false) {
   struct Cost {
     int tm, tn;
     double alone, shared, start;
   };
-  static constexpr Cost kCosts[] = {{Large::TM, Large::TN, 1.25, 1.45, 9.0},
-                                    {Small::TM, Small::TN, 0.64, 0.55, 4.5},
-                                    {Low::TM, Low::TN, 0.50, 0.42, 4.5},
-                                    {Flat::TM, Flat::TN, 0.45, 0.36, 4.5}};
+  static constexpr Cost kCosts[2][4] = {{{Large::TM, Large::TN, 1.25, 1.45, 9.0},
+                                         {Small::TM, Small::TN, 0.64, 0.55, 4.5},
+                                         {Low::TM, Low::TN, 0.50, 0.42, 4.5},
+                                         {Flat::TM, Flat::TN, 0.45, 0.36, 4.5}},
+                                        {{Large::TM, Large::TN, 1.72, 2.00, 9.0},
+                                         {Small::TM, Small::TN, 1.08, 0.78, 4.5},
+                                         {Low::TM, Low::TN, 0.88, 0.56, 4.5},
+                                         {Flat::TM, Flat::TN, 0.85, 0.52, 4.5}}};
   const int64_t steps = tiles(k, kK);
   Plan best{kSmall, 1};
   double least = 1e30;
   for (int s = 0; s < 4; ++s) {
-    const Cost &c = kCosts[s];
+    const Cost &c = kCosts[w4][s];
     // a flatter tile only reads the columns' operand more often
     if ((s == kLow && rows > 2 * Low::TM) || (s == kFlat && rows > 2 * Flat::TM)) continue;
     const int64_t grid = tiles(rows, c.tm) * tiles(cols, c.tn);
@@ -498,8 +503,8 @@ inline Plan plan_of(int64_t rows, int64_t cols, int64_t k) {
   }
   return best;
 }
-inline size_t part_bytes(int64_t rows, int64_t cols, int64_t k) {
-  const int r = plan_of(rows, cols, k).ranges;
+inline size_t part_bytes(int64_t rows, int64_t cols, int64_t k, bool w4 = false) {
+  const int r = plan_of(rows, cols, k, w4).ranges;
   return r == 1 ? 0 : (size_t)r * rows * cols * sizeof(float);
 }
 // f of the plan's shape (a value of its type).

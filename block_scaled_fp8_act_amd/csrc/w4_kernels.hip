@@ -214,6 +214,7 @@ struct W4Loader {
 // G32: groups of 32, two a stage; else a stage lies within a group.
 template <bool G32>
 struct W4 : Weights {
+  static constexpr bool kFourBits = true;
   // (a lane then holds outputs of one column of each fragment: one scale)
   template <typename S>
   using Place = typename S::Across;
@@ -514,6 +515,218 @@ __global__ __launch_bounds__(256) void w4_few_kernel(W4Few p) {
   p.out[m * p.I + n] = (uint16_t)T::bits(y);
 }
 
+// ---------------------------------------------------------------------------
+// Up to 48 rows of x (decode batches): matrix instructions on codes that never pass
+// through LDS.  A workgroup's eight waves share NR blocks of 16 rows of W and split K
+// among them, 128 at a time.  A wave loads its codes and x row by row (16 bytes a lane,
+// neighbouring lanes on neighbouring bytes: loaded in the instructions' order, a row
+// a lane, 16 rows of 14336 -> 4096 took 22.8 us instead of 13.7) and turns them through
+// LDS of its own; a 4 x 4 exchange of dwords among the four lanes of a row of codes
+// then gives each instruction 32 neighbouring K, so a group never shares one with
+// another.  No wave waits for another until their sums meet at the end.  Codes enter
+// as 16 + q (see above), x in the same order of k; the sums of x that the bias asks
+// for come from one more instruction on ones, for all blocks together.  Bound: the
+// codes' HBM traffic, then x's from L2 (4 MF / NR bytes a byte of codes).
+//
+// GS: groups in 128 of K; MF: blocks of 16 rows of x.
+template <typename T, bool PAIR, int GS, int NR, int MF>
+__global__ __launch_bounds__(512, MF == 1 ? 4 : 2) void w4_slab_kernel(W4Few p) {
+  using P = Pairs<T>;
+  constexpr int kWaves = 8, kOut = PAIR ? NR / 2 : NR;
+  // a wave's codes and x on their way to the instructions' order, then its sums
+  struct Wave {
+    uint8_t w[NR][16 * 64], x[MF][16 * 256];
+  };
+  union Smem {
+    Wave wave[kWaves];
+    float red[kWaves][NR * MF * 4][64];
+  };
+  __shared__ __align__(16) Smem sm;
+  const int lane = threadIdx.x & 63, r16 = lane & 15, q = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int64_t n0 = (int64_t)blockIdx.x * (kOut * 16);
+  const int64_t groups = p.K >> p.w.shift;
+  // loads: four lanes on a row's 64 bytes of codes, sixteen on a row's 256 bytes of x
+  const uint8_t *codes[NR];
+  const uint16_t *scale[NR];
+  const uint8_t *zeros[NR];
+  const bool has_zeros = p.w.zeros != nullptr;
+#pragma unroll
+  for (int b = 0; b < NR; ++b) {
+    const int64_t from = n0 + b % kOut * 16, half = b >= kOut ? p.I : 0;
+    codes[b] = p.w.codes + (min(from + (lane >> 2), p.I - 1) + half) * (p.K / 2);
+    const int64_t n = min(from + r16, p.I - 1) + half;
+    scale[b] = p.w.scale + n * groups;
+    // (without zero points their loads bring bytes of the scales, not used)
+    zeros[b] = (has_zeros ? p.w.zeros : reinterpret_cast<const uint8_t *>(p.w.scale)) + n * groups;
+  }
+  const uint16_t *x[MF][4];
+#pragma unroll
+  for (int m = 0; m < MF; ++m)
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      x[m][i] = p.x + (int64_t)min(m * 16 + 4 * i + (lane >> 4), p.M - 1) * p.ldx;
+
+  struct Chunk {
+    v4u c[NR], x[MF][4];
+    uint32_t s[NR], z[NR];     // of the group that lane q stands for
+  };
+  // K values from chunk * 128 on; past the last one x counts as zero.
+  auto load = [&](int64_t chunk, Chunk &t) {
+    const int64_t k0 = chunk * 128;
+    const int left = (int)min(p.K - k0, (int64_t)128);
+    const int64_t kc = k0 / 2 + ((lane & 3) * 32 < left ? (lane & 3) * 16 : 0);
+    const int64_t kx = k0 + (8 * r16 < left ? 8 * r16 : 0);
+#pragma unroll
+    for (int b = 0; b < NR; ++b) t.c[b] = *reinterpret_cast<const v4u *>(codes[b] + kc);
+#pragma unroll
+    for (int m = 0; m < MF; ++m)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) t.x[m][i] = *reinterpret_cast<const v4u_any *>(x[m][i] + kx);
+    const int64_t g = min(chunk * GS + q * GS / 4, groups - 1);
+#pragma unroll
+    for (int b = 0; b < NR; ++b) {
+      t.s[b] = scale[b][g];
+      t.z[b] = zeros[b][g];
+    }
+  };
+  Wave &mine = sm.wave[wave];
+  v4f acc[NR][MF];
+#pragma unroll
+  for (int b = 0; b < NR; ++b)
+#pragma unroll
+    for (int m = 0; m < MF; ++m) acc[b][m] = v4f{0, 0, 0, 0};
+  const v4u ones = {P::kOne, P::kOne, P::kOne, P::kOne};
+  auto compute = [&](int64_t chunk, const Chunk &t) {
+    const int left = (int)min(p.K - chunk * 128, (int64_t)128);
+    // through the wave's own LDS, whose accesses stay in order: no barrier.  A row's
+    // 16-byte pieces are kept at c ^ (row / 4 % 4) of its codes and c ^ row of its x.
+#pragma unroll
+    for (int b = 0; b < NR; ++b)
+      *reinterpret_cast<v4u *>(mine.w[b] + (lane >> 2) * 64 +
+                               (((lane & 3) ^ (lane >> 4)) << 4)) = t.c[b];
+#pragma unroll
+    for (int m = 0; m < MF; ++m)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int row = 4 * i + (lane >> 4);
+        *reinterpret_cast<v4u *>(mine.x[m] + row * 256 + ((r16 ^ row) << 4)) =
+            8 * r16 < left ? pair_order(t.x[m][i]) : v4u{0, 0, 0, 0};
+      }
+    __builtin_amdgcn_wave_barrier();
+    uint32_t c[NR][4];
+#pragma unroll
+    for (int b = 0; b < NR; ++b) {
+      const v4u own = *reinterpret_cast<const v4u *>(mine.w[b] + r16 * 64 + ((q ^ (r16 >> 2)) << 4));
+      // lane q's dword j <- lane j's dword q
+      const auto e = __builtin_amdgcn_permlane32_swap(own[0], own[2], false, false);
+      const auto f = __builtin_amdgcn_permlane32_swap(own[1], own[3], false, false);
+      const auto g = __builtin_amdgcn_permlane16_swap(e[0], f[0], false, false);
+      const auto h = __builtin_amdgcn_permlane16_swap(e[1], f[1], false, false);
+      c[b][0] = g[0];
+      c[b][1] = g[1];
+      c[b][2] = h[0];
+      c[b][3] = h[1];
+    }
+    // each group's scale and zero point to all four lanes of a row
+    uint32_t sz[NR][GS];
+#pragma unroll
+    for (int b = 0; b < NR; ++b) {
+      const uint32_t v = t.s[b] | ((has_zeros ? t.z[b] : 8u) << 16);
+      if constexpr (GS == 1) {
+        sz[b][0] = v;
+      } else {
+        const auto e = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+        if constexpr (GS == 2) {
+          sz[b][0] = e[0];
+          sz[b][1] = e[1];
+        } else {
+          const auto f = __builtin_amdgcn_permlane16_swap(e[0], e[0], false, false);
+          const auto g = __builtin_amdgcn_permlane16_swap(e[1], e[1], false, false);
+          sz[b][0] = f[0];
+          sz[b][1] = f[1];
+          sz[b][2] = g[0];
+          sz[b][3] = g[1];
+        }
+      }
+    }
+    constexpr int kEach = 4 / GS;
+#pragma unroll
+    for (int g = 0; g < GS; ++g) {
+      v4f part[NR][MF], sum[MF];
+#pragma unroll
+      for (int i = 0; i < kEach; ++i) {
+        const int j = g * kEach + i;
+        v4u w[NR];
+#pragma unroll
+        for (int b = 0; b < NR; ++b)
+          w[b] = v4u{P::template codes<0>(c[b][j]), P::template codes<1>(c[b][j]),
+                     P::template codes<2>(c[b][j]), P::template codes<3>(c[b][j])};
+#pragma unroll
+        for (int m = 0; m < MF; ++m) {
+          const v4u xv = *reinterpret_cast<const v4u *>(mine.x[m] + r16 * 256 +
+                                                        (((4 * j + q) ^ r16) << 4));
+          const v4f zero = {0, 0, 0, 0};
+          sum[m] = T::mfma(xv, ones, i ? sum[m] : zero);
+#pragma unroll
+          for (int b = 0; b < NR; ++b)
+            part[b][m] = T::mfma(xv, w[b], i ? part[b][m] : zero);
+        }
+      }
+#pragma unroll
+      for (int b = 0; b < NR; ++b) {
+        const float s = T::value(sz[b][g] & 0xffffu), bias = -16.0f - (float)(sz[b][g] >> 16);
+#pragma unroll
+        for (int m = 0; m < MF; ++m)
+#pragma unroll
+          for (int r = 0; r < 4; ++r)
+            acc[b][m][r] = __builtin_fmaf(s, __builtin_fmaf(bias, sum[m][r], part[b][m][r]),
+                                          acc[b][m][r]);
+      }
+    }
+    __builtin_amdgcn_wave_barrier();
+  };
+  // two chunks in turn, the next one's loads ahead of the products; past the last
+  // one it is loaded again, and not used
+  const int64_t chunks = (p.K + 127) / 128;
+  Chunk t[2];
+  if (wave < chunks) {
+    load(wave, t[0]);
+    for (int64_t i = wave; i < chunks; i += 2 * kWaves) {
+      load(min(i + kWaves, chunks - 1), t[1]);
+      compute(i, t[0]);
+      if (i + kWaves >= chunks) break;
+      load(min(i + 2 * kWaves, chunks - 1), t[0]);
+      compute(i + kWaves, t[1]);
+    }
+  }
+  __syncthreads();      // (the sums take the place of the other waves' codes and x)
+#pragma unroll
+  for (int b = 0; b < NR; ++b)
+#pragma unroll
+    for (int m = 0; m < MF; ++m)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) sm.red[wave][(b * MF + m) * 4 + r][lane] = acc[b][m][r];
+  __syncthreads();
+  // a lane of each output's place adds the waves' sums, in order
+  for (int e = threadIdx.x; e < kOut * MF * 256; e += kWaves * 64) {
+    const int l = e & 63, v = e >> 6;       // v = (block * MF + m) * 4 + r
+    float y[PAIR ? 2 : 1];
+#pragma unroll
+    for (int h = 0; h < (PAIR ? 2 : 1); ++h) {
+      y[h] = 0.0f;
+#pragma unroll
+      for (int i = 0; i < kWaves; ++i) y[h] += sm.red[i][h * kOut * MF * 4 + v][l];
+    }
+    const int m = v / 4 % MF * 16 + 4 * (l >> 4) + v % 4;
+    const int64_t n = n0 + v / (4 * MF) * 16 + (l & 15);
+    if (m >= p.M || n >= p.I) continue;
+    float out = y[0];
+    if constexpr (PAIR) out = act_any(p.act, y[0]) * y[1];
+    p.out[m * p.I + n] = (uint16_t)T::bits(out);
+  }
+}
+
 __global__ __launch_bounds__(256) void align_x_kernel(const uint16_t *in, int64_t ld, int64_t rows,
                                                       int64_t cols, uint16_t *out) {
   align_rows(in, ld, rows, cols, out, cols);
@@ -541,7 +754,7 @@ hipError_t lay_x(const W4Call &c, Operand &a, Space &s, hipStream_t stream) {
   return hipGetLastError();
 }
 
-constexpr int64_t kFewRows = 4;
+constexpr int64_t kFewRows = 2;
 
 template <typename T, bool PAIR, int MT>
 hipError_t few(const W4Few &p, hipStream_t stream) {
@@ -561,13 +774,43 @@ hipError_t few(const W4Call &c, int act, void *out, hipStream_t stream) {
                                                           : few<T, PAIR, 4>(p, stream);
 }
 
+constexpr int64_t kSlabRows = 48;
+
+template <typename T, bool PAIR, int GS, int NR, int MF>
+hipError_t slab(const W4Few &p, hipStream_t stream) {
+  w4_slab_kernel<T, PAIR, GS, NR, MF>
+      <<<dim3((unsigned)tiles(p.I, (PAIR ? NR / 2 : NR) * 16)), 512, 0, stream>>>(p);
+  return hipGetLastError();
+}
+template <typename T, bool PAIR, int GS>
+hipError_t slab(const W4Few &p, hipStream_t stream) {
+  // two blocks of rows read x half as often, where they still give every compute
+  // unit a workgroup (four: 2-14 % faster or 30 % slower, by size)
+  constexpr int kNarrow = PAIR ? 2 : 1;
+  const bool narrow = p.I < 32 * kCUs;
+  if (p.M <= 16)
+    return narrow ? slab<T, PAIR, GS, kNarrow, 1>(p, stream) : slab<T, PAIR, GS, 2, 1>(p, stream);
+  if (p.M <= 32)
+    return narrow ? slab<T, PAIR, GS, kNarrow, 2>(p, stream) : slab<T, PAIR, GS, 2, 2>(p, stream);
+  return narrow ? slab<T, PAIR, GS, kNarrow, 3>(p, stream) : slab<T, PAIR, GS, 2, 3>(p, stream);
+}
+template <typename T, bool PAIR>
+hipError_t slab(const W4Call &c, int act, void *out, hipStream_t stream) {
+  const W4Few p{weights(c), static_cast<const uint16_t *>(c.x), c.ldx, c.K,
+                PAIR ? c.rows / 2 : c.rows, (int)c.M, act, static_cast<uint16_t *>(out)};
+  return c.group == 128 ? slab<T, PAIR, 1>(p, stream)
+                        : c.group == 64 ? slab<T, PAIR, 2>(p, stream)
+                                        : slab<T, PAIR, 4>(p, stream);
+}
+
 template <typename T, bool G32>
 hipError_t linear(const W4Call &c, void *y, void *work, hipStream_t stream) {
   if (c.M <= kFewRows) return few<T, false>(c, 0, y, stream);
+  if (c.M <= kSlabRows) return slab<T, false>(c, 0, y, stream);
   Space s{static_cast<uint8_t *>(work), 0};
   Operand a;
   if (hipError_t e = lay_x(c, a, s, stream)) return e;
-  const Plan plan = plan_of(c.M, c.rows, c.K);
+  const Plan plan = plan_of(c.M, c.rows, c.K, true);
   Out p{c.M, c.rows, static_cast<uint16_t *>(y), reinterpret_cast<float *>(s.base + s.used)};
   const W4<G32> w{weights(c)};
   with_shape(plan.shape, [&](auto shape) {
@@ -585,6 +828,7 @@ hipError_t linear(const W4Call &c, void *y, void *work, hipStream_t stream) {
 template <typename T, bool G32>
 hipError_t gated(const W4Call &c, int act, void *h, void *work, hipStream_t stream) {
   if (c.M <= kFewRows) return few<T, true>(c, act, h, stream);
+  if (c.M <= kSlabRows) return slab<T, true>(c, act, h, stream);
   Space s{static_cast<uint8_t *>(work), 0};
   Operand a;
   if (hipError_t e = lay_x(c, a, s, stream)) return e;
@@ -635,17 +879,17 @@ bool w4_fits(int64_t M, int64_t rows) {
 }
 
 size_t w4_linear_workspace_bytes(int64_t M, int64_t N, int64_t K, int64_t ldx) {
-  if (M <= kFewRows) return 0;
+  if (M <= kSlabRows) return 0;
   Space s{nullptr, 0};
   x_space(M, K, ldx, s);
-  return s.used + part_bytes(M, N, K);
+  return s.used + part_bytes(M, N, K, true);
 }
 
 size_t w4_gated_workspace_bytes(int64_t M, int64_t I, int64_t K, int64_t ldx) {
-  if (M <= kFewRows) return 0;
+  if (M <= kSlabRows) return 0;
   Space s{nullptr, 0};
   x_space(M, K, ldx, s);
-  return s.used + part_bytes(M, 2 * I, K);
+  return s.used + part_bytes(M, 2 * I, K, true);
 }
 
 hipError_t launch_w4_linear(const W4Call &c, void *y, void *work, hipStream_t stream) {
