@@ -1074,6 +1074,11 @@ _HALF_TYPES = tuple(_HALF)
 ACTS = {"silu": 0, "gelu": 1, "gelu_tanh": 2}      # FP8BLK_SILU, ...
 
 
+def _stream_of(t):
+    """The current stream of t's device, which is the current one (checked)."""
+    return _raw_stream(t.get_device()) if _raw_stream is not None else _stream()
+
+
 def _act(act):
     if act not in ACTS:
         raise ValueError(f"act must be one of {tuple(ACTS)}, got {act!r}")
@@ -1087,6 +1092,11 @@ def factor_row(I):
 
 def _gated_in(x, w, *more, factors=None):
     """Row stride of x, sizes (M, I, K); ``more`` are (tensor, name) of [M,I]."""
+    if not more and x.dim() == 2 and w.dim() == 2 and x.dtype in _HALF:
+        (M, K), rows = x.shape, w.shape[0]
+        if K and rows % 2 == 0 and _plain(x.get_device(), (x, x.dtype, (M, K)),
+                                          (w, x.dtype, (rows, K))):
+            return K, M, rows // 2, K
     ldx = _rows_2d(x, "x", _HALF_TYPES)
     _need(w, "w", (x.dtype,), 2)
     M, K = x.shape
@@ -1110,7 +1120,7 @@ def _gated_in(x, w, *more, factors=None):
 def _gated_call(x, ldx, w, act, M, I, K, h, factors, workspace):
     _check(load_library().fp8blk_gated_linear(
         x.data_ptr(), ldx, w.data_ptr(), _HALF[x.dtype], act, M, I, K, h.data_ptr(), _at(factors),
-        _at(workspace), _bytes(workspace), _stream()), "fp8blk_gated_linear")
+        _at(workspace), _bytes(workspace), _stream_of(x)), "fp8blk_gated_linear")
 
 
 def fp8blk_gated_linear(x, w, act, h, factors, workspace=None):
@@ -1126,7 +1136,7 @@ def fp8blk_gated_linear(x, w, act, h, factors, workspace=None):
 def _gated_back_call(d_h, x, ldx, w, factors, act, M, I, K, d_x, d_w, workspace):
     _check(load_library().fp8blk_gated_linear_backward(
         d_h.data_ptr(), x.data_ptr(), ldx, w.data_ptr(), _at(factors), _HALF[x.dtype], act, M, I, K,
-        _at(d_x), _at(d_w), _at(workspace), _bytes(workspace), _stream()),
+        _at(d_x), _at(d_w), _at(workspace), _bytes(workspace), _stream_of(x)),
         "fp8blk_gated_linear_backward")
 
 
@@ -1200,12 +1210,24 @@ def _w4_in(codes, scale, zeros):
 
 def _w4_product_in(x, codes, scale, zeros):
     """Row stride of x, sizes (M, N, K, group)."""
+    if x.dim() == 2 and codes.dim() == 2 and scale.dim() == 2 and x.dtype in _HALF:
+        (M, K), (N, groups) = x.shape, scale.shape
+        if (groups and K % groups == 0 and K // groups in W4_GROUPS and
+                _plain(x.get_device(), (x, x.dtype, (M, K)), (codes, torch.uint8, (N, K // 2)),
+                       (scale, x.dtype, (N, groups)), (zeros, torch.uint8, (N, groups)))):
+            return K, M, N, K, K // groups
     N, K, group = _w4_in(codes, scale, zeros)
     ldx = _rows_2d(x, "x", (scale.dtype,))
     if x.shape[1] != K:
         raise ValueError("x and codes disagree on K")
     _same_device(x, codes, scale, zeros)
     return ldx, x.shape[0], N, K, group
+
+
+def _w4_quant_call(w, group, codes, scale, zeros):
+    _check(load_library().fp8blk_w4_quant(
+        w.data_ptr(), _HALF[w.dtype], w.shape[0], w.shape[1], group, codes.data_ptr(),
+        scale.data_ptr(), _at(zeros), _stream_of(w)), "fp8blk_w4_quant")
 
 
 def fp8blk_w4_quant(w, codes, scale, zeros):
@@ -1215,8 +1237,13 @@ def fp8blk_w4_quant(w, codes, scale, zeros):
     N, K, group = _w4_in(codes, scale, zeros)
     _shape_eq(w, (N, K), "w")
     _same_device(w, codes, scale, zeros)
-    _check(load_library().fp8blk_w4_quant(w.data_ptr(), _HALF[w.dtype], N, K, group, codes.data_ptr(),
-                                          scale.data_ptr(), _at(zeros), _stream()), "fp8blk_w4_quant")
+    _w4_quant_call(w, group, codes, scale, zeros)
+
+
+def _w4_dequant_call(codes, scale, zeros, N, K, group, w):
+    _check(load_library().fp8blk_w4_dequant(
+        codes.data_ptr(), scale.data_ptr(), _at(zeros), _HALF[w.dtype], N, K, group, w.data_ptr(),
+        _stream_of(w)), "fp8blk_w4_dequant")
 
 
 def fp8blk_w4_dequant(codes, scale, zeros, w):
@@ -1225,16 +1252,14 @@ def fp8blk_w4_dequant(codes, scale, zeros, w):
     _need(w, "w", (scale.dtype,), 2)
     _shape_eq(w, (N, K), "w")
     _same_device(w, codes, scale, zeros)
-    _check(load_library().fp8blk_w4_dequant(codes.data_ptr(), scale.data_ptr(), _at(zeros),
-                                            _HALF[w.dtype], N, K, group, w.data_ptr(), _stream()),
-           "fp8blk_w4_dequant")
+    _w4_dequant_call(codes, scale, zeros, N, K, group, w)
 
 
 def _w4_call(x, sizes, codes, scale, zeros, y, workspace):
     ldx, M, N, K, group = sizes
     _check(load_library().fp8blk_w4_linear(
         x.data_ptr(), ldx, codes.data_ptr(), scale.data_ptr(), _at(zeros), _HALF[x.dtype], group, M,
-        N, K, y.data_ptr(), _at(workspace), _bytes(workspace), _stream()), "fp8blk_w4_linear")
+        N, K, y.data_ptr(), _at(workspace), _bytes(workspace), _stream_of(x)), "fp8blk_w4_linear")
 
 
 def fp8blk_w4_linear(x, codes, scale, zeros, y, workspace=None):
@@ -1259,7 +1284,7 @@ def _w4_gated_call(x, sizes, codes, scale, zeros, act, h, workspace):
     ldx, M, N, K, group = sizes
     _check(load_library().fp8blk_w4_gated_linear(
         x.data_ptr(), ldx, codes.data_ptr(), scale.data_ptr(), _at(zeros), _HALF[x.dtype], group, act,
-        M, N // 2, K, h.data_ptr(), _at(workspace), _bytes(workspace), _stream()),
+        M, N // 2, K, h.data_ptr(), _at(workspace), _bytes(workspace), _stream_of(x)),
         "fp8blk_w4_gated_linear")
 
 
@@ -1286,15 +1311,16 @@ def w4_quant(w, group=128, zeros=False):
         raise ValueError(f"K must be a positive multiple of the group, got {K}")
     q = W4Weight(w.new_empty((N, K // 2), dtype=torch.uint8), w.new_empty((N, K // group)),
                  w.new_empty((N, K // group), dtype=torch.uint8) if zeros else None)
-    fp8blk_w4_quant(w, *q)
+    _w4_quant_call(w, group, *q)
     return q
 
 
 def w4_dequant(codes, scale, zeros=None):
     """The weights [N,K] that 4-bit codes stand for, in the scales' type."""
-    N, K, _ = _w4_in(codes, scale, zeros)
+    N, K, group = _w4_in(codes, scale, zeros)
+    _same_device(codes, scale, zeros)
     w = scale.new_empty((N, K))
-    fp8blk_w4_dequant(codes, scale, zeros, w)
+    _w4_dequant_call(codes, scale, zeros, N, K, group, w)
     return w
 
 

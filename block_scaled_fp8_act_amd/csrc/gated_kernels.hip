@@ -242,19 +242,26 @@ hipError_t align(const uint16_t *in, int64_t ld, int64_t rows, int64_t cols, uin
   return hipGetLastError();
 }
 
+// out [rows, cols] = A B^T.
 template <typename T, Kind KA, Kind KB>
-hipError_t product(const Operand &a, const Operand &b, Out p, hipStream_t stream) {
-  const Plan plan = plan_of(p.rows, p.cols, a.k);
-  with_shape(plan.shape, [&](auto shape) {
-    using S = decltype(shape);
-    const dim3 grid = p.tile<S>(plan, a.k);
-    product_kernel<T, S, KA, KB><<<grid, S::kThreads, 0, stream>>>(a, b, p);
+hipError_t product(const Operand &a, const Operand &b, void *out, int64_t rows, int64_t cols,
+                   float *parts, hipStream_t stream) {
+  hipError_t e = hipSuccess;
+  each_launch(cut_of(rows, cols, a.k), cols, [&](int64_t first, int64_t n, const Plan &plan) {
+    if (e != hipSuccess) return;
+    Operand part = b;
+    part.p += first * (KB == kRows ? b.ld : 1);
+    part.rows -= first;
+    Out p{rows, n, static_cast<uint16_t *>(out) + first, cols, parts};
+    with_shape(plan.shape, [&](auto shape) {
+      using S = decltype(shape);
+      const dim3 grid = p.tile<S>(plan, a.k);
+      product_kernel<T, S, KA, KB><<<grid, S::kThreads, 0, stream>>>(a, part, p);
+    });
+    e = hipGetLastError();
+    if (e == hipSuccess && p.ranges > 1) e = join<T>(p, stream);
   });
-  if (p.ranges > 1) {
-    if (hipError_t e = hipGetLastError()) return e;
-    join_kernel<T><<<groups(tiles(p.rows * p.cols, 4)), 256, 0, stream>>>(p);
-  }
-  return hipGetLastError();
+  return e;
 }
 
 hipError_t zero(void *out, int64_t n, hipStream_t stream) {
@@ -344,18 +351,16 @@ hipError_t backward(const GatedCall &c, const void *dh, const void *factors, voi
     p.ld_dgu = ld;
     if (hipError_t e = launch_glu<T, true>(p, Dense{in.w, in.ldw}, stream)) return e;
   }
-  if (dx) {
-    const Out o{c.M, c.K, static_cast<uint16_t *>(dx), parts};
+  if (dx)
     if (hipError_t e = product<T, kRows, kCols>(Operand{dgu, ld, c.M, ld},
-                                                Operand{in.w, in.ldw, kp, 2 * c.I}, o, stream))
+                                                Operand{in.w, in.ldw, kp, 2 * c.I}, dx, c.M, c.K,
+                                                parts, stream))
       return e;
-  }
-  if (dw) {
-    const Out o{2 * c.I, c.K, static_cast<uint16_t *>(dw), parts};
+  if (dw)
     if (hipError_t e = product<T, kCols, kCols>(Operand{dgu, ld, ld, c.M},
-                                                Operand{in.x, in.ldx, kp, c.M}, o, stream))
+                                                Operand{in.x, in.ldx, kp, c.M}, dw, 2 * c.I, c.K,
+                                                parts, stream))
       return e;
-  }
   return hipSuccess;
 }
 

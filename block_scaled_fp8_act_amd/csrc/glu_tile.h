@@ -17,9 +17,10 @@ __host__ __device__ inline int64_t factor_row(int64_t I) { return 2 * factor_hal
 struct GluArgs {
   const uint16_t *x;
   int64_t ldx, M, I, K;
+  int64_t first, outs;            // of the I outputs, those of this launch
   int tiles_m, tiles_n;
   int steps, ranges;              // of K
-  float *parts;                   // [ranges][M][2I], ranges > 1
+  float *parts;                   // [ranges][M][2 outs], ranges > 1
   int act;
   uint16_t *h;                    // forward
   uint8_t *factors;               // rows of factor_row(I) bytes, or NULL
@@ -128,7 +129,7 @@ __global__ __launch_bounds__(Tile::kThreads) void glu_kernel(GluArgs p, W w) {
   tile_of(blockIdx.x - range * tiles, p.tiles_m, p.tiles_n, tm, tn);
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int64_t m = (int64_t)tm * S::TM, n = (int64_t)tn * (S::TN / 2);
+  const int64_t m = (int64_t)tm * S::TM, n = p.first + (int64_t)tn * (S::TN / 2);
   Loader<kRows, S::TM, S::kWaves> la;
   la.init(Operand{p.x + m * p.ldx, p.ldx, min(p.M - m, (int64_t)S::TM), p.K}, wave, lane);
   typename W::template Pair<T, S> lb;
@@ -140,13 +141,14 @@ __global__ __launch_bounds__(Tile::kThreads) void glu_kernel(GluArgs p, W w) {
   const int row = wave_row<S>(), col = wave_col<S>() / 2;
   if (p.ranges > 1) {
     constexpr int kHalf = S::kFN / 2;
-    float *parts = p.parts + ((int64_t)range * p.M + m + row) * 2 * p.I + n + col;
+    float *parts = p.parts + ((int64_t)range * p.M + m + row) * 2 * p.outs + n - p.first + col;
 #pragma unroll
     for (int i = 0; i < S::kFM; ++i)
 #pragma unroll
       for (int j = 0; j < S::kFN; ++j)
-        store_part<S>(parts + i * 32 * p.I + (j >= kHalf ? p.I : 0) + j % kHalf * 16, 2 * p.I,
-                      p.M - m - row - i * 16, p.I - n - col - j % kHalf * 16, acc[i][j], lane);
+        store_part<S>(parts + i * 32 * p.outs + (j >= kHalf ? p.outs : 0) + j % kHalf * 16,
+                      2 * p.outs, p.M - m - row - i * 16,
+                      p.first + p.outs - n - col - j % kHalf * 16, acc[i][j], lane);
     return;
   }
   uint8_t *lds = reinterpret_cast<uint8_t *>(&sm);
@@ -185,11 +187,11 @@ __device__ __forceinline__ void glu_store4(const GluArgs &p, int64_t m, int64_t 
 }
 template <typename T, bool GRAD>
 __global__ __launch_bounds__(256) void glu_join_kernel(GluArgs p) {
-  const int64_t quads = (p.I + 3) / 4, step = p.M * 2 * p.I;
+  const int64_t quads = (p.outs + 3) / 4, step = p.M * 2 * p.outs;
   for (int64_t at = first_item(); at < p.M * quads; at += all_threads()) {
-    const int64_t m = at / quads, n = (at - m * quads) * 4;
-    const float *q = p.parts + m * 2 * p.I + n;
-    const v4f g = join4(q, p.ranges, step, p.I - n), u = join4(q + p.I, p.ranges, step, p.I - n);
+    const int64_t m = at / quads, c = (at - m * quads) * 4, left = p.outs - c, n = p.first + c;
+    const float *q = p.parts + m * 2 * p.outs + c;
+    const v4f g = join4(q, p.ranges, step, left), u = join4(q + p.outs, p.ranges, step, left);
     if (p.act == kSilu) glu_store4<T, kSilu, GRAD>(p, m, n, g, u);
     else if (p.act == kGelu) glu_store4<T, kGelu, GRAD>(p, m, n, g, u);
     else glu_store4<T, kGeluTanh, GRAD>(p, m, n, g, u);
@@ -199,21 +201,28 @@ __global__ __launch_bounds__(256) void glu_join_kernel(GluArgs p) {
 // Launches by plan; p's sizes, pointers and act are set.
 template <typename T, bool GRAD, typename W>
 hipError_t launch_glu(GluArgs p, const W &w, hipStream_t stream) {
-  const Plan plan = plan_of(p.M, 2 * p.I, p.K, W::kFourBits);
-  with_shape(plan.shape, [&](auto shape) {
-    using S = decltype(shape);
+  hipError_t e = hipSuccess;
+  each_launch(cut_of(p.M, 2 * p.I, p.K, W::kFourBits), 2 * p.I,
+              [&](int64_t first, int64_t cols, const Plan &plan) {
+    if (e != hipSuccess) return;
+    p.first = first / 2;      // (whole tiles, half of them gates)
+    p.outs = cols / 2;
     p.steps = (int)tiles(p.K, kK);
     p.ranges = plan.ranges;
-    p.tiles_m = (int)tiles(p.M, S::TM);
-    p.tiles_n = (int)tiles(p.I, S::TN / 2);
-    glu_kernel<T, S, GRAD, W>
-        <<<dim3((unsigned)p.tiles_m * p.tiles_n * p.ranges), S::kThreads, 0, stream>>>(p, w);
+    with_shape(plan.shape, [&](auto shape) {
+      using S = decltype(shape);
+      p.tiles_m = (int)tiles(p.M, S::TM);
+      p.tiles_n = (int)tiles(p.outs, S::TN / 2);
+      glu_kernel<T, S, GRAD, W>
+          <<<dim3((unsigned)p.tiles_m * p.tiles_n * p.ranges), S::kThreads, 0, stream>>>(p, w);
+    });
+    e = hipGetLastError();
+    if (e == hipSuccess && p.ranges > 1) {
+      glu_join_kernel<T, GRAD><<<groups(p.M * tiles(p.outs, 4)), 256, 0, stream>>>(p);
+      e = hipGetLastError();
+    }
   });
-  if (p.ranges > 1) {
-    if (hipError_t e = hipGetLastError()) return e;
-    glu_join_kernel<T, GRAD><<<groups(p.M * tiles(p.I, 4)), 256, 0, stream>>>(p);
-  }
-  return hipGetLastError();
+  return e;
 }
 
 }  // namespace t16

@@ -468,6 +468,7 @@ enum ShapeId { kLarge, kSmall, kLow, kFlat };
 struct Plan {
   ShapeId shape;
   int ranges;
+  double us;      // by the model
 };
 inline Plan plan_of(int64_t rows, int64_t cols, int64_t k, bool w4 = false) {
   struct Cost {
@@ -483,8 +484,7 @@ inline Plan plan_of(int64_t rows, int64_t cols, int64_t k, bool w4 = false) {
                                          {Low::TM, Low::TN, 0.88, 0.56, 4.5},
                                          {Flat::TM, Flat::TN, 0.85, 0.52, 4.5}}};
   const int64_t steps = tiles(k, kK);
-  Plan best{kSmall, 1};
-  double least = 1e30;
+  Plan best{kSmall, 1, 1e30};
   for (int s = 0; s < 4; ++s) {
     const Cost &c = kCosts[w4][s];
     // a flatter tile only reads the columns' operand more often
@@ -495,17 +495,44 @@ inline Plan plan_of(int64_t rows, int64_t cols, int64_t k, bool w4 = false) {
       const double per = n == 1 && (s != kLarge || grid * r <= kCUs / 2) ? c.alone : n * c.shared;
       double t = c.start + per * tiles(steps, r);
       if (r > 1) t += 4.0 + 8e-6 / 5 * r * (double)rows * (double)cols;
-      if (t < least) {
-        least = t;
-        best = {(ShapeId)s, r};
-      }
+      if (t < best.us) best = {(ShapeId)s, r, t};
     }
   }
   return best;
 }
+// A product's columns in one or two launches: where large tiles leave the last round
+// of compute units mostly idle, the columns of the whole rounds first, then the others
+// by a plan of their own (2048 x 7168 -> 18432 with 4-bit weights, 2.25 rounds: 649 ->
+// 565 us).
+struct Cut {
+  int64_t first;      // columns of the first launch (all of them: no second)
+  Plan plan, rest;
+};
+inline Cut cut_of(int64_t rows, int64_t cols, int64_t k, bool w4 = false) {
+  Cut cut{cols, plan_of(rows, cols, k, w4), {}};
+  const int64_t tm = tiles(rows, Large::TM), tn = tiles(cols, Large::TN);
+  const int64_t rounds = tm * tn / kCUs;
+  if (rounds < 1 || tm * tn % kCUs == 0) return cut;
+  const int64_t first = rounds * kCUs / tm * Large::TN;
+  if (first < Large::TN || first >= cols) return cut;
+  const Plan whole = plan_of(rows, first, k, w4), rest = plan_of(rows, cols - first, k, w4);
+  // (by a clear margin: the model is no better than that)
+  if (whole.shape != kLarge || whole.ranges > 1 || whole.us + rest.us > 0.95 * cut.plan.us)
+    return cut;
+  return {first, whole, rest};
+}
 inline size_t part_bytes(int64_t rows, int64_t cols, int64_t k, bool w4 = false) {
-  const int r = plan_of(rows, cols, k, w4).ranges;
-  return r == 1 ? 0 : (size_t)r * rows * cols * sizeof(float);
+  const Cut c = cut_of(rows, cols, k, w4);
+  const Plan &p = c.first < cols ? c.rest : c.plan;      // (the first of two has none)
+  return p.ranges == 1 ? 0
+                       : (size_t)p.ranges * rows * (c.first < cols ? cols - c.first : cols) *
+                             sizeof(float);
+}
+// f(first column, columns, plan) for each launch.
+template <typename F>
+void each_launch(const Cut &c, int64_t cols, F f) {
+  f((int64_t)0, c.first, c.plan);
+  if (c.first < cols) f(c.first, cols - c.first, c.rest);
 }
 // f of the plan's shape (a value of its type).
 template <typename F>
@@ -521,7 +548,8 @@ void with_shape(ShapeId s, F f) {
 // A product's outputs, or its parts.
 struct Out {
   int64_t rows, cols;
-  uint16_t *out;          // [rows, cols]
+  uint16_t *out;          // rows ld apart
+  int64_t ld;
   float *parts;           // [ranges][rows][cols], ranges > 1
   int steps, ranges;
   int tiles_m, tiles_n;
@@ -635,18 +663,24 @@ __device__ __forceinline__ void store_tile(const Out &p, const typename S::Acc &
       stage4<T, S, S::TN>(lds, row, col, i, j, v, lane);
     }
   __syncthreads();
-  store_staged<S::kThreads, S::TM, S::TN>(lds, p.out + m0 * p.cols + n0, p.cols, p.rows - m0,
+  store_staged<S::kThreads, S::TM, S::TN>(lds, p.out + m0 * p.ld + n0, p.ld, p.rows - m0,
                                           p.cols - n0);
 }
 
 template <typename T>
 __global__ __launch_bounds__(256) void join_kernel(Out p) {
-  const int64_t n = p.rows * p.cols;
-  for (int64_t i = first_item() * 4; i < n; i += all_threads() * 4) {
-    const v4f s = join4(p.parts + i, p.ranges, n, n - i);
+  const int64_t quads = (p.cols + 3) / 4, step = p.rows * p.cols;
+  for (int64_t at = first_item(); at < p.rows * quads; at += all_threads()) {
+    const int64_t m = at / quads, n = (at - m * quads) * 4, left = p.cols - n;
+    const v4f s = join4(p.parts + m * p.cols + n, p.ranges, step, left);
     const float v[4] = {s[0], s[1], s[2], s[3]};
-    store4<T>(p.out + i, v, n - i);
+    store4<T>(p.out + m * p.ld + n, v, left);
   }
+}
+template <typename T>
+hipError_t join(const Out &p, hipStream_t stream) {
+  join_kernel<T><<<groups(p.rows * tiles(p.cols, 4)), 256, 0, stream>>>(p);
+  return hipGetLastError();
 }
 
 // The sums over a wave of N values (a power of two up to 64) of each lane, to out[N]:

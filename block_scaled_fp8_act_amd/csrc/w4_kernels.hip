@@ -810,19 +810,25 @@ hipError_t linear(const W4Call &c, void *y, void *work, hipStream_t stream) {
   Space s{static_cast<uint8_t *>(work), 0};
   Operand a;
   if (hipError_t e = lay_x(c, a, s, stream)) return e;
-  const Plan plan = plan_of(c.M, c.rows, c.K, true);
-  Out p{c.M, c.rows, static_cast<uint16_t *>(y), reinterpret_cast<float *>(s.base + s.used)};
-  const W4<G32> w{weights(c)};
-  with_shape(plan.shape, [&](auto shape) {
-    using S = decltype(shape);
-    const dim3 grid = p.tile<S>(plan, c.K);
-    w4_product_kernel<T, S, G32><<<grid, S::kThreads, 0, stream>>>(a, w, p);
+  float *parts = reinterpret_cast<float *>(s.base + s.used);
+  hipError_t e = hipSuccess;
+  each_launch(cut_of(c.M, c.rows, c.K, true), c.rows,
+              [&](int64_t first, int64_t n, const Plan &plan) {
+    if (e != hipSuccess) return;
+    W4<G32> w{weights(c)};
+    w.codes += first * (c.K / 2);
+    w.scale += first * (c.K / c.group);
+    if (w.zeros) w.zeros += first * (c.K / c.group);
+    Out p{c.M, n, static_cast<uint16_t *>(y) + first, c.rows, parts};
+    with_shape(plan.shape, [&](auto shape) {
+      using S = decltype(shape);
+      const dim3 grid = p.tile<S>(plan, c.K);
+      w4_product_kernel<T, S, G32><<<grid, S::kThreads, 0, stream>>>(a, w, p);
+    });
+    e = hipGetLastError();
+    if (e == hipSuccess && p.ranges > 1) e = join<T>(p, stream);
   });
-  if (p.ranges > 1) {
-    if (hipError_t e = hipGetLastError()) return e;
-    join_kernel<T><<<groups(tiles(p.rows * p.cols, 4)), 256, 0, stream>>>(p);
-  }
-  return hipGetLastError();
+  return e;
 }
 
 template <typename T, bool G32>

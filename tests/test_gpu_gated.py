@@ -130,7 +130,9 @@ def against_64(x, w, d, act, what, bound):
         assert err < bound, (what, name, err)
 
 
-@pytest.mark.parametrize("M,I,K", [(3900, 1610, 96), (1000, 4100, 1032), (520, 13000, 264)])
+# (the last two: columns of whole rounds of tiles, then the others, in all three products)
+@pytest.mark.parametrize("M,I,K", [(3900, 1610, 96), (1000, 4100, 1032), (520, 13000, 264), (4000, 2203, 2056),
+                                   (2100, 1500, 7904)])
 @pytest.mark.parametrize("act", ["silu", "gelu"])
 def test_gated_large_tiles(M, I, K, act):
     """Grids of 256 x 256 tiles.  A result's own rounding leaves at most half a

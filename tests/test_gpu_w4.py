@@ -163,7 +163,8 @@ def test_w4_outlier_under_a_zero_weight(M):
     assert np.all(np.abs(got - want) <= tol + 2.0 ** -8 * (np.abs(want) + tol))
 
 
-@pytest.mark.parametrize("M,N,K", [(2100, 6200, 192), (600, 5120, 1024)])
+# (the last: columns of whole rounds of tiles, then the others)
+@pytest.mark.parametrize("M,N,K", [(2100, 6200, 192), (600, 5120, 1024), (2100, 7682, 2048)])
 def test_w4_large_tiles(M, N, K):
     g = torch.Generator(device=dev()).manual_seed(M)
     w = (torch.randn(N, K, device=dev(), generator=g) * K ** -0.5).bfloat16()
