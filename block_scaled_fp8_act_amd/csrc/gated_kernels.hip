@@ -155,11 +155,12 @@ __global__ __launch_bounds__(256) void few_kernel(FewArgs p) {
     g += red[w0 + i][r * MT + m];
     u += red[w0 + i][(R + r) * MT + m];
   }
-  const float a = act_any(p.act, g);
+  float a, slope;
+  both_any(p.act, g, a, slope);
   p.h[m * p.I + n] = (uint16_t)T::bits(a * u);
   if (p.factors) {
     uint8_t *f = p.factors + m * factor_row(p.I) + n * 3;
-    store_24_one(f, u * slope_any(p.act, g));
+    store_24_one(f, u * slope);
     store_24_one(f + factor_half(p.I), a);
   }
 }

@@ -53,8 +53,9 @@ template <int ACT>
 __device__ __forceinline__ void glu_factors(v4f g, v4f u, float (&f)[4], float (&a)[4]) {
 #pragma unroll
   for (int r = 0; r < 4; ++r) {
-    f[r] = u[r] * act_slope<ACT>(g[r]);
-    a[r] = act_value<ACT>(g[r]);
+    float slope;
+    act_both<ACT>(g[r], a[r], slope);
+    f[r] = u[r] * slope;
   }
 }
 __device__ __forceinline__ void save_factors(const GluArgs &p, int64_t m, int64_t n,
