@@ -129,7 +129,7 @@ __global__ __launch_bounds__(256) void few_kernel(FewArgs p) {
 #pragma unroll 2
   for (int64_t k = (int64_t)(wave % KS) * 512; k < whole; k += KS * 512) {
 #pragma unroll
-    for (int i = 0; i < kRows; ++i) wv[i] = *reinterpret_cast<const v4u_any *>(w[i] + k);
+    for (int i = 0; i < kRows; ++i) wv[i] = __builtin_nontemporal_load(reinterpret_cast<const v4u_any *>(w[i] + k));
 #pragma unroll
     for (int m = 0; m < MT; ++m) xv[m] = *reinterpret_cast<const v4u_any *>(x[m] + k);
     add(wv, xv);
@@ -167,9 +167,11 @@ __global__ __launch_bounds__(256) void few_kernel(FewArgs p) {
 
 template <typename T, int MT>
 hipError_t few(const FewArgs &p, hipStream_t stream) {
-  // whole K a wave where the rows alone give the chip enough waves
-  constexpr int R = MT == 4 ? 2 : 4;
-  if (p.I / R >= 2048 || p.K < 1024)
+  // an output a wave and K shared by four (4096 -> 14336: 33.9 us for a row, 41.3 for
+  // two; two outputs 34.9 and 49.1, four and all of K a wave 48.9), but not pieces of a
+  // few loads
+  constexpr int R = 1;
+  if (p.K < 1024)
     few_kernel<T, R, MT, 1><<<dim3((unsigned)tiles(p.I, 4 * R)), 256, 0, stream>>>(p);
   else
     few_kernel<T, R, MT, 4><<<dim3((unsigned)tiles(p.I, R)), 256, 0, stream>>>(p);
@@ -312,7 +314,8 @@ GluArgs glu_args(const GatedCall &c, const Inputs &in, const Space &s) {
   return p;
 }
 
-constexpr int64_t kFewRows = 4;
+// More rows take longer here (3 rows of 4096 -> 14336: 71 us) than on tiles (58).
+constexpr int64_t kFewRows = 2;
 
 template <typename T>
 hipError_t forward(const GatedCall &c, void *h, void *factors, void *work, hipStream_t stream) {
@@ -320,7 +323,7 @@ hipError_t forward(const GatedCall &c, void *h, void *factors, void *work, hipSt
     const FewArgs p{static_cast<const uint16_t *>(c.x), static_cast<const uint16_t *>(c.w), c.ldx,
                     c.K, c.I, (int)c.M, c.act, static_cast<uint16_t *>(h),
                     static_cast<uint8_t *>(factors)};
-    return c.M == 1 ? few<T, 1>(p, stream) : c.M == 2 ? few<T, 2>(p, stream) : few<T, 4>(p, stream);
+    return c.M == 1 ? few<T, 1>(p, stream) : few<T, 2>(p, stream);
   }
   Space s{static_cast<uint8_t *>(work), 0};
   Inputs in;
