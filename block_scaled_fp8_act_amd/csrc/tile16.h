@@ -7,7 +7,7 @@
 // operand is a column of memory), so that a layer's forward product, the
 // gradient of its input and that of its weights all read their operands where
 // they are.  Both kinds pass through LDS by direct-to-LDS loads, 64 of K a
-// stage, two stages:
+// stage, two stages or four:
 //   kRows  [rows][64 of K], 128 bytes a row, 16-byte chunk c of row r kept at
 //          c ^ swz_f(r); a fragment is two ds_read_b128 a lane.
 //   kCols  [64 of K][rows], 32-byte pairs p of K row k kept at p ^ col_f(k); a
@@ -127,14 +127,16 @@ __device__ __forceinline__ int col_f(int k) {
 // four outputs of each fragment (i, j): of one row, neighbouring columns, or (ACROSS,
 // where the products with the operands exchanged are formed) of one column,
 // neighbouring rows; row(i, r, lane) and col(j, r, lane) are the r-th's place.
-template <int WM, int WN, int FM, int FN, bool ACROSS = false>
+// STAGES (a power of two) are in LDS at a time.
+template <int WM, int WN, int FM, int FN, int STAGES = 2, bool ACROSS = false>
 struct Shape {
   static constexpr int kFM = FM, kFN = FN, kWM = WM, kWN = WN;
   static constexpr bool kAcross = ACROSS;
+  static constexpr int kStages = STAGES;
   static constexpr int kWaves = WM * WN, kThreads = kWaves * 64;
   static constexpr int kWaveM = FM * 16, kWaveN = FN * 16;
   static constexpr int TM = WM * kWaveM, TN = WN * kWaveN;
-  using Across = Shape<WM, WN, FM, FN, true>;
+  using Across = Shape<WM, WN, FM, FN, 2, true>;
   using Acc = v4f[FM][FN];
   static __device__ __forceinline__ int row(int i, int r, int lane) {
     return 16 * i + (ACROSS ? 4 * (lane >> 4) + r : lane & 15);
@@ -143,17 +145,19 @@ struct Shape {
     return 16 * j + (ACROSS ? lane & 15 : 4 * (lane >> 4) + r);
   }
   struct Smem {
-    uint8_t a[2][TM * kK * 2];
-    uint8_t b[2][TN * kK * 2];
+    uint8_t a[STAGES][TM * kK * 2];
+    uint8_t b[STAGES][TN * kK * 2];
   };
   static_assert(sizeof(Smem) >= TM * TN * 2, "room for the outputs on their way out");
 };
 // 256 x 256 on 8 waves (a wave 128 x 64); 128 x 128, 64 x 128 and 32 x 128 on 4 for
-// grids that the larger tiles would leave mostly idle, and for few rows.
+// grids that the larger tiles would leave mostly idle, and for few rows.  The flat ones
+// keep four stages: their time is the loads' latency (64 rows of 4096 -> 14336: 69 ->
+// 56 us; four stages of 128 x 128, one workgroup a compute unit, gained nothing).
 using Large = Shape<2, 4, 8, 4>;
 using Small = Shape<2, 2, 4, 4>;
-using Low = Shape<2, 2, 2, 4>;
-using Flat = Shape<2, 2, 1, 4>;
+using Low = Shape<2, 2, 2, 4, 4>;
+using Flat = Shape<2, 2, 1, 4, 4>;
 
 // An operand in memory: `rows` of it along the output, `k` along the sum, both
 // counted from p; `ld` elements from one row of memory to the next.  Rows of
@@ -171,7 +175,8 @@ struct Operand {
 enum Kind { kRows, kCols };
 template <Kind KIND, int ROWS, int WAVES>
 struct Loader {
-  static constexpr int kLoads = ROWS / 8, kDma = (kLoads + WAVES - 1) / WAVES;
+  static constexpr int kDma = ROWS / 8 / WAVES;
+  static_assert(kDma * 8 * WAVES == ROWS, "as many loads for each wave");
   uint32_t off[kDma];
   uint32_t chunk[kDma];   // kRows: the lane's chunk of the stage's K
   int wave;
@@ -182,10 +187,6 @@ struct Loader {
   uint32_t row_bytes;     // kCols: valid bytes of a row
   int k;                  // left at the first stage
 
-  // Whether load i of this wave exists (where the loads do not divide evenly).
-  __device__ __forceinline__ bool has(int i) const {
-    return kLoads % WAVES == 0 || kDma * wave + i < kLoads;
-  }
   __device__ __forceinline__ void place(const Operand &o, int wave_) {
     wave = wave_;
     base = uniform((uint64_t)(uintptr_t)o.p);
@@ -213,10 +214,9 @@ struct Loader {
   }
   template <typename F>
   __device__ __forceinline__ void each(F f) const {
-    if (has(0)) f(std::true_type{}, 0);
+    f(std::true_type{}, 0);
 #pragma unroll
-    for (int i = 1; i < kDma; ++i)
-      if (has(i)) f(std::false_type{}, i);
+    for (int i = 1; i < kDma; ++i) f(std::false_type{}, i);
   }
   __device__ __forceinline__ void issue(int step, const uint8_t *stage) const {
     const uint64_t from = base + (uint64_t)(uint32_t)step * step_bytes;
@@ -270,19 +270,31 @@ __device__ __forceinline__ Frag read_frag(const uint8_t *stage, int row0, int la
 
 // The wave's sums over `steps` >= 1 stages from `step0`, as Shape places them.
 //
-// Step s reads stage s & 1.  Its barrier sits before the last row of fragments'
-// matrix instructions: every wave has then read the stage, and the next one has
-// landed in the other.  That stage's first fragments are read under the last row's
-// instructions, and the loads of the stage after it go out into the one just read, a
-// whole step ahead, so the matrix cores do not wait at a step's start.  Past the last
-// step the loads bring the last stage again, which nobody uses: a branch inside the
+// Step s reads stage s % N of the N in LDS.  Its barrier sits before the last row of
+// fragments' matrix instructions: every wave has then read the stage, and the next one
+// has landed in its own.  That stage's first fragments are read under the last row's
+// instructions, and the loads of stage s + N go out into the one just read, N - 1 whole
+// steps ahead, so the matrix cores do not wait at a step's start.  Past the last step
+// the loads bring the last stage again, which nobody uses: a branch inside the
 // unrolled instructions would cost more.
+//
+// Barrier for stages: at most LEFT of the wave's loads are still in flight, and its LDS
+// reads are done.
+template <int LEFT>
+__device__ __forceinline__ void stage_barrier() {
+  static_assert(LEFT <= 63, "the counter's range");
+  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" : : "n"(LEFT) : "memory");
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
+  __builtin_amdgcn_s_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
+}
+
 template <typename T, typename S, Kind KA, Kind KB, typename LoadA, typename LoadB>
 __device__ __forceinline__ void multiply(const LoadA &la, const LoadB &lb, int step0, int steps,
                                          typename S::Smem &sm, typename S::Acc &acc) {
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  constexpr int FM = S::kFM, FN = S::kFN;
+  constexpr int FM = S::kFM, FN = S::kFN, N = S::kStages, kEach = LoadA::kDma + LoadB::kDma;
   const int arow = wave / S::kWN * S::kWaveM, brow = wave % S::kWN * S::kWaveN;
 #pragma unroll
   for (int mi = 0; mi < FM; ++mi)
@@ -290,8 +302,8 @@ __device__ __forceinline__ void multiply(const LoadA &la, const LoadB &lb, int s
     for (int ni = 0; ni < FN; ++ni) acc[mi][ni] = v4f{0, 0, 0, 0};
   auto issue = [&](int s) {
     const int at = step0 + min(s, steps - 1);
-    la.issue(at, sm.a[s & 1]);
-    lb.issue(at, sm.b[s & 1]);
+    la.issue(at, sm.a[s % N]);
+    lb.issue(at, sm.b[s % N]);
   };
   auto read_a = [&](int st, int mi) {
     return read_frag<KA, S::TM>(sm.a[st], arow + mi * 16, lane);
@@ -299,25 +311,23 @@ __device__ __forceinline__ void multiply(const LoadA &la, const LoadB &lb, int s
   auto read_b = [&](int st, int ni) {
     return read_frag<KB, S::TN>(sm.b[st], brow + ni * 16, lane);
   };
-  issue(0);
-  issue(1);
-  __builtin_amdgcn_s_waitcnt(0);
-  __syncthreads();
+#pragma unroll
+  for (int s = 0; s < N; ++s) issue(s);
+  stage_barrier<(N - 1) * kEach>();
   Frag bf[FN], af = read_a(0, 0);
 #pragma unroll
   for (int ni = 0; ni < FN; ++ni) bf[ni] = read_b(0, ni);
   for (int s = 0; s < steps; ++s) {
-    const int st = s & 1;
+    const int st = s % N, next = (s + 1) % N;
 #pragma unroll
     for (int mi = 0; mi < FM; ++mi) {
       Frag an;
       if (mi < FM - 1) {
         an = read_a(st, mi + 1);
       } else {
-        __builtin_amdgcn_s_waitcnt(0);
-        __syncthreads();
-        issue(s + 2);
-        an = read_a(st ^ 1, 0);
+        stage_barrier<(N - 2) * kEach>();
+        issue(s + N);
+        an = read_a(next, 0);
       }
       __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
@@ -327,14 +337,15 @@ __device__ __forceinline__ void multiply(const LoadA &la, const LoadB &lb, int s
           acc[mi][ni] = T::mfma(bf[ni].h[h], af.h[h], acc[mi][ni]);
           if (mi == FM - 1 && h == 1) {
             __builtin_amdgcn_sched_barrier(0);
-            bf[ni] = read_b(st ^ 1, ni);
+            bf[ni] = read_b(next, ni);
             __builtin_amdgcn_sched_barrier(0);
           }
         }
       af = an;
     }
   }
-  __builtin_amdgcn_s_waitcnt(0);    // LDS is left with no load into it in flight
+  // LDS is left with no load into it in flight
+  asm volatile("s_waitcnt vmcnt(0)" : : : "memory");
 }
 
 // Tile (tm, tn) of workgroup `bid` of tiles_m x tiles_n: workgroups go round-robin

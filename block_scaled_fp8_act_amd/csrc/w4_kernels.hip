@@ -342,7 +342,8 @@ struct W4 : Weights {
       }
       __builtin_amdgcn_sched_barrier(0);
     }
-    __builtin_amdgcn_s_waitcnt(0);    // LDS is left with no load into it in flight
+    // LDS is left with no load into it in flight
+    asm volatile("s_waitcnt vmcnt(0)" : : : "memory");
   }
 };
 
