@@ -56,6 +56,16 @@ fp8blk_*, same order of arguments as the wrappers' with the outputs last):
     lora_add(base, x, a, b, ids, scale, groups, out) -> out bf16 [T,N]
     lora_linear(x, w_q, w_scale, a, b, ids, scale, groups) -> y bf16 [M,N]   (linear, then its adapters)
     moe_experts(x, routing, gate_up_q, gate_up_s, down_q, down_s, base) -> y bf16 [T,N]
+
+The gated feed-forward block in 16 bits (bf16 or fp16), with its gradients, and
+weights in 4 bits (low-level names fp8blk_*, as above); act is one of ACTS:
+
+    gated_linear(x, w, act, save) -> h [M,I]   (and with save the factors), w [2I,K] gates first
+    gated_linear_backward(d_h, x, w, factors, act, need_x, need_w) -> (d_x, d_w)
+    w4_quant(w, group, zeros) -> W4Weight(codes, scale, zeros)
+    w4_dequant(codes, scale, zeros) -> w [N,K]
+    w4_linear(x, codes, scale, zeros) -> y [M,N]
+    w4_gated_linear(x, codes, scale, zeros, act) -> h [M,I]
 """
 from __future__ import annotations
 
@@ -1233,8 +1243,8 @@ def _w4_quant_call(w, group, codes, scale, zeros):
 def fp8blk_w4_quant(w, codes, scale, zeros):
     """Weights w [N,K] to 4 bits into codes, scale and (None: no zero points)
     zeros; the group is K over scale's columns."""
-    _need(w, "w", (scale.dtype,), 2)
     N, K, group = _w4_in(codes, scale, zeros)
+    _need(w, "w", (scale.dtype,), 2)
     _shape_eq(w, (N, K), "w")
     _same_device(w, codes, scale, zeros)
     _w4_quant_call(w, group, codes, scale, zeros)

@@ -5,7 +5,22 @@
 //   d_x = dgu W,  d_W = dgu^T x.
 //
 // One kernel does both projections, the activation and the product (glu_tile.h);
-// the gradients are two more products on the same tiles (tile16.h).
+// the gradients are two more products on the same tiles (tile16.h), whose operands are
+// read where they lie, with the sum along rows or columns.
+//
+// Measured on one MI355X, on which a large 16-bit library product runs at 1.39 to 1.53
+// PFLOP/s and a large copy at 5.0 TB/s:
+//   4096 x 7168 -> 18432        1.65 ms, 1.31 PFLOP/s: matrix instructions at the 1.5 GHz
+//                               that they leave the chip, then the operands' way into LDS
+//   4096 x 4096 -> 14336, all   forward 795 us (with factors), factors 118, d_x 714
+//                               (1.35 PFLOP/s), d_W 770 (1.25)
+//   1003 x 1536 -> 4099, all    174 us: each product one partly empty round of tiles
+//   515 x 1000 -> 2731          20.4 us: 16 steps' latency and the copies to a 16-byte
+//                               pitch (3 us)
+//   1 x 4096 -> 14336           33.7 us: W at 7.0 TB/s
+// The factors are saved rather than g and u, so that the gradient needs no activation;
+// without them the first product runs again with the gradient's epilogue (1003 rows:
+// 56 us).
 #include <algorithm>
 
 #include "glu_tile.h"
@@ -58,11 +73,11 @@ struct Dense {
 };
 
 // ---------------------------------------------------------------------------
-// A few rows of x (single decoding sequences): W streams past once, a wave per few
-// outputs, 8 values a lane and row, 512 of K at a time; a lane's products are summed
+// One or two rows of x (single decoding sequences): W streams past once, 8 values a lane
+// and row, 512 of K at a time; a lane's products are summed
 // by the two-element dot product and the lanes' sums joined at the end.  Rows of any
 // width: 16 bytes at any even address, the last few of K one by one.  Bound: HBM
-// traffic of W.
+// traffic of W, which is loaded past the caches.
 template <typename T>
 struct Dot;
 template <>
@@ -129,7 +144,8 @@ __global__ __launch_bounds__(256) void few_kernel(FewArgs p) {
 #pragma unroll 2
   for (int64_t k = (int64_t)(wave % KS) * 512; k < whole; k += KS * 512) {
 #pragma unroll
-    for (int i = 0; i < kRows; ++i) wv[i] = __builtin_nontemporal_load(reinterpret_cast<const v4u_any *>(w[i] + k));
+    for (int i = 0; i < kRows; ++i)
+      wv[i] = __builtin_nontemporal_load(reinterpret_cast<const v4u_any *>(w[i] + k));
 #pragma unroll
     for (int m = 0; m < MT; ++m) xv[m] = *reinterpret_cast<const v4u_any *>(x[m] + k);
     add(wv, xv);
@@ -178,7 +194,8 @@ hipError_t few(const FewArgs &p, hipStream_t stream) {
   return hipGetLastError();
 }
 
-// dgu from the saved factors, 4 outputs a thread.
+// dgu from the saved factors, 4 outputs a thread.  Bound: HBM traffic (4096 x 14336:
+// 118 us, 704 MB, 6.0 TB/s).
 template <typename T>
 __global__ __launch_bounds__(256) void factors_kernel(const uint16_t *dh, const uint8_t *factors,
                                                       int64_t M, int64_t I, uint16_t *dgu,

@@ -2,6 +2,15 @@
 //   W[n, k] = (q[n, k] - z[n, k / group]) * s[n, k / group],   q in 0..15,
 // z = 8 where no zero points are kept.  Two codes a byte, even k in the low half;
 // scales in the activations' type (bf16 or fp16), zero points a byte each.
+//
+// Measured on one MI355X:
+//   quantizer, 18432 x 7168          75 us, and back 60: HBM (0.34 GB: 4.5, 5.6 TB/s)
+//   1 x 14336 -> 4096                9.1 us, gated 4096 -> 14336 14.1 us: the launch, then HBM
+//   37 x 7168 -> 2111                16.4 us: the loads' latency, 7 chunks a wave
+//   128 x 4096 -> 14336, gated       61 us: a stage's latency and its decoding
+//   2048 x 7168 -> 18432             570 us, 0.95 PFLOP/s: vector instructions (decoding, and
+//                                    the multiply-adds that scale each group's sum) beside
+//                                    the matrix instructions
 #include "glu_tile.h"
 
 namespace fp8blk {
@@ -9,9 +18,6 @@ namespace fp8blk {
 using namespace t16;
 
 namespace {
-
-
-
 
 struct Weights {
   const uint8_t *codes;      // [rows, K / 2]
@@ -370,7 +376,7 @@ __global__ __launch_bounds__(Tile::kThreads) void w4_product_kernel(Operand a, W
 }
 
 // ---------------------------------------------------------------------------
-// A few rows of x (single decoding sequences): the weights stream past once, a
+// One or two rows of x (single decoding sequences): the weights stream past once, a
 // wave per few rows of W, 32 codes a lane and row.  Bound: HBM traffic of the
 // codes.
 //
@@ -882,8 +888,9 @@ hipError_t launch_w4_dequant(const W4Call &c, void *w, hipStream_t stream) {
   return hipGetLastError();
 }
 
+// (the kernels of few rows launch 32 threads a row of W at most: 2^32 in all are too many)
 bool w4_fits(int64_t M, int64_t rows) {
-  return rows < (int64_t(1) << 28) && grid_fits(M, rows);
+  return rows <= (int64_t(1) << 26) && grid_fits(M, rows);
 }
 
 size_t w4_linear_workspace_bytes(int64_t M, int64_t N, int64_t K, int64_t ldx) {

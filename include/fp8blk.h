@@ -584,9 +584,11 @@ FP8BLK_API fp8blk_status fp8blk_gated_linear_backward(
  *   scale [N,K/group] of type
  *   zeros [N,K/group] bytes in 0..15, or NULL: every z is 8
  *   group: 32, 64 or 128; K a multiple of it, K <= 2^22
- * Products: N < 2^28 rows (2I of them for the gated form), M < 2^31, K <= x_stride <=
+ * Products: N <= 2^26 rows (2I of them for the gated form), M < 2^31, K <= x_stride <=
  * 2^22, and fewer than 2^23 tiles of 256 x 256 in a product
- * (FP8BLK_ERR_SHAPE). */
+ * (FP8BLK_ERR_SHAPE).  Codes meet x before the scale does: 31 |x| summed over a group
+ * stays finite in fp32 (|x| < 2^116 suffices).  Past that, and in rows of x that hold an
+ * infinity or NaN, an output may be NaN. */
 
 /* Weights [N,K] of type to 4 bits; per group
  *   with zero points: lo = min(0, least weight), hi = max(0, largest),

@@ -44,7 +44,7 @@ def gated(lib, x=A, ldx=None, kind=1, M=4, N=0, K=256, group=64, codes=B, s=C, z
 @pytest.mark.parametrize("bad,want", WEIGHTS + [
     (dict(N=4, x=NULL), NULL_), (dict(N=4, y=NULL), NULL_), (dict(N=4, x=MIS), ALIGN), (dict(N=4, y=MIS), ALIGN),
     (dict(N=4, M=-1), SHAPE), (dict(N=4, M=1 << 31), SHAPE), (dict(N=4, ldx=255), SHAPE),
-    (dict(N=4, ldx=(1 << 22) + 8), SHAPE), (dict(N=1 << 26, M=1 << 30), SHAPE), (dict(N=1 << 28), SHAPE),
+    (dict(N=4, ldx=(1 << 22) + 8), SHAPE), (dict(N=1 << 26, M=1 << 30), SHAPE), (dict(N=(1 << 26) + 1), SHAPE), (dict(N=1 << 28), SHAPE),
     (dict(N=4, M=300, ldx=257, work=NULL), NULL_), (dict(N=4, M=300, ldx=257, nbytes=16), SHAPE),
     (dict(N=4, M=300, ldx=257, work=MIS), ALIGN)])
 def test_w4_product_arguments(lib, call, bad, want):  # noqa: F811
