@@ -4,7 +4,7 @@
 // scales in the activations' type (bf16 or fp16), zero points a byte each.
 //
 // Measured on one MI355X:
-//   quantizer, 18432 x 7168          75 us, and back 60: HBM (0.34 GB: 4.5, 5.6 TB/s)
+//   quantizer, 18432 x 7168          57 us, and back 47: HBM (0.33 GB: 5.9, 7.1 TB/s)
 //   1 x 14336 -> 4096                9.1 us, gated 4096 -> 14336 14.1 us: the launch, then HBM
 //   37 x 7168 -> 2111                16.4 us: the loads' latency, 7 chunks a wave
 //   128 x 4096 -> 14336, gated       61 us: a stage's latency and its decoding
@@ -39,60 +39,110 @@ struct Weights {
 // far further from one than fp32's rounding, so rint of the fp32 quotient is that
 // of the exact one.
 //
-// fl32(w / s): the product with the reciprocal, corrected once by its exact
-// residual.  For tiny s both are scaled by 2^100 first (exactly), so that neither
-// the reciprocal overflows nor the residual underflows.
+// The quotient w / s: the product with the reciprocal, corrected once by its exact
+// residual, which makes it exact where it is representable (half whole numbers, ties,
+// are).  For tiny s both are scaled by 2^100 first (exactly), so that neither the
+// reciprocal overflows nor the residual underflows.
 struct Quotient {
   float f, s, y;
   __device__ __forceinline__ explicit Quotient(float step) {
     f = step < 0x1p-64f ? 0x1p100f : 1.0f;
     s = step * f;
-    y = step > 0.0f ? 1.0f / s : 0.0f;
+    y = step > 0.0f ? __builtin_amdgcn_rcpf(s) : 0.0f;
   }
-  __device__ __forceinline__ float operator()(float w) const {
+  // rint(w / s), of quotients far below 2^22: 1.5 2^23 + it, whose low bits it is.
+  __device__ __forceinline__ int operator()(float w) const {
     const float v = w * f, q = v * y;
-    return __builtin_fmaf(__builtin_fmaf(-q, s, v), y, q);
+    return __float_as_int(__builtin_fmaf(__builtin_fmaf(-q, s, v), y, q) + 0x1.8p23f) - 0x4b400000;
   }
 };
+// fl32(a / D) of a small odd D.  What the one correction leaves wrong is below 2^-24
+// of the last place, and a / D lies 1 / (2 D) of a place off any tie.
+template <int D>
+__device__ __forceinline__ float over(float a) {
+  constexpr float kInverse = 1.0f / D;
+  const float q = a * kInverse;
+  return __builtin_fmaf(__builtin_fmaf(-q, (float)D, a), kInverse, q);
+}
+// f over the LANES (4, 8 or 16) neighbouring lanes of a group: lanes trade 1 and 2 apart,
+// then halves of 8 and of 16 mirrored, equal within themselves by then.
+template <int LANES, typename V, typename F>
+__device__ __forceinline__ V over_lanes(V v, F f) {
+  static_assert(sizeof(V) == 4 && (LANES == 4 || LANES == 8 || LANES == 16), "");
+  auto from = [](V u, auto ctrl) {
+    return __builtin_bit_cast(
+        V, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, u), ctrl.value, 0xf, 0xf, true));
+  };
+  v = f(v, from(v, std::integral_constant<int, 0xb1>{}));      // 1 0 3 2
+  v = f(v, from(v, std::integral_constant<int, 0x4e>{}));      // 2 3 0 1
+  if constexpr (LANES >= 8) v = f(v, from(v, std::integral_constant<int, 0x141>{}));
+  if constexpr (LANES >= 16) v = f(v, from(v, std::integral_constant<int, 0x140>{}));
+  return v;
+}
 
-template <typename T, int GROUP>
+// Chunks a thread loads ahead (18432 x 7168: one 61 us, two 57, four 55 to quantize; back,
+// two 47, four 55), w past the caches (back by plain stores: 60).
+constexpr int kAhead = 2;
+
+// Bound: HBM, with about as much time in vector instructions, hence the reciprocals and
+// lane exchanges above (divisions and shuffles: 76 us at 18432 x 7168, 66 without them and
+// one chunk a thread, now 57).
+template <typename T, int GROUP, bool ZEROS>
 __global__ __launch_bounds__(256) void w4_quant_kernel(const uint16_t *w, int64_t chunks,
                                                        uint32_t *codes, uint16_t *scale,
                                                        uint8_t *zeros) {
   constexpr int kLanes = GROUP / 8;
-  // chunks is whole groups, and a group's lanes share a wave: they run together
-  for (int64_t at = first_item(); at < chunks; at += all_threads()) {
-    const v4u v = *reinterpret_cast<const v4u *>(w + at * 8);
+  auto one = [&](int64_t at, v4u v) {
     float e[8];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       e[2 * j] = T::value(v[j] & 0xffff);
       e[2 * j + 1] = T::value(v[j] >> 16);
     }
-    float lo = 0.0f, hi = 0.0f;
+    float range, lo = 0.0f;
+    if constexpr (ZEROS) {
+      float hi = 0.0f;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      lo = fminf(lo, e[j]);
-      hi = fmaxf(hi, e[j]);
-    }
+      for (int j = 0; j < 8; ++j) {
+        lo = fminf(lo, e[j]);
+        hi = fmaxf(hi, e[j]);
+      }
+      lo = over_lanes<kLanes>(lo, [](float a, float b) { return fminf(a, b); });
+      hi = over_lanes<kLanes>(hi, [](float a, float b) { return fmaxf(a, b); });
+      range = over<15>(hi - lo);
+    } else {
+      // magnitudes are ordered as their bits are
+      typedef unsigned short v2us __attribute__((ext_vector_type(2)));
+      auto larger = [](v2us a, v2us b) { return __builtin_elementwise_max(a, b); };
+      v2us m = {0, 0};
 #pragma unroll
-    for (int d = 1; d < kLanes; d *= 2) {
-      lo = fminf(lo, __shfl_xor(lo, d));
-      hi = fmaxf(hi, __shfl_xor(hi, d));
+      for (int j = 0; j < 4; ++j) m = larger(m, __builtin_bit_cast(v2us, v[j] & 0x7fff7fffu));
+      m = over_lanes<kLanes>(m, larger);
+      range = over<7>(T::value(m[0] > m[1] ? m[0] : m[1]));
     }
-    const float range = zeros ? (hi - lo) / 15.0f : fmaxf(hi, -lo) / 7.0f;
     const uint32_t bits = T::bits(range);
-    const Quotient over(T::value(bits));
-    const float z = zeros ? fminf(fmaxf(rintf(over(-lo)), 0.0f), 15.0f) : 8.0f;
+    const Quotient quotient(T::value(bits));
+    const int z = ZEROS ? min(max(quotient(-lo), 0), 15) : 8;
     uint32_t c = 0;
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
-      c |= (uint32_t)fminf(fmaxf(rintf(over(e[j])) + z, 0.0f), 15.0f) << (4 * j);
-    codes[at] = c;
+    for (int j = 0; j < 8; ++j) c |= (uint32_t)min(max(quotient(e[j]) + z, 0), 15) << (4 * j);
+    __builtin_nontemporal_store(c, codes + at);
     if (at % kLanes == 0) {
       scale[at / kLanes] = (uint16_t)bits;
-      if (zeros) zeros[at / kLanes] = (uint8_t)z;
+      if constexpr (ZEROS) zeros[at / kLanes] = (uint8_t)z;
     }
+  };
+  // chunks is whole groups, and a group's lanes share a wave: they run together
+  for (int64_t at = (int64_t)blockIdx.x * (256 * kAhead) + threadIdx.x; at < chunks;
+       at += (int64_t)gridDim.x * (256 * kAhead)) {
+    v4u v[kAhead];
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i)
+      v[i] = __builtin_nontemporal_load(
+          reinterpret_cast<const v4u *>(w + min(at + i * 256, chunks - 1) * 8));
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i)
+      if (at + i * 256 < chunks) one(at + i * 256, v[i]);
   }
 }
 
@@ -109,14 +159,28 @@ __device__ __forceinline__ void decode8(uint32_t c, float z, float (&w)[8]) {
 
 template <typename T>
 __global__ __launch_bounds__(256) void w4_dequant_kernel(Weights p, int64_t chunks, uint16_t *w) {
-  for (int64_t at = first_item(); at < chunks; at += all_threads()) {
-    const int64_t g = at * 8 >> p.shift;
-    const float s = T::value(p.scale[g]);
-    float v[8];     // (the products are exact in fp32: at most 5 + 11 bits)
-    decode8(reinterpret_cast<const uint32_t *>(p.codes)[at], p.zeros ? (float)p.zeros[g] : 8.0f, v);
-    *reinterpret_cast<v4u *>(w + at * 8) =
-        v4u{pack2<T>(v[0] * s, v[1] * s), pack2<T>(v[2] * s, v[3] * s),
-            pack2<T>(v[4] * s, v[5] * s), pack2<T>(v[6] * s, v[7] * s)};
+  for (int64_t from = (int64_t)blockIdx.x * (256 * kAhead) + threadIdx.x; from < chunks;
+       from += (int64_t)gridDim.x * (256 * kAhead)) {
+    uint32_t c[kAhead];
+    float s[kAhead], z[kAhead];
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      const int64_t at = min(from + i * 256, chunks - 1), g = at * 8 >> p.shift;
+      c[i] = reinterpret_cast<const uint32_t *>(p.codes)[at];
+      s[i] = T::value(p.scale[g]);
+      z[i] = p.zeros ? (float)p.zeros[g] : 8.0f;
+    }
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      const int64_t at = from + i * 256;
+      float v[8];     // (the products are exact in fp32: at most 5 + 11 bits)
+      decode8(c[i], z[i], v);
+      if (at < chunks)
+        __builtin_nontemporal_store(
+            v4u{pack2<T>(v[0] * s[i], v[1] * s[i]), pack2<T>(v[2] * s[i], v[3] * s[i]),
+                pack2<T>(v[4] * s[i], v[5] * s[i]), pack2<T>(v[6] * s[i], v[7] * s[i])},
+            reinterpret_cast<v4u *>(w + at * 8));
+    }
   }
 }
 
@@ -861,13 +925,19 @@ hipError_t gated(const W4Call &c, int act, void *h, void *work, hipStream_t stre
 template <typename T>
 hipError_t quant(const void *w, int64_t chunks, int group, void *codes, void *scale, void *zeros,
                  hipStream_t stream) {
-  const uint16_t *in = static_cast<const uint16_t *>(w);
-  uint32_t *q = static_cast<uint32_t *>(codes);
-  uint16_t *s = static_cast<uint16_t *>(scale);
-  uint8_t *z = static_cast<uint8_t *>(zeros);
-  if (group == 32) w4_quant_kernel<T, 32><<<groups(chunks), 256, 0, stream>>>(in, chunks, q, s, z);
-  else if (group == 64) w4_quant_kernel<T, 64><<<groups(chunks), 256, 0, stream>>>(in, chunks, q, s, z);
-  else w4_quant_kernel<T, 128><<<groups(chunks), 256, 0, stream>>>(in, chunks, q, s, z);
+  auto run = [&](auto size) {
+    constexpr int G = size.value;
+    const uint16_t *in = static_cast<const uint16_t *>(w);
+    uint32_t *q = static_cast<uint32_t *>(codes);
+    uint16_t *s = static_cast<uint16_t *>(scale);
+    uint8_t *z = static_cast<uint8_t *>(zeros);
+    const dim3 grid = groups(tiles(chunks, kAhead));
+    if (z) w4_quant_kernel<T, G, true><<<grid, 256, 0, stream>>>(in, chunks, q, s, z);
+    else w4_quant_kernel<T, G, false><<<grid, 256, 0, stream>>>(in, chunks, q, s, z);
+  };
+  if (group == 32) run(std::integral_constant<int, 32>{});
+  else if (group == 64) run(std::integral_constant<int, 64>{});
+  else run(std::integral_constant<int, 128>{});
   return hipGetLastError();
 }
 
@@ -883,8 +953,9 @@ hipError_t launch_w4_quant(const void *w, bool bf16, int64_t rows, int64_t K, in
 hipError_t launch_w4_dequant(const W4Call &c, void *w, hipStream_t stream) {
   const int64_t chunks = c.rows * (c.K / 8);
   uint16_t *out = static_cast<uint16_t *>(w);
-  if (c.bf16) w4_dequant_kernel<Bf16><<<groups(chunks), 256, 0, stream>>>(weights(c), chunks, out);
-  else w4_dequant_kernel<F16><<<groups(chunks), 256, 0, stream>>>(weights(c), chunks, out);
+  const dim3 grid = groups(tiles(chunks, kAhead));
+  if (c.bf16) w4_dequant_kernel<Bf16><<<grid, 256, 0, stream>>>(weights(c), chunks, out);
+  else w4_dequant_kernel<F16><<<grid, 256, 0, stream>>>(weights(c), chunks, out);
   return hipGetLastError();
 }
 
