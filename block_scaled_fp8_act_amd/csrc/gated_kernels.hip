@@ -15,7 +15,7 @@
 //   4096 x 4096 -> 14336, all   forward 795 us (with factors), factors 118, d_x 714
 //                               (1.35 PFLOP/s), d_W 770 (1.25)
 //   1003 x 1536 -> 4099, all    174 us: each product one partly empty round of tiles
-//   515 x 1000 -> 2731          20.4 us: 16 steps' latency and the copies to a 16-byte
+//   515 x 1000 -> 2731          20.4 us: 16 steps' latency and the copy of x to a 16-byte
 //                               pitch (3 us)
 //   1 x 4096 -> 14336           33.7 us: W at 7.0 TB/s
 // The factors are saved rather than g and u, so that the gradient needs no activation;
