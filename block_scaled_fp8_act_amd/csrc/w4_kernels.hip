@@ -4,13 +4,13 @@
 // scales in the activations' type (bf16 or fp16), zero points a byte each.
 //
 // Measured on one MI355X:
-//   quantizer, 18432 x 7168          57 us, and back 47: HBM (0.33 GB: 5.9, 7.1 TB/s)
+//   quantizer, 18432 x 7168          57 us, and back 48: HBM (0.33 GB: 5.9, 6.9 TB/s)
 //   1 x 14336 -> 4096                9.1 us, gated 4096 -> 14336 14.1 us: the launch, then HBM
 //   37 x 7168 -> 2111                16.4 us: the loads' latency, 7 chunks a wave
 //   128 x 4096 -> 14336, gated       61 us: a stage's latency and its decoding
-//   2048 x 7168 -> 18432             570 us, 0.95 PFLOP/s: vector instructions (decoding, and
-//                                    the multiply-adds that scale each group's sum) beside
-//                                    the matrix instructions
+//   2048 x 7168 -> 18432             570 us, 0.95 PFLOP/s: vector instructions (69 % of the
+//                                    busy cycles: decoding, and the multiply-adds that scale
+//                                    each group's sum) beside the matrix ones (48 %)
 #include "glu_tile.h"
 
 namespace fp8blk {
