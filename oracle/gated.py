@@ -7,8 +7,7 @@ Test infrastructure: see the package docstring for who may import this.
 
 Each result comes with the largest error that the library's roundings allow:
 fp32 sums of n terms in any order, at most 2^-23 of their magnitudes an
-addition; the activation within 2^-17 (its exponential's argument, 2^7 at most, is
-rounded to 24 bits); one rounding to the 16-bit type (half a
+addition; the activation within 2^-20; one rounding to the 16-bit type (half a
 step, `half`) of h, of dgu, and of the gradients; 24 bits of the factors where
 they are saved.
 """
@@ -20,7 +19,7 @@ import numpy as np
 
 HALF = {"bfloat16": 2.0 ** -8, "float16": 2.0 ** -11}
 TINY = {"bfloat16": 2.0 ** -133, "float16": 2.0 ** -25}    # half the smallest step
-ADD, EVAL, KEPT = 2.0 ** -23, 2.0 ** -17, 2.0 ** -16
+ADD, EVAL, KEPT = 2.0 ** -23, 2.0 ** -20, 2.0 ** -16
 SLOPE = 1.13        # |act'| <= 1.129 and |act''| <= 1 for all three
 
 _erf = np.vectorize(math.erf, otypes=[np.float64])
