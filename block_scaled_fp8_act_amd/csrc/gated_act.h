@@ -54,8 +54,9 @@ __device__ __forceinline__ float normal(float g, float &bell) {
 
 // z of the form by tanh, g (1 + tanh(z / 2)) / 2 = g / (1 + e^-z): sqrt(8 / pi) (g +
 // 0.044715 g^3).  Past |g| = 12 its logistic is 1 or 0 in fp32, and a cube could overflow.
+// NaN stays NaN (fmax and fmin would make a number of it, and the slope 0).
 __device__ __forceinline__ float within12(float g) {
-  return __builtin_fminf(__builtin_fmaxf(g, -12.0f), 12.0f);
+  return __builtin_elementwise_minimum(__builtin_elementwise_maximum(g, -12.0f), 12.0f);
 }
 // z = c (A + B c^2), A = sqrt(8 / pi), B = 0.044715 A, and what its roundings leave out:
 // z passes 100, and in one part its error would be that many units of 2^-24 in the tail.
