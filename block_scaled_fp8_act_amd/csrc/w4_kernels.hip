@@ -34,7 +34,9 @@ struct Weights {
 //   with zero points: s = T(fl32((hi - lo) / 15)), lo and hi its least and largest
 //     weight with 0 among them; z = clamp(rint(-lo / s), 0, 15)
 //   without: s = T(fl32(max |w| / 7)), z = 8
-//   q = clamp(rint(w / s) + z, 0, 15);  s = 0: q = z (0 or 8).
+//   q = clamp(rint(w / s) + z, 0, 15);  s = 0, infinite or NaN: q = z (0 or 8).
+// A NaN in a group makes s NaN, an infinity makes it infinite (both maxima and minima
+// hand NaN on), so that neither is taken for a weight.
 // w and s are 16-bit floats: a quotient that is not half a whole number itself is
 // far further from one than fp32's rounding, so rint of the fp32 quotient is that
 // of the exact one.
@@ -57,12 +59,13 @@ struct Quotient {
   }
 };
 // fl32(a / D) of a small odd D.  What the one correction leaves wrong is below 2^-24
-// of the last place, and a / D lies 1 / (2 D) of a place off any tie.
+// of the last place, and a / D lies 1 / (2 D) of a place off any tie.  An infinity has no
+// residual and stays one.
 template <int D>
 __device__ __forceinline__ float over(float a) {
   constexpr float kInverse = 1.0f / D;
   const float q = a * kInverse;
-  return __builtin_fmaf(__builtin_fmaf(-q, (float)D, a), kInverse, q);
+  return a < __builtin_inff() ? __builtin_fmaf(__builtin_fmaf(-q, (float)D, a), kInverse, q) : a;
 }
 // f over the LANES (4, 8 or 16) neighbouring lanes of a group: lanes trade 1 and 2 apart,
 // then halves of 8 and of 16 mirrored, equal within themselves by then.
@@ -104,11 +107,11 @@ __global__ __launch_bounds__(256) void w4_quant_kernel(const uint16_t *w, int64_
       float hi = 0.0f;
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        lo = fminf(lo, e[j]);
-        hi = fmaxf(hi, e[j]);
+        lo = __builtin_elementwise_minimum(lo, e[j]);
+        hi = __builtin_elementwise_maximum(hi, e[j]);
       }
-      lo = over_lanes<kLanes>(lo, [](float a, float b) { return fminf(a, b); });
-      hi = over_lanes<kLanes>(hi, [](float a, float b) { return fmaxf(a, b); });
+      lo = over_lanes<kLanes>(lo, [](float a, float b) { return __builtin_elementwise_minimum(a, b); });
+      hi = over_lanes<kLanes>(hi, [](float a, float b) { return __builtin_elementwise_maximum(a, b); });
       range = over<15>(hi - lo);
     } else {
       // magnitudes are ordered as their bits are
@@ -121,11 +124,14 @@ __global__ __launch_bounds__(256) void w4_quant_kernel(const uint16_t *w, int64_
       range = over<7>(T::value(m[0] > m[1] ? m[0] : m[1]));
     }
     const uint32_t bits = T::bits(range);
-    const Quotient quotient(T::value(bits));
-    const int z = ZEROS ? min(max(quotient(-lo), 0), 15) : 8;
+    const float step = T::value(bits);
+    const Quotient quotient(step);
+    const bool finite = step < __builtin_inff();      // (not of NaN)
+    const int z = ZEROS ? (finite ? min(max(quotient(-lo), 0), 15) : 0) : 8;
     uint32_t c = 0;
 #pragma unroll
     for (int j = 0; j < 8; ++j) c |= (uint32_t)min(max(quotient(e[j]) + z, 0), 15) << (4 * j);
+    if (!finite) c = ZEROS ? 0u : 0x88888888u;
     __builtin_nontemporal_store(c, codes + at);
     if (at % kLanes == 0) {
       scale[at / kLanes] = (uint16_t)bits;

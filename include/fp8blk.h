@@ -595,8 +595,10 @@ FP8BLK_API fp8blk_status fp8blk_gated_linear_backward(
  *     s = type(fl32(fl32(hi - lo) / 15)), z = clamp(rint(-lo / s), 0, 15)
  *   zeros NULL: s = type(fl32(max |w| / 7)), z = 8
  *   q = clamp(rint(w / s) + z, 0, 15)
- * rint to the nearest whole number, ties to even; s = 0 gives q = z (0 with zero
- * points).  hi - lo has to be finite in fp32. */
+ * rint to the nearest whole number, ties to even.  A group that holds a NaN has a NaN
+ * scale; one that holds an infinity, or whose hi - lo passes fp32's range, an infinite
+ * one: the values that such a group stands for are NaN.  s = 0, infinite or NaN gives
+ * q = z, with zero points z = 0. */
 FP8BLK_API fp8blk_status fp8blk_w4_quant(const void *w, int type, int64_t N, int64_t K, int group,
                                          void *codes, void *scale, void *zeros, void *stream);
 

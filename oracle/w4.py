@@ -3,7 +3,8 @@
 Test infrastructure: see the package docstring for who may import this.
 
     W[n,k] = (q - z) s;  s = T(fl32(fl32(hi - lo) / 15)), z = clamp(rint(-lo / s), 0, 15)
-    (without zero points s = T(fl32(max |w| / 7)), z = 8), q = clamp(rint(w / s) + z, 0, 15)
+    (without zero points s = T(fl32(max |w| / 7)), z = 8), q = clamp(rint(w / s) + z, 0, 15);
+    s = 0, infinite or NaN: q = z, with zero points z = 0
 """
 from __future__ import annotations
 
@@ -28,12 +29,14 @@ def quant(w, group, zeros, dtype):
     v = w.reshape(n, k // group, group)
     if zeros:
         lo, hi = np.minimum(v.min(2), 0), np.maximum(v.max(2), 0)
-        s = to_type(((hi - lo).astype(np.float32) / np.float32(15)), dtype)
+        with np.errstate(over="ignore"):
+            s = to_type(((hi - lo).astype(np.float32) / np.float32(15)), dtype)
     else:
         s = to_type(np.abs(v).max(2).astype(np.float32) / np.float32(7), dtype)
+    ok = (s > 0) & (s < np.inf)
     with np.errstate(divide="ignore", invalid="ignore"):
-        z = np.clip(np.rint(np.where(s > 0, -lo / s, 0)), 0, 15) if zeros else np.full(s.shape, 8.0)
-        r = np.rint(np.where(s[:, :, None] > 0, v / s[:, :, None], 0))
+        z = np.clip(np.rint(np.where(ok, -lo / s, 0)), 0, 15) if zeros else np.full(s.shape, 8.0)
+        r = np.rint(np.where(ok[:, :, None], v / s[:, :, None], 0))
     q = np.clip(r + z[:, :, None], 0, 15).reshape(n, k).astype(np.uint8)
     return q, s, z.astype(np.uint8)
 
