@@ -502,6 +502,37 @@ struct W4Few {
   uint16_t *out;          // [M, I]
 };
 
+// Output n of row m from codes less their zero point, as the tiles form it, by one thread:
+// where the sum with the bias is not finite.  The bias makes NaN of an infinite x (the
+// same infinity is added and taken off) and may pass fp32's range where the sum does not.
+template <typename T>
+__device__ __forceinline__ float w4_plain(const W4Few &p, int64_t m, int64_t n) {
+  const uint16_t *x = p.x + m * p.ldx;
+  const uint8_t *codes = p.w.codes + n * (p.K / 2);
+  const int64_t groups = p.K >> p.w.shift;
+  float acc = 0.0f;
+  for (int64_t g = 0; g < groups; ++g) {
+    const int64_t at = n * groups + g, end = (g + 1) << p.w.shift;
+    const float z = p.w.zeros ? (float)p.w.zeros[at] : 8.0f;
+    float sum = 0.0f;
+    for (int64_t k = g << p.w.shift; k < end; k += 8) {
+      float w[8];
+      decode8(*reinterpret_cast<const uint32_t *>(codes + k / 2), z, w);
+      const v4u v = *reinterpret_cast<const v4u_any *>(x + k);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        sum = __builtin_fmaf(w[2 * j], T::value(v[j] & 0xffff), sum);
+        sum = __builtin_fmaf(w[2 * j + 1], T::value(v[j] >> 16), sum);
+      }
+    }
+    acc = __builtin_fmaf(sum, T::value(p.w.scale[at]), acc);
+  }
+  return acc;
+}
+__device__ __forceinline__ bool finite(float v) {
+  return __builtin_fabsf(v) < __builtin_inff();
+}
+
 // R outputs a wave, MT rows of x (M of them there), the K range shared by KS waves.
 template <typename T, bool PAIR, int R, int MT, int KS>
 __global__ __launch_bounds__(256) void w4_few_kernel(W4Few p) {
@@ -586,6 +617,7 @@ __global__ __launch_bounds__(256) void w4_few_kernel(W4Few p) {
     v[h] = 0.0f;
 #pragma unroll
     for (int i = 0; i < KS; ++i) v[h] += red[w0 + i][(h * R + r) * MT + m];
+    if (!finite(v[h])) v[h] = w4_plain<T>(p, m, n + h * p.I);
   }
   float y = v[0];
   if constexpr (PAIR) y = act_any(p.act, v[0]) * v[1];
@@ -798,6 +830,9 @@ __global__ __launch_bounds__(512, MF == 1 ? 4 : 2) void w4_slab_kernel(W4Few p) 
     const int m = v / 4 % MF * 16 + 4 * (l >> 4) + v % 4;
     const int64_t n = n0 + v / (4 * MF) * 16 + (l & 15);
     if (m >= p.M || n >= p.I) continue;
+#pragma unroll
+    for (int h = 0; h < (PAIR ? 2 : 1); ++h)
+      if (!finite(y[h])) y[h] = w4_plain<T>(p, m, n + h * p.I);
     float out = y[0];
     if constexpr (PAIR) out = act_any(p.act, y[0]) * y[1];
     p.out[m * p.I + n] = (uint16_t)T::bits(out);

@@ -586,9 +586,9 @@ FP8BLK_API fp8blk_status fp8blk_gated_linear_backward(
  *   group: 32, 64 or 128; K a multiple of it, K <= 2^22
  * Products: N <= 2^26 rows (2I of them for the gated form), M < 2^31, K <= x_stride <=
  * 2^22, and fewer than 2^23 tiles of 256 x 256 in a product
- * (FP8BLK_ERR_SHAPE).  Codes meet x before the scale does: 31 |x| summed over a group
- * stays finite in fp32 (|x| < 2^116 suffices).  Past that, and in rows of x that hold an
- * infinity or NaN, an output may be NaN. */
+ * (FP8BLK_ERR_SHAPE).  Codes meet x before the scale does: 15 |x| summed over a group
+ * has to stay finite in fp32.  An infinity in x gives what (q - z) x does: an infinity,
+ * or NaN where q = z; other rows are not touched by it. */
 
 /* Weights [N,K] of type to 4 bits; per group
  *   with zero points: lo = min(0, least weight), hi = max(0, largest),
