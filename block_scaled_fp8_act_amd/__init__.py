@@ -1102,7 +1102,8 @@ def factor_row(I):
 
 def _gated_in(x, w, *more, factors=None):
     """Row stride of x, sizes (M, I, K); ``more`` are (tensor, name) of [M,I]."""
-    if not more and x.dim() == 2 and w.dim() == 2 and x.dtype in _HALF:
+    if (not more and isinstance(x, torch.Tensor) and isinstance(w, torch.Tensor) and
+            x.dim() == 2 and w.dim() == 2 and x.dtype in _HALF):
         (M, K), rows = x.shape, w.shape[0]
         if K and rows % 2 == 0 and _plain(x.get_device(), (x, x.dtype, (M, K)),
                                           (w, x.dtype, (rows, K))):
@@ -1220,7 +1221,9 @@ def _w4_in(codes, scale, zeros):
 
 def _w4_product_in(x, codes, scale, zeros):
     """Row stride of x, sizes (M, N, K, group)."""
-    if x.dim() == 2 and codes.dim() == 2 and scale.dim() == 2 and x.dtype in _HALF:
+    if (isinstance(x, torch.Tensor) and isinstance(codes, torch.Tensor) and
+            isinstance(scale, torch.Tensor) and (zeros is None or isinstance(zeros, torch.Tensor)) and
+            x.dim() == 2 and codes.dim() == 2 and scale.dim() == 2 and x.dtype in _HALF):
         (M, K), (N, groups) = x.shape, scale.shape
         if (groups and K % groups == 0 and K // groups in W4_GROUPS and
                 _plain(x.get_device(), (x, x.dtype, (M, K)), (codes, torch.uint8, (N, K // 2)),
