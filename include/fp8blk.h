@@ -562,7 +562,9 @@ FP8BLK_API fp8blk_status fp8blk_gated_linear(const void *x, int64_t x_stride, co
                                              size_t workspace_bytes, void *stream);
 
 /* Gradients of fp8blk_gated_linear: dgu = (d_h u act'(g), d_h act(g)) rounded
- * once to type, d_x = dgu W, d_w = dgu^T x.
+ * once to type, d_x = dgu W, d_w = dgu^T x.  The rounding has type's range: in fp16 a
+ * dgu past 65504 is an infinity, which d_x's row and d_w's row of it show (as infinities
+ * or NaN), and one below 2^-25 is zero, so fp16 gradients want the loss scaled.
  *   d_h [M,I] in
  *   factors in, as the forward call wrote it, or NULL: g and u are then
  *       computed again (act is read only in this case)
