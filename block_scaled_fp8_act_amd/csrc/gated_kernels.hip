@@ -10,17 +10,23 @@
 //
 // Measured on one MI355X, on which a large 16-bit library product runs at 1.39 to 1.53
 // PFLOP/s and a large copy at 5.0 TB/s:
-//   4096 x 7168 -> 18432        1.65 ms, 1.31 PFLOP/s: matrix instructions at the 1.5 GHz
+//   4096 x 7168 -> 18432        1.63 ms, 1.33 PFLOP/s: matrix instructions at the 1.5 GHz
 //                               that they leave the chip, then the operands' way into LDS
 //   4096 x 4096 -> 14336, all   forward 795 us (with factors), factors 118, d_x 714
 //                               (1.35 PFLOP/s), d_W 770 (1.25)
-//   1003 x 1536 -> 4099, all    174 us: each product one partly empty round of tiles
-//   515 x 1000 -> 2731          20.4 us: 16 steps' latency and the copy of x to a 16-byte
+//   1003 x 1536 -> 4099, all    177 us: each product one partly empty round of tiles
+//   515 x 1000 -> 2731          20.6 us: 16 steps' latency and the copy of x to a 16-byte
 //                               pitch (3 us)
 //   1 x 4096 -> 14336           33.7 us: W at 7.0 TB/s
 // The factors are saved rather than g and u, so that the gradient needs no activation;
 // without them the first product runs again with the gradient's epilogue (1003 rows:
-// 56 us).
+// 60 us).
+//
+// dgu is rounded to 16 bits once, as the matrix instructions take it.  With that and their
+// own rounding d_x and d_W are 1.41 times as far from binary64 as fp32 sums of an unrounded
+// dgu (bf16 0.0023 against 0.0017, fp16 0.00029 against 0.00021, relative).  A second 16-bit
+// part of it would take the difference away and run both products again (at 4096 x 4096 ->
+// 14336 another 714 and 770 us beside the step's 2400).
 #include <algorithm>
 
 #include "glu_tile.h"

@@ -5,12 +5,15 @@
 //
 // Measured on one MI355X:
 //   quantizer, 18432 x 7168          57 us, and back 48: HBM (0.33 GB: 5.9, 6.9 TB/s)
-//   1 x 14336 -> 4096                9.1 us, gated 4096 -> 14336 14.1 us: the launch, then HBM
-//   37 x 7168 -> 2111                16.4 us: the loads' latency, 7 chunks a wave
+//   1 x 14336 -> 4096                9.1 us: four waves' two rounds of 2048 of K, the second
+//                                    loaded behind the first's products
+//   1 x 4096 -> 14336, gated         14.2 us: HBM
+//   37 x 7168 -> 2111                16.5 us: the loads' latency, 7 chunks a wave
 //   128 x 4096 -> 14336, gated       61 us: a stage's latency and its decoding
-//   2048 x 7168 -> 18432             570 us, 0.95 PFLOP/s: vector instructions (69 % of the
+//   2048 x 7168 -> 18432             560 us, 0.97 PFLOP/s: vector instructions (69 % of the
 //                                    busy cycles: decoding, and the multiply-adds that scale
-//                                    each group's sum) beside the matrix ones (48 %)
+//                                    each group's sum) beside the matrix ones (48 %); LDS
+//                                    bank conflicts (18 %, their source not found)
 #include "glu_tile.h"
 
 namespace fp8blk {
@@ -871,8 +874,12 @@ constexpr int64_t kFewRows = 2;
 
 template <typename T, bool PAIR, int MT>
 hipError_t few(const W4Few &p, hipStream_t stream) {
-  // four rows of W a wave; whole K a wave where those alone give the chip enough waves
-  // (gated 4096 -> 14336: 14.1 us; K shared by four waves 17.9)
+  // Four rows of W a wave; whole K a wave where those alone give the chip enough waves,
+  // else K shared by four.  One row, weights from HBM, us (whole K, shared): 4096 -> 8192
+  // 9.6, 9.8; 4096 -> 14336 12, 14; 4096 -> 28672 18, 25; gated 4096 -> 8192 12.4, 15.6,
+  // 4096 -> 14336 18, 25, 7168 -> 18432 39, 44.  Below the border 14336 -> 4096 17, 11.7;
+  // gated 8192 -> 3584 13.6, 11.7.  The rule loses where many rows meet a long K (14336 ->
+  // 8192 23, 19; 8192 -> 16384 24.5, 23.3, but two rows of it 28, 35).
   constexpr int R = PAIR ? 2 : 4;
   if (p.I / R >= 2048 || p.K <= 2048)
     w4_few_kernel<T, PAIR, R, MT, 1><<<dim3((unsigned)tiles(p.I, 4 * R)), 256, 0, stream>>>(p);
@@ -887,6 +894,10 @@ hipError_t few(const W4Call &c, int act, void *out, hipStream_t stream) {
   return c.M == 1 ? few<T, PAIR, 1>(p, stream) : few<T, PAIR, 2>(p, stream);
 }
 
+// With more the kernel's registers run out.  Against the tiles, weights from HBM, us (here,
+// tiles): 3 rows of 4096 -> 4096 9.9, 17.3, of 4096 -> 28672 28, 46; 32 rows 9.5, 19 and
+// 45, 48; 48 rows 12, 21 and 58, 52, of 7168 -> 18432 63, 52, of 14336 -> 4096 32, 31.5,
+// gated of 4096 -> 4096 15, 27, of 4096 -> 14336 58, 52.
 constexpr int64_t kSlabRows = 48;
 
 template <typename T, bool PAIR, int GS, int NR, int MF>
@@ -897,8 +908,10 @@ hipError_t slab(const W4Few &p, hipStream_t stream) {
 }
 template <typename T, bool PAIR, int GS>
 hipError_t slab(const W4Few &p, hipStream_t stream) {
-  // two blocks of rows read x half as often, where they still give every compute
-  // unit a workgroup (four: 2-14 % faster or 30 % slower, by size)
+  // Two blocks of rows read x half as often, where they still give every compute unit a
+  // workgroup.  us (one block, two): 16 rows of 14336 -> 4096 17, 25, of 4096 -> 8192 10.4,
+  // 9.7, of 4096 -> 28672 32, 30; 48 rows 32, 40; 21.5, 15; 80, 58.  The gated form takes
+  // two at any size, gates and ups.
   constexpr int kNarrow = PAIR ? 2 : 1;
   const bool narrow = p.I < 32 * kCUs;
   if (p.M <= 16)
