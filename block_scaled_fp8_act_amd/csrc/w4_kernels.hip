@@ -505,35 +505,70 @@ struct W4Few {
   uint16_t *out;          // [M, I]
 };
 
-// Output n of row m from codes less their zero point, as the tiles form it, by one thread:
-// where the sum with the bias is not finite.  The bias makes NaN of an infinite x (the
-// same infinity is added and taken off) and may pass fp32's range where the sum does not.
+// Where the sum with the bias is not finite, the output is formed again from codes less
+// their zero point, as the tiles do it.  The bias makes NaN of an infinite x (the same
+// infinity is added and taken off) and may pass fp32's range where the sum does not.
+// A wave together, a row's outputs one after another; a row with a NaN, as the unused
+// rows of a padded batch may hold, is NaN without them.
+__device__ __forceinline__ bool finite(float v) {
+  return __builtin_fabsf(v) < __builtin_inff();
+}
 template <typename T>
-__device__ __forceinline__ float w4_plain(const W4Few &p, int64_t m, int64_t n) {
+__device__ __forceinline__ float w4_plain(const W4Few &p, int64_t m, int64_t n, int lane) {
   const uint16_t *x = p.x + m * p.ldx;
   const uint8_t *codes = p.w.codes + n * (p.K / 2);
-  const int64_t groups = p.K >> p.w.shift;
+  const int64_t first = n * (p.K >> p.w.shift);
   float acc = 0.0f;
-  for (int64_t g = 0; g < groups; ++g) {
-    const int64_t at = n * groups + g, end = (g + 1) << p.w.shift;
-    const float z = p.w.zeros ? (float)p.w.zeros[at] : 8.0f;
-    float sum = 0.0f;
-    for (int64_t k = g << p.w.shift; k < end; k += 8) {
-      float w[8];
-      decode8(*reinterpret_cast<const uint32_t *>(codes + k / 2), z, w);
-      const v4u v = *reinterpret_cast<const v4u_any *>(x + k);
+#pragma unroll 1
+  for (int64_t k = lane * 8; k < p.K; k += 512) {      // (8 of K are in one group)
+    const int64_t at = first + (k >> p.w.shift);
+    const v4u v = *reinterpret_cast<const v4u_any *>(x + k);
+    float w[8], sum = 0.0f;
+    decode8(*reinterpret_cast<const uint32_t *>(codes + k / 2),
+            p.w.zeros ? (float)p.w.zeros[at] : 8.0f, w);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        sum = __builtin_fmaf(w[2 * j], T::value(v[j] & 0xffff), sum);
-        sum = __builtin_fmaf(w[2 * j + 1], T::value(v[j] >> 16), sum);
-      }
+    for (int j = 0; j < 4; ++j) {
+      sum = __builtin_fmaf(w[2 * j], T::value(v[j] & 0xffff), sum);
+      sum = __builtin_fmaf(w[2 * j + 1], T::value(v[j] >> 16), sum);
     }
     acc = __builtin_fmaf(sum, T::value(p.w.scale[at]), acc);
   }
+  for (int d = 32; d >= 1; d /= 2) acc += __shfl_xor(acc, d);
   return acc;
 }
-__device__ __forceinline__ bool finite(float v) {
-  return __builtin_fabsf(v) < __builtin_inff();
+// Whether row m of x holds a NaN, by a wave.
+template <typename T>
+__device__ __forceinline__ bool w4_nan_row(const W4Few &p, int64_t m, int lane) {
+  const uint16_t *x = p.x + m * p.ldx;
+  bool nan = false;
+#pragma unroll 2
+  for (int64_t k = lane * 8; k < p.K; k += 512) {
+    const v4u v = *reinterpret_cast<const v4u_any *>(x + k);
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      nan |= __builtin_isunordered(T::value(v[j] & 0xffff), T::value(v[j] >> 16));
+  }
+  return __ballot(nan) != 0;
+}
+// v, output n of row m, if it is finite, else that sum (by a whole wave; lanes without an
+// output bring a zero).
+template <typename T>
+__device__ __forceinline__ float w4_finish(const W4Few &p, float v, int m, int64_t n, int lane) {
+  for (uint64_t left = __ballot(!finite(v)); left;) {
+    const int row = __shfl(m, __builtin_ctzll(left));
+    uint64_t same = left & __ballot(m == row);      // the row's
+    left &= ~same;
+    if (w4_nan_row<T>(p, row, lane)) {
+      if (same >> lane & 1) v = __builtin_nanf("");
+      continue;
+    }
+    for (; same; same &= same - 1) {
+      const int from = __builtin_ctzll(same);
+      const float sum = w4_plain<T>(p, row, __shfl((long long)n, from), lane);
+      if (lane == from) v = sum;
+    }
+  }
+  return v;
 }
 
 // R outputs a wave, MT rows of x (M of them there), the K range shared by KS waves.
@@ -610,18 +645,22 @@ __global__ __launch_bounds__(256) void w4_few_kernel(W4Few p) {
   wave_sums<kRows * MT>(acc, red[wave], lane);
   __syncthreads();
   // a thread an output
-  if ((int)threadIdx.x >= kOuts * MT) return;
-  const int m = threadIdx.x % MT, o = threadIdx.x / MT, r = o % R, w0 = o / R * KS;
+  static_assert(kOuts * MT <= 64, "a wave's");
+  if (wave) return;
+  const int m = lane % MT, o = lane / MT, r = o % R, w0 = o / R * KS;
   const int64_t n = n0 + o;
-  if (m >= p.M || n >= p.I) return;
+  const bool there = lane < kOuts * MT && m < p.M && n < p.I;
   float v[kHalves];
 #pragma unroll
   for (int h = 0; h < kHalves; ++h) {
     v[h] = 0.0f;
+    if (there) {
 #pragma unroll
-    for (int i = 0; i < KS; ++i) v[h] += red[w0 + i][(h * R + r) * MT + m];
-    if (!finite(v[h])) v[h] = w4_plain<T>(p, m, n + h * p.I);
+      for (int i = 0; i < KS; ++i) v[h] += red[w0 + i][(h * R + r) * MT + m];
+    }
+    v[h] = w4_finish<T>(p, v[h], m, n + h * p.I, lane);
   }
+  if (!there) return;
   float y = v[0];
   if constexpr (PAIR) y = act_any(p.act, v[0]) * v[1];
   p.out[m * p.I + n] = (uint16_t)T::bits(y);
@@ -823,19 +862,18 @@ __global__ __launch_bounds__(512, MF == 1 ? 4 : 2) void w4_slab_kernel(W4Few p) 
   // a lane of each output's place adds the waves' sums, in order
   for (int e = threadIdx.x; e < kOut * MF * 256; e += kWaves * 64) {
     const int l = e & 63, v = e >> 6;       // v = (block * MF + m) * 4 + r
+    const int m = v / 4 % MF * 16 + 4 * (l >> 4) + v % 4;
+    const int64_t n = n0 + v / (4 * MF) * 16 + (l & 15);
+    const bool there = m < p.M && n < p.I;
     float y[PAIR ? 2 : 1];
 #pragma unroll
     for (int h = 0; h < (PAIR ? 2 : 1); ++h) {
       y[h] = 0.0f;
 #pragma unroll
       for (int i = 0; i < kWaves; ++i) y[h] += sm.red[i][h * kOut * MF * 4 + v][l];
+      y[h] = w4_finish<T>(p, there ? y[h] : 0.0f, m, n + h * p.I, lane);
     }
-    const int m = v / 4 % MF * 16 + 4 * (l >> 4) + v % 4;
-    const int64_t n = n0 + v / (4 * MF) * 16 + (l & 15);
-    if (m >= p.M || n >= p.I) continue;
-#pragma unroll
-    for (int h = 0; h < (PAIR ? 2 : 1); ++h)
-      if (!finite(y[h])) y[h] = w4_plain<T>(p, m, n + h * p.I);
+    if (!there) continue;
     float out = y[0];
     if constexpr (PAIR) out = act_any(p.act, y[0]) * y[1];
     p.out[m * p.I + n] = (uint16_t)T::bits(out);

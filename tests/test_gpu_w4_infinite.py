@@ -66,3 +66,41 @@ def test_w4_largest_x(M, zeros):
     want, tol = ow.product(n64(x), codes.numpy(), n64(scale), None if z is None else z.numpy(), group)
     near(y, want, tol, "bfloat16", "largest")
     assert np.abs(want).max() > 2.0 ** 100 and og.HALF["bfloat16"] == 2.0 ** -8
+
+
+@pytest.mark.parametrize("M", ROWS)
+@pytest.mark.parametrize("group,K", [(32, 96), (128, 14336)])
+@pytest.mark.parametrize("dtype", list(DTYPES))
+def test_w4_rows_of_every_kind_in_one_batch(M, group, K, dtype):
+    """Finite rows, all NaN (as the unused rows of a padded batch), NaN beside an
+    infinity, and infinities of both signs; x a slice with an odd stride."""
+    N = 70
+    t = weights(M, N, K, group, True, dtype)
+    x = torch.randn(M, K, generator=torch.Generator().manual_seed(M)).to(DTYPES[dtype])
+    inf = float("inf")
+    for r in range(M):
+        kind = (r + M) % 5
+        if kind == 1:
+            x[r] = float("nan")
+        elif kind == 2:
+            x[r, 40], x[r, K - 1] = inf, float("nan")
+        elif kind == 3:
+            x[r, 3], x[r, K - 2] = inf, -inf
+        elif kind == 4:
+            x[r, K - 1] = -inf
+    wide = torch.full((M, K + 3), float("nan"), dtype=x.dtype, device=dev())
+    wide[:, :K] = x.to(dev())
+    y = n64(fb.w4_linear(wide[:, :K], *on(t)))
+    values = ow.values(t[0].numpy(), n64(t[1]), t[2].numpy(), group)
+    for r in range(M):
+        with np.errstate(invalid="ignore"):
+            want = (n64(x)[r] * values).sum(1)
+        if np.isfinite(want).all():
+            want, tol = ow.product(n64(x)[r:r + 1], t[0].numpy(), n64(t[1]), t[2].numpy(), group)
+            tol = tol + og.HALF[dtype] * (np.abs(want) + tol) + og.TINY[dtype]
+            assert np.all(np.abs(y[r:r + 1] - want) <= tol), r
+        else:
+            assert np.array_equal(y[r], want, equal_nan=True), r
+    h = n64(fb.w4_gated_linear(wide[:, :K], *on(t)))
+    assert np.isnan(h[[(r + M) % 5 in (1, 2) for r in range(M)]]).all()
+    assert np.isfinite(h[[(r + M) % 5 == 0 for r in range(M)]]).all()
